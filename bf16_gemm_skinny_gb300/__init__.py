@@ -10,6 +10,8 @@ from ._native import (  # noqa: F401
     BIAS_COLUMN,
     BIAS_NONE,
     BIAS_ROW,
+    CACHE_BF16,
+    CACHE_E4M3,
     COL_MAJOR,
     FP8_E4M3,
     FP8_E5M2,
@@ -17,7 +19,11 @@ from ._native import (  # noqa: F401
     OUT_F32,
     ROW_MAJOR,
     BskError,
+    chunk_attention,
+    chunk_attention_enqueue,
+    decode_attention,
     decode_attention_bf16,
+    decode_attention_enqueue,
     gemm_f16,
     gemm_f16_colmajor,
     gemm_f16_colmajor_enqueue,
@@ -27,6 +33,10 @@ from ._native import (  # noqa: F401
     gemm_fp8_enqueue,
     gemv_bf16,
     gemv_bf16_enqueue,
+    kv_cache_append,
+    kv_cache_append_enqueue,
+    kv_cache_gather,
+    kv_cache_gather_enqueue,
     last_error,
     library_path,
     set_option,

@@ -54,6 +54,8 @@ EXPORTS = (
     "bsk_stream_check", "bsk_last_error", "bsk_status_string", "bsk_version", "gemm_f16_colmajor_noalloc",
     "decode_attention_bf16", "bsk_decode_attention_bf16_enqueue", "gemm_f16", "bsk_gemm_f16_enqueue",
     "gemm_fp8", "bsk_gemm_fp8_enqueue", "gemm_f16_colmajor_host", "gemv_bf16_host",
+    "kv_cache_append", "bsk_kv_cache_append_enqueue", "kv_cache_gather", "bsk_kv_cache_gather_enqueue",
+    "chunk_attention", "bsk_chunk_attention_enqueue", "decode_attention", "bsk_decode_attention_enqueue",
 )
 # Tuning options and test hooks (csrc/bsk_tuning.h): exported for the tests and
 # the benchmark, not part of the C ABI.
@@ -63,6 +65,7 @@ COL_MAJOR, ROW_MAJOR = 0, 1
 BIAS_NONE, BIAS_ROW, BIAS_COLUMN = 0, 1, 2
 FP8_E4M3, FP8_E5M2 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+CACHE_BF16, CACHE_E4M3 = 0, 1
 
 
 class BskError(RuntimeError):
@@ -104,6 +107,20 @@ def load():
             getattr(lib, name).restype = i
         for name in ("decode_attention_bf16", "bsk_decode_attention_bf16_enqueue"):
             getattr(lib, name).argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, i, i, ctypes.c_float, i, p]
+            getattr(lib, name).restype = i
+        for name in ("kv_cache_append", "bsk_kv_cache_append_enqueue"):
+            getattr(lib, name).argtypes = [i, p, p, p, p, p, i, p, i, p, p, p, i, i, i, i, i, i, i, p]
+            getattr(lib, name).restype = i
+        for name in ("kv_cache_gather", "bsk_kv_cache_gather_enqueue"):
+            getattr(lib, name).argtypes = [i, p, p, p, p, p, p, p, p, p, i, i, i, i, i, i, i, p]
+            getattr(lib, name).restype = i
+        for name in ("chunk_attention", "bsk_chunk_attention_enqueue"):
+            getattr(lib, name).argtypes = [i, p, p, p, p, p, i, p, i, p, p, p, i, i, i, i, i, i, i, i, i, i,
+                                           ctypes.c_float, i, i, i, p]
+            getattr(lib, name).restype = i
+        for name in ("decode_attention", "bsk_decode_attention_enqueue"):
+            getattr(lib, name).argtypes = [i, p, p, p, p, p, i, p, i, p, p, i, i, i, i, i, i, i, i,
+                                           ctypes.c_float, i, i, i, p]
             getattr(lib, name).restype = i
         lib.bsk_stream_check.argtypes = [p]
         lib.bsk_stream_check.restype = i
@@ -262,6 +279,102 @@ def decode_attention_bf16_enqueue(q, k_cache, v_cache, block_tables, seq_lens, o
         _addr(q), _addr(k_cache), _addr(v_cache), _addr(block_tables), _addr(seq_lens), _addr(out), num_seqs,
         num_q_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks, max_seq_len, softmax_scale,
         num_segments, _stream(stream)))
+
+
+def kv_cache_append(cache_type: int, k_cache, v_cache, k_scales, v_scales, k, k_stride: int, v, v_stride: int,
+                    cu_tokens, block_tables, seq_lens, num_seqs: int, num_tokens: int, num_kv_heads: int,
+                    head_dim: int, block_size: int, max_blocks: int, num_blocks: int, stream=None) -> None:
+    """New tokens' keys and values into a paged cache, BF16 or quantised to E4M3 with a power-of-two scale per row
+    (see include/bsk.h); blocks until done."""
+    _check(load().kv_cache_append(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
+                                  _addr(k), k_stride, _addr(v), v_stride, _addr(cu_tokens), _addr(block_tables),
+                                  _addr(seq_lens), num_seqs, num_tokens, num_kv_heads, head_dim, block_size,
+                                  max_blocks, num_blocks, _stream(stream)))
+
+
+def kv_cache_append_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, k, k_stride: int, v,
+                            v_stride: int, cu_tokens, block_tables, seq_lens, num_seqs: int, num_tokens: int,
+                            num_kv_heads: int, head_dim: int, block_size: int, max_blocks: int, num_blocks: int,
+                            stream=None) -> None:
+    """Asynchronous variant of kv_cache_append (check with stream_check)."""
+    _check(load().bsk_kv_cache_append_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
+                                              _addr(v_scales), _addr(k), k_stride, _addr(v), v_stride,
+                                              _addr(cu_tokens), _addr(block_tables), _addr(seq_lens), num_seqs,
+                                              num_tokens, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
+                                              _stream(stream)))
+
+
+def kv_cache_gather(cache_type: int, k_cache, v_cache, k_scales, v_scales, k_out, v_out, cu_tokens, block_tables,
+                    seq_lens, num_seqs: int, num_tokens: int, num_kv_heads: int, head_dim: int, block_size: int,
+                    max_blocks: int, num_blocks: int, stream=None) -> None:
+    """The last tokens of each sequence read back from the cache as BF16; blocks until done."""
+    _check(load().kv_cache_gather(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
+                                  _addr(k_out), _addr(v_out), _addr(cu_tokens), _addr(block_tables), _addr(seq_lens),
+                                  num_seqs, num_tokens, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
+                                  _stream(stream)))
+
+
+def kv_cache_gather_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, k_out, v_out, cu_tokens,
+                            block_tables, seq_lens, num_seqs: int, num_tokens: int, num_kv_heads: int, head_dim: int,
+                            block_size: int, max_blocks: int, num_blocks: int, stream=None) -> None:
+    """Asynchronous variant of kv_cache_gather (check with stream_check)."""
+    _check(load().bsk_kv_cache_gather_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
+                                              _addr(v_scales), _addr(k_out), _addr(v_out), _addr(cu_tokens),
+                                              _addr(block_tables), _addr(seq_lens), num_seqs, num_tokens, num_kv_heads,
+                                              head_dim, block_size, max_blocks, num_blocks, _stream(stream)))
+
+
+def chunk_attention(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out, out_stride: int,
+                    cu_tokens, block_tables, seq_lens, num_seqs: int, num_tokens: int, max_chunk: int,
+                    num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int, max_blocks: int,
+                    num_blocks: int, max_seq_len: int, softmax_scale: float, window: int = 0, sinks: int = 0,
+                    num_segments: int = 0, stream=None) -> None:
+    """Attention of a chunk of new tokens per sequence over a paged cache, causal, with an optional sliding window and
+    sinks (see include/bsk.h); blocks until done."""
+    _check(load().chunk_attention(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
+                                  _addr(q), q_stride, _addr(out), out_stride, _addr(cu_tokens), _addr(block_tables),
+                                  _addr(seq_lens), num_seqs, num_tokens, max_chunk, num_q_heads, num_kv_heads,
+                                  head_dim, block_size, max_blocks, num_blocks, max_seq_len, softmax_scale, window,
+                                  sinks, num_segments, _stream(stream)))
+
+
+def chunk_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out,
+                            out_stride: int, cu_tokens, block_tables, seq_lens, num_seqs: int, num_tokens: int,
+                            max_chunk: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                            max_blocks: int, num_blocks: int, max_seq_len: int, softmax_scale: float,
+                            window: int = 0, sinks: int = 0, num_segments: int = 0, stream=None) -> None:
+    """Asynchronous variant of chunk_attention (check with stream_check)."""
+    _check(load().bsk_chunk_attention_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
+                                              _addr(v_scales), _addr(q), q_stride, _addr(out), out_stride,
+                                              _addr(cu_tokens), _addr(block_tables), _addr(seq_lens), num_seqs,
+                                              num_tokens, max_chunk, num_q_heads, num_kv_heads, head_dim, block_size,
+                                              max_blocks, num_blocks, max_seq_len, softmax_scale, window, sinks,
+                                              num_segments, _stream(stream)))
+
+
+def decode_attention(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out, out_stride: int,
+                     block_tables, seq_lens, num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                     block_size: int, max_blocks: int, num_blocks: int, max_seq_len: int, softmax_scale: float,
+                     window: int = 0, sinks: int = 0, num_segments: int = 0, stream=None) -> None:
+    """Attention of one new token per sequence over a paged cache (chunk_attention's form for single tokens); blocks
+    until done."""
+    _check(load().decode_attention(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
+                                   _addr(q), q_stride, _addr(out), out_stride, _addr(block_tables), _addr(seq_lens),
+                                   num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
+                                   max_seq_len, softmax_scale, window, sinks, num_segments, _stream(stream)))
+
+
+def decode_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out,
+                             out_stride: int, block_tables, seq_lens, num_seqs: int, num_q_heads: int,
+                             num_kv_heads: int, head_dim: int, block_size: int, max_blocks: int, num_blocks: int,
+                             max_seq_len: int, softmax_scale: float, window: int = 0, sinks: int = 0,
+                             num_segments: int = 0, stream=None) -> None:
+    """Asynchronous variant of decode_attention (check with stream_check)."""
+    _check(load().bsk_decode_attention_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
+                                               _addr(v_scales), _addr(q), q_stride, _addr(out), out_stride,
+                                               _addr(block_tables), _addr(seq_lens), num_seqs, num_q_heads,
+                                               num_kv_heads, head_dim, block_size, max_blocks, num_blocks, max_seq_len,
+                                               softmax_scale, window, sinks, num_segments, _stream(stream)))
 
 
 def stream_check(stream=None) -> None:

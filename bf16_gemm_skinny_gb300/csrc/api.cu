@@ -22,6 +22,7 @@
 #include "bsk.h"
 #include "bsk_internal.h"
 #include "bsk_tuning.h"
+#include "kv_internal.h"
 
 namespace {
 
@@ -125,6 +126,8 @@ int check_status_word()
         *g_status_host = 0;
         if (code == bsk::kDevErrBadIndex)
             return fail(BSK_ERR_INVALID_ARG, "a block-table entry was out of range; its tokens were skipped");
+        if (code == bsk::kDevErrChunkTooLong)
+            return fail(BSK_ERR_INVALID_ARG, "a sequence has more new tokens than max_chunk; the output is undefined");
         return fail(BSK_ERR_TIMEOUT, "a device-side wait gave up (site %d); the output is undefined",
                     code - bsk::kDevErrTimeoutBase);
     }
@@ -1100,6 +1103,15 @@ int enqueue_gemm_f16_colmajor_fixed(const uint16_t* A, const uint16_t* B, uint16
     return enqueue_gemm_general(0, 0, A, M > 1 ? M : 1, B, K > 1 ? K : 1, C, M > 1 ? M : 1, M, N, K, nullptr, 0,
                                 stream, &scratch);
 }
+
+int api_prepare(int* sms, int** status)
+{
+    const int st = prepare_device(sms);
+    *status = g_status_dev;
+    return st;
+}
+
+int api_sync_and_check(cudaStream_t s) { return sync_and_check(s); }
 
 void record_error(const char* msg)
 {

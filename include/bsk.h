@@ -9,7 +9,11 @@
  *   gemv_bf16          BF16 linear layer y = x W^T: the HBM-bound decode GEMV for
  *                      n <= 3 tokens (CUDA cores), the tensor-core GEMM for
  *                      larger n (skinny decode batches, prefill projections);
- *   decode_attention_bf16  split-KV decode attention over a paged BF16 KV cache.
+ *   decode_attention_bf16  split-KV decode attention over a paged BF16 KV cache;
+ *   kv_cache_append    new tokens' keys and values into a paged cache, in BF16 or
+ *                      quantised to E4M3; kv_cache_gather reads them back;
+ *   chunk_attention    attention of a chunk of new tokens over such a cache, and
+ *   decode_attention   of single tokens, with an optional sliding window and sinks.
  *
  * Conventions shared by every call:
  *  - Matrix pointers are DEVICE pointers (cudaMalloc / torch CUDA tensors) to
@@ -191,6 +195,106 @@ int decode_attention_bf16(const uint16_t* q, const uint16_t* k_cache, const uint
                           int num_q_heads, int num_kv_heads, int head_dim, int block_size, int max_blocks,
                           int num_blocks, int max_seq_len, float softmax_scale, int num_segments, void* stream);
 
+/* Element type of a paged KV cache. */
+typedef enum bsk_cache_type {
+    BSK_CACHE_BF16 = 0,
+    BSK_CACHE_E4M3 = 1 /* OCP E4M3 codes and one E8M0 scale per row (token x KV head) */
+} bsk_cache_type;
+
+/*
+ * A paged KV cache, as the four calls below take it:
+ *
+ *   k_cache, v_cache    [num_blocks, block_size, num_kv_heads, head_dim] BF16, or
+ *                       E4M3 codes (cache_type, a bsk_cache_type)
+ *   k_scales, v_scales  [num_blocks, block_size, num_kv_heads] bytes, E4M3 caches only
+ *                       (else NULL): b stands for 2^(b - 127), 255 for NaN
+ *   block_tables        [num_seqs, max_blocks] int32: physical block of each
+ *                       block_size-token chunk of a sequence
+ *   seq_lens            [num_seqs] int32: tokens of each sequence, its new ones included
+ *   cu_tokens           [num_seqs + 1] int32, not decreasing: the new tokens of sequence
+ *                       s are rows cu_tokens[s] .. cu_tokens[s+1] - 1 of the token arrays
+ *                       and the last ones of the sequence: with n of them, row
+ *                       cu_tokens[s] + i is position seq_lens[s] - n + i.  NULL: one new
+ *                       token per sequence (num_tokens == num_seqs)
+ *
+ * All are device pointers.  head_dim is 64, 128 or 256.  The caches and the
+ * token arrays are 16-byte aligned (E4M3 caches too), the strides (elements
+ * between the rows of consecutive tokens; the heads of a token lie side by
+ * side) multiples of 8 and at least heads * head_dim, so that q, k and v may be
+ * parts of one projection's output.  A block-table entry outside
+ * [0, num_blocks) that a call needs, or a position past max_blocks blocks, is
+ * skipped and reported as BSK_ERR_INVALID_ARG by the blocking call (or the next
+ * bsk_stream_check); entries that no token needs are not read.  Token rows
+ * outside every sequence (past cu_tokens[num_seqs]) are left alone.
+ */
+
+/*
+ * Writes the new tokens' K and V rows into their pages.  k and v are BF16,
+ * [num_tokens, num_kv_heads, head_dim] with k_stride / v_stride elements
+ * between tokens.  BSK_CACHE_E4M3 quantises each row x as it is written: with
+ * a = max|x|, its scale is 2^e with the least integer e such that
+ * a <= 448 * 2^e, kept within [-117, 120], and its codes are x * 2^-e rounded to
+ * nearest even (at e = 120 to at most 240 in magnitude); the values the codes
+ * stand for are finite BF16 values, so reading them back as BF16 is exact.  A row with an Inf or a NaN gets the scale byte 255.
+ * Only the rows of the new tokens are written.  The new tokens of a call have
+ * distinct places in the cache.  Blocking; bsk_kv_cache_append_enqueue only launches.
+ */
+int kv_cache_append(int cache_type, void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales,
+                    const uint16_t* k, int k_stride, const uint16_t* v, int v_stride, const int32_t* cu_tokens,
+                    const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int num_tokens,
+                    int num_kv_heads, int head_dim, int block_size, int max_blocks, int num_blocks, void* stream);
+
+/*
+ * Reads cached tokens back as BF16: row cu_tokens[s] + i of k_out and v_out
+ * ([num_tokens, num_kv_heads, head_dim], contiguous) is position
+ * seq_lens[s] - n + i of sequence s, so n = seq_lens[s] reads a whole sequence.
+ * A position that does not exist (negative, or in a bad block) gives zeros.
+ * Blocking; bsk_kv_cache_gather_enqueue only launches.
+ */
+int kv_cache_gather(int cache_type, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
+                    const uint8_t* v_scales, uint16_t* k_out, uint16_t* v_out, const int32_t* cu_tokens,
+                    const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int num_tokens,
+                    int num_kv_heads, int head_dim, int block_size, int max_blocks, int num_blocks, void* stream);
+
+/*
+ * Attention of the new tokens over the cache, which already holds their own
+ * keys and values (kv_cache_append first).  The query at position p sees the
+ * positions t <= p with t > p - window or t < sinks; window 0 means all t <= p.
+ *     out = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q.k_t - max)
+ * over the visible t, per query head; query head h reads KV head
+ * h / (num_q_heads / num_kv_heads), any whole ratio.  A token that sees nothing
+ * (a negative position, only bad blocks), or whose visible scores are all -inf,
+ * gives zeros; an Inf or NaN in a key or value that a token does not see leaves
+ * its output alone.
+ *
+ *   q    [num_tokens, num_q_heads, head_dim] BF16, q_stride elements between tokens
+ *   out  the same shape, BF16, out_stride elements between tokens
+ *   max_chunk     an upper bound of the new tokens per sequence (host side; a longer
+ *                 one is reported like a bad block-table entry, its output undefined)
+ *   max_seq_len   an upper bound of seq_lens (longer ones count as max_seq_len)
+ *   softmax_scale finite; 1/sqrt(head_dim) is usual
+ *   num_segments  parts that the visible positions are split into when one call has
+ *                 too few tokens to fill the GPU, 1..256; 0 = automatic
+ *
+ * FP32 scores, statistics and sums; the weights are rounded to BF16 for the
+ * tensor cores, the output once, to nearest even.  With more than one segment a
+ * workspace of num_tokens * num_q_heads * segments * (head_dim + 2) floats is
+ * allocated in stream order.  Blocking; the _enqueue forms only launch.
+ * decode_attention is the form for one new token per sequence (q and out have
+ * num_seqs rows).
+ */
+int chunk_attention(int cache_type, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
+                    const uint8_t* v_scales, const uint16_t* q, int q_stride, uint16_t* out, int out_stride,
+                    const int32_t* cu_tokens, const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                    int num_tokens, int max_chunk, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                    int max_blocks, int num_blocks, int max_seq_len, float softmax_scale, int window, int sinks,
+                    int num_segments, void* stream);
+int decode_attention(int cache_type, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
+                     const uint8_t* v_scales, const uint16_t* q, int q_stride, uint16_t* out, int out_stride,
+                     const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int num_q_heads,
+                     int num_kv_heads, int head_dim, int block_size, int max_blocks, int num_blocks,
+                     int max_seq_len, float softmax_scale, int window, int sinks, int num_segments, void* stream);
+
 /*
  * gemm_f16_colmajor for callers that cannot allocate device memory during a
  * call (for example a serving process whose own allocator reserved all free
@@ -267,6 +371,30 @@ int bsk_decode_attention_bf16_enqueue(const uint16_t* q, const uint16_t* k_cache
                                       int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                       int max_blocks, int num_blocks, int max_seq_len, float softmax_scale,
                                       int num_segments, void* stream);
+
+int bsk_kv_cache_append_enqueue(int cache_type, void* k_cache, void* v_cache, uint8_t* k_scales,
+                                uint8_t* v_scales, const uint16_t* k, int k_stride, const uint16_t* v,
+                                int v_stride, const int32_t* cu_tokens, const int32_t* block_tables,
+                                const int32_t* seq_lens, int num_seqs, int num_tokens, int num_kv_heads,
+                                int head_dim, int block_size, int max_blocks, int num_blocks, void* stream);
+int bsk_kv_cache_gather_enqueue(int cache_type, const void* k_cache, const void* v_cache,
+                                const uint8_t* k_scales, const uint8_t* v_scales, uint16_t* k_out,
+                                uint16_t* v_out, const int32_t* cu_tokens, const int32_t* block_tables,
+                                const int32_t* seq_lens, int num_seqs, int num_tokens, int num_kv_heads,
+                                int head_dim, int block_size, int max_blocks, int num_blocks, void* stream);
+int bsk_chunk_attention_enqueue(int cache_type, const void* k_cache, const void* v_cache,
+                                const uint8_t* k_scales, const uint8_t* v_scales, const uint16_t* q,
+                                int q_stride, uint16_t* out, int out_stride, const int32_t* cu_tokens,
+                                const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                                int num_tokens, int max_chunk, int num_q_heads, int num_kv_heads, int head_dim,
+                                int block_size, int max_blocks, int num_blocks, int max_seq_len,
+                                float softmax_scale, int window, int sinks, int num_segments, void* stream);
+int bsk_decode_attention_enqueue(int cache_type, const void* k_cache, const void* v_cache,
+                                 const uint8_t* k_scales, const uint8_t* v_scales, const uint16_t* q,
+                                 int q_stride, uint16_t* out, int out_stride, const int32_t* block_tables,
+                                 const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                 int head_dim, int block_size, int max_blocks, int num_blocks, int max_seq_len,
+                                 float softmax_scale, int window, int sinks, int num_segments, void* stream);
 
 /* Synchronise `stream`, then report BSK_ERR_CUDA for a pending CUDA error or
  * BSK_ERR_TIMEOUT if a device-side wait gave up since the last check. */
