@@ -25,6 +25,28 @@ int fail(int status, const char* fmt, ...)
     return status;
 }
 
+// Stream-ordered workspace, freed in stream order after use.
+struct Workspace {
+    void* ptr = nullptr;
+    cudaStream_t s;
+    explicit Workspace(cudaStream_t stream) : s(stream) {}
+    Workspace(const Workspace&) = delete;
+    Workspace& operator=(const Workspace&) = delete;
+    ~Workspace()
+    {
+        if (ptr != nullptr) cudaFreeAsync(ptr, s);
+    }
+    cudaError_t take(size_t bytes)
+    {
+        const cudaError_t e = cudaMallocAsync(&ptr, bytes, s);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            ptr = nullptr;
+        }
+        return e;
+    }
+};
+
 struct Span {
     const void* p;
     long long bytes;
@@ -205,6 +227,16 @@ int enqueue_attention(bsk::KvAttnLaunch& a, int num_segments, cudaStream_t s)
     const long long limit_us = bsk_get_option(BSK_OPT_WAIT_LIMIT_US);
     if (limit_us > 0) a.wait_limit_ns = static_cast<unsigned long long>(limit_us) * 1000ull;
     a.pdl = bsk_get_option(BSK_OPT_PDL) != 1;
+    a.segments = num_segments > 0 ? num_segments : bsk::kv_attention_segments(a);
+    Workspace ws(s);
+    const size_t bytes = bsk::kv_attention_workspace(a);
+    if (bytes > 0) {
+        const cudaError_t e = ws.take(bytes);
+        if (e != cudaSuccess)
+            return fail(BSK_ERR_NO_MEMORY, "cudaMallocAsync(%zu bytes) for a workspace failed: %s", bytes,
+                        cudaGetErrorString(e));
+        a.workspace = static_cast<float*>(ws.ptr);
+    }
     char msg[512] = "";
     if (bsk::launch_kv_attention(a, s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
     return BSK_OK;

@@ -65,6 +65,9 @@ struct KvAttnLaunch {
     unsigned long long wait_limit_ns = 2000000000ull;
     bool pdl = true;
 };
+// Segments that a call without a choice of its own splits the keys into (>= 1).
+int kv_attention_segments(const KvAttnLaunch& a);
+size_t kv_attention_workspace(const KvAttnLaunch& a);
 int launch_kv_attention(const KvAttnLaunch& a, cudaStream_t stream, char* msg, size_t msg_len);
 
 // What the entry points of kv_api.cu share with api.cu: the device check (sets
