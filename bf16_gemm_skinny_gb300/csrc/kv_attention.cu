@@ -10,12 +10,13 @@
 // then stay below 2^8, which costs no precision), so O is seldom touched.
 //
 // A CTA has 128 query rows (token x query head, the heads of one KV head side by
-// side, so they share the keys) and walks 128-position tiles of the keys:
-//   S = Q K^T   tcgen05.mma, Q and K from shared memory, S in TMEM, two buffers
-//   P = 2^(..)  eight warps, S from TMEM to registers and P back, as BF16, over S
+// side, so they share the keys) and walks the keys in tiles of kTile positions:
+//   S = Q K^T   tcgen05.mma, Q from TMEM, K from shared memory, S in TMEM (two buffers)
+//   P = 2^(..)  eight warps, S from TMEM to registers and P back, 16 bits, over S
 //   O += P V    tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // The MMAs of S for tile j+1 and of PV for tile j-1 run while the warps work on
-// tile j.  TMEM: 2 x 128 columns of S, head_dim columns of O.
+// tile j.  Q lies in TMEM, so that shared memory holds nothing but keys and values
+// on their way and an MMA reads one operand from it.
 #include <cmath>
 #include <cstdio>
 
@@ -40,7 +41,17 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], A 128 x 16 BF16, two values per column.
+// Cache rows of one KV head, a multiple of 8 of them, from the 4-D view below.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], A 128 x 16 16-bit values, two values per column.
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate)
 {
@@ -62,6 +73,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -115,6 +135,19 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two E4M3 codes -> two FP16 values (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    return h;
+}
 // Two E4M3 codes -> their values.
 __device__ __forceinline__ float2 e4m3x2_values(uint32_t two)
 {
@@ -126,40 +159,52 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t two)
         : "r"(h));
     return f;
 }
-// 16 bytes global -> shared, asynchronous; `in` false: zeros.
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool in)
+// mbar_wait for waits that come several times a microsecond: it looks at the
+// clock and the abort flag only after many tries (each try suspends the warp for
+// a while by itself).
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, const WaitCtl& w, int site)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, w, site);
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // ---------------------------------------------------------------------------
 // Geometry
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;        // query rows per CTA (the M of the MMAs)
-constexpr int kTile = 128;        // key positions per tile
-constexpr int kProducers = 128;   // threads of warps 0..3
-constexpr int kSoftmax = 256;     // threads of warps 4..11
-constexpr int kThreads = kProducers + kSoftmax + 32;   // warp 12 issues the MMAs
-constexpr int kStageBytes = 16384;
-constexpr int kSlots = 8;         // tiles whose masks and scales are kept
-constexpr int kStaging = 4;       // E4M3: stages of raw codes on their way
+constexpr int kSoftmaxWarps = 8;  // warps 4..11
+constexpr int kConvertWarps = 4;  // warps 12..15, E4M3 only
+constexpr int kSlots = 8;         // tiles whose masks (and scales) are kept
 
-enum AttnSite : int { kSiteKvEmpty = 0x30, kSiteKvFull, kSiteKvQ, kSiteKvScores, kSiteKvWeights, kSiteKvOutput, kSiteKvDrain };
+// Warps 0..3: keys' loads, MMAs, values' loads, E4M3 scales.
+enum AttnWarp : int { kWarpK = 0, kWarpMma = 1, kWarpV = 2, kWarpScales = 3 };
+enum AttnSite : int {
+    kSiteKvEmpty = 0x30, kSiteKvFull, kSiteKvQ, kSiteKvScores, kSiteKvWeights, kSiteKvOutput, kSiteKvDrain,
+    kSiteKvRaw, kSiteKvMeta
+};
 
 template <bool E4M3, int HD>
 struct Geo {
     static constexpr int kBlocks = HD / 64;                    // 64-element (128-byte) blocks of a row
-    static constexpr int kQBytes = kRows * HD * 2;
-    // K stage: 128 positions x 64 dimensions; V stage: kVTok positions x HD
-    static constexpr int kVTok = kStageBytes / (HD * 2);
-    static constexpr int kStages = HD == 256 ? (E4M3 ? 7 : 9) : (E4M3 ? 8 : 10);
-    static constexpr int kStagingBytes = E4M3 ? kStaging * 8192 : 0;
-    static constexpr int kScaleBytes = E4M3 ? kSlots * kTile * 12 : 0;   // K and V factors, row indexes
-    static constexpr int kMisc = kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + (2 * kStages + 8) * 8 + 16;
-    static constexpr int kBytes = 1024 + kQBytes + kStages * kStageBytes + kStagingBytes + kScaleBytes + kMisc;
+    // Positions per tile.  TMEM's 512 columns hold two S tiles, Q (HD / 2 columns)
+    // and O (HD): with HD = 256 that leaves 2 x 64.
+    static constexpr int kTile = HD == 256 ? 64 : 128;
+    static constexpr int kCols = kTile / 2;                    // S columns per softmax warp
+    static constexpr int kColQ = 2 * kTile, kColO = HD == 64 ? 320 : 512 - HD;   // TMEM columns of Q and O
+    // A stage: one tile's keys or values in 16 bits, [kTile / 8][kBlocks] swizzle atoms
+    // of 8 rows x 128 bytes.  Keys are read as a K-major operand (8-row groups
+    // kBlocks * 1024 bytes apart), values as an MN-major one (64-dimension blocks 1024
+    // bytes apart, groups as before): one layout and one kind of load serves both.
+    static constexpr int kStageBytes = kTile * HD * 2;
+    static constexpr int kStages = E4M3 && HD != 64 ? 2 : 3;   // of keys, and of values
+    static constexpr int kRawBytes = E4M3 ? kTile * HD : 0;    // a tile's codes, rows side by side
+    static constexpr int kRawStages = E4M3 ? 2 : 0;
+    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kBars = 4 * kStages + 4 * kRawStages + 2 * kSlots + 8;
+    static constexpr int kScaleBytes = E4M3 ? kSlots * (kTile * 8 + 8) : 0;
+    static constexpr int kMisc = kScaleBytes + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
+    static constexpr int kBytes = 1024 + 2 * kStages * kStageBytes + 2 * kRawStages * kRawBytes + kMisc;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
 
@@ -170,6 +215,7 @@ struct AttnParams {
     long long q_stride, out_stride;
     int num_q_heads, group, max_chunk, max_seq_len;
     int tiles, segments;          // row tiles per sequence and KV head, key segments per tile
+    int box;                      // rows per TMA box, or 4: pages of an odd size, gathers only
     float scale_log2;             // |softmax scale| * log2(e), > 0
     uint32_t q_sign;              // 0x80008000 for a negative scale
     int window, sinks;
@@ -178,16 +224,34 @@ struct AttnParams {
     unsigned long long wait_limit_ns;
 };
 
+// Tensor maps of the cache.  Gathers see it as [num_blocks * block_size] rows of
+// heads * HD values.  Boxes are `box` rows of one head: of a BF16 cache, seen as
+// [rows / 8][heads * HD / 64][8][64], as the stages want them, of an E4M3 cache, seen
+// as for gathers, row after row.
+struct KvMaps {
+    CUtensorMap k_box, v_box, k_row, v_row;
+};
+
 // The key tiles that some row of a CTA sees: those of the sinks, then those from
 // the window's first on.  A position holds a key when it is below kv_end and not
 // between sink_end and lo.
+template <int kTile>
 struct Keys {
     int sink_tiles, lo_tile;      // tile i lies at i, or at i - sink_tiles + lo_tile
     int begin, end;               // this segment's tiles
     int lo, sink_end, kv_end;
     __device__ __forceinline__ int base(int i) const { return (i < sink_tiles ? i : i - sink_tiles + lo_tile) * kTile; }
     __device__ __forceinline__ bool holds(int t) const { return t < kv_end && (t >= lo || t < sink_end); }
+    // all of t .. t + n - 1 hold a key / none does
+    __device__ __forceinline__ bool all(int t, int n) const { return t + n <= kv_end && (t >= lo || t + n <= sink_end); }
+    __device__ __forceinline__ bool none(int t, int n) const { return t >= kv_end || (t >= sink_end && t + n <= lo); }
 };
+
+// The k lowest of 64 bits.
+__device__ __forceinline__ unsigned long long low_bits(int k)
+{
+    return k <= 0 ? 0ull : (k >= 64 ? ~0ull : (1ull << k) - 1);
+}
 
 // ---------------------------------------------------------------------------
 // One row by one warp, in FP32: for rows whose O is not finite although their
@@ -245,10 +309,11 @@ __device__ __forceinline__ void row_add(const KvBatch& b, const int32_t* table, 
 }
 
 template <bool E4M3, int HD>
-__device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* table, const Keys& keys, int kvh, int token,
+__device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* table, const Keys<Geo<E4M3, HD>::kTile>& keys, int kvh, int token,
                                         int head, int pos, int seg)
 {
     constexpr int EPL = HD / 32;
+    constexpr int kTile = Geo<E4M3, HD>::kTile;
     const int lane = threadIdx.x & 31;
     float q[EPL], o[EPL];
     load_slice<false, EPL>(p.q, token * p.q_stride + static_cast<long long>(head) * HD + lane * EPL, q);
@@ -286,36 +351,46 @@ __device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* tabl
 // The kernel
 // ---------------------------------------------------------------------------
 template <bool E4M3, int HD>
-__global__ void __launch_bounds__(kThreads, 1)
-    kv_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
+    kv_attention_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnParams p)
 {
     using G = Geo<E4M3, HD>;
     constexpr int S = G::kStages;
-    constexpr int NB = G::kBlocks;      // K stages of a tile
-    constexpr int VT = G::kVTok;
-    constexpr uint32_t kIdescS = idesc_f16(true, false, false, kRows, kTile);
-    constexpr uint32_t kIdescO = idesc_f16(true, false, true, kRows, HD);
+    constexpr int RS = E4M3 ? G::kRawStages : 1;
+    constexpr int NB = G::kBlocks;
+    constexpr int kTile = G::kTile;
+    constexpr int C = G::kCols;
+    constexpr uint32_t kIdescS = idesc_f16(!E4M3, false, false, kRows, kTile);
+    constexpr uint32_t kIdescO = idesc_f16(!E4M3, false, true, kRows, HD);
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* sQ = smem;
-    uint8_t* ring = sQ + G::kQBytes;
-    uint8_t* staging = ring + S * kStageBytes;
-    float* s_kf = reinterpret_cast<float*>(staging + G::kStagingBytes);   // E4M3: [kSlots][kTile] K scales
-    float* s_vf = s_kf + (E4M3 ? kSlots * kTile : 0);                     //       V scales
-    int* s_row = reinterpret_cast<int*>(s_vf + (E4M3 ? kSlots * kTile : 0));   //  cache rows (-1: none)
-    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_row + (E4M3 ? kSlots * kTile : 0));   // [kSlots][4] positions that hold a key
-    float* s_max = reinterpret_cast<float*>(s_mask + kSlots * 4);         // [2][2][kRows]
-    int* s_flag = reinterpret_cast<int*>(s_max + 4 * kRows);              // [kRows] rows to repair
+    uint8_t* s_k = smem;                                            // [S] keys
+    uint8_t* s_v = s_k + S * G::kStageBytes;                        // [S] values
+    uint8_t* r_k = s_v + S * G::kStageBytes;                        // E4M3: [RS] keys' codes
+    uint8_t* r_v = r_k + G::kRawStages * G::kRawBytes;              //       [RS] values' codes
+    float* s_kf = reinterpret_cast<float*>(r_v + G::kRawStages * G::kRawBytes);   // E4M3: [kSlots][kTile] K scales
+    float* s_vf = s_kf + (E4M3 ? kSlots * kTile : 0);               //       V scales
+    int2* s_exp = reinterpret_cast<int2*>(s_vf + (E4M3 ? kSlots * kTile : 0));    // [kSlots] V scales' range
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_exp + (E4M3 ? kSlots : 0));  // [kSlots][4] positions that hold a key
+    float* s_max = reinterpret_cast<float*>(s_mask + kSlots * 4);   // [2][2][kRows]
+    int* s_flag = reinterpret_cast<int*>(s_max + 4 * kRows);        // [kRows] rows to repair
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_flag + kRows);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::kBars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    const uint32_t full0 = smem_u32(bars);          // S: stage filled
-    const uint32_t empty0 = full0 + 8 * S;          // S: stage read
-    const uint32_t q_full = empty0 + 8 * S;         // Q in shared memory
-    const uint32_t s_full0 = q_full + 8;            // 2: scores ready
-    const uint32_t p_full0 = s_full0 + 16;          // 2: weights ready
+    const uint32_t k_full0 = smem_u32(bars);                // S: a tile's keys are there
+    const uint32_t k_empty0 = k_full0 + 8 * S;              // S: ... and read
+    const uint32_t v_full0 = k_empty0 + 8 * S;
+    const uint32_t v_empty0 = v_full0 + 8 * S;
+    const uint32_t rk_full0 = v_empty0 + 8 * S;             // kRawStages: codes are there
+    const uint32_t rk_empty0 = rk_full0 + 8 * G::kRawStages;
+    const uint32_t rv_full0 = rk_empty0 + 8 * G::kRawStages;
+    const uint32_t rv_empty0 = rv_full0 + 8 * G::kRawStages;
+    const uint32_t m_full0 = rv_empty0 + 8 * G::kRawStages; // kSlots: a tile's mask and scales
+    const uint32_t m_empty0 = m_full0 + 8 * kSlots;
+    const uint32_t q_full = m_empty0 + 8 * kSlots;          // Q in TMEM
+    const uint32_t s_full0 = q_full + 8;                    // 2: scores ready
+    const uint32_t p_full0 = s_full0 + 16;                  // 2: weights ready
     // 2 (tiles in turn): a tile's PV done.  One barrier would not do: with tile j's
     // scores at hand, PV of j - 2 is done, but those of j - 1 and j may or may not
     // be, and a wait tells two neighbouring phases apart, not three.
@@ -353,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rows <= 0) return;
     const int pos0 = len - n;                              // position of the sequence's first new token
     const int pmin = pos0 + row0 / p.group, pmax = pos0 + (row0 + rows - 1) / p.group;
-    Keys keys;
+    Keys<kTile> keys;
     keys.kv_end = max(pmax + 1, 0);
     keys.lo = p.window > 0 && pmin - p.window + 1 > 0 ? pmin - p.window + 1 : 0;
     keys.sink_end = min(p.sinks, keys.lo);
@@ -369,14 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nt <= 0) {
         // nothing to see in this segment
         if (p.segments == 1) {
-            for (int i = threadIdx.x; i < rows * (HD / 8); i += kThreads) {
+            for (int i = threadIdx.x; i < rows * (HD / 8); i += G::kThreads) {
                 const int r = row0 + i / (HD / 8);
                 uint16_t* o = p.out + (first + r / p.group) * p.out_stride +
                               (static_cast<long long>(kvh) * p.group + r % p.group) * HD + (i % (HD / 8)) * 8;
                 *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
             }
         } else {
-            for (int i = threadIdx.x; i < rows; i += kThreads) {
+            for (int i = threadIdx.x; i < rows; i += G::kThreads) {
                 const int r = row0 + i;
                 const long long at = (static_cast<long long>(first + r / p.group) * p.num_q_heads +
                                       kvh * p.group + r % p.group) * p.segments + seg;
@@ -389,26 +464,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- barriers, TMEM ----------------------------------------------------
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, E4M3 ? kProducers / 32 : 1);
-            mbar_init(empty0 + 8 * s, 1);
+            mbar_init(k_full0 + 8 * s, E4M3 ? kConvertWarps : 1);
+            mbar_init(k_empty0 + 8 * s, 1);
+            mbar_init(v_full0 + 8 * s, E4M3 ? kConvertWarps : 1);
+            mbar_init(v_empty0 + 8 * s, 1);
         }
-        mbar_init(q_full, kSoftmax / 32);
+        for (int s = 0; s < G::kRawStages; ++s) {
+            mbar_init(rk_full0 + 8 * s, 1);
+            mbar_init(rk_empty0 + 8 * s, kConvertWarps);
+            mbar_init(rv_full0 + 8 * s, 1);
+            mbar_init(rv_empty0 + 8 * s, kConvertWarps);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(m_full0 + 8 * s, 1);
+            mbar_init(m_empty0 + 8 * s, kSoftmaxWarps);
+        }
+        mbar_init(q_full, kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full0 + 8 * i, 1);
-            mbar_init(p_full0 + 8 * i, kSoftmax / 32);
+            mbar_init(p_full0 + 8 * i, kSoftmaxWarps);
             mbar_init(o_done0 + 8 * i, 1);
         }
         mbar_init(drain, 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == kWarpMma) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish_alloc_permit();
     }
-    if (warp >= 4 && warp < 12) {
-        for (int i = threadIdx.x - kProducers; i < kRows; i += kSoftmax) s_flag[i] = 0;
-    }
+    if (warp >= 4 && warp < 8) s_flag[threadIdx.x - 128] = 0;
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -416,286 +501,189 @@ __global__ void __launch_bounds__(kThreads, 1)
     const WaitCtl wc{abort_flag, p.b.status, p.wait_limit_ns};
     uint32_t never = 0u;
     const WaitCtl wc_drain{&never, p.b.status, p.wait_limit_ns};
-    // V stages of tile i: positions past kv_end are not multiplied
-    auto v_stages = [&](int i) { return (min(kTile, keys.kv_end - keys.base(i)) + VT - 1) / VT; };
 
-    if (warp < 4) {
+    if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------------------------
-        // Producers: K of tile 0, K 1, V 0, K 2, V 1, ... (the MMAs' order)
+        // Loads: one warp for the keys, one for the values.  Lane i has positions
+        // i * box .. of each tile: one page's rows side by side (box divides the page
+        // size), a box if all of them hold a key.  The others are gathered four by
+        // four, a position without a key from past the last row: zeros.  Issuing is
+        // what limits these warps (about 80 clocks an instruction, one lane after the
+        // other), so a box covers all of a head's dimensions; gathers by four rows
+        // alone took 11.8 us for 128 x 256 keys and values.
         // ------------------------------------------------------------------
+        const bool is_k = warp == kWarpK;
+        const CUtensorMap* box_map = is_k ? &maps.k_box : &maps.v_box;
+        const CUtensorMap* row_map = is_k ? &maps.k_row : &maps.v_row;
+        constexpr int RING = E4M3 ? RS : S;
+        constexpr int kBytes = E4M3 ? G::kRawBytes : G::kStageBytes;
+        const uint32_t full0 = E4M3 ? (is_k ? rk_full0 : rv_full0) : (is_k ? k_full0 : v_full0);
+        const uint32_t empty0 = E4M3 ? (is_k ? rk_empty0 : rv_empty0) : (is_k ? k_empty0 : v_empty0);
+        const uint32_t dst0 = smem_u32(E4M3 ? (is_k ? r_k : r_v) : (is_k ? s_k : s_v));
+        const int none = p.b.num_blocks * p.b.block_size;
+        const int box = p.box;
+        const int mine = lane * box;            // first position of this lane in a tile
+        const bool active = mine < kTile;
+        // block-table entries of this lane's positions (with pages of an odd size, four
+        // positions may lie in as many pages), loaded one tile ahead
+        int entry[4] = {-1, -1, -1, -1}, slot = 0;
+        const bool odd_pages = box == 4;
+        auto look_up = [&](int i) {
+            const int t = keys.base(i) + (active ? mine : 0);
+            int at = t / p.b.block_size;
+            slot = t - at * p.b.block_size;
+            entry[0] = at < p.b.max_blocks ? table[at] : -1;
+            if (odd_pages) {
+                int sl = slot;
+#pragma unroll
+                for (int u = 1; u < 4; ++u) {
+                    if (++sl == p.b.block_size) {
+                        sl = 0;
+                        ++at;
+                    }
+                    entry[u] = at < p.b.max_blocks ? table[at] : -1;
+                }
+            }
+        };
+        look_up(keys.begin);
         int stage = 0;
         uint32_t phase = 0;
-        if constexpr (!E4M3) {
-            // warp 0: lane i holds the cache rows of positions 4i .. 4i+3 of a tile and
-            // gathers them; a position without a key reads past the last row: zeros
-            if (warp == 0) {
-                const int none = p.b.num_blocks * p.b.block_size;
-                long long issued = 0;
-                bool ok = true;
-                auto rows_of = [&](int i) {
-                    int r[4];
-                    uint32_t have = 0;
-                    const int t = keys.base(i) + 4 * lane;
+        bool ok = true;
+        int issued = 0;
+        for (int i = keys.begin; i < keys.end; ++i) {
+            const int t = keys.base(i) + mine;
+            const bool good = static_cast<unsigned>(entry[0]) < static_cast<unsigned>(p.b.num_blocks);
+            const int row = good ? entry[0] * p.b.block_size + slot : none;
+            int r4[4] = {none, none, none, none};
+            uint32_t bad = 0;   // bit u: position t + u should hold a key and its page is none
+            if (odd_pages) {
+                int sl = slot;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const long long row = keys.holds(t + u) ? kv_row(p.b, table, t + u) : -1;
-                        r[u] = row < 0 ? none : static_cast<int>(row);
-                        have |= (row < 0 ? 0u : 1u) << u;
-                    }
-                    // 8 lanes' bits make one word of the tile's mask
-                    have <<= 4 * (lane & 7);
-#pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) have |= __shfl_xor_sync(0xffffffffu, have, o);
-                    if ((lane & 7) == 0) s_mask[((i - keys.begin) % kSlots) * 4 + (lane >> 3)] = have;
-                    __syncwarp();
-                    return make_int4(r[0], r[1], r[2], r[3]);
-                };
-                auto next = [&](uint32_t& dst, uint32_t& bar) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, wc, kSiteKvEmpty));
-                    if (!ok) return;
-                    dst = smem_u32(ring + stage * kStageBytes);
-                    bar = full0 + 8 * stage;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, kStageBytes);
-                    __syncwarp();
-                    ++issued;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                };
-                auto load_k = [&](const int4& r) {
-                    for (int kb = 0; kb < NB && ok; ++kb) {
-                        uint32_t dst, bar;
-                        next(dst, bar);
-                        if (ok) tma_gather4(dst + lane * 512, &tmK, bar, kvh * HD + kb * 64, r);
-                    }
-                };
-                auto load_v = [&](const int4& r, int count) {
-                    constexpr int GR = VT / 4;   // gathers per 64-element block of a stage
-                    const int g = lane % GR, blk = lane / GR;
-                    for (int v = 0; v < count && ok; ++v) {
-                        uint32_t dst, bar;
-                        next(dst, bar);
-                        int4 x;
-                        x.x = __shfl_sync(0xffffffffu, r.x, v * GR + g);
-                        x.y = __shfl_sync(0xffffffffu, r.y, v * GR + g);
-                        x.z = __shfl_sync(0xffffffffu, r.z, v * GR + g);
-                        x.w = __shfl_sync(0xffffffffu, r.w, v * GR + g);
-                        if (ok) tma_gather4(dst + blk * (VT * 128) + g * 512, &tmV, bar, kvh * HD + blk * 64, x);
-                    }
-                };
-                int4 cur = rows_of(keys.begin);
-                load_k(cur);
-                for (int i = keys.begin; i < keys.end && ok; ++i) {
-                    int4 nxt = cur;
-                    if (i + 1 < keys.end) {
-                        nxt = rows_of(i + 1);
-                        load_k(nxt);
-                    }
-                    if (ok) load_v(cur, v_stages(i));
-                    cur = nxt;
+                for (int u = 0; u < 4; ++u) {
+                    const bool h = active && keys.holds(t + u);
+                    const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
+                    r4[u] = h && g ? entry[u] * p.b.block_size + sl : none;
+                    bad |= (h && !g ? 1u : 0u) << u;
+                    if (++sl == p.b.block_size) sl = 0;
                 }
-                if (!ok) {
-                    // abort: the loads already issued land before the CTA exits
-                    const long long pending = issued < S ? issued : S;
-                    for (long long j = 1; j <= pending; ++j) {
-                        const int s = (stage - static_cast<int>(j) + S) % S;
-                        const uint32_t ph = (stage - static_cast<int>(j) < 0) ? (phase ^ 1u) : phase;
-                        mbar_wait(full0 + 8 * s, ph, wc_drain, kSiteKvDrain);
-                    }
-                }
+            } else if (active && !good && !keys.none(t, box)) {
+                bad = 1u;
             }
-        } else {
-            // All four warps: each thread copies 16-code chunks of the rows into its own
-            // places of a staging ring (cp.async, kStaging - 1 stages ahead) and later
-            // writes them, as BF16, where the MMAs read them.
-            const int tid = threadIdx.x;
-            const uint8_t* kc = static_cast<const uint8_t*>(p.b.k);
-            const uint8_t* vc = static_cast<const uint8_t*>(p.b.v);
-            // Rows, scales and mask of a tile, one position per thread, in two steps
-            // a tile apart, so that the loads of each are in flight meanwhile.
-            int pend_row = -1;
-            uint32_t pend_k = 127u, pend_v = 127u;
-            auto look_up = [&](int i) {
-                pend_row = -1;
-                pend_k = pend_v = 127u;
-                if (i >= keys.end) return;
-                const int t = keys.base(i) + tid;
-                if (!keys.holds(t)) return;
-                const long long row = kv_row(p.b, table, t);
-                if (row < 0) return;
-                pend_row = static_cast<int>(row);
-                pend_k = p.b.k_scales[row * p.b.num_kv_heads + kvh];
-                pend_v = p.b.v_scales[row * p.b.num_kv_heads + kvh];
-            };
-            auto publish = [&](int i) {   // what look_up(i) found
-                const int slot = (i - keys.begin) % kSlots;
-                const uint32_t have = __ballot_sync(0xffffffffu, pend_row >= 0);
-                if (lane == 0) s_mask[slot * 4 + warp] = have;
-                s_row[slot * kTile + tid] = pend_row;
-                s_kf[slot * kTile + tid] = e8m0_value(pend_k);
-                s_vf[slot * kTile + tid] = e8m0_value(pend_v);
-                named_barrier(5, kProducers);
-            };
-            // The stages in order, as (tile, K or V, index); kept twice: for the copies
-            // and, kStaging - 1 stages behind, for the conversion.
-            struct Cursor {
-                int i, j;      // tile; stage of it: 0 .. NB-1 K, then V of the tile before
-                bool v;
-            };
-            auto advance = [&](Cursor& c) -> bool {   // to the next stage; false at the end
-                // K of tile i, then V of tile i - 1
-                while (true) {
-                    ++c.j;
-                    if (!c.v) {
-                        if (c.i < keys.end && c.j < NB) return true;
-                        c.v = true;
-                        c.j = -1;
-                    } else {
-                        const int vi = c.i - 1;
-                        if (vi >= keys.begin && c.j < v_stages(vi)) return true;
-                        c.v = false;
-                        c.j = -1;
-                        if (++c.i > keys.end) return false;
-                    }
+            if (i + 1 < keys.end) look_up(i + 1);
+            if (!E4M3 && is_k) {
+                // the mask: the positions below kv_end and not between the sinks and the window
+                uint32_t* mask = s_mask + ((i - keys.begin) % kSlots) * 4;
+                if (lane < kTile / 32) {
+                    const int b = keys.base(i) + 32 * lane;
+                    mask[lane] = static_cast<uint32_t>(low_bits(keys.kv_end - b) &
+                                                       (~low_bits(keys.lo - b) | low_bits(keys.sink_end - b)));
                 }
-            };
-            auto copy = [&](const Cursor& c, int buf) {
-                const int i = c.v ? c.i - 1 : c.i;
-                const int slot = (i - keys.begin) % kSlots;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int ch = u * kProducers + tid;
-                    int t, off;
-                    if (!c.v) {
-                        t = ch >> 2;
-                        off = c.j * 64 + (ch & 3) * 16;
-                    } else {
-                        t = c.j * VT + ch / (HD / 16);
-                        off = (ch % (HD / 16)) * 16;
-                    }
-                    const int row = s_row[slot * kTile + t];
-                    const uint8_t* src = (c.v ? vc : kc) +
-                                         (static_cast<long long>(row < 0 ? 0 : row) * p.b.num_kv_heads + kvh) * HD + off;
-                    cp_async_16(smem_u32(staging + buf * 8192 + ch * 16), src, row >= 0);
-                }
-            };
-            auto convert = [&](const Cursor& c, int buf) {
-                mbar_wait(empty0 + 8 * stage, phase ^ 1u, wc, kSiteKvEmpty);
-                uint8_t* dst = ring + stage * kStageBytes;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int ch = u * kProducers + tid;
-                    const uint4 x = *reinterpret_cast<const uint4*>(staging + buf * 8192 + ch * 16);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 f = e4m3x2_values(w[k >> 1] >> (16 * (k & 1)));
-                        o[k] = bf16x2(f.x, f.y);
-                    }
-                    // 128-byte rows of 64 values, their 16-byte chunks permuted by the row
-                    int r, blk, c16;
-                    if (!c.v) {
-                        r = ch >> 2;
-                        blk = 0;
-                        c16 = (ch & 3) * 2;
-                    } else {
-                        r = ch / (HD / 16);
-                        const int e = ch % (HD / 16);
-                        blk = e >> 2;
-                        c16 = (e & 3) * 2;
-                    }
-                    uint8_t* d = dst + blk * (VT * 128) + r * 128;
-                    *reinterpret_cast<uint4*>(d + ((c16 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(d + (((c16 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full0 + 8 * stage);
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
+                if (bad != 0) {
+                    *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
+                    for (int u = 0; u < box; ++u)
+                        if (!odd_pages || ((bad >> u) & 1u)) atomicAnd(&mask[(mine + u) >> 5], ~(1u << ((mine + u) & 31)));
                 }
-            };
-            Cursor ahead{keys.begin, -1, false}, behind{keys.begin, -1, false};
-            look_up(keys.begin);
-            publish(keys.begin);
-            look_up(keys.begin + 1);
-            bool more = true;
-            int in = 0;
-            auto step_ahead = [&]() {
-                if (more) {
-                    more = advance(ahead);
-                    if (more) {
-                        if (!ahead.v && ahead.j == 0 && ahead.i > keys.begin) {
-                            publish(ahead.i);
-                            look_up(ahead.i + 1);
+                __syncwarp();
+            }
+            if (!wait_long(empty0 + 8 * stage, phase ^ 1u, wc, kSiteKvEmpty)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t bar = full0 + 8 * stage;
+            const uint32_t dst = dst0 + stage * kBytes;
+            if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
+            __syncwarp();
+            ++issued;
+            if (active) {
+                if (!odd_pages && (!good || keys.none(t, box) || keys.all(t, box))) {
+                    const int from = keys.none(t, box) ? none : row;   // from past the end: zeros
+                    if constexpr (E4M3)
+                        tma_load_2d(dst + mine * HD, box_map, bar, kvh * HD, from);
+                    else
+                        tma_load_4d(dst + (mine >> 3) * (NB * 1024), box_map, bar, 0, kvh * NB, from >> 3);
+                } else {
+                    for (int u = 0; u < box; u += 4) {
+                        int4 r;
+                        if (odd_pages) {
+                            r = make_int4(r4[0], r4[1], r4[2], r4[3]);
+                        } else {
+                            r.x = keys.holds(t + u) ? row + u : none;
+                            r.y = keys.holds(t + u + 1) ? row + u + 1 : none;
+                            r.z = keys.holds(t + u + 2) ? row + u + 2 : none;
+                            r.w = keys.holds(t + u + 3) ? row + u + 3 : none;
                         }
-                        copy(ahead, in % kStaging);
+                        const int at = mine + u;
+                        if constexpr (E4M3) {
+                            tma_gather4(dst + at * HD, row_map, bar, kvh * HD, r);
+                        } else {
+                            for (int blk = 0; blk < NB; ++blk)
+                                tma_gather4(dst + ((at >> 3) * NB + blk) * 1024 + (at & 7) * 128, row_map, bar,
+                                            kvh * HD + blk * 64, r);
+                        }
                     }
                 }
-                ++in;
-                cp_async_commit();
-            };
-            for (int k = 0; k < kStaging - 1; ++k) step_ahead();
-            for (int k = 0; advance(behind); ++k) {
-                cp_async_wait<kStaging - 2>();
-                convert(behind, k % kStaging);
-                step_ahead();
             }
-            cp_async_wait<0>();
+            __syncwarp();
+            if (++stage == RING) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
-    } else if (warp == 12) {
+        if (!ok) {
+            // abort: the loads already issued land before the CTA exits
+            const int pending = issued < RING ? issued : RING;
+            for (int j = 1; j <= pending; ++j) {
+                const int s = (stage - j + RING) % RING;
+                mbar_wait(full0 + 8 * s, stage - j < 0 ? phase ^ 1u : phase, wc_drain, kSiteKvDrain);
+            }
+        }
+    } else if (warp == kWarpMma) {
         // ------------------------------------------------------------------
         // MMA issuer
         // ------------------------------------------------------------------
         if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = mbar_wait(q_full, 0, wc, kSiteKvQ);
+            bool ok = wait_long(q_full, 0, wc, kSiteKvQ);
             tc_fence_after_sync();
-            const uint32_t q_base = smem_u32(sQ);
-            const uint32_t o_tmem = tmem + 256;
-            auto next = [&]() {
-                ok = ok && mbar_wait(full0 + 8 * stage, phase, wc, kSiteKvFull);
-                tc_fence_after_sync();
-                return smem_u32(ring + stage * kStageBytes);
-            };
-            auto done = [&]() {
-                mma_commit(empty0 + 8 * stage);
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            };
+            const uint32_t q_tmem = tmem + G::kColQ, o_tmem = tmem + G::kColO;
+            int ks = 0, vs = 0;
+            uint32_t kph = 0, vph = 0;
             auto scores = [&](int j) {
-                for (int kb = 0; kb < NB && ok; ++kb) {
-                    const uint32_t b = next();
-                    if (!ok) break;
+                ok = ok && wait_long(k_full0 + 8 * ks, kph, wc, kSiteKvFull);
+                if (!ok) return;
+                tc_fence_after_sync();
+                const uint32_t b = smem_u32(s_k + ks * G::kStageBytes);
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + (j & 1) * 128, smem_desc_sw128(q_base + kb * (kRows * 128) + kk * 32, 16, 1024),
-                                smem_desc_sw128(b + kk * 32, 16, 1024), kIdescS, (kb | kk) != 0 ? 1u : 0u);
-                    done();
+                        mma_f16_tmem_a(tmem + (j & 1) * kTile, q_tmem + (kb * 4 + kk) * 8,
+                                       smem_desc_sw128(b + kb * 1024 + kk * 32, 16, NB * 1024), kIdescS,
+                                       (kb | kk) != 0 ? 1u : 0u);
+                mma_commit(s_full0 + 8 * (j & 1));
+                mma_commit(k_empty0 + 8 * ks);
+                if (++ks == S) {
+                    ks = 0;
+                    kph ^= 1u;
                 }
-                if (ok) mma_commit(s_full0 + 8 * (j & 1));
             };
             auto weighted = [&](int j) {
-                ok = ok && mbar_wait(p_full0 + 8 * (j & 1), (j >> 1) & 1, wc, kSiteKvWeights);
+                ok = ok && wait_long(v_full0 + 8 * vs, vph, wc, kSiteKvFull);
+                ok = ok && wait_long(p_full0 + 8 * (j & 1), (j >> 1) & 1, wc, kSiteKvWeights);
+                if (!ok) return;
                 tc_fence_after_sync();
-                const int count = v_stages(keys.begin + j);
-                for (int v = 0; v < count && ok; ++v) {
-                    const uint32_t b = next();
-                    if (!ok) break;
-#pragma unroll
-                    for (int kk = 0; kk < VT / 16; ++kk)
-                        mma_f16_tmem_a(o_tmem, tmem + (j & 1) * 128 + (v * VT / 16 + kk) * 8,
-                                       smem_desc_sw128(b + kk * 2048, VT * 128, 1024), kIdescO,
-                                       (j | v | kk) != 0 ? 1u : 0u);
-                    done();
+                const uint32_t b = smem_u32(s_v + vs * G::kStageBytes);
+                // 16 positions an MMA; those past kv_end are not multiplied
+                const int steps = min(kTile / 16, (keys.kv_end - keys.base(keys.begin + j) + 15) / 16);
+                for (int kk = 0; kk < steps; ++kk)
+                    mma_f16_tmem_a(o_tmem, tmem + (j & 1) * kTile + kk * 8,
+                                   smem_desc_sw128(b + kk * (NB * 2048), 1024, NB * 1024), kIdescO,
+                                   (j | kk) != 0 ? 1u : 0u);
+                mma_commit(o_done0 + 8 * (j & 1));
+                mma_commit(v_empty0 + 8 * vs);
+                if (++vs == S) {
+                    vs = 0;
+                    vph ^= 1u;
                 }
-                if (ok) mma_commit(o_done0 + 8 * (j & 1));
             };
             if (ok) scores(0);
             for (int j = 0; j < nt && ok; ++j) {
@@ -709,10 +697,121 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == kWarpScales) {
+        if constexpr (E4M3) {
+            // ----------------------------------------------------------------
+            // Masks and scales, kTile / 32 positions per lane: block-table entries are
+            // loaded two tiles ahead, the scales one.
+            // ----------------------------------------------------------------
+            constexpr int PL = kTile / 32;
+            int entry[PL];
+            uint32_t kb[PL], vb[PL], have = 0;
+            auto look_up = [&](int i) {
+#pragma unroll
+                for (int u = 0; u < PL; ++u) {
+                    const int at = (keys.base(min(i, keys.end - 1)) + u * 32 + lane) / p.b.block_size;
+                    entry[u] = at < p.b.max_blocks ? table[at] : -1;
+                }
+            };
+            auto fetch = [&](int i) {
+                have = 0;
+#pragma unroll
+                for (int u = 0; u < PL; ++u) {
+                    const int t = keys.base(i) + u * 32 + lane;
+                    const bool h = i < keys.end && keys.holds(t);
+                    const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
+                    if (h && !g) *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
+                    kb[u] = vb[u] = 127u;
+                    if (h && g) {
+                        const long long row = static_cast<long long>(entry[u]) * p.b.block_size + t % p.b.block_size;
+                        kb[u] = p.b.k_scales[row * p.b.num_kv_heads + kvh];
+                        vb[u] = p.b.v_scales[row * p.b.num_kv_heads + kvh];
+                        have |= 1u << u;
+                    }
+                }
+            };
+            look_up(keys.begin);
+            fetch(keys.begin);
+            look_up(keys.begin + 1);
+            bool ok = true;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int slot = j % kSlots;
+                ok = __all_sync(0xffffffffu, wait_long(m_empty0 + 8 * slot, ((j / kSlots) & 1) ^ 1, wc, kSiteKvMeta));
+                if (!ok) break;
+                // the range of V's exponents, all-zero rows (the least scale) left out
+                int top = 0, low = 255;
+#pragma unroll
+                for (int u = 0; u < PL; ++u) {
+                    const bool h = ((have >> u) & 1u) != 0;
+                    s_kf[slot * kTile + u * 32 + lane] = e8m0_value(kb[u]);
+                    s_vf[slot * kTile + u * 32 + lane] = e8m0_value(vb[u]);
+                    const uint32_t word = __ballot_sync(0xffffffffu, h);
+                    if (lane == 0) s_mask[slot * 4 + u] = word;
+                    if (h && vb[u] > 10u && vb[u] != 255u) {
+                        top = max(top, static_cast<int>(vb[u]));
+                        low = min(low, static_cast<int>(vb[u]));
+                    }
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                low = __reduce_min_sync(0xffffffffu, low);
+                if (lane == 0) s_exp[slot] = make_int2(top, low);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m_full0 + 8 * slot);
+                fetch(keys.begin + j + 1);
+                look_up(keys.begin + j + 2);
+            }
+        }
+    } else if (warp >= 12) {
+        if constexpr (E4M3) {
+            // ----------------------------------------------------------------
+            // Codes -> FP16, where the MMAs read them: K 0, K 1, V 0, K 2, V 1, ...
+            // A failed wait does not leave the loop (see the softmax warps).
+            // ----------------------------------------------------------------
+            const int tid = threadIdx.x - 384;
+            constexpr int kChunks = G::kRawBytes / 16 / 128;   // 16 codes each, per thread
+            constexpr int CPR = HD / 16;                       // chunks per row
+            auto convert = [&](int j, bool v) {
+                const int rs = j % RS, ss = j % S;
+                const uint8_t* raw = (v ? r_v : r_k) + rs * G::kRawBytes;
+                uint8_t* dst = (v ? s_v : s_k) + ss * G::kStageBytes;
+                wait_long((v ? rv_full0 : rk_full0) + 8 * rs, (j / RS) & 1, wc, kSiteKvRaw);
+                uint4 x[kChunks];
+#pragma unroll
+                for (int u = 0; u < kChunks; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + (u * 128 + tid) * 16);
+                wait_long((v ? v_empty0 : k_empty0) + 8 * ss, ((j / S) & 1) ^ 1, wc, kSiteKvEmpty);
+#pragma unroll
+                for (int u = 0; u < kChunks; ++u) {
+                    const int ch = u * 128 + tid;
+                    const int r = ch / CPR, e = ch % CPR;
+                    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = e4m3x2_f16x2(w[k >> 1] >> (16 * (k & 1)));
+                    uint8_t* d = dst + ((r >> 3) * NB + (e >> 2)) * 1024 + (r & 7) * 128;
+                    // 16-byte chunks permuted by the row; lanes of odd blocks write the later one
+                    // first, so that a row's lanes meet distinct banks
+                    const int c16 = (e & 3) * 2, flip = (e >> 2) & 1;
+                    const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4*>(d + (((c16 + flip) ^ (r & 7)) << 4)) = flip ? b : a;
+                    *reinterpret_cast<uint4*>(d + (((c16 + 1 - flip) ^ (r & 7)) << 4)) = flip ? a : b;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive((v ? rv_empty0 : rk_empty0) + 8 * rs);
+                    mbar_arrive((v ? v_full0 : k_full0) + 8 * ss);
+                }
+            };
+            convert(0, false);
+            for (int j = 0; j < nt; ++j) {
+                if (j + 1 < nt) convert(j + 1, false);
+                convert(j, true);
+            }
+        }
     } else {
         // ------------------------------------------------------------------
         // Softmax: warp (quarter, half) has TMEM lanes 32 * quarter .. and half of
-        // the columns: of S positions 64 * half .., of O dimensions HD/2 * half ..
+        // the columns: of S positions kTile/2 * half .., of O dimensions HD/2 * half ..
         // A failed wait (abort flag up) does not leave the loop: the barriers below
         // stay matched, the waits return at once and the output is undefined.
         // ------------------------------------------------------------------
@@ -725,67 +824,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int token = first + my / p.group;
         const int head = kvh * p.group + my % p.group;
         const int pos = pos0 + my / p.group;
-        {
-            // Q: row r's chunks, the two halves of the warps taking turns; 128-byte rows of
-            // 64 values, their 16-byte chunks permuted by the row
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + static_cast<long long>(head) * HD);
+        float row_scale = p.scale_log2;
+        if (!idle) {
+            // this half of Q's row: 16-bit pairs, one per TMEM column
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + static_cast<long long>(head) * HD +
+                                                              half * (HD / 2));
+            uint32_t w[HD / 4];
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) {
-                const int ch = half * (HD / 16) + c;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    x = src[ch];
-                    x.x ^= p.q_sign;
-                    x.y ^= p.q_sign;
-                    x.z ^= p.q_sign;
-                    x.w ^= p.q_sign;
-                }
-                *reinterpret_cast<uint4*>(sQ + (ch >> 3) * (kRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+                const uint4 x = src[c];
+                w[4 * c] = x.x ^ p.q_sign;
+                w[4 * c + 1] = x.y ^ p.q_sign;
+                w[4 * c + 2] = x.z ^ p.q_sign;
+                w[4 * c + 3] = x.w ^ p.q_sign;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            if constexpr (E4M3) {
+                // FP16 beside FP16 keys: the row times a power of two that brings its largest
+                // value to [2^14, 2^15).  What FP16 then drops is under 2^-39 of the largest.
+                uint32_t m = 0;
+#pragma unroll
+                for (int c = 0; c < HD / 4; ++c) m = __vmaxu2(m, w[c] & 0x7fff7fffu);
+                m = max(m & 0xffffu, m >> 16);
+                uint32_t* sm = reinterpret_cast<uint32_t*>(s_max);
+                sm[half * kRows + r] = m;
+                named_barrier(1 + quarter, 64);
+                m = max(m, sm[(half ^ 1) * kRows + r]);
+                int e = static_cast<int>(m >> 7) - 127 - 14;               // q * 2^-e
+                e = max(-126, min(e, 113));
+                const float f = exp2f(static_cast<float>(-e));
+                row_scale *= exp2f(static_cast<float>(e));
+#pragma unroll
+                for (int c = 0; c < HD / 4; ++c)
+                    w[c] = f16x2(__uint_as_float(w[c] << 16) * f, __uint_as_float(w[c] & 0xffff0000u) * f);
+                named_barrier(1 + quarter, 64);   // s_max is free again
+            }
+            const uint32_t q_addr = lane_addr + G::kColQ + half * (HD / 4);
+            if constexpr (HD >= 128) {
+#pragma unroll
+                for (int c = 0; c < HD / 128; ++c) {
+                    uint32_t t[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) t[i] = w[32 * c + i];
+                    tmem_st_32x32b_x32(q_addr + 32 * c, t);
+                }
+            } else {
+                uint32_t t[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) t[i] = w[i];
+                tmem_st_32x32b_x16(q_addr, t);
+            }
+            tmem_st_wait();
+            tc_fence_before_sync();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
         const int lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;   // this row's window
         const int lo_max = p.window > 0 ? pmax - p.window + 1 : 0;                        // the last row's
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
+        // E4M3: O and l hold 2^(3 - E) of their values, E the V scales' largest exponent so
+        // far or up to 4 less, so that weight x scale stays below FP16's 65504 and
+        // loses at most 2^-27 of the largest.  Scales too far apart for that, or far
+        // from 1, set `wide`: then the rows are computed one by one (repair_row).
+        int E = 0, low_e = 1000;
+        bool wide = false;
         for (int j = 0; j < nt; ++j) {
             const int buf = j & 1;
             const int slot = j % kSlots;
-            mbar_wait(s_full0 + 8 * buf, (j >> 1) & 1, wc, kSiteKvScores);
+            if constexpr (E4M3) wait_long(m_full0 + 8 * slot, (j / kSlots) & 1, wc, kSiteKvMeta);
+            wait_long(s_full0 + 8 * buf, (j >> 1) & 1, wc, kSiteKvScores);
             tc_fence_after_sync();
             if (!idle) {
-                const uint32_t s_addr = lane_addr + buf * 128 + half * 64;
-                uint32_t raw[2][32];
-                tmem_ld_32x32b_x32(s_addr, raw[0]);
-                tmem_ld_32x32b_x32(s_addr + 32, raw[1]);
-                tmem_ld_wait();
-                float2 x[32];
+                const uint32_t s_addr = lane_addr + buf * kTile + half * C;
+                float2 x[C / 2];
+                {
+                    uint32_t raw[C / 32][32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    x[c] = make_float2(__uint_as_float(raw[c >> 4][(2 * c) & 31]), __uint_as_float(raw[c >> 4][(2 * c + 1) & 31]));
+                    for (int c = 0; c < C / 32; ++c) tmem_ld_32x32b_x32(s_addr + 32 * c, raw[c]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < C / 2; ++c)
+                        x[c] = make_float2(__uint_as_float(raw[c >> 4][(2 * c) & 31]),
+                                           __uint_as_float(raw[c >> 4][(2 * c + 1) & 31]));
+                }
+                float grow_e = 1.f;   // E4M3: factor of O and l for a new E
                 if constexpr (E4M3) {
-                    const float4* kf = reinterpret_cast<const float4*>(s_kf + slot * kTile + half * 64);
+                    const float4* kf = reinterpret_cast<const float4*>(s_kf + slot * kTile + half * C);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < C / 4; ++c) {
                         const float4 f = kf[c];
                         x[2 * c] = mul2(x[2 * c], make_float2(f.x, f.y));
                         x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(f.z, f.w));
                     }
+                    const int2 range = s_exp[slot];
+                    if (range.x > 0) {
+                        const int top = range.x - 127;
+                        if (low_e == 1000 || top > E + 4) {   // the first scales, or larger ones
+                            grow_e = exp2_fast(static_cast<float>(E - top));
+                            E = top;
+                        }
+                        low_e = min(low_e, range.y - 127);
+                        wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
+                    }
                 }
                 // positions that hold no key, or that this row does not see
-                const int t0 = keys.base(keys.begin + j) + half * 64;
-                const uint2 have = *reinterpret_cast<const uint2*>(s_mask + slot * 4 + half * 2);
-                if ((have.x & have.y) != 0xffffffffu || t0 + 63 > pmin || (t0 < lo_max && t0 + 64 > p.sinks)) {
-                    auto below = [](int k) {   // the k lowest of 64 bits
-                        return k <= 0 ? 0ull : (k >= 64 ? ~0ull : (1ull << k) - 1);
-                    };
+                const int t0 = keys.base(keys.begin + j) + half * C;
+                uint2 have;
+                if constexpr (C == 64)
+                    have = *reinterpret_cast<const uint2*>(s_mask + slot * 4 + half * 2);
+                else
+                    have = make_uint2(s_mask[slot * 4 + half], 0xffffffffu);
+                if ((have.x & have.y) != 0xffffffffu || t0 + C - 1 > pmin || (t0 < lo_max && t0 + C > p.sinks)) {
                     const unsigned long long seen = (static_cast<unsigned long long>(have.y) << 32 | have.x) &
-                                                    below(pos + 1 - t0) & (~below(lo - t0) | below(p.sinks - t0));
+                                                    low_bits(pos + 1 - t0) & (~low_bits(lo - t0) | low_bits(p.sinks - t0));
                     const uint32_t lo32 = static_cast<uint32_t>(seen), hi32 = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
+                    for (int c = 0; c < C / 2; ++c) {
                         const uint32_t w = c < 16 ? lo32 : hi32;
                         if (!((w >> ((2 * c) & 31)) & 1u)) x[c].x = -INFINITY;
                         if (!((w >> ((2 * c + 1) & 31)) & 1u)) x[c].y = -INFINITY;
@@ -793,29 +947,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; ++c) mx[c & 3] = max3(mx[c & 3], x[c].x, x[c].y);
+                for (int c = 0; c < C / 2; ++c) mx[c & 3] = max3(mx[c & 3], x[c].x, x[c].y);
                 float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 // the row's other half; also: both warps have read S, P may go over it
                 float* sm = s_max + buf * 2 * kRows;
                 sm[half * kRows + r] = top;
                 named_barrier(1 + quarter, 64);
-                top = fmaxf(top, sm[(half ^ 1) * kRows + r]) * p.scale_log2;
+                top = fmaxf(top, sm[(half ^ 1) * kRows + r]) * row_scale;
                 const float mn = fmaxf(m, top);
                 if (j == 0) {
                     m = mn;
-                } else if (__any_sync(0xffffffffu, mn > m + 8.f)) {
-                    float f = 1.f;
+                } else if (__any_sync(0xffffffffu, mn > m + 8.f) || (E4M3 && grow_e != 1.f)) {
+                    float f = grow_e;
                     if (mn > m + 8.f) {
-                        f = exp2_fast(m - mn);
+                        f *= exp2_fast(m - mn);
                         m = mn;
                     }
-                    const float2 f2 = make_float2(f, f);
-                    l2 = mul2(l2, f2);
-                    mbar_wait(o_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, wc, kSiteKvOutput);   // PV of j - 1
+                    l2 = mul2(l2, make_float2(f, f));
+                    wait_long(o_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, wc, kSiteKvOutput);   // PV of j - 1
                     tc_fence_after_sync();
                     // this half of the row's O
                     for (int c = 0; c < HD / 64; ++c) {
-                        const uint32_t o_addr = lane_addr + 256 + half * (HD / 2) + c * 32;
+                        const uint32_t o_addr = lane_addr + G::kColO + half * (HD / 2) + c * 32;
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(o_addr, o);
                         tmem_ld_wait();
@@ -824,30 +977,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st_32x32b_x32(o_addr, o);
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
-                uint32_t w[32];
+                float base = m == -INFINITY ? 0.f : m;
+                if constexpr (E4M3) base -= static_cast<float>(3 - E);
+                const float2 sc = make_float2(row_scale, row_scale), nb = make_float2(-base, -base);
+                uint32_t w[C / 2];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < C / 2; ++c) {
                     float2 e = fma2(x[c], sc, nb);
                     e.x = exp2_fast(e.x);
                     e.y = exp2_fast(e.y);
                     l2 = add2(l2, e);
                     if constexpr (E4M3) {
-                        const float2 f = *reinterpret_cast<const float2*>(s_vf + slot * kTile + half * 64 + 2 * c);
+                        const float2 f = *reinterpret_cast<const float2*>(s_vf + slot * kTile + half * C + 2 * c);
                         e = mul2(e, f);
+                        w[c] = f16x2(e.x, e.y);
+                    } else {
+                        w[c] = bf16x2(e.x, e.y);
                     }
-                    w[c] = bf16x2(e.x, e.y);
                 }
-                tmem_st_32x32b_x32(lane_addr + buf * 128 + half * 32, w);
+                const uint32_t p_addr = lane_addr + buf * kTile + half * (C / 2);
+                if constexpr (C == 64)
+                    tmem_st_32x32b_x32(p_addr, w);
+                else
+                    tmem_st_32x32b_x16(p_addr, w);
                 tmem_st_wait();
                 tc_fence_before_sync();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full0 + 8 * buf);
+            if (lane == 0) {
+                mbar_arrive(p_full0 + 8 * buf);
+                if constexpr (E4M3) mbar_arrive(m_empty0 + 8 * slot);
+            }
         }
         // ---- the rows' results ---------------------------------------------
-        mbar_wait(o_done0 + 8 * ((nt - 1) & 1), ((nt - 1) >> 1) & 1, wc, kSiteKvOutput);
+        wait_long(o_done0 + 8 * ((nt - 1) & 1), ((nt - 1) >> 1) & 1, wc, kSiteKvOutput);
         tc_fence_after_sync();
         if (!idle) {
             float l = l2.x + l2.y;
@@ -857,11 +1020,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             l = sm[r] + sm[kRows + r];   // the same order for both halves
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long at = (static_cast<long long>(token) * p.num_q_heads + head) * p.segments + seg;
+            // a split row's partial sums leave out E4M3's 2^(3 - E)
+            const float plain = E4M3 ? exp2f(static_cast<float>(E - 3)) : 1.f;
             float odd = 0.f;   // NaN once a value is not finite
             for (int c = 0; c < HD / 64; ++c) {
                 const int d0 = half * (HD / 2) + c * 32;
                 uint32_t o[32];
-                tmem_ld_32x32b_x32(lane_addr + 256 + d0, o);
+                tmem_ld_32x32b_x32(lane_addr + G::kColO + d0, o);
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(o[i]), 0.f, odd);
@@ -878,14 +1043,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * HD + d0);
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + d0);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(o[4 * i]) * plain, __uint_as_float(o[4 * i + 1]) * plain,
+                                                 __uint_as_float(o[4 * i + 2]) * plain, __uint_as_float(o[4 * i + 3]) * plain);
                     }
                 }
             }
-            if (p.segments > 1 && half == 0 && r < rows) p.part_ml[at] = make_float2(m, l);
-            if (odd != 0.f && l - l == 0.f && r < rows) s_flag[r] = 1;   // odd is NaN, l is finite
+            if (p.segments > 1 && half == 0 && r < rows) p.part_ml[at] = make_float2(m, l * plain);
+            if (((odd != 0.f && l - l == 0.f) || wide) && r < rows) s_flag[r] = 1;   // odd is NaN, l is finite
             named_barrier(1 + quarter, 64);
             for (int i = half; i < 32; i += 2) {
                 const int rr = quarter * 32 + i;
@@ -899,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kWarpMma) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
@@ -994,25 +1161,37 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     const long long rows = static_cast<long long>(a.b.num_tokens) * a.num_q_heads;
     p.part_ml = reinterpret_cast<float2*>(a.workspace + rows * a.segments * HD);
     p.wait_limit_ns = a.wait_limit_ns;
-    CUtensorMap maps[2] = {};
-    if constexpr (!E4M3) {
-        TmapEncodeFn enc = tmap_encoder();
-        if (enc == nullptr) {
-            snprintf(msg, msg_len, "cuTensorMapEncodeTiled is not available from the driver");
-            return cudaErrorNotSupported;
-        }
-        const cuuint64_t width = static_cast<cuuint64_t>(a.b.num_kv_heads) * HD;
-        const cuuint64_t dims[2] = {width, static_cast<cuuint64_t>(a.b.num_blocks) * a.b.block_size};
-        const cuuint64_t strides[1] = {width * 2};
-        const cuuint32_t box[2] = {64, 1}, ones[2] = {1, 1};
-        for (int i = 0; i < 2; ++i) {
-            const CUresult r = enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, i == 0 ? a.b.k : a.b.v, dims, strides,
-                                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-            if (r != CUDA_SUCCESS) {
-                snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for the cache", static_cast<int>(r));
-                return cudaErrorInvalidValue;
-            }
+    KvMaps maps = {};
+    TmapEncodeFn enc = tmap_encoder();
+    if (enc == nullptr) {
+        snprintf(msg, msg_len, "cuTensorMapEncodeTiled is not available from the driver");
+        return cudaErrorNotSupported;
+    }
+    // a box is whole 8-row atoms of one page and fits a stage
+    p.box = 4;
+    for (int r = 8; r <= Geo<E4M3, HD>::kTile; r *= 2)
+        if (a.b.block_size % r == 0) p.box = r;
+    const cuuint64_t width = static_cast<cuuint64_t>(a.b.num_kv_heads) * HD;
+    const cuuint64_t cache_rows = static_cast<cuuint64_t>(a.b.num_blocks) * a.b.block_size;
+    const cuuint64_t pitch = E4M3 ? width : width * 2;
+    const cuuint64_t dims[4] = {64, 8, width / 64, cache_rows / 8};
+    const cuuint64_t strides[3] = {pitch, 128, pitch * 8};
+    const cuuint64_t row_dims[2] = {width, cache_rows};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 8, HD / 64, static_cast<cuuint32_t>(p.box / 8)};
+    const cuuint32_t raw_box[2] = {HD, static_cast<cuuint32_t>(p.box)};
+    const cuuint32_t row_box[2] = {E4M3 ? HD : 64, 1};
+    CUtensorMap* const map[4] = {&maps.k_row, &maps.v_row, &maps.k_box, &maps.v_box};
+    for (int i = 0; i < (p.box >= 8 ? 4 : 2); ++i) {
+        const bool flat = i < 2 || E4M3;
+        const CUresult r = enc(map[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                               flat ? 2 : 4, i % 2 == 0 ? a.b.k : a.b.v, flat ? row_dims : dims, strides,
+                               i < 2 ? row_box : (E4M3 ? raw_box : box), ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) {
+            snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for the cache", static_cast<int>(r));
+            return cudaErrorInvalidValue;
         }
     }
     auto kern = kv_attention_kernel<E4M3, HD>;
@@ -1021,8 +1200,8 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(p.tiles) * a.b.num_kv_heads * a.b.num_seqs * a.segments;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    e = launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Geo<E4M3, HD>::kBytes, stream, a.pdl,
-                      maps[0], maps[1], p);
+    e = launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(Geo<E4M3, HD>::kThreads), Geo<E4M3, HD>::kBytes, stream, a.pdl,
+                      maps, p);
     if (e != cudaSuccess || a.segments == 1) return e;
     constexpr int kPerCta = 256 / (HD / 4);
     if (rows < 4 * a.num_sms)
@@ -1043,7 +1222,8 @@ int kv_attention_segments(const KvAttnLaunch& a)
     long long keys = a.max_seq_len;
     if (a.window > 0 && static_cast<long long>(a.window) + a.max_chunk + a.sinks < keys)
         keys = static_cast<long long>(a.window) + a.max_chunk + a.sinks;
-    const long long tiles = (keys + kTile - 1) / kTile;
+    const int tile = a.b.head_dim == 256 ? 64 : 128;
+    const long long tiles = (keys + tile - 1) / tile;
     const double rows = static_cast<double>(a.b.num_tokens) * a.num_q_heads;
     // Time in units of one tile's work on one CTA: a CTA starts and ends in about
     // 6, a join costs about 6 more and the traffic of the partial rows.
