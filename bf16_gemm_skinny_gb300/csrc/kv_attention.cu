@@ -41,7 +41,15 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Cache rows of one KV head, a multiple of 8 of them, from the 4-D view below.
+// One box of a tensor map, from its first dimensions' start (x of a 2-D map).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z)
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z, int w)
 {
     asm volatile(
@@ -85,6 +93,21 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One lane of a converged warp, always the same.  A branch on this (and not on
+// lane == 0) tells the compiler that a single thread issues the TMA or MMA
+// instruction in it; otherwise it takes the active lanes one after the other, at
+// 80 to 100 clocks an instruction.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
 
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {
@@ -175,10 +198,10 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, const W
 constexpr int kRows = 128;        // query rows per CTA (the M of the MMAs)
 constexpr int kSoftmaxWarps = 8;  // warps 4..11
 constexpr int kConvertWarps = 4;  // warps 12..15, E4M3 only
-constexpr int kSlots = 8;         // tiles whose masks (and scales) are kept
+constexpr int kSlots = 8;         // tiles whose cache rows, masks and scales are kept
 
-// Warps 0..3: keys' loads, MMAs, values' loads, E4M3 scales.
-enum AttnWarp : int { kWarpK = 0, kWarpMma = 1, kWarpV = 2, kWarpScales = 3 };
+// Warps 0..3: keys' loads, MMAs, values' loads, look-ups in the block table.
+enum AttnWarp : int { kWarpK = 0, kWarpMma = 1, kWarpV = 2, kWarpPages = 3 };
 enum AttnSite : int {
     kSiteKvEmpty = 0x30, kSiteKvFull, kSiteKvQ, kSiteKvScores, kSiteKvWeights, kSiteKvOutput, kSiteKvDrain,
     kSiteKvRaw, kSiteKvMeta
@@ -203,7 +226,7 @@ struct Geo {
     static constexpr int kThreads = E4M3 ? 512 : 384;
     static constexpr int kBars = 4 * kStages + 4 * kRawStages + 2 * kSlots + 8;
     static constexpr int kScaleBytes = E4M3 ? kSlots * (kTile * 8 + 8) : 0;
-    static constexpr int kMisc = kScaleBytes + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
+    static constexpr int kMisc = kScaleBytes + kSlots * kTile * 4 + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
     static constexpr int kBytes = 1024 + 2 * kStages * kStageBytes + 2 * kRawStages * kRawBytes + kMisc;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
@@ -225,9 +248,10 @@ struct AttnParams {
 };
 
 // Tensor maps of the cache.  Gathers see it as [num_blocks * block_size] rows of
-// heads * HD values.  Boxes are `box` rows of one head: of a BF16 cache, seen as
-// [rows / 8][heads * HD / 64][8][64], as the stages want them, of an E4M3 cache, seen
-// as for gathers, row after row.
+// heads * HD values.  Boxes are `box` rows of one head: of a BF16 cache as the stages
+// want them ([rows / 8][heads * HD / 64][8][64]), of an E4M3 cache in lines of at
+// most 128 codes ([heads * HD / 128][rows][128] with HD = 256), each swizzled: without
+// swizzling the TMA unit writes 31 bytes a clock, with it 57.
 struct KvMaps {
     CUtensorMap k_box, v_box, k_row, v_row;
 };
@@ -372,7 +396,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
     float* s_kf = reinterpret_cast<float*>(r_v + G::kRawStages * G::kRawBytes);   // E4M3: [kSlots][kTile] K scales
     float* s_vf = s_kf + (E4M3 ? kSlots * kTile : 0);               //       V scales
     int2* s_exp = reinterpret_cast<int2*>(s_vf + (E4M3 ? kSlots * kTile : 0));    // [kSlots] V scales' range
-    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_exp + (E4M3 ? kSlots : 0));  // [kSlots][4] positions that hold a key
+    int* s_row = reinterpret_cast<int*>(s_exp + (E4M3 ? kSlots : 0));   // [kSlots][kTile] cache row of each position
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_row + kSlots * kTile);       // [kSlots][4] positions that hold a key
     float* s_max = reinterpret_cast<float*>(s_mask + kSlots * 4);   // [2][2][kRows]
     int* s_flag = reinterpret_cast<int*>(s_max + 4 * kRows);        // [kRows] rows to repair
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_flag + kRows);
@@ -386,7 +411,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
     const uint32_t rk_empty0 = rk_full0 + 8 * G::kRawStages;
     const uint32_t rv_full0 = rk_empty0 + 8 * G::kRawStages;
     const uint32_t rv_empty0 = rv_full0 + 8 * G::kRawStages;
-    const uint32_t m_full0 = rv_empty0 + 8 * G::kRawStages; // kSlots: a tile's mask and scales
+    const uint32_t m_full0 = rv_empty0 + 8 * G::kRawStages; // kSlots: a tile's rows, mask and scales
     const uint32_t m_empty0 = m_full0 + 8 * kSlots;
     const uint32_t q_full = m_empty0 + 8 * kSlots;          // Q in TMEM
     const uint32_t s_full0 = q_full + 8;                    // 2: scores ready
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(m_full0 + 8 * s, 1);
-            mbar_init(m_empty0 + 8 * s, kSoftmaxWarps);
+            mbar_init(m_empty0 + 8 * s, kSoftmaxWarps + 1);
         }
         mbar_init(q_full, kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
@@ -504,13 +529,12 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
 
     if (warp == kWarpK || warp == kWarpV) {
         // ------------------------------------------------------------------
-        // Loads: one warp for the keys, one for the values.  Lane i has positions
-        // i * box .. of each tile: one page's rows side by side (box divides the page
-        // size), a box if all of them hold a key.  The others are gathered four by
-        // four, a position without a key from past the last row: zeros.  Issuing is
-        // what limits these warps (about 80 clocks an instruction, one lane after the
-        // other), so a box covers all of a head's dimensions; gathers by four rows
-        // alone took 11.8 us for 128 x 256 keys and values.
+        // Loads: one warp for the keys, one for the values.  `box` positions lie in
+        // one page, side by side (box divides the page size), and come as one TMA box
+        // when all of them hold a key.  Others are gathered four by four, a position
+        // without a key from past the last row: zeros.  A box costs its warp about 57
+        // clocks and 2.2 for each 128 bytes that the TMA unit writes (so 57 bytes a
+        // clock at best); with two warps one's overhead hides behind the other's.
         // ------------------------------------------------------------------
         const bool is_k = warp == kWarpK;
         const CUtensorMap* box_map = is_k ? &maps.k_box : &maps.v_box;
@@ -520,110 +544,63 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         const uint32_t full0 = E4M3 ? (is_k ? rk_full0 : rv_full0) : (is_k ? k_full0 : v_full0);
         const uint32_t empty0 = E4M3 ? (is_k ? rk_empty0 : rv_empty0) : (is_k ? k_empty0 : v_empty0);
         const uint32_t dst0 = smem_u32(E4M3 ? (is_k ? r_k : r_v) : (is_k ? s_k : s_v));
-        const int none = p.b.num_blocks * p.b.block_size;
         const int box = p.box;
-        const int mine = lane * box;            // first position of this lane in a tile
-        const bool active = mine < kTile;
-        // block-table entries of this lane's positions (with pages of an odd size, four
-        // positions may lie in as many pages), loaded one tile ahead
-        int entry[4] = {-1, -1, -1, -1}, slot = 0;
-        const bool odd_pages = box == 4;
-        auto look_up = [&](int i) {
-            const int t = keys.base(i) + (active ? mine : 0);
-            int at = t / p.b.block_size;
-            slot = t - at * p.b.block_size;
-            entry[0] = at < p.b.max_blocks ? table[at] : -1;
-            if (odd_pages) {
-                int sl = slot;
-#pragma unroll
-                for (int u = 1; u < 4; ++u) {
-                    if (++sl == p.b.block_size) {
-                        sl = 0;
-                        ++at;
-                    }
-                    entry[u] = at < p.b.max_blocks ? table[at] : -1;
-                }
-            }
-        };
-        look_up(keys.begin);
+        // the positions of a box as bits of a mask word (a box of 64 or 128 is whole words)
+        const uint32_t box_bits = box >= 32 ? 0xffffffffu : (1u << box) - 1u;
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         int issued = 0;
-        for (int i = keys.begin; i < keys.end; ++i) {
-            const int t = keys.base(i) + mine;
-            const bool good = static_cast<unsigned>(entry[0]) < static_cast<unsigned>(p.b.num_blocks);
-            const int row = good ? entry[0] * p.b.block_size + slot : none;
-            int r4[4] = {none, none, none, none};
-            uint32_t bad = 0;   // bit u: position t + u should hold a key and its page is none
-            if (odd_pages) {
-                int sl = slot;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const bool h = active && keys.holds(t + u);
-                    const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
-                    r4[u] = h && g ? entry[u] * p.b.block_size + sl : none;
-                    bad |= (h && !g ? 1u : 0u) << u;
-                    if (++sl == p.b.block_size) sl = 0;
-                }
-            } else if (active && !good && !keys.none(t, box)) {
-                bad = 1u;
-            }
-            if (i + 1 < keys.end) look_up(i + 1);
-            if (!E4M3 && is_k) {
-                // the mask: the positions below kv_end and not between the sinks and the window
-                uint32_t* mask = s_mask + ((i - keys.begin) % kSlots) * 4;
-                if (lane < kTile / 32) {
-                    const int b = keys.base(i) + 32 * lane;
-                    mask[lane] = static_cast<uint32_t>(low_bits(keys.kv_end - b) &
-                                                       (~low_bits(keys.lo - b) | low_bits(keys.sink_end - b)));
-                }
-                __syncwarp();
-                if (bad != 0) {
-                    *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
-                    for (int u = 0; u < box; ++u)
-                        if (!odd_pages || ((bad >> u) & 1u)) atomicAnd(&mask[(mine + u) >> 5], ~(1u << ((mine + u) & 31)));
-                }
-                __syncwarp();
-            }
-            if (!wait_long(empty0 + 8 * stage, phase ^ 1u, wc, kSiteKvEmpty)) ok = false;
+        for (int j = 0; j < nt; ++j) {
+            const int slot = j % kSlots;
+            ok = wait_long(m_full0 + 8 * slot, (j / kSlots) & 1, wc, kSiteKvMeta) &&
+                 wait_long(empty0 + 8 * stage, phase ^ 1u, wc, kSiteKvEmpty);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const uint32_t bar = full0 + 8 * stage;
-            const uint32_t dst = dst0 + stage * kBytes;
-            if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
-            __syncwarp();
             ++issued;
-            if (active) {
-                if (!odd_pages && (!good || keys.none(t, box) || keys.all(t, box))) {
-                    const int from = keys.none(t, box) ? none : row;   // from past the end: zeros
-                    if constexpr (E4M3)
-                        tma_load_2d(dst + mine * HD, box_map, bar, kvh * HD, from);
-                    else
-                        tma_load_4d(dst + (mine >> 3) * (NB * 1024), box_map, bar, 0, kvh * NB, from >> 3);
-                } else {
-                    for (int u = 0; u < box; u += 4) {
-                        int4 r;
-                        if (odd_pages) {
-                            r = make_int4(r4[0], r4[1], r4[2], r4[3]);
-                        } else {
-                            r.x = keys.holds(t + u) ? row + u : none;
-                            r.y = keys.holds(t + u + 1) ? row + u + 1 : none;
-                            r.z = keys.holds(t + u + 2) ? row + u + 2 : none;
-                            r.w = keys.holds(t + u + 3) ? row + u + 3 : none;
-                        }
-                        const int at = mine + u;
-                        if constexpr (E4M3) {
-                            tma_gather4(dst + at * HD, row_map, bar, kvh * HD, r);
-                        } else {
-                            for (int blk = 0; blk < NB; ++blk)
-                                tma_gather4(dst + ((at >> 3) * NB + blk) * 1024 + (at & 7) * 128, row_map, bar,
-                                            kvh * HD + blk * 64, r);
+            if (elect_one()) {
+                const uint32_t bar = full0 + 8 * stage;
+                const uint32_t dst = dst0 + stage * kBytes;
+                const int* rows_of = s_row + slot * kTile;
+                const uint32_t* mask = s_mask + slot * 4;
+                mbar_arrive_expect_tx(bar, kBytes);
+                for (int k = 0; k < kTile; k += box) {
+                    uint32_t all = box_bits, any = 0u;
+                    for (int w = k; w < k + box; w += 32) {
+                        const uint32_t m = (mask[w >> 5] >> (w & 31)) & box_bits;
+                        all &= m;
+                        any |= m;
+                    }
+                    if (box >= 8 && (all == box_bits || any == 0u)) {
+                        const int row = rows_of[k];
+                        if constexpr (!E4M3 && HD > 64)
+                            tma_load_4d(dst + (k >> 3) * (NB * 1024), box_map, bar, 0, kvh * NB, row >> 3);
+                        else if constexpr (!E4M3)
+                            tma_load_2d(dst + k * 128, box_map, bar, kvh * HD, row);
+                        else if constexpr (HD == 256)
+                            tma_load_3d(dst + k * HD, box_map, bar, row, kvh * 2);
+                        else
+                            tma_load_2d(dst + k * HD, box_map, bar, kvh * HD, row);
+                    } else {
+                        for (int u = k; u < k + box; u += 4) {
+                            const int4 r = *reinterpret_cast<const int4*>(rows_of + u);
+                            if constexpr (!E4M3) {
+                                for (int blk = 0; blk < NB; ++blk)
+                                    tma_gather4(dst + ((u >> 3) * NB + blk) * 1024 + (u & 7) * 128, row_map, bar,
+                                                kvh * HD + blk * 64, r);
+                            } else if constexpr (HD == 256) {
+                                for (int h = 0; h < 2; ++h)
+                                    tma_gather4(dst + k * HD + (h * box + u - k) * 128, row_map, bar,
+                                                kvh * HD + h * 128, r);
+                            } else {
+                                tma_gather4(dst + u * HD, row_map, bar, kvh * HD, r);
+                            }
                         }
                     }
                 }
             }
             __syncwarp();
+            if (!is_k && lane == 0) mbar_arrive(m_empty0 + 8 * slot);
             if (++stage == RING) {
                 stage = 0;
                 phase ^= 1u;
@@ -641,26 +618,29 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         // ------------------------------------------------------------------
         // MMA issuer
         // ------------------------------------------------------------------
-        if (lane == 0) {
-            bool ok = wait_long(q_full, 0, wc, kSiteKvQ);
+        {
+            bool ok = __all_sync(0xffffffffu, wait_long(q_full, 0, wc, kSiteKvQ));
             tc_fence_after_sync();
             const uint32_t q_tmem = tmem + G::kColQ, o_tmem = tmem + G::kColO;
             int ks = 0, vs = 0;
             uint32_t kph = 0, vph = 0;
             auto scores = [&](int j) {
-                ok = ok && wait_long(k_full0 + 8 * ks, kph, wc, kSiteKvFull);
+                ok = __all_sync(0xffffffffu, ok && wait_long(k_full0 + 8 * ks, kph, wc, kSiteKvFull));
                 if (!ok) return;
                 tc_fence_after_sync();
                 const uint32_t b = smem_u32(s_k + ks * G::kStageBytes);
+                if (elect_one()) {
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb)
+                    for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_tmem_a(tmem + (j & 1) * kTile, q_tmem + (kb * 4 + kk) * 8,
-                                       smem_desc_sw128(b + kb * 1024 + kk * 32, 16, NB * 1024), kIdescS,
-                                       (kb | kk) != 0 ? 1u : 0u);
-                mma_commit(s_full0 + 8 * (j & 1));
-                mma_commit(k_empty0 + 8 * ks);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_tmem_a(tmem + (j & 1) * kTile, q_tmem + (kb * 4 + kk) * 8,
+                                           smem_desc_sw128(b + kb * 1024 + kk * 32, 16, NB * 1024), kIdescS,
+                                           (kb | kk) != 0 ? 1u : 0u);
+                    mma_commit(s_full0 + 8 * (j & 1));
+                    mma_commit(k_empty0 + 8 * ks);
+                }
+                __syncwarp();
                 if (++ks == S) {
                     ks = 0;
                     kph ^= 1u;
@@ -669,17 +649,23 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             auto weighted = [&](int j) {
                 ok = ok && wait_long(v_full0 + 8 * vs, vph, wc, kSiteKvFull);
                 ok = ok && wait_long(p_full0 + 8 * (j & 1), (j >> 1) & 1, wc, kSiteKvWeights);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
                 tc_fence_after_sync();
                 const uint32_t b = smem_u32(s_v + vs * G::kStageBytes);
                 // 16 positions an MMA; those past kv_end are not multiplied
                 const int steps = min(kTile / 16, (keys.kv_end - keys.base(keys.begin + j) + 15) / 16);
-                for (int kk = 0; kk < steps; ++kk)
-                    mma_f16_tmem_a(o_tmem, tmem + (j & 1) * kTile + kk * 8,
-                                   smem_desc_sw128(b + kk * (NB * 2048), 1024, NB * 1024), kIdescO,
-                                   (j | kk) != 0 ? 1u : 0u);
-                mma_commit(o_done0 + 8 * (j & 1));
-                mma_commit(v_empty0 + 8 * vs);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        if (kk < steps)
+                            mma_f16_tmem_a(o_tmem, tmem + (j & 1) * kTile + kk * 8,
+                                           smem_desc_sw128(b + kk * (NB * 2048), 1024, NB * 1024), kIdescO,
+                                           (j | kk) != 0 ? 1u : 0u);
+                    mma_commit(o_done0 + 8 * (j & 1));
+                    mma_commit(v_empty0 + 8 * vs);
+                }
+                __syncwarp();
                 if (++vs == S) {
                     vs = 0;
                     vph ^= 1u;
@@ -692,74 +678,104 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             }
             if (!ok) {
                 // abort: every MMA issued so far finishes before TMEM is freed
-                mma_commit(drain);
+                if (elect_one()) mma_commit(drain);
+                __syncwarp();
                 mbar_wait(drain, 0u, wc_drain, kSiteKvDrain);
             }
         }
         __syncwarp();
-    } else if (warp == kWarpScales) {
-        if constexpr (E4M3) {
-            // ----------------------------------------------------------------
-            // Masks and scales, kTile / 32 positions per lane: block-table entries are
-            // loaded two tiles ahead, the scales one.
-            // ----------------------------------------------------------------
-            constexpr int PL = kTile / 32;
-            int entry[PL];
-            uint32_t kb[PL], vb[PL], have = 0;
-            auto look_up = [&](int i) {
-#pragma unroll
-                for (int u = 0; u < PL; ++u) {
-                    const int at = (keys.base(min(i, keys.end - 1)) + u * 32 + lane) / p.b.block_size;
-                    entry[u] = at < p.b.max_blocks ? table[at] : -1;
-                }
-            };
-            auto fetch = [&](int i) {
-                have = 0;
+    } else if (warp == kWarpPages) {
+        // ------------------------------------------------------------------
+        // Look-ups, some tiles ahead of the loads: each position's cache row (past the
+        // last row where it holds no key), the mask and the scales; kTile / 32
+        // positions per lane.  Block-table entries are loaded two tiles before they
+        // are published, scales one.
+        // ------------------------------------------------------------------
+        constexpr int PL = kTile / 32;
+        const int bs = p.b.block_size;
+        const int none = p.b.num_blocks * bs;
+        const int tile_pages = kTile / bs, tile_slots = kTile - tile_pages * bs;
+        int page[PL], off[PL];              // of the next tile to look up
+        int entry[PL], entry_off[PL];       // looked up: block-table entry and place in the page
+        int row[PL];                        // of the next tile to publish
+        uint32_t kb[PL], vb[PL], have = 0;
+        auto look_up = [&](int i) {         // tiles in turn
+            if (i >= keys.end) return;
+            if (i == keys.begin || i == keys.sink_tiles) {
 #pragma unroll
                 for (int u = 0; u < PL; ++u) {
                     const int t = keys.base(i) + u * 32 + lane;
-                    const bool h = i < keys.end && keys.holds(t);
-                    const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
-                    if (h && !g) *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
+                    page[u] = t / bs;
+                    off[u] = t - page[u] * bs;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < PL; ++u) {
+                entry[u] = page[u] < p.b.max_blocks ? table[page[u]] : -1;
+                entry_off[u] = off[u];
+                page[u] += tile_pages;
+                off[u] += tile_slots;
+                if (off[u] >= bs) {
+                    off[u] -= bs;
+                    ++page[u];
+                }
+            }
+        };
+        auto fetch = [&](int i) {           // the tile looked up last
+            if (i >= keys.end) return;
+            have = 0;
+            bool bad = false;
+#pragma unroll
+            for (int u = 0; u < PL; ++u) {
+                const bool h = keys.holds(keys.base(i) + u * 32 + lane);
+                const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
+                bad = bad || (h && !g);
+                row[u] = h && g ? entry[u] * bs + entry_off[u] : none;
+                have |= (h && g ? 1u : 0u) << u;
+                if constexpr (E4M3) {
                     kb[u] = vb[u] = 127u;
                     if (h && g) {
-                        const long long row = static_cast<long long>(entry[u]) * p.b.block_size + t % p.b.block_size;
-                        kb[u] = p.b.k_scales[row * p.b.num_kv_heads + kvh];
-                        vb[u] = p.b.v_scales[row * p.b.num_kv_heads + kvh];
-                        have |= 1u << u;
+                        const long long at = static_cast<long long>(row[u]) * p.b.num_kv_heads + kvh;
+                        kb[u] = p.b.k_scales[at];
+                        vb[u] = p.b.v_scales[at];
                     }
                 }
-            };
-            look_up(keys.begin);
-            fetch(keys.begin);
-            look_up(keys.begin + 1);
-            bool ok = true;
-            for (int j = 0; j < nt && ok; ++j) {
-                const int slot = j % kSlots;
-                ok = __all_sync(0xffffffffu, wait_long(m_empty0 + 8 * slot, ((j / kSlots) & 1) ^ 1, wc, kSiteKvMeta));
-                if (!ok) break;
-                // the range of V's exponents, all-zero rows (the least scale) left out
-                int top = 0, low = 255;
+            }
+            if (bad) *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
+        };
+        look_up(keys.begin);
+        fetch(keys.begin);
+        look_up(keys.begin + 1);
+        bool ok = true;
+        for (int j = 0; j < nt && ok; ++j) {
+            const int slot = j % kSlots;
+            ok = __all_sync(0xffffffffu, wait_long(m_empty0 + 8 * slot, ((j / kSlots) & 1) ^ 1, wc, kSiteKvMeta));
+            if (!ok) break;
+            int top = 0, low = 255;   // E4M3: the range of V's exponents, all-zero rows (the least scale) left out
 #pragma unroll
-                for (int u = 0; u < PL; ++u) {
-                    const bool h = ((have >> u) & 1u) != 0;
+            for (int u = 0; u < PL; ++u) {
+                const bool h = ((have >> u) & 1u) != 0;
+                s_row[slot * kTile + u * 32 + lane] = row[u];
+                const uint32_t word = __ballot_sync(0xffffffffu, h);
+                if (lane == 0) s_mask[slot * 4 + u] = word;
+                if constexpr (E4M3) {
                     s_kf[slot * kTile + u * 32 + lane] = e8m0_value(kb[u]);
                     s_vf[slot * kTile + u * 32 + lane] = e8m0_value(vb[u]);
-                    const uint32_t word = __ballot_sync(0xffffffffu, h);
-                    if (lane == 0) s_mask[slot * 4 + u] = word;
                     if (h && vb[u] > 10u && vb[u] != 255u) {
                         top = max(top, static_cast<int>(vb[u]));
                         low = min(low, static_cast<int>(vb[u]));
                     }
                 }
+            }
+            if constexpr (E4M3) {
                 top = __reduce_max_sync(0xffffffffu, top);
                 low = __reduce_min_sync(0xffffffffu, low);
                 if (lane == 0) s_exp[slot] = make_int2(top, low);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(m_full0 + 8 * slot);
-                fetch(keys.begin + j + 1);
-                look_up(keys.begin + j + 2);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(m_full0 + 8 * slot);
+            fetch(keys.begin + j + 1);
+            look_up(keys.begin + j + 2);
         }
     } else if (warp >= 12) {
         if constexpr (E4M3) {
@@ -777,7 +793,19 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                 wait_long((v ? rv_full0 : rk_full0) + 8 * rs, (j / RS) & 1, wc, kSiteKvRaw);
                 uint4 x[kChunks];
 #pragma unroll
-                for (int u = 0; u < kChunks; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + (u * 128 + tid) * 16);
+                for (int u = 0; u < kChunks; ++u) {
+                    const int ch = u * 128 + tid;
+                    const int r = ch / CPR, e = ch % CPR;
+                    // the line (128 bytes; 64 with HD = 64) of row r's codes, and the chunk in it,
+                    // swizzled by the line's place
+                    int line = r * (HD == 64 ? 64 : 128), c = e;
+                    if constexpr (HD == 256) {   // boxes of [2][box] lines
+                        line = ((r / p.box) * 2 + (e >> 3)) * (p.box * 128) + (r % p.box) * 128;
+                        c = e & 7;
+                    }
+                    c ^= (line >> 7) & (HD == 64 ? 3 : 7);
+                    x[u] = *reinterpret_cast<const uint4*>(raw + line + c * 16);
+                }
                 wait_long((v ? v_empty0 : k_empty0) + 8 * ss, ((j / S) & 1) ^ 1, wc, kSiteKvEmpty);
 #pragma unroll
                 for (int u = 0; u < kChunks; ++u) {
@@ -1006,7 +1034,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(p_full0 + 8 * buf);
-                if constexpr (E4M3) mbar_arrive(m_empty0 + 8 * slot);
+                mbar_arrive(m_empty0 + 8 * slot);
             }
         }
         // ---- the rows' results ---------------------------------------------
@@ -1174,21 +1202,27 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     const cuuint64_t width = static_cast<cuuint64_t>(a.b.num_kv_heads) * HD;
     const cuuint64_t cache_rows = static_cast<cuuint64_t>(a.b.num_blocks) * a.b.block_size;
     const cuuint64_t pitch = E4M3 ? width : width * 2;
-    const cuuint64_t dims[4] = {64, 8, width / 64, cache_rows / 8};
-    const cuuint64_t strides[3] = {pitch, 128, pitch * 8};
-    const cuuint64_t row_dims[2] = {width, cache_rows};
+    const cuuint32_t rows8 = static_cast<cuuint32_t>(p.box);
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const cuuint32_t box[4] = {64, 8, HD / 64, static_cast<cuuint32_t>(p.box / 8)};
-    const cuuint32_t raw_box[2] = {HD, static_cast<cuuint32_t>(p.box)};
-    const cuuint32_t row_box[2] = {E4M3 ? HD : 64, 1};
+    // (as in the kernel) 4-D: BF16; 3-D: E4M3 with HD = 256; 2-D: HD = 64, E4M3 with HD = 128, gathers
+    constexpr int kBoxDims = !E4M3 && HD > 64 ? 4 : (E4M3 && HD == 256 ? 3 : 2);
+    constexpr cuuint32_t kLine = E4M3 ? (HD < 128 ? HD : 128) : 64;   // elements of a swizzled line
+    const cuuint64_t dims2[2] = {width, cache_rows};
+    const cuuint64_t dims3[3] = {128, cache_rows, width / 128};
+    const cuuint64_t dims4[4] = {64, 8, width / 64, cache_rows / 8};
+    const cuuint64_t strides2[1] = {pitch}, strides3[2] = {pitch, 128}, strides4[3] = {pitch, 128, pitch * 8};
+    const cuuint32_t row_box[2] = {kLine, 1}, box2[2] = {kLine, rows8}, box3[3] = {128, rows8, 2};
+    const cuuint32_t box4[4] = {64, 8, HD / 64, rows8 / 8};
     CUtensorMap* const map[4] = {&maps.k_row, &maps.v_row, &maps.k_box, &maps.v_box};
     for (int i = 0; i < (p.box >= 8 ? 4 : 2); ++i) {
-        const bool flat = i < 2 || E4M3;
-        const CUresult r = enc(map[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                               flat ? 2 : 4, i % 2 == 0 ? a.b.k : a.b.v, flat ? row_dims : dims, strides,
-                               i < 2 ? row_box : (E4M3 ? raw_box : box), ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                               E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        const int d = i < 2 ? 2 : kBoxDims;
+        const CUresult r =
+            enc(map[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                static_cast<cuuint32_t>(d), i % 2 == 0 ? a.b.k : a.b.v, d == 2 ? dims2 : (d == 3 ? dims3 : dims4),
+                d == 2 ? strides2 : (d == 3 ? strides3 : strides4),
+                i < 2 ? row_box : (d == 2 ? box2 : (d == 3 ? box3 : box4)), ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                E4M3 && HD == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) {
             snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for the cache", static_cast<int>(r));
             return cudaErrorInvalidValue;
