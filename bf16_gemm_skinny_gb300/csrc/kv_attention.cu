@@ -41,15 +41,7 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// One box of a tensor map, from its first dimensions' start (x of a 2-D map).
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z)
-        : "memory");
-}
+// Cache rows of one KV head, a multiple of 8 of them, from the 4-D view below.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z, int w)
 {
     asm volatile(
@@ -202,6 +194,9 @@ constexpr int kSlots = 8;         // tiles whose cache rows, masks and scales ar
 
 // Warps 0..3: keys' loads, MMAs, values' loads, look-ups in the block table.
 enum AttnWarp : int { kWarpK = 0, kWarpMma = 1, kWarpV = 2, kWarpPages = 3 };
+// How a tile is loaded: its rows lie side by side (one box), its boxes are each
+// whole or without a key, or some box is neither.
+enum LoadKind : int { kLoadTile = 0, kLoadBoxes = 1, kLoadRows = 2 };
 enum AttnSite : int {
     kSiteKvEmpty = 0x30, kSiteKvFull, kSiteKvQ, kSiteKvScores, kSiteKvWeights, kSiteKvOutput, kSiteKvDrain,
     kSiteKvRaw, kSiteKvMeta
@@ -226,7 +221,7 @@ struct Geo {
     static constexpr int kThreads = E4M3 ? 512 : 384;
     static constexpr int kBars = 4 * kStages + 4 * kRawStages + 2 * kSlots + 8;
     static constexpr int kScaleBytes = E4M3 ? kSlots * (kTile * 8 + 8) : 0;
-    static constexpr int kMisc = kScaleBytes + kSlots * kTile * 4 + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
+    static constexpr int kMisc = kScaleBytes + kSlots * (kTile + 36) * 4 + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
     static constexpr int kBytes = 1024 + 2 * kStages * kStageBytes + 2 * kRawStages * kRawBytes + kMisc;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
 };
@@ -239,6 +234,7 @@ struct AttnParams {
     int num_q_heads, group, max_chunk, max_seq_len;
     int tiles, segments;          // row tiles per sequence and KV head, key segments per tile
     int box;                      // rows per TMA box, or 4: pages of an odd size, gathers only
+    int tile_rows;                // cache rows that boxes of a tile's rows may cover
     float scale_log2;             // |softmax scale| * log2(e), > 0
     uint32_t q_sign;              // 0x80008000 for a negative scale
     int window, sinks;
@@ -250,10 +246,11 @@ struct AttnParams {
 // Tensor maps of the cache.  Gathers see it as [num_blocks * block_size] rows of
 // heads * HD values.  Boxes are `box` rows of one head: of a BF16 cache as the stages
 // want them ([rows / 8][heads * HD / 64][8][64]), of an E4M3 cache in lines of at
-// most 128 codes ([heads * HD / 128][rows][128] with HD = 256), each swizzled: without
-// swizzling the TMA unit writes 31 bytes a clock, with it 57.
+// most 128 codes, each swizzled: without
+// swizzling the TMA unit writes 31 bytes a clock, with it 57.  Tile boxes are the
+// same with a tile's rows.
 struct KvMaps {
-    CUtensorMap k_box, v_box, k_row, v_row;
+    CUtensorMap k_tile, v_tile, k_box, v_box, k_row, v_row;
 };
 
 // The key tiles that some row of a CTA sees: those of the sinks, then those from
@@ -270,6 +267,20 @@ struct Keys {
     __device__ __forceinline__ bool all(int t, int n) const { return t + n <= kv_end && (t >= lo || t + n <= sink_end); }
     __device__ __forceinline__ bool none(int t, int n) const { return t >= kv_end || (t >= sink_end && t + n <= lo); }
 };
+
+// Of the positions k .. k + box - 1 (box a power of two), by a tile's mask: 0 none
+// holds a key, 1 all do, 2 some.
+__device__ __forceinline__ int box_state(const uint32_t* mask, int k, int box)
+{
+    const uint32_t bits = box >= 32 ? 0xffffffffu : (1u << box) - 1u;
+    uint32_t all = bits, any = 0u;
+    for (int w = k; w < k + box; w += 32) {
+        const uint32_t m = (mask[w >> 5] >> (w & 31)) & bits;
+        all &= m;
+        any |= m;
+    }
+    return all == bits ? 1 : (any == 0u ? 0 : 2);
+}
 
 // The k lowest of 64 bits.
 __device__ __forceinline__ unsigned long long low_bits(int k)
@@ -397,7 +408,9 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
     float* s_vf = s_kf + (E4M3 ? kSlots * kTile : 0);               //       V scales
     int2* s_exp = reinterpret_cast<int2*>(s_vf + (E4M3 ? kSlots * kTile : 0));    // [kSlots] V scales' range
     int* s_row = reinterpret_cast<int*>(s_exp + (E4M3 ? kSlots : 0));   // [kSlots][kTile] cache row of each position
-    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_row + kSlots * kTile);       // [kSlots][4] positions that hold a key
+    int* s_box = s_row + kSlots * kTile;                            // [kSlots][32] cache row of each box
+    int* s_kind = s_box + kSlots * 32;                              // [kSlots][4] (first used) LoadKind of the tile
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(s_kind + kSlots * 4);          // [kSlots][4] positions that hold a key
     float* s_max = reinterpret_cast<float*>(s_mask + kSlots * 4);   // [2][2][kRows]
     int* s_flag = reinterpret_cast<int*>(s_max + 4 * kRows);        // [kRows] rows to repair
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_flag + kRows);
@@ -537,6 +550,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         // clock at best); with two warps one's overhead hides behind the other's.
         // ------------------------------------------------------------------
         const bool is_k = warp == kWarpK;
+        const CUtensorMap* tile_map = is_k ? &maps.k_tile : &maps.v_tile;
         const CUtensorMap* box_map = is_k ? &maps.k_box : &maps.v_box;
         const CUtensorMap* row_map = is_k ? &maps.k_row : &maps.v_row;
         constexpr int RING = E4M3 ? RS : S;
@@ -545,8 +559,20 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         const uint32_t empty0 = E4M3 ? (is_k ? rk_empty0 : rv_empty0) : (is_k ? k_empty0 : v_empty0);
         const uint32_t dst0 = smem_u32(E4M3 ? (is_k ? r_k : r_v) : (is_k ? s_k : s_v));
         const int box = p.box;
-        // the positions of a box as bits of a mask word (a box of 64 or 128 is whole words)
-        const uint32_t box_bits = box >= 32 ? 0xffffffffu : (1u << box) - 1u;
+        // the rows from `row` on, as positions k .. of a tile
+        auto load_box = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row) {
+            if constexpr (!E4M3 && HD > 64) {
+                tma_load_4d(dst + (k >> 3) * (NB * 1024), map, bar, 0, kvh * NB, row >> 3);
+            } else if constexpr (!E4M3) {
+                tma_load_2d(dst + k * 128, map, bar, kvh * HD, row);
+            } else if constexpr (HD == 256) {
+                // two lines of 128 codes a row, kTile lines apart
+                tma_load_2d(dst + k * 128, map, bar, kvh * HD, row);
+                tma_load_2d(dst + kTile * 128 + k * 128, map, bar, kvh * HD + 128, row);
+            } else {
+                tma_load_2d(dst + k * HD, map, bar, kvh * HD, row);
+            }
+        };
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -561,27 +587,27 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             if (elect_one()) {
                 const uint32_t bar = full0 + 8 * stage;
                 const uint32_t dst = dst0 + stage * kBytes;
-                const int* rows_of = s_row + slot * kTile;
-                const uint32_t* mask = s_mask + slot * 4;
+                const int kind = s_kind[slot * 4];
+                const int4* boxes = reinterpret_cast<const int4*>(s_box + slot * 32);
                 mbar_arrive_expect_tx(bar, kBytes);
-                for (int k = 0; k < kTile; k += box) {
-                    uint32_t all = box_bits, any = 0u;
-                    for (int w = k; w < k + box; w += 32) {
-                        const uint32_t m = (mask[w >> 5] >> (w & 31)) & box_bits;
-                        all &= m;
-                        any |= m;
+                if (kind == kLoadTile) {
+                    load_box(dst, tile_map, bar, 0, boxes[0].x);
+                } else if (kind == kLoadBoxes) {
+                    for (int k = 0; k < kTile; k += 4 * box) {
+                        const int4 r = boxes[k / box >> 2];
+                        load_box(dst, box_map, bar, k, r.x);
+                        if (k + box < kTile) load_box(dst, box_map, bar, k + box, r.y);
+                        if (k + 2 * box < kTile) load_box(dst, box_map, bar, k + 2 * box, r.z);
+                        if (k + 3 * box < kTile) load_box(dst, box_map, bar, k + 3 * box, r.w);
                     }
-                    if (box >= 8 && (all == box_bits || any == 0u)) {
-                        const int row = rows_of[k];
-                        if constexpr (!E4M3 && HD > 64)
-                            tma_load_4d(dst + (k >> 3) * (NB * 1024), box_map, bar, 0, kvh * NB, row >> 3);
-                        else if constexpr (!E4M3)
-                            tma_load_2d(dst + k * 128, box_map, bar, kvh * HD, row);
-                        else if constexpr (HD == 256)
-                            tma_load_3d(dst + k * HD, box_map, bar, row, kvh * 2);
-                        else
-                            tma_load_2d(dst + k * HD, box_map, bar, kvh * HD, row);
-                    } else {
+                } else {
+                    const int* rows_of = s_row + slot * kTile;
+                    const uint32_t* mask = s_mask + slot * 4;
+                    for (int k = 0; k < kTile; k += box) {
+                        if (box >= 8 && box_state(mask, k, box) != 2) {
+                            load_box(dst, box_map, bar, k, rows_of[k]);
+                            continue;
+                        }
                         for (int u = k; u < k + box; u += 4) {
                             const int4 r = *reinterpret_cast<const int4*>(rows_of + u);
                             if constexpr (!E4M3) {
@@ -590,8 +616,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                                                 kvh * HD + blk * 64, r);
                             } else if constexpr (HD == 256) {
                                 for (int h = 0; h < 2; ++h)
-                                    tma_gather4(dst + k * HD + (h * box + u - k) * 128, row_map, bar,
-                                                kvh * HD + h * 128, r);
+                                    tma_gather4(dst + h * (kTile * 128) + u * 128, row_map, bar, kvh * HD + h * 128, r);
                             } else {
                                 tma_gather4(dst + u * HD, row_map, bar, kvh * HD, r);
                             }
@@ -773,6 +798,22 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                 if (lane == 0) s_exp[slot] = make_int2(top, low);
             }
             __syncwarp();
+            {
+                // lane's box (pages of an odd size: four positions, gathers only unless the tile is one box)
+                const int k = lane * p.box;
+                const bool in = k < kTile;
+                const int state = in ? box_state(s_mask + slot * 4, k, p.box) : 0;
+                const int first_row = s_row[slot * kTile + (in ? k : 0)];
+                const int row0 = __shfl_sync(0xffffffffu, first_row, 0);
+                const bool run = !in || (state == 1 && first_row == row0 + k &&
+                                         (p.box >= 8 || s_row[slot * kTile + k + 3] == first_row + 3));
+                const bool tiled = __all_sync(0xffffffffu, run) && p.tile_rows > 0 && row0 + kTile <= p.tile_rows &&
+                                   (E4M3 || HD == 64 || (row0 & 7) == 0);
+                const bool boxed = p.box >= 8 && __all_sync(0xffffffffu, state != 2);
+                if (in) s_box[slot * 32 + lane] = first_row;
+                if (lane == 0) s_kind[slot * 4] = tiled ? kLoadTile : (boxed ? kLoadBoxes : kLoadRows);
+            }
+            __syncwarp();
             if (lane == 0) mbar_arrive(m_full0 + 8 * slot);
             fetch(keys.begin + j + 1);
             look_up(keys.begin + j + 2);
@@ -798,12 +839,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                     const int r = ch / CPR, e = ch % CPR;
                     // the line (128 bytes; 64 with HD = 64) of row r's codes, and the chunk in it,
                     // swizzled by the line's place
-                    int line = r * (HD == 64 ? 64 : 128), c = e;
-                    if constexpr (HD == 256) {   // boxes of [2][box] lines
-                        line = ((r / p.box) * 2 + (e >> 3)) * (p.box * 128) + (r % p.box) * 128;
-                        c = e & 7;
-                    }
-                    c ^= (line >> 7) & (HD == 64 ? 3 : 7);
+                    const int line = ((e >> 3) * kTile + r) * (HD == 64 ? 64 : 128);
+                    const int c = (e & 7) ^ ((line >> 7) & (HD == 64 ? 3 : 7));
                     x[u] = *reinterpret_cast<const uint4*>(raw + line + c * 16);
                 }
                 wait_long((v ? v_empty0 : k_empty0) + 8 * ss, ((j / S) & 1) ^ 1, wc, kSiteKvEmpty);
@@ -1204,23 +1241,21 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     const cuuint64_t pitch = E4M3 ? width : width * 2;
     const cuuint32_t rows8 = static_cast<cuuint32_t>(p.box);
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    // (as in the kernel) 4-D: BF16; 3-D: E4M3 with HD = 256; 2-D: HD = 64, E4M3 with HD = 128, gathers
-    constexpr int kBoxDims = !E4M3 && HD > 64 ? 4 : (E4M3 && HD == 256 ? 3 : 2);
+    constexpr int kBoxDims = !E4M3 && HD > 64 ? 4 : 2;   // as in the kernel
+    constexpr int kTile = Geo<E4M3, HD>::kTile;
     constexpr cuuint32_t kLine = E4M3 ? (HD < 128 ? HD : 128) : 64;   // elements of a swizzled line
-    const cuuint64_t dims2[2] = {width, cache_rows};
-    const cuuint64_t dims3[3] = {128, cache_rows, width / 128};
-    const cuuint64_t dims4[4] = {64, 8, width / 64, cache_rows / 8};
-    const cuuint64_t strides2[1] = {pitch}, strides3[2] = {pitch, 128}, strides4[3] = {pitch, 128, pitch * 8};
-    const cuuint32_t row_box[2] = {kLine, 1}, box2[2] = {kLine, rows8}, box3[3] = {128, rows8, 2};
-    const cuuint32_t box4[4] = {64, 8, HD / 64, rows8 / 8};
-    CUtensorMap* const map[4] = {&maps.k_row, &maps.v_row, &maps.k_box, &maps.v_box};
-    for (int i = 0; i < (p.box >= 8 ? 4 : 2); ++i) {
+    p.tile_rows = static_cast<int>(cache_rows / 8 * 8);
+    const cuuint64_t dims2[2] = {width, cache_rows}, dims4[4] = {64, 8, width / 64, cache_rows / 8};
+    const cuuint64_t strides2[1] = {pitch}, strides4[3] = {pitch, 128, pitch * 8};
+    CUtensorMap* const map[6] = {&maps.k_row, &maps.v_row, &maps.k_tile, &maps.v_tile, &maps.k_box, &maps.v_box};
+    for (int i = 0; i < (p.box >= 8 ? 6 : (p.tile_rows > 0 ? 4 : 2)); ++i) {
         const int d = i < 2 ? 2 : kBoxDims;
+        const cuuint32_t r8 = i < 2 ? 1 : (i < 4 ? kTile : rows8);
+        const cuuint32_t box2[2] = {kLine, r8}, box4[4] = {64, 8, HD / 64, r8 / 8};
         const CUresult r =
             enc(map[i], E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                static_cast<cuuint32_t>(d), i % 2 == 0 ? a.b.k : a.b.v, d == 2 ? dims2 : (d == 3 ? dims3 : dims4),
-                d == 2 ? strides2 : (d == 3 ? strides3 : strides4),
-                i < 2 ? row_box : (d == 2 ? box2 : (d == 3 ? box3 : box4)), ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                static_cast<cuuint32_t>(d), i % 2 == 0 ? a.b.k : a.b.v, d == 2 ? dims2 : dims4,
+                d == 2 ? strides2 : strides4, d == 2 ? box2 : box4, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 E4M3 && HD == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) {
