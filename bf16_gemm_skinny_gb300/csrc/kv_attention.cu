@@ -84,6 +84,17 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
+// Each lane reads 16 consecutive columns of its TMEM lane.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // One lane of a converged warp, always the same.  A branch on this (and not on
@@ -980,6 +991,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                         const float4 f = kf[c];
                         x[2 * c] = mul2(x[2 * c], make_float2(f.x, f.y));
                         x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(f.z, f.w));
+                        if (c % 4 == 3) asm volatile("" ::: "memory");   // no more loads ahead: registers
                     }
                     const int2 range = s_exp[slot];
                     if (range.x > 0) {
@@ -1031,40 +1043,48 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                     l2 = mul2(l2, make_float2(f, f));
                     wait_long(o_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, wc, kSiteKvOutput);   // PV of j - 1
                     tc_fence_after_sync();
-                    // this half of the row's O
-                    for (int c = 0; c < HD / 64; ++c) {
-                        const uint32_t o_addr = lane_addr + G::kColO + half * (HD / 2) + c * 32;
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(o_addr, o);
+                    // this half of the row's O, 16 columns at a time (beside x in registers)
+#pragma unroll 1
+                    for (int c = 0; c < HD / 32; ++c) {
+                        const uint32_t o_addr = lane_addr + G::kColO + half * (HD / 2) + c * 16;
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(o_addr, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st_32x32b_x32(o_addr, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st_32x32b_x16(o_addr, o);
                     }
                 }
                 float base = m == -INFINITY ? 0.f : m;
                 if constexpr (E4M3) base -= static_cast<float>(3 - E);
                 const float2 sc = make_float2(row_scale, row_scale), nb = make_float2(-base, -base);
-                uint32_t w[C / 2];
-#pragma unroll
-                for (int c = 0; c < C / 2; ++c) {
-                    float2 e = fma2(x[c], sc, nb);
-                    e.x = exp2_fast(e.x);
-                    e.y = exp2_fast(e.y);
-                    l2 = add2(l2, e);
-                    if constexpr (E4M3) {
-                        const float2 f = *reinterpret_cast<const float2*>(s_vf + slot * kTile + half * C + 2 * c);
-                        e = mul2(e, f);
-                        w[c] = f16x2(e.x, e.y);
-                    } else {
-                        w[c] = bf16x2(e.x, e.y);
-                    }
-                }
                 const uint32_t p_addr = lane_addr + buf * kTile + half * (C / 2);
-                if constexpr (C == 64)
-                    tmem_st_32x32b_x32(p_addr, w);
-                else
-                    tmem_st_32x32b_x16(p_addr, w);
+#pragma unroll
+                for (int g = 0; g < C / 32; ++g) {   // 32 columns, 16 of P, at a time
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        float2 e0 = fma2(x[16 * g + c], sc, nb), e1 = fma2(x[16 * g + c + 1], sc, nb);
+                        e0.x = exp2_fast(e0.x);
+                        e0.y = exp2_fast(e0.y);
+                        e1.x = exp2_fast(e1.x);
+                        e1.y = exp2_fast(e1.y);
+                        l2 = add2(l2, add2(e0, e1));
+                        if constexpr (E4M3) {
+                            const float4 f =
+                                *reinterpret_cast<const float4*>(s_vf + slot * kTile + half * C + 32 * g + 2 * c);
+                            e0 = mul2(e0, make_float2(f.x, f.y));
+                            e1 = mul2(e1, make_float2(f.z, f.w));
+                            w[c] = f16x2(e0.x, e0.y);
+                            w[c + 1] = f16x2(e1.x, e1.y);
+                            if (c % 8 == 6) asm volatile("" ::: "memory");
+                        } else {
+                            w[c] = bf16x2(e0.x, e0.y);
+                            w[c + 1] = bf16x2(e1.x, e1.y);
+                        }
+                    }
+                    tmem_st_32x32b_x16(p_addr + 16 * g, w);
+                }
                 tmem_st_wait();
                 tc_fence_before_sync();
             }
