@@ -1023,10 +1023,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ At
     }
 }
 
-// Whether a call takes the kernel for few query rows per KV head.
-bool few_rows(const KvAttnLaunch& a)
+// Rows per CTA of the kernel for few query rows per KV head, or 0: the call takes
+// the other kernel.
+int few_rows(const KvAttnLaunch& a)
 {
-    return static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads) <= 32;
+    const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
+    return rows <= 8 ? 8 : (rows <= 32 ? 16 : 0);
 }
 
 template <bool E4M3, int HD>
@@ -1043,7 +1045,8 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     p.max_chunk = a.max_chunk;
     p.max_seq_len = a.max_seq_len;
     const long long max_rows = static_cast<long long>(a.max_chunk) * p.group;
-    const int cta_rows = few_rows(a) ? 8 : kRows;
+    const int few = few_rows(a);
+    const int cta_rows = few > 0 ? few : kRows;
     p.tiles = static_cast<int>((max_rows + cta_rows - 1) / cta_rows);
     p.segments = a.segments;
     // a zero scale still has to keep -inf (a position not seen) at -inf
@@ -1063,8 +1066,8 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
         return launch_kernel(kv_join_kernel<HD, false>, dim3(static_cast<unsigned>((rows + kPerCta - 1) / kPerCta)),
                              dim3(256), 0, stream, a.pdl, p);
     };
-    if (few_rows(a)) {
-        const cudaError_t e = launch_few_rows<E4M3, HD>(p, a.pdl, stream);
+    if (few > 0) {
+        const cudaError_t e = launch_few_rows<E4M3, HD>(p, few, a.pdl, stream);
         return e != cudaSuccess ? e : join();
     }
     KvMaps maps = {};
@@ -1119,8 +1122,8 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
 
 int kv_attention_segments(const KvAttnLaunch& a)
 {
-    const bool few = few_rows(a);
-    const int cta_rows = few ? 8 : kRows;
+    const int few = few_rows(a);
+    const int cta_rows = few ? few : kRows;
     const int tile = few ? 64 : (a.b.head_dim == 256 ? 64 : 128);
     const long long group = a.num_q_heads / a.b.num_kv_heads;
     const long long per_seq = (static_cast<long long>(a.max_chunk) * group + cta_rows - 1) / cta_rows;

@@ -209,10 +209,10 @@ __device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* tabl
     }
 }
 
-// Launches the kernel for few query rows: 8 rows per CTA, p.tiles of them per
-// sequence and KV head.
+// Launches the kernel for few query rows: `rows` (8 or 16) per CTA, p.tiles of them
+// per sequence and KV head.
 template <bool E4M3, int HD>
-cudaError_t launch_few_rows(const AttnParams& p, bool pdl, cudaStream_t stream);
+cudaError_t launch_few_rows(const AttnParams& p, int rows, bool pdl, cudaStream_t stream);
 
 }  // namespace kv
 }  // namespace bsk

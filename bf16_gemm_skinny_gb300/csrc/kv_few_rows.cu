@@ -3,9 +3,9 @@
 //
 // The same one-pass sums as kv_attention.cu, but the cache is read once for at
 // most 8 rows, so what counts is the stream from HBM; the tcgen05 path would send
-// every key through shared memory twice for an MMA of 128 rows.  Here keys and
-// values go from global memory to registers and from there into mma.sync, with
-// the positions as the M of the products:
+// every key through shared memory twice for an MMA of 128 rows.  Here each lane
+// copies (cp.async) what it will itself need, a few groups ahead, and feeds it
+// from registers into mma.sync, with the positions as the M of the products:
 //   S^T (16 positions x 8 rows) = K Q^T,   O^T (16 dimensions x 8 rows) += V^T P^T
 // The order of the dimensions within a product is free, so each lane loads 16
 // contiguous bytes of a key's row and uses them as its fragments of several MMAs
@@ -14,9 +14,8 @@
 // of P^T by movmatrix.  E4M3 codes become FP16 pairs by one instruction each
 // (exact), and Q, scaled by a power of two per row, FP16 too.
 //
-// A warp takes every fourth group of 16 positions of its CTA's segment; the next
-// group's keys load while this one's values are used and the other way round.
-// The CTA's four warps are joined in shared memory, the segments by kv_join_kernel.
+// The warps of a CTA take the groups of 16 positions of its segment in turn.  They
+// are joined in shared memory, the segments by kv_join_kernel.
 #include <cstdio>
 
 #include "bsk_internal.h"
@@ -26,9 +25,7 @@ namespace bsk {
 namespace kv {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kGroup = 16;   // positions per step of a warp
-constexpr int kRows8 = 8;    // query rows per CTA (the N of the MMAs)
 
 template <bool E4M3>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -55,31 +52,54 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-// A 16-byte load that leaves no line in L1 (the cache is read once).
-__device__ __forceinline__ uint4 load_once(const void* p)
+// 16 bytes global -> shared, asynchronous; `in` false: zeros.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool in)
 {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <bool E4M3, int HD>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __grid_constant__ AttnParams p)
+// Sizes.  `kAhead` groups per warp are on their way: two CTAs of an SM have 100 to
+// 200 KB in flight, which the latency times HBM's rate needs (about 45 KB) with
+// room for uneven progress.
+template <bool E4M3, int HD, int R>
+struct Few {
+    static constexpr int kRows = 8 * R;                 // query rows per CTA (R MMAs of N = 8)
+    static constexpr int kElem = E4M3 ? 1 : 2;
+    static constexpr int kVec = 16 / kElem;             // values in 16 bytes
+    static constexpr int kKeyVecs = HD / (4 * kVec);    // 16-byte pieces of a key's row per lane (4 lanes a row)
+    // values: 8 lanes a row.  With HD = 64 in E4M3 a lane's share is 8 bytes; it takes
+    // the 16 around them and uses its half.
+    static constexpr bool kHalf = E4M3 && HD == 64;
+    static constexpr int kValVecs = kHalf ? 1 : HD / (8 * kVec);
+    static constexpr int kRowBytes = HD * kElem;
+    static constexpr int kWarps = kRowBytes == 512 ? 3 : 4;
+    static constexpr int kAhead = kRowBytes == 512 ? 2 : (kRowBytes == 256 ? 3 : 4);
+    static constexpr int kCtas = HD == 256 || R > 1 || kRowBytes == 256 ? 2 : 3;   // of an SM
+    static constexpr int kKeyBytes = 2 * kKeyVecs * 512, kValBytes = 4 * kValVecs * 512;   // of a group
+    static constexpr int kWarpRing = kAhead * (kKeyBytes + kValBytes);
+    static constexpr int kRing = kWarps * kWarpRing;
+    static constexpr int kOut = kWarps * kRows * HD * 4;   // the warps' O, over the ring
+    static constexpr int kPitch = HD + 8;                   // Q rows, padded against bank conflicts
+    static constexpr int kBytes = (kRing > kOut ? kRing : kOut) + kRows * kPitch * 2;
+};
+
+template <bool E4M3, int HD, int R>
+__global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R>::kCtas) kv_few_rows_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr int kElem = E4M3 ? 1 : 2;
-    constexpr int kVec = 16 / kElem;             // values in 16 bytes
-    constexpr int kKeyVecs = HD / (4 * kVec);    // 16-byte loads of a key's row per lane (4 lanes a row)
-    // values: 8 lanes a row.  With HD = 64 in E4M3 a lane's share is 8 bytes; it
-    // loads the 16 around them and uses its half.
-    constexpr bool kHalf = E4M3 && HD == 64;
-    constexpr int kValVecs = kHalf ? 1 : HD / (8 * kVec);
+    using F = Few<E4M3, HD, R>;
+    constexpr int kWarps = F::kWarps, kElem = F::kElem, kVec = F::kVec, kKeyVecs = F::kKeyVecs, kValVecs = F::kValVecs;
+    constexpr bool kHalf = F::kHalf;
+    constexpr int A = F::kAhead;
     constexpr int kDim = HD / 16;                // O^T tiles
-    constexpr int kPitch = HD + 8;               // Q rows in shared memory, padded against bank conflicts
-    __shared__ __align__(16) uint16_t s_q[kRows8 * kPitch];
-    __shared__ float s_o[kWarps][kRows8][HD];
-    __shared__ float s_m[kWarps][kRows8], s_l[kWarps][kRows8], s_scale[kRows8];
+    constexpr int kPitch = F::kPitch;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + F::kBytes - F::kRows * kPitch * 2);
+    float* s_o = reinterpret_cast<float*>(smem);          // [kWarps][F::kRows][HD], once the ring is done with
+    __shared__ uint32_t s_meta[kWarps][A + 1][kGroup];   // scale bytes, and bit 16: holds a key
+    __shared__ float s_m[kWarps][F::kRows], s_l[kWarps][F::kRows], s_scale[F::kRows];
     __shared__ int s_flag;
 
     const int warp = threadIdx.x >> 5;
@@ -108,8 +128,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
     }
     int len = p.b.seq_lens[seq];
     len = len < 0 ? 0 : (len > p.max_seq_len ? p.max_seq_len : len);
-    const int row0 = tile * kRows8;
-    const int rows = min(kRows8, n * p.group - row0);
+    const int row0 = tile * F::kRows;
+    const int rows = min(F::kRows, n * p.group - row0);
     if (rows <= 0) return;
     const int pos0 = len - n;
     const int pmin = pos0 + row0 / p.group, pmax = pos0 + (row0 + rows - 1) / p.group;
@@ -128,7 +148,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
 
     // ---- Q: 16-bit rows in shared memory; rows that do not exist are zero ----
     if (threadIdx.x == 0) s_flag = 0;
-    for (int r = warp; r < kRows8; r += kWarps) {
+    for (int r = warp; r < F::kRows; r += kWarps) {
         constexpr int kPairs = HD / 64;   // 32-bit pairs per lane
         uint32_t w[kPairs];
         const int my = row0 + min(r, rows - 1);
@@ -157,21 +177,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
     }
     __syncthreads();
 
-    // this lane's two rows (columns 2c, 2c+1 of S^T)
-    float row_scale[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int row_pos[2], row_lo[2];
+    // this lane's rows: 8 n + 2c and 8 n + 2c + 1 (columns 2c, 2c + 1 of S^T n)
+    float row_scale[R][2], m[R][2], l[R][2];
+    int row_pos[R][2], row_lo[R][2];
+    float o[R][kDim][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        row_scale[i] = s_scale[2 * c + i];
-        row_pos[i] = 2 * c + i < rows ? pos0 + (row0 + 2 * c + i) / p.group : -1;
-        row_lo[i] = p.window > 0 && row_pos[i] - p.window + 1 > 0 ? row_pos[i] - p.window + 1 : 0;
+    for (int n8 = 0; n8 < R; ++n8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 8 * n8 + 2 * c + i;
+            row_scale[n8][i] = s_scale[r];
+            row_pos[n8][i] = r < rows ? pos0 + (row0 + r) / p.group : -1;
+            row_lo[n8][i] = p.window > 0 && row_pos[n8][i] - p.window + 1 > 0 ? row_pos[n8][i] - p.window + 1 : 0;
+            m[n8][i] = -INFINITY;
+            l[n8][i] = 0.f;
+        }
+#pragma unroll
+        for (int d = 0; d < kDim; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n8][d][i] = 0.f;
     }
     const int lo_max = p.window > 0 ? pmax - p.window + 1 : 0;
-    float o[kDim][4];
-#pragma unroll
-    for (int d = 0; d < kDim; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[d][i] = 0.f;
     // E4M3 (as in kv_attention.cu): o and l hold 2^(3 - E) of their values
     int E = 0, low_e = 1000;
     bool wide = false;
@@ -180,102 +206,151 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
     const uint8_t* vc = static_cast<const uint8_t*>(p.b.v) + static_cast<long long>(kvh) * HD * kElem;
     const long long pitch = static_cast<long long>(p.b.num_kv_heads) * HD * kElem;
     const int mine = lane & 15;   // the position of a group whose page this lane looks up
-    int entry = -1, row = -1;     // block-table entry of the group after next, cache row in the next
+    int entry = -1, row = -1;     // block-table entry of the group looked up last, cache row of the one found last
     uint32_t kb = 127u, vb = 127u;
+    // page and place in it of the group to look up next, stepped from group to group
+    const int bs = p.b.block_size;
+    const int step_pages = kWarps * kGroup / bs, step_slots = kWarps * kGroup - step_pages * bs;
+    int page = 0, off = 0, entry_off = 0;
+    bool fresh = true, in_sinks = false;
     auto look_up = [&](int i) {
         entry = -1;
         if (i < keys.end) {
-            const int at = (keys.base(i) + mine) / p.b.block_size;
-            if (at < p.b.max_blocks) entry = table[at];
+            if (fresh || (in_sinks && i >= keys.sink_tiles)) {
+                const int t = keys.base(i) + mine;
+                page = t / bs;
+                off = t - page * bs;
+                fresh = false;
+                in_sinks = i < keys.sink_tiles;
+            }
+            if (page < p.b.max_blocks) entry = table[page];
+            entry_off = off;
+            page += step_pages;
+            off += step_slots;
+            if (off >= bs) {
+                off -= bs;
+                ++page;
+            }
         }
     };
     auto find = [&](int i) {   // the group looked up last
         row = -1;
         kb = vb = 127u;
-        if (i < keys.end) {
-            const int t = keys.base(i) + mine;
-            if (keys.holds(t)) {
-                if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks)) {
-                    row = entry * p.b.block_size + t % p.b.block_size;
-                    if constexpr (E4M3) {
-                        kb = p.b.k_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
-                        vb = p.b.v_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
-                    }
-                } else {
-                    *reinterpret_cast<volatile int*>(p.b.status) = 0x200;   // kDevErrBadIndex
+        if (i < keys.end && keys.holds(keys.base(i) + mine)) {
+            if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks)) {
+                row = entry * bs + entry_off;
+                if constexpr (E4M3) {
+                    kb = p.b.k_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
+                    vb = p.b.v_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
                 }
+            } else {
+                *reinterpret_cast<volatile int*>(p.b.status) = 0x200;   // kDevErrBadIndex
             }
         }
     };
-    uint4 kreg[2][kKeyVecs], vreg[4][kValVecs];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    auto load_keys = [&]() {   // of the group whose rows `row` holds
+    uint8_t* ring = smem + warp * F::kWarpRing + lane * 16;   // this lane's 16 bytes of each 512
+    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    auto load_keys = [&](int at) {     // of the group whose rows `row` holds
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = __shfl_sync(0xffffffffu, row, g + 8 * i);
-            const uint8_t* src = kc + r * pitch + c * 16;
+            const uint8_t* src = kc + (r < 0 ? 0 : r) * pitch + c * 16;
 #pragma unroll
-            for (int v = 0; v < kKeyVecs; ++v) kreg[i][v] = r >= 0 ? load_once(src + v * 64) : zero;
+            for (int v = 0; v < kKeyVecs; ++v)
+                cp_async_16(ring32 + at * F::kKeyBytes + (i * kKeyVecs + v) * 512, src + v * 64, r >= 0);
         }
+        cp_async_commit();
     };
-    auto load_values = [&]() {
+    auto load_values = [&](int at) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = __shfl_sync(0xffffffffu, row, 2 * c + (i & 1) + 8 * (i >> 1));
-            const uint8_t* src = vc + r * pitch + (kHalf ? (g >> 1) : g) * 16;
+            const uint8_t* src = vc + (r < 0 ? 0 : r) * pitch + (kHalf ? (g >> 1) : g) * 16;
 #pragma unroll
-            for (int v = 0; v < kValVecs; ++v) vreg[i][v] = r >= 0 ? load_once(src + v * 128) : zero;
+            for (int v = 0; v < kValVecs; ++v)
+                cp_async_16(ring32 + A * F::kKeyBytes + at * F::kValBytes + (i * kValVecs + v) * 512, src + v * 128, r >= 0);
         }
+        cp_async_commit();
+    };
+    auto note = [&](int slot) {        // what find() found, for the group's turn
+        if (lane < kGroup) s_meta[warp][slot][lane] = kb | (vb << 8) | (row >= 0 ? 0x10000u : 0u);
     };
 
-    int i0 = keys.begin + warp;
+    const int i0 = keys.begin + warp;
     look_up(i0);
-    find(i0);
-    look_up(i0 + kWarps);
-    load_keys();
-    load_values();
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+        find(i0 + a * kWarps);
+        look_up(i0 + (a + 1) * kWarps);
+        load_keys(a);
+        load_values(a);
+        if (a + 1 < A) note(a);
+    }
+    int at = 0, slot = 0, slot_in = A - 1;   // ring place; places of this group's note and of the last one found
     for (int i = i0; i < keys.end; i += kWarps) {
         const int base = keys.base(i);
-        const uint32_t have = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;   // positions that hold a key
-        const uint32_t kb_now = kb, vb_now = vb;
+        note(slot_in);
+        if (++slot_in > A) slot_in = 0;
+        __syncwarp();
+        const uint32_t meta = s_meta[warp][slot][mine];
+        if (++slot > A) slot = 0;
+        const uint32_t have = __ballot_sync(0xffffffffu, (meta >> 16) != 0) & 0xffffu;   // positions that hold a key
+        const uint32_t kb_now = meta & 255u, vb_now = (meta >> 8) & 255u;
+        cp_async_wait<2 * A - 1>();      // this group's keys
+        const uint8_t* ks = ring + at * F::kKeyBytes;
         // S^T
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float s[R][2][4];
+#pragma unroll
+        for (int n8 = 0; n8 < R; ++n8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[n8][0][k] = s[n8][1][k] = 0.f;
 #pragma unroll
         for (int v = 0; v < kKeyVecs; ++v) {
-            const uint32_t x[2][4] = {{kreg[0][v].x, kreg[0][v].y, kreg[0][v].z, kreg[0][v].w},
-                                      {kreg[1][v].x, kreg[1][v].y, kreg[1][v].z, kreg[1][v].w}};
-            const uint4* qs = reinterpret_cast<const uint4*>(s_q + g * kPitch + v * 4 * kVec + c * kVec);
-            if constexpr (E4M3) {
+            const uint4 k0 = *reinterpret_cast<const uint4*>(ks + v * 512);
+            const uint4 k1 = *reinterpret_cast<const uint4*>(ks + (kKeyVecs + v) * 512);
+            const uint32_t x[2][4] = {{k0.x, k0.y, k0.z, k0.w}, {k1.x, k1.y, k1.z, k1.w}};
+            const uint16_t* qs = s_q + g * kPitch + v * 4 * kVec + c * kVec;
+            constexpr int kHalves = E4M3 ? 2 : 1;   // 8 values of each row: two MMAs
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 q = qs[h];   // 8 values: two MMAs
-                    mma16816<true>(s[0], e4m3x2_f16x2(x[0][2 * h]), e4m3x2_f16x2(x[1][2 * h]),
-                                   e4m3x2_f16x2(x[0][2 * h] >> 16), e4m3x2_f16x2(x[1][2 * h] >> 16), q.x, q.y);
-                    mma16816<true>(s[1], e4m3x2_f16x2(x[0][2 * h + 1]), e4m3x2_f16x2(x[1][2 * h + 1]),
-                                   e4m3x2_f16x2(x[0][2 * h + 1] >> 16), e4m3x2_f16x2(x[1][2 * h + 1] >> 16), q.z, q.w);
+            for (int h = 0; h < kHalves; ++h) {
+                uint32_t a[2][4];
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        a[u][0] = e4m3x2_f16x2(x[0][2 * h + u]);
+                        a[u][1] = e4m3x2_f16x2(x[1][2 * h + u]);
+                        a[u][2] = e4m3x2_f16x2(x[0][2 * h + u] >> 16);
+                        a[u][3] = e4m3x2_f16x2(x[1][2 * h + u] >> 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        a[u][0] = x[0][2 * u];
+                        a[u][1] = x[1][2 * u];
+                        a[u][2] = x[0][2 * u + 1];
+                        a[u][3] = x[1][2 * u + 1];
+                    }
                 }
-            } else {
-                const uint4 q = qs[0];
-                mma16816<false>(s[0], x[0][0], x[1][0], x[0][1], x[1][1], q.x, q.y);
-                mma16816<false>(s[1], x[0][2], x[1][2], x[0][3], x[1][3], q.z, q.w);
+#pragma unroll
+                for (int n8 = 0; n8 < R; ++n8) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(qs + n8 * 8 * kPitch + h * 8);
+                    mma16816<E4M3>(s[n8][0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+                    mma16816<E4M3>(s[n8][1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                }
             }
         }
-        // the next group's rows, and its keys on their way
-        find(i + kWarps);
-        look_up(i + 2 * kWarps);
-        load_keys();
-        // weights: lane (g, c) has positions g, g + 8 and rows 2c, 2c + 1
-        float x[4] = {s[0][0] + s[1][0], s[0][1] + s[1][1], s[0][2] + s[1][2], s[0][3] + s[1][3]};
-        float grow_e = 1.f, vf[2] = {1.f, 1.f};
+        // a later group's rows, and its keys on their way to this one's place
+        find(i + A * kWarps);
+        look_up(i + (A + 1) * kWarps);
+        load_keys(at);
+        // weights: lane (g, c) has positions g, g + 8 and rows 8 n + 2c, 8 n + 2c + 1
+        float grow_e = 1.f, kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f};
         if constexpr (E4M3) {
-            const uint32_t k0 = __shfl_sync(0xffffffffu, kb_now, g), k1 = __shfl_sync(0xffffffffu, kb_now, g + 8);
-            const float f0 = e8m0_value(k0), f1 = e8m0_value(k1);
-            x[0] *= f0;
-            x[1] *= f0;
-            x[2] *= f1;
-            x[3] *= f1;
-            vf[0] = e8m0_value(__shfl_sync(0xffffffffu, vb_now, g));
-            vf[1] = e8m0_value(__shfl_sync(0xffffffffu, vb_now, g + 8));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                kf[k] = e8m0_value(__shfl_sync(0xffffffffu, kb_now, g + 8 * k));
+                vf[k] = e8m0_value(__shfl_sync(0xffffffffu, vb_now, g + 8 * k));
+            }
             // the range of V's exponents, all-zero rows (the least scale) left out
             const bool h = ((have >> mine) & 1u) != 0 && vb_now > 10u && vb_now != 255u;
             const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
@@ -289,66 +364,82 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
                 wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
             }
         }
-        if (have != 0xffffu || base + kGroup - 1 > pmin || (base < lo_max && base + kGroup > p.sinks) || rows < kRows8) {
+        const bool masked = have != 0xffffu || base + kGroup - 1 > pmin || (base < lo_max && base + kGroup > p.sinks) ||
+                            rows < F::kRows;
+        uint32_t pt[R][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int at = g + 8 * (k >> 1), t = base + at;
-                const bool seen = ((have >> at) & 1u) != 0 && t <= row_pos[k & 1] && (t >= row_lo[k & 1] || t < p.sinks);
-                if (!seen) x[k] = -INFINITY;
+        for (int n8 = 0; n8 < R; ++n8) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = (s[n8][0][k] + s[n8][1][k]) * kf[k >> 1];
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int pl = g + 8 * (k >> 1), t = base + pl;
+                    const bool seen = ((have >> pl) & 1u) != 0 && t <= row_pos[n8][k & 1] &&
+                                      (t >= row_lo[n8][k & 1] || t < p.sinks);
+                    if (!seen) x[k] = -INFINITY;
+                }
             }
-        }
-        float mn[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float t = fmaxf(x[k], x[k + 2]);
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            mn[k] = fmaxf(m[k], t * row_scale[k]);
-        }
-        // O and l move to a new maximum only once it is 2^8 larger (or E changes)
-        if (__any_sync(0xffffffffu, mn[0] > m[0] + 8.f || mn[1] > m[1] + 8.f) || grow_e != 1.f) {
-            float f[2];
+            float mn[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                f[k] = grow_e;
-                if (mn[k] > m[k] + 8.f) {
-                    f[k] *= exp2_fast(m[k] - mn[k]);
-                    m[k] = mn[k];
+                float t = fmaxf(x[k], x[k + 2]);
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                mn[k] = fmaxf(m[n8][k], t * row_scale[n8][k]);
+            }
+            // O and l move to a new maximum only once it is 2^8 larger (or E changes)
+            if (__any_sync(0xffffffffu, mn[0] > m[n8][0] + 8.f || mn[1] > m[n8][1] + 8.f) || grow_e != 1.f) {
+                float f[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    f[k] = grow_e;
+                    if (mn[k] > m[n8][k] + 8.f) {
+                        f[k] *= exp2_fast(m[n8][k] - mn[k]);
+                        m[n8][k] = mn[k];
+                    }
+                    l[n8][k] *= f[k];
                 }
-                l[k] *= f[k];
-            }
 #pragma unroll
-            for (int d = 0; d < kDim; ++d) {
-                o[d][0] *= f[0];
-                o[d][1] *= f[1];
-                o[d][2] *= f[0];
-                o[d][3] *= f[1];
+                for (int d = 0; d < kDim; ++d) {
+                    o[n8][d][0] *= f[0];
+                    o[n8][d][1] *= f[1];
+                    o[n8][d][2] *= f[0];
+                    o[n8][d][3] *= f[1];
+                }
             }
-        }
-        uint32_t pt[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {   // positions g + 8 k
-            float w[2];
+            float b[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float b = m[q] == -INFINITY ? 0.f : m[q];
-                if constexpr (E4M3) b -= static_cast<float>(3 - E);
-                w[q] = exp2_fast(fmaf(x[2 * k + q], row_scale[q], -b));
-                l[q] += w[q];
+                b[q] = m[n8][q] == -INFINITY ? 0.f : m[n8][q];
+                if constexpr (E4M3) b[q] -= static_cast<float>(3 - E);
             }
-            pt[k] = transpose8x8(E4M3 ? f16x2(w[0] * vf[k], w[1] * vf[k]) : bf16x2(w[0], w[1]));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {   // positions g + 8 k
+                float w[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    w[q] = exp2_fast(fmaf(x[2 * k + q], row_scale[n8][q], -b[q]));
+                    l[n8][q] += w[q];
+                }
+                pt[n8][k] = transpose8x8(E4M3 ? f16x2(w[0] * vf[k], w[1] * vf[k]) : bf16x2(w[0], w[1]));
+            }
         }
         // O^T
+        cp_async_wait<2 * A - 1>();      // this group's values
+        const uint8_t* vs = ring + A * F::kKeyBytes + at * F::kValBytes;
 #pragma unroll
         for (int v = 0; v < kValVecs; ++v) {
             uint32_t y[4][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                y[k][0] = vreg[k][v].x;
-                y[k][1] = vreg[k][v].y;
-                y[k][2] = vreg[k][v].z;
-                y[k][3] = vreg[k][v].w;
+                const uint4 x = *reinterpret_cast<const uint4*>(vs + (k * kValVecs + v) * 512);
+                y[k][0] = x.x;
+                y[k][1] = x.y;
+                y[k][2] = x.z;
+                y[k][3] = x.w;
                 if constexpr (kHalf) {
                     if (g & 1) {
                         y[k][0] = y[k][2];
@@ -363,34 +454,45 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     u[k] = E4M3 ? e4m3x2_f16x2(y[k][(d >> 1) & 3] >> (16 * (d & 1))) : y[k][d & 3];
-                mma16816<E4M3>(o[v * kPairs + d], __byte_perm(u[0], u[1], 0x5410), __byte_perm(u[0], u[1], 0x7632),
-                               __byte_perm(u[2], u[3], 0x5410), __byte_perm(u[2], u[3], 0x7632), pt[0], pt[1]);
+                const uint32_t a0 = __byte_perm(u[0], u[1], 0x5410), a1 = __byte_perm(u[0], u[1], 0x7632);
+                const uint32_t a2 = __byte_perm(u[2], u[3], 0x5410), a3 = __byte_perm(u[2], u[3], 0x7632);
+#pragma unroll
+                for (int n8 = 0; n8 < R; ++n8)
+                    mma16816<E4M3>(o[n8][v * kPairs + d], a0, a1, a2, a3, pt[n8][0], pt[n8][1]);
             }
         }
-        load_values();
+        load_values(at);
+        if (++at == A) at = 0;
     }
+    cp_async_wait<0>();
+    __syncthreads();   // the ring becomes s_o
 
     // ---- the warps' results ---------------------------------------------------
     const float plain = E4M3 ? exp2f(static_cast<float>(E - 3)) : 1.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 4);
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 8);
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 16);
-        if (g == 0) {
-            s_m[warp][2 * c + k] = m[k];
-            s_l[warp][2 * c + k] = l[k] * plain;
-        }
-    }
     constexpr int kPairs = kHalf ? 4 : kVec / 2;
 #pragma unroll
-    for (int d = 0; d < kDim; ++d) {
-        const int dim = kHalf ? g * 8 + d * 2 : (d / kPairs) * (8 * kVec) + g * kVec + (d % kPairs) * 2;
+    for (int n8 = 0; n8 < R; ++n8) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float2*>(&s_o[warp][2 * c + k][dim]) = make_float2(o[d][k] * plain, o[d][2 + k] * plain);
+        for (int k = 0; k < 2; ++k) {
+            float t = l[n8][k];
+            t += __shfl_xor_sync(0xffffffffu, t, 4);
+            t += __shfl_xor_sync(0xffffffffu, t, 8);
+            t += __shfl_xor_sync(0xffffffffu, t, 16);
+            if (g == 0) {
+                s_m[warp][8 * n8 + 2 * c + k] = m[n8][k];
+                s_l[warp][8 * n8 + 2 * c + k] = t * plain;
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kDim; ++d) {
+            const int dim = kHalf ? g * 8 + d * 2 : (d / kPairs) * (8 * kVec) + g * kVec + (d % kPairs) * 2;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float2*>(s_o + (warp * F::kRows + 8 * n8 + 2 * c + k) * HD + dim) =
+                    make_float2(o[n8][d][k] * plain, o[n8][d][2 + k] * plain);
+        }
     }
-    if (wide && lane == 0) atomicOr(&s_flag, 0xff);
+    if (wide && lane == 0) atomicOr(&s_flag, 0xffff);
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (HD / 4); i += kWarps * 32) {
         const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
@@ -403,7 +505,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = exp2f(s_m[w][r] - b);
-            const float4 v = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
+            const float4 v = *reinterpret_cast<const float4*>(s_o + (w * F::kRows + r) * HD + d);
             L = fmaf(f, s_l[w][r], L);
             O.x = fmaf(f, v.x, O.x);
             O.y = fmaf(f, v.y, O.y);
@@ -438,20 +540,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_few_rows_kernel(const __gri
 }  // namespace
 
 template <bool E4M3, int HD>
-cudaError_t launch_few_rows(const AttnParams& p, bool pdl, cudaStream_t stream)
+cudaError_t launch_few_rows(const AttnParams& p, int rows, bool pdl, cudaStream_t stream)
 {
     const long long ctas = static_cast<long long>(p.tiles) * p.b.num_kv_heads * p.b.num_seqs * p.segments;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_kernel(kv_few_rows_kernel<E4M3, HD>, dim3(static_cast<unsigned>(ctas)), dim3(kWarps * 32), 0, stream,
-                         pdl, p);
+    auto launch = [&](auto kern, int threads, int bytes, SmemOptIn& smem_opt) {
+        const cudaError_t e = smem_opt.ensure(reinterpret_cast<const void*>(kern), bytes);
+        if (e != cudaSuccess) return e;
+        return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), bytes, stream, pdl, p);
+    };
+    static SmemOptIn one, two;
+    if (rows <= 8)
+        return launch(kv_few_rows_kernel<E4M3, HD, 1>, Few<E4M3, HD, 1>::kWarps * 32, Few<E4M3, HD, 1>::kBytes, one);
+    return launch(kv_few_rows_kernel<E4M3, HD, 2>, Few<E4M3, HD, 2>::kWarps * 32, Few<E4M3, HD, 2>::kBytes, two);
 }
 
-template cudaError_t launch_few_rows<false, 64>(const AttnParams&, bool, cudaStream_t);
-template cudaError_t launch_few_rows<false, 128>(const AttnParams&, bool, cudaStream_t);
-template cudaError_t launch_few_rows<false, 256>(const AttnParams&, bool, cudaStream_t);
-template cudaError_t launch_few_rows<true, 64>(const AttnParams&, bool, cudaStream_t);
-template cudaError_t launch_few_rows<true, 128>(const AttnParams&, bool, cudaStream_t);
-template cudaError_t launch_few_rows<true, 256>(const AttnParams&, bool, cudaStream_t);
+template cudaError_t launch_few_rows<false, 64>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<false, 128>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<false, 256>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<true, 64>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<true, 128>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<true, 256>(const AttnParams&, int, bool, cudaStream_t);
 
 }  // namespace kv
 }  // namespace bsk
