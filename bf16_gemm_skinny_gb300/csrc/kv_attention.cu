@@ -287,8 +287,9 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
     keys.sink_tiles = min((keys.sink_end + kTile - 1) / kTile, keys.lo_tile);
     {
         const int total = keys.kv_end > 0 ? keys.sink_tiles + (keys.kv_end + kTile - 1) / kTile - keys.lo_tile : 0;
-        keys.begin = static_cast<int>(static_cast<long long>(total) * seg / p.segments);
-        keys.end = static_cast<int>(static_cast<long long>(total) * (seg + 1) / p.segments);
+        const int each = p.segment_keys / kTile;
+        keys.begin = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(each) * seg));
+        keys.end = seg + 1 == p.segments ? total : min(total, keys.begin + each);
     }
     const int32_t* table = p.b.block_tables + static_cast<long long>(seq) * p.b.max_blocks;
     const int nt = keys.end - keys.begin;
@@ -1023,6 +1024,13 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ At
     }
 }
 
+// The most positions that the rows of a CTA may see.
+long long most_keys(const KvAttnLaunch& a)
+{
+    const long long seen = static_cast<long long>(a.window) + a.max_chunk + a.sinks;
+    return a.window > 0 && seen < a.max_seq_len ? seen : a.max_seq_len;
+}
+
 // Rows per CTA of the kernel for few query rows per KV head, or 0: the call takes
 // the other kernel.
 int few_rows(const KvAttnLaunch& a)
@@ -1049,6 +1057,9 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     const int cta_rows = few > 0 ? few : kRows;
     p.tiles = static_cast<int>((max_rows + cta_rows - 1) / cta_rows);
     p.segments = a.segments;
+    // Segments are as many positions for short sequences as for long ones, so that
+    // CTAs have equal work in a batch of uneven lengths.
+    p.segment_keys = static_cast<int>((most_keys(a) + a.segments * 128LL - 1) / (a.segments * 128LL) * 128);
     // a zero scale still has to keep -inf (a position not seen) at -inf
     p.scale_log2 = a.scale == 0.f ? 1e-37f : std::fabs(a.scale) * 1.4426950408889634f;
     p.q_sign = a.scale < 0.f ? 0x80008000u : 0u;
@@ -1130,10 +1141,7 @@ int kv_attention_segments(const KvAttnLaunch& a)
     long long row_tiles = (static_cast<long long>(a.b.num_tokens) * group + cta_rows - 1) / cta_rows + a.b.num_seqs - 1;
     if (row_tiles > per_seq * a.b.num_seqs) row_tiles = per_seq * a.b.num_seqs;
     const long long ctas = row_tiles * a.b.num_kv_heads;
-    long long keys = a.max_seq_len;
-    if (a.window > 0 && static_cast<long long>(a.window) + a.max_chunk + a.sinks < keys)
-        keys = static_cast<long long>(a.window) + a.max_chunk + a.sinks;
-    const long long tiles = (keys + tile - 1) / tile;
+    const long long tiles = (most_keys(a) + tile - 1) / tile;
     const double rows = static_cast<double>(a.b.num_tokens) * a.num_q_heads;
     // Time in units of one tile's work on one CTA: a CTA starts and ends in about
     // `fixed`, a join costs about as much and the traffic of the partial rows.

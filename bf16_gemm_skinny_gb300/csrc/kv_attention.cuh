@@ -86,6 +86,7 @@ struct AttnParams {
     long long q_stride, out_stride;
     int num_q_heads, group, max_chunk, max_seq_len;
     int tiles, segments;          // row tiles (128 rows, or 8) per sequence and KV head, key segments per tile
+    int segment_keys;             // positions of a segment, a multiple of 128 (the last one takes the rest)
     int box;                      // rows per TMA box, or 4: pages of an odd size, gathers only
     int tile_rows;                // cache rows that boxes of a tile's rows may cover
     float scale_log2;             // |softmax scale| * log2(e), > 0

@@ -14,7 +14,7 @@
 // of P^T by movmatrix.  E4M3 codes become FP16 pairs by one instruction each
 // (exact), and Q, scaled by a power of two per row, FP16 too.
 //
-// The warps of a CTA take the groups of 16 positions of its segment in turn.  They
+// The warps of a CTA take the groups of 16 or 32 positions of its segment in turn.  They
 // are joined in shared memory, the segments by kv_join_kernel.
 #include <cstdio>
 
@@ -25,7 +25,6 @@ namespace bsk {
 namespace kv {
 namespace {
 
-constexpr int kGroup = 16;   // positions per step of a warp
 
 template <bool E4M3>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -61,7 +60,7 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Sizes.  `kAhead` groups per warp are on their way: two CTAs of an SM have 100 to
+// Sizes.  `kAhead` steps per warp are on their way: the CTAs of an SM have 100 to
 // 200 KB in flight, which the latency times HBM's rate needs (about 45 KB) with
 // room for uneven progress.
 template <bool E4M3, int HD, int R>
@@ -75,10 +74,14 @@ struct Few {
     static constexpr bool kHalf = E4M3 && HD == 64;
     static constexpr int kValVecs = kHalf ? 1 : HD / (8 * kVec);
     static constexpr int kRowBytes = HD * kElem;
-    static constexpr int kWarps = kRowBytes == 512 ? 3 : 4;
-    static constexpr int kAhead = kRowBytes == 512 ? 2 : (kRowBytes == 256 ? 3 : 4);
-    static constexpr int kCtas = HD == 256 || R > 1 || kRowBytes == 256 ? 2 : 3;   // of an SM
-    static constexpr int kKeyBytes = 2 * kKeyVecs * 512, kValBytes = 4 * kValVecs * 512;   // of a group
+    // A warp's step: 16 positions, or 32 where two steps' copies fit beside each other
+    // (the work per step that does not depend on its size is over half of it).
+    static constexpr int kSub = kRowBytes == 512 ? 1 : 2;
+    static constexpr int kGroup = 16 * kSub;
+    static constexpr int kWarps = kRowBytes >= 256 ? 3 : 4;
+    static constexpr int kAhead = kRowBytes == 64 ? 3 : 2;
+    static constexpr int kCtas = R > 1 || kRowBytes >= 256 ? 2 : 3;   // of an SM
+    static constexpr int kKeyBytes = kSub * 2 * kKeyVecs * 512, kValBytes = kSub * 4 * kValVecs * 512;   // of a step
     static constexpr int kWarpRing = kAhead * (kKeyBytes + kValBytes);
     static constexpr int kRing = kWarps * kWarpRing;
     static constexpr int kOut = kWarps * kRows * HD * 4;   // the warps' O, over the ring
@@ -92,13 +95,13 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     using F = Few<E4M3, HD, R>;
     constexpr int kWarps = F::kWarps, kElem = F::kElem, kVec = F::kVec, kKeyVecs = F::kKeyVecs, kValVecs = F::kValVecs;
     constexpr bool kHalf = F::kHalf;
-    constexpr int A = F::kAhead;
+    constexpr int A = F::kAhead, SUB = F::kSub;
     constexpr int kDim = HD / 16;                // O^T tiles
     constexpr int kPitch = F::kPitch;
     extern __shared__ __align__(16) uint8_t smem[];
     uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + F::kBytes - F::kRows * kPitch * 2);
     float* s_o = reinterpret_cast<float*>(smem);          // [kWarps][F::kRows][HD], once the ring is done with
-    __shared__ uint32_t s_meta[kWarps][A + 1][kGroup];   // scale bytes, and bit 16: holds a key
+    __shared__ uint32_t s_meta[kWarps][A + 1][32];   // scale bytes, and bit 16: holds a key
     __shared__ float s_m[kWarps][F::kRows], s_l[kWarps][F::kRows], s_scale[F::kRows];
     __shared__ int s_flag;
 
@@ -133,19 +136,118 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     if (rows <= 0) return;
     const int pos0 = len - n;
     const int pmin = pos0 + row0 / p.group, pmax = pos0 + (row0 + rows - 1) / p.group;
-    Keys<kGroup> keys;
+    Keys<F::kGroup> keys;
     keys.kv_end = max(pmax + 1, 0);
     keys.lo = p.window > 0 && pmin - p.window + 1 > 0 ? pmin - p.window + 1 : 0;
     keys.sink_end = min(p.sinks, keys.lo);
-    keys.lo_tile = keys.lo / kGroup;
-    keys.sink_tiles = min((keys.sink_end + kGroup - 1) / kGroup, keys.lo_tile);
+    keys.lo_tile = keys.lo / F::kGroup;
+    keys.sink_tiles = min((keys.sink_end + F::kGroup - 1) / F::kGroup, keys.lo_tile);
     {
-        const int total = keys.kv_end > 0 ? keys.sink_tiles + (keys.kv_end + kGroup - 1) / kGroup - keys.lo_tile : 0;
-        keys.begin = static_cast<int>(static_cast<long long>(total) * seg / p.segments);
-        keys.end = static_cast<int>(static_cast<long long>(total) * (seg + 1) / p.segments);
+        const int total = keys.kv_end > 0 ? keys.sink_tiles + (keys.kv_end + F::kGroup - 1) / F::kGroup - keys.lo_tile : 0;
+        const int each = p.segment_keys / F::kGroup;
+        keys.begin = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(each) * seg));
+        keys.end = seg + 1 == p.segments ? total : min(total, keys.begin + each);
     }
     const int32_t* table = p.b.block_tables + static_cast<long long>(seq) * p.b.max_blocks;
 
+    const uint8_t* kc = static_cast<const uint8_t*>(p.b.k) + static_cast<long long>(kvh) * HD * kElem;
+    const uint8_t* vc = static_cast<const uint8_t*>(p.b.v) + static_cast<long long>(kvh) * HD * kElem;
+    const long long pitch = static_cast<long long>(p.b.num_kv_heads) * HD * kElem;
+    const int mine = lane & (F::kGroup - 1);   // the position of a step whose page this lane looks up
+    int entry = -1, row = -1;     // block-table entry of the group looked up last, cache row of the one found last
+    uint32_t kb = 127u, vb = 127u;
+    // page and place in it of the group to look up next, stepped from group to group
+    const int bs = p.b.block_size;
+    const int step_pages = kWarps * F::kGroup / bs, step_slots = kWarps * F::kGroup - step_pages * bs;
+    int page = 0, off = 0, entry_off = 0;
+    bool fresh = true, in_sinks = false;
+    auto look_up = [&](int i) {
+        entry = -1;
+        if (i < keys.end) {
+            if (fresh || (in_sinks && i >= keys.sink_tiles)) {
+                const int t = keys.base(i) + mine;
+                page = t / bs;
+                off = t - page * bs;
+                fresh = false;
+                in_sinks = i < keys.sink_tiles;
+            }
+            if (page < p.b.max_blocks) entry = table[page];
+            entry_off = off;
+            page += step_pages;
+            off += step_slots;
+            if (off >= bs) {
+                off -= bs;
+                ++page;
+            }
+        }
+    };
+    auto find = [&](int i) {   // the group looked up last
+        row = -1;
+        kb = vb = 127u;
+        if (i < keys.end && keys.holds(keys.base(i) + mine)) {
+            if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks)) {
+                row = entry * bs + entry_off;
+                if constexpr (E4M3) {
+                    kb = p.b.k_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
+                    vb = p.b.v_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
+                }
+            } else {
+                *reinterpret_cast<volatile int*>(p.b.status) = 0x200;   // kDevErrBadIndex
+            }
+        }
+    };
+    uint8_t* ring = smem + warp * F::kWarpRing + lane * 16;   // this lane's 16 bytes of each 512
+    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    auto load_keys = [&](int at) {     // of the step whose rows `row` holds
+#pragma unroll
+        for (int i = 0; i < 2 * SUB; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, g + 8 * i);
+            const uint8_t* src = kc + (r < 0 ? 0 : r) * pitch + c * 16;
+#pragma unroll
+            for (int v = 0; v < kKeyVecs; ++v)
+                cp_async_16(ring32 + at * F::kKeyBytes + (i * kKeyVecs + v) * 512, src + v * 64, r >= 0);
+        }
+        cp_async_commit();
+    };
+    auto load_values = [&](int at) {
+#pragma unroll
+        for (int i = 0; i < 4 * SUB; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, 2 * c + (i & 1) + 8 * (i >> 1));
+            const uint8_t* src = vc + (r < 0 ? 0 : r) * pitch + (kHalf ? (g >> 1) : g) * 16;
+#pragma unroll
+            for (int v = 0; v < kValVecs; ++v)
+                cp_async_16(ring32 + A * F::kKeyBytes + at * F::kValBytes + (i * kValVecs + v) * 512, src + v * 128, r >= 0);
+        }
+        cp_async_commit();
+    };
+    // What find() found, for the step's turn: noted two steps later, so that the scale
+    // bytes' loads have that long.
+    uint32_t found_k[2] = {127u, 127u}, found_v[2] = {127u, 127u}, found[2] = {0u, 0u};   // the last, the one before
+    auto keep = [&]() {
+        found_k[1] = found_k[0];
+        found_v[1] = found_v[0];
+        found[1] = found[0];
+        found_k[0] = kb;
+        found_v[0] = vb;
+        found[0] = row >= 0 ? 0x10000u : 0u;
+    };
+    auto note = [&](int slot, int which) { s_meta[warp][slot][lane] = found_k[which] | (found_v[which] << 8) | found[which]; };
+
+    // Steps in turn: copies are issued A steps ahead of their use, rows (and scale
+    // bytes) found one step before that, block-table entries loaded one before that.
+    const int i0 = keys.begin + warp;
+    look_up(i0);
+    find(i0);
+    look_up(i0 + kWarps);
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+        load_keys(a);
+        load_values(a);
+        keep();
+        if (a > 0) note(a - 1, 1);
+        find(i0 + (a + 1) * kWarps);
+        look_up(i0 + (a + 2) * kWarps);
+    }
     // ---- Q: 16-bit rows in shared memory; rows that do not exist are zero ----
     if (threadIdx.x == 0) s_flag = 0;
     for (int r = warp; r < F::kRows; r += kWarps) {
@@ -202,157 +304,78 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     int E = 0, low_e = 1000;
     bool wide = false;
 
-    const uint8_t* kc = static_cast<const uint8_t*>(p.b.k) + static_cast<long long>(kvh) * HD * kElem;
-    const uint8_t* vc = static_cast<const uint8_t*>(p.b.v) + static_cast<long long>(kvh) * HD * kElem;
-    const long long pitch = static_cast<long long>(p.b.num_kv_heads) * HD * kElem;
-    const int mine = lane & 15;   // the position of a group whose page this lane looks up
-    int entry = -1, row = -1;     // block-table entry of the group looked up last, cache row of the one found last
-    uint32_t kb = 127u, vb = 127u;
-    // page and place in it of the group to look up next, stepped from group to group
-    const int bs = p.b.block_size;
-    const int step_pages = kWarps * kGroup / bs, step_slots = kWarps * kGroup - step_pages * bs;
-    int page = 0, off = 0, entry_off = 0;
-    bool fresh = true, in_sinks = false;
-    auto look_up = [&](int i) {
-        entry = -1;
-        if (i < keys.end) {
-            if (fresh || (in_sinks && i >= keys.sink_tiles)) {
-                const int t = keys.base(i) + mine;
-                page = t / bs;
-                off = t - page * bs;
-                fresh = false;
-                in_sinks = i < keys.sink_tiles;
-            }
-            if (page < p.b.max_blocks) entry = table[page];
-            entry_off = off;
-            page += step_pages;
-            off += step_slots;
-            if (off >= bs) {
-                off -= bs;
-                ++page;
-            }
-        }
-    };
-    auto find = [&](int i) {   // the group looked up last
-        row = -1;
-        kb = vb = 127u;
-        if (i < keys.end && keys.holds(keys.base(i) + mine)) {
-            if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks)) {
-                row = entry * bs + entry_off;
-                if constexpr (E4M3) {
-                    kb = p.b.k_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
-                    vb = p.b.v_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
-                }
-            } else {
-                *reinterpret_cast<volatile int*>(p.b.status) = 0x200;   // kDevErrBadIndex
-            }
-        }
-    };
-    uint8_t* ring = smem + warp * F::kWarpRing + lane * 16;   // this lane's 16 bytes of each 512
-    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    auto load_keys = [&](int at) {     // of the group whose rows `row` holds
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = __shfl_sync(0xffffffffu, row, g + 8 * i);
-            const uint8_t* src = kc + (r < 0 ? 0 : r) * pitch + c * 16;
-#pragma unroll
-            for (int v = 0; v < kKeyVecs; ++v)
-                cp_async_16(ring32 + at * F::kKeyBytes + (i * kKeyVecs + v) * 512, src + v * 64, r >= 0);
-        }
-        cp_async_commit();
-    };
-    auto load_values = [&](int at) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = __shfl_sync(0xffffffffu, row, 2 * c + (i & 1) + 8 * (i >> 1));
-            const uint8_t* src = vc + (r < 0 ? 0 : r) * pitch + (kHalf ? (g >> 1) : g) * 16;
-#pragma unroll
-            for (int v = 0; v < kValVecs; ++v)
-                cp_async_16(ring32 + A * F::kKeyBytes + at * F::kValBytes + (i * kValVecs + v) * 512, src + v * 128, r >= 0);
-        }
-        cp_async_commit();
-    };
-    auto note = [&](int slot) {        // what find() found, for the group's turn
-        if (lane < kGroup) s_meta[warp][slot][lane] = kb | (vb << 8) | (row >= 0 ? 0x10000u : 0u);
-    };
 
-    const int i0 = keys.begin + warp;
-    look_up(i0);
-#pragma unroll
-    for (int a = 0; a < A; ++a) {
-        find(i0 + a * kWarps);
-        look_up(i0 + (a + 1) * kWarps);
-        load_keys(a);
-        load_values(a);
-        if (a + 1 < A) note(a);
-    }
-    int at = 0, slot = 0, slot_in = A - 1;   // ring place; places of this group's note and of the last one found
+    int at = 0, slot = 0, slot_in = A - 1;   // ring place; places of this step's note and of the next one written
     for (int i = i0; i < keys.end; i += kWarps) {
         const int base = keys.base(i);
-        note(slot_in);
+        note(slot_in, 0);   // found two steps ago: `keep` of the step before the one about to be issued
         if (++slot_in > A) slot_in = 0;
         __syncwarp();
         const uint32_t meta = s_meta[warp][slot][mine];
         if (++slot > A) slot = 0;
-        const uint32_t have = __ballot_sync(0xffffffffu, (meta >> 16) != 0) & 0xffffu;   // positions that hold a key
+        const uint32_t have = __ballot_sync(0xffffffffu, (meta >> 16) != 0);   // positions that hold a key
         const uint32_t kb_now = meta & 255u, vb_now = (meta >> 8) & 255u;
         cp_async_wait<2 * A - 1>();      // this group's keys
         const uint8_t* ks = ring + at * F::kKeyBytes;
-        // S^T
-        float s[R][2][4];
+        // S^T, 16 positions at a time
+        float s[R][SUB][4];
 #pragma unroll
-        for (int n8 = 0; n8 < R; ++n8)
+        for (int b = 0; b < SUB; ++b) {
+            float t[R][2][4];   // two chains of MMAs
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[n8][0][k] = s[n8][1][k] = 0.f;
+            for (int n8 = 0; n8 < R; ++n8)
 #pragma unroll
-        for (int v = 0; v < kKeyVecs; ++v) {
-            const uint4 k0 = *reinterpret_cast<const uint4*>(ks + v * 512);
-            const uint4 k1 = *reinterpret_cast<const uint4*>(ks + (kKeyVecs + v) * 512);
-            const uint32_t x[2][4] = {{k0.x, k0.y, k0.z, k0.w}, {k1.x, k1.y, k1.z, k1.w}};
-            const uint16_t* qs = s_q + g * kPitch + v * 4 * kVec + c * kVec;
-            constexpr int kHalves = E4M3 ? 2 : 1;   // 8 values of each row: two MMAs
+                for (int k = 0; k < 4; ++k) t[n8][0][k] = t[n8][1][k] = 0.f;
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-                uint32_t a[2][4];
-                if constexpr (E4M3) {
+            for (int v = 0; v < kKeyVecs; ++v) {
+                const uint4 k0 = *reinterpret_cast<const uint4*>(ks + (2 * b * kKeyVecs + v) * 512);
+                const uint4 k1 = *reinterpret_cast<const uint4*>(ks + ((2 * b + 1) * kKeyVecs + v) * 512);
+                const uint32_t x[2][4] = {{k0.x, k0.y, k0.z, k0.w}, {k1.x, k1.y, k1.z, k1.w}};
+                const uint16_t* qs = s_q + g * kPitch + v * 4 * kVec + c * kVec;
+                constexpr int kHalves = E4M3 ? 2 : 1;   // 8 values of each row: two MMAs
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        a[u][0] = e4m3x2_f16x2(x[0][2 * h + u]);
-                        a[u][1] = e4m3x2_f16x2(x[1][2 * h + u]);
-                        a[u][2] = e4m3x2_f16x2(x[0][2 * h + u] >> 16);
-                        a[u][3] = e4m3x2_f16x2(x[1][2 * h + u] >> 16);
-                    }
-                } else {
+                for (int h = 0; h < kHalves; ++h) {
+                    uint32_t a[2][4];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        a[u][0] = x[0][2 * u];
-                        a[u][1] = x[1][2 * u];
-                        a[u][2] = x[0][2 * u + 1];
-                        a[u][3] = x[1][2 * u + 1];
+                        if constexpr (E4M3) {
+                            a[u][0] = e4m3x2_f16x2(x[0][2 * h + u]);
+                            a[u][1] = e4m3x2_f16x2(x[1][2 * h + u]);
+                            a[u][2] = e4m3x2_f16x2(x[0][2 * h + u] >> 16);
+                            a[u][3] = e4m3x2_f16x2(x[1][2 * h + u] >> 16);
+                        } else {
+                            a[u][0] = x[0][2 * u];
+                            a[u][1] = x[1][2 * u];
+                            a[u][2] = x[0][2 * u + 1];
+                            a[u][3] = x[1][2 * u + 1];
+                        }
                     }
-                }
 #pragma unroll
-                for (int n8 = 0; n8 < R; ++n8) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(qs + n8 * 8 * kPitch + h * 8);
-                    mma16816<E4M3>(s[n8][0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
-                    mma16816<E4M3>(s[n8][1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                    for (int n8 = 0; n8 < R; ++n8) {
+                        const uint4 q = *reinterpret_cast<const uint4*>(qs + n8 * 8 * kPitch + h * 8);
+                        mma16816<E4M3>(t[n8][0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+                        mma16816<E4M3>(t[n8][1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                    }
                 }
             }
-        }
-        // a later group's rows, and its keys on their way to this one's place
-        find(i + A * kWarps);
-        look_up(i + (A + 1) * kWarps);
-        load_keys(at);
-        // weights: lane (g, c) has positions g, g + 8 and rows 8 n + 2c, 8 n + 2c + 1
-        float grow_e = 1.f, kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f};
-        if constexpr (E4M3) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                kf[k] = e8m0_value(__shfl_sync(0xffffffffu, kb_now, g + 8 * k));
-                vf[k] = e8m0_value(__shfl_sync(0xffffffffu, vb_now, g + 8 * k));
+            for (int n8 = 0; n8 < R; ++n8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[n8][b][k] = t[n8][0][k] + t[n8][1][k];
+        }
+        // a later step's keys on their way to this one's place
+        load_keys(at);
+        // weights: lane (g, c) has positions g + 8 k and rows 8 n + 2c, 8 n + 2c + 1
+        float grow_e = 1.f, kf[2 * SUB], vf[2 * SUB];
+        if constexpr (E4M3) {
+            const float own_k = e8m0_value(kb_now), own_v = e8m0_value(vb_now);
+#pragma unroll
+            for (int k = 0; k < 2 * SUB; ++k) {
+                kf[k] = __shfl_sync(0xffffffffu, own_k, g + 8 * k);
+                vf[k] = __shfl_sync(0xffffffffu, own_v, g + 8 * k);
             }
             // the range of V's exponents, all-zero rows (the least scale) left out
-            const bool h = ((have >> mine) & 1u) != 0 && vb_now > 10u && vb_now != 255u;
+            const bool h = (meta >> 16) != 0 && vb_now > 10u && vb_now != 255u;
             const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
             const int low = __reduce_min_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : 1000);
             if (top > -1000) {
@@ -364,31 +387,39 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                 wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
             }
         }
-        const bool masked = have != 0xffffu || base + kGroup - 1 > pmin || (base < lo_max && base + kGroup > p.sinks) ||
-                            rows < F::kRows;
-        uint32_t pt[R][2];
+        const bool masked = have != 0xffffffffu || base + F::kGroup - 1 > pmin ||
+                            (base < lo_max && base + F::kGroup > p.sinks);
+        uint32_t pt[R][2 * SUB];
 #pragma unroll
         for (int n8 = 0; n8 < R; ++n8) {
-            float x[4];
+            float x[2 * SUB][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = (s[n8][0][k] + s[n8][1][k]) * kf[k >> 1];
+            for (int k = 0; k < 2 * SUB; ++k)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    x[k][q] = s[n8][k >> 1][2 * (k & 1) + q];
+                    if constexpr (E4M3) x[k][q] *= kf[k];
+                }
             if (masked) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int pl = g + 8 * (k >> 1), t = base + pl;
-                    const bool seen = ((have >> pl) & 1u) != 0 && t <= row_pos[n8][k & 1] &&
-                                      (t >= row_lo[n8][k & 1] || t < p.sinks);
-                    if (!seen) x[k] = -INFINITY;
-                }
+                for (int k = 0; k < 2 * SUB; ++k)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int pl = g + 8 * k, t = base + pl;
+                        const bool seen = ((have >> pl) & 1u) != 0 && t <= row_pos[n8][q] &&
+                                          (t >= row_lo[n8][q] || t < p.sinks);
+                        if (!seen) x[k][q] = -INFINITY;
+                    }
             }
             float mn[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float t = fmaxf(x[k], x[k + 2]);
+            for (int q = 0; q < 2; ++q) {
+                float t = fmaxf(x[0][q], x[1][q]);
+                if constexpr (SUB == 2) t = max3(t, x[2][q], x[3][q]);
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                mn[k] = fmaxf(m[n8][k], t * row_scale[n8][k]);
+                mn[q] = fmaxf(m[n8][q], t * row_scale[n8][q]);
             }
             // O and l move to a new maximum only once it is 2^8 larger (or E changes)
             if (__any_sync(0xffffffffu, mn[0] > m[n8][0] + 8.f || mn[1] > m[n8][1] + 8.f) || grow_e != 1.f) {
@@ -417,52 +448,78 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                 if constexpr (E4M3) b[q] -= static_cast<float>(3 - E);
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {   // positions g + 8 k
+            for (int k = 0; k < 2 * SUB; ++k) {   // positions g + 8 k
                 float w[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    w[q] = exp2_fast(fmaf(x[2 * k + q], row_scale[n8][q], -b[q]));
+                    w[q] = exp2_fast(fmaf(x[k][q], row_scale[n8][q], -b[q]));
                     l[n8][q] += w[q];
                 }
-                pt[n8][k] = transpose8x8(E4M3 ? f16x2(w[0] * vf[k], w[1] * vf[k]) : bf16x2(w[0], w[1]));
+                if constexpr (E4M3)
+                    pt[n8][k] = transpose8x8(f16x2(w[0] * vf[k], w[1] * vf[k]));
+                else
+                    pt[n8][k] = transpose8x8(bf16x2(w[0], w[1]));
             }
         }
         // O^T
         cp_async_wait<2 * A - 1>();      // this group's values
         const uint8_t* vs = ring + A * F::kKeyBytes + at * F::kValBytes;
 #pragma unroll
-        for (int v = 0; v < kValVecs; ++v) {
-            uint32_t y[4][4];
+        for (int b = 0; b < SUB; ++b) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint4 x = *reinterpret_cast<const uint4*>(vs + (k * kValVecs + v) * 512);
-                y[k][0] = x.x;
-                y[k][1] = x.y;
-                y[k][2] = x.z;
-                y[k][3] = x.w;
-                if constexpr (kHalf) {
-                    if (g & 1) {
-                        y[k][0] = y[k][2];
-                        y[k][1] = y[k][3];
+            for (int v = 0; v < kValVecs; ++v) {
+                uint32_t y[4][4];   // positions 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(vs + ((4 * b + k) * kValVecs + v) * 512);
+                    y[k][0] = x.x;
+                    y[k][1] = x.y;
+                    y[k][2] = x.z;
+                    y[k][3] = x.w;
+                    if constexpr (kHalf) {
+                        if (g & 1) {
+                            y[k][0] = y[k][2];
+                            y[k][1] = y[k][3];
+                        }
                     }
                 }
-            }
-            constexpr int kPairs = kHalf ? 4 : kVec / 2;   // pairs of dimensions a lane has per position
+                constexpr int kPairs = kHalf ? 4 : kVec / 2;   // pairs of dimensions a lane has per position
+                if constexpr (E4M3) {
+                    // two positions' codes byte by byte beside each other, four dimensions at a time
 #pragma unroll
-            for (int d = 0; d < kPairs; ++d) {
-                uint32_t u[4];
+                    for (int d = 0; d < kPairs; d += 2) {
+                        const uint32_t u0 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x5140);
+                        const uint32_t u1 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x7362);
+                        const uint32_t u2 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x5140);
+                        const uint32_t u3 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x7362);
+                        const uint32_t a[2][4] = {{e4m3x2_f16x2(u0), e4m3x2_f16x2(u0 >> 16), e4m3x2_f16x2(u2),
+                                                   e4m3x2_f16x2(u2 >> 16)},
+                                                  {e4m3x2_f16x2(u1), e4m3x2_f16x2(u1 >> 16), e4m3x2_f16x2(u3),
+                                                   e4m3x2_f16x2(u3 >> 16)}};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    u[k] = E4M3 ? e4m3x2_f16x2(y[k][(d >> 1) & 3] >> (16 * (d & 1))) : y[k][d & 3];
-                const uint32_t a0 = __byte_perm(u[0], u[1], 0x5410), a1 = __byte_perm(u[0], u[1], 0x7632);
-                const uint32_t a2 = __byte_perm(u[2], u[3], 0x5410), a3 = __byte_perm(u[2], u[3], 0x7632);
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int n8 = 0; n8 < R; ++n8)
-                    mma16816<E4M3>(o[n8][v * kPairs + d], a0, a1, a2, a3, pt[n8][0], pt[n8][1]);
+                            for (int n8 = 0; n8 < R; ++n8)
+                                mma16816<true>(o[n8][v * kPairs + d + u], a[u][0], a[u][1], a[u][2], a[u][3],
+                                               pt[n8][2 * b], pt[n8][2 * b + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int d = 0; d < kPairs; ++d) {
+                        const uint32_t a0 = __byte_perm(y[0][d], y[1][d], 0x5410), a1 = __byte_perm(y[0][d], y[1][d], 0x7632);
+                        const uint32_t a2 = __byte_perm(y[2][d], y[3][d], 0x5410), a3 = __byte_perm(y[2][d], y[3][d], 0x7632);
+#pragma unroll
+                        for (int n8 = 0; n8 < R; ++n8)
+                            mma16816<false>(o[n8][v * kPairs + d], a0, a1, a2, a3, pt[n8][2 * b], pt[n8][2 * b + 1]);
+                    }
+                }
             }
         }
         load_values(at);
         if (++at == A) at = 0;
+        keep();
+        find(i + (A + 1) * kWarps);
+        look_up(i + (A + 2) * kWarps);
     }
     cp_async_wait<0>();
     __syncthreads();   // the ring becomes s_o
@@ -531,7 +588,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         for (int r = warp; r < rows; r += kWarps) {
             if (!((s_flag >> r) & 1)) continue;
             const int my = row0 + r;
-            repair_row<E4M3, HD, kGroup>(p, table, keys, kvh, first + my / p.group, kvh * p.group + my % p.group,
+            repair_row<E4M3, HD, F::kGroup>(p, table, keys, kvh, first + my / p.group, kvh * p.group + my % p.group,
                                          pos0 + my / p.group, seg);
         }
     }
