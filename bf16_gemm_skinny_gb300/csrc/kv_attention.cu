@@ -962,64 +962,93 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Joins the segments of split rows: M = max m_s, out = sum_s O_s 2^(m_s - M) /
-// sum_s l_s 2^(m_s - M), in segment order.  LANES = HD / 4 threads have a row's
-// four values each; with WIDE the 256 threads share one row's segments, else
-// they take 256 / LANES rows.
+// sum_s l_s 2^(m_s - M), in a fixed order.  256 threads have 64 dimensions of one
+// row (WIDE: few rows, up to 256 segments; 16 groups of 16 threads share the
+// segments) or of 16 rows (a group each).  Latency is what counts: the loads of
+// (m, l) are one round, those of O as many as the registers allow.
 // ---------------------------------------------------------------------------
 template <int HD, bool WIDE>
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr int LANES = HD / 4;
-    constexpr int GROUPS = 256 / LANES;
-    __shared__ float4 s_o[GROUPS][LANES];
-    __shared__ float s_l[GROUPS];
-    const int g = threadIdx.x / LANES, e = threadIdx.x % LANES;
+    __shared__ float4 s_o[16][16];
+    __shared__ float s_w[256], s_red[8], s_l[8];
+    const int g = threadIdx.x >> 4, e = threadIdx.x & 15;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_wait();
     griddep_launch_dependents();
-    const long long row = WIDE ? blockIdx.x : static_cast<long long>(blockIdx.x) * GROUPS + g;
+    const long long row = WIDE ? blockIdx.x : static_cast<long long>(blockIdx.x) * 16 + g;
     const int token = static_cast<int>(row / p.num_q_heads);
     // a row of some sequence
     const bool in = token < p.b.num_tokens &&
                     (p.b.cu_tokens == nullptr || (token >= p.b.cu_tokens[0] && token < p.b.cu_tokens[p.b.num_seqs]));
+    if (WIDE ? !in : false) return;
     const float2* ml = p.part_ml + row * p.segments;
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.segments * HD) + e;
-    float M = -INFINITY, L = 0.f;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.segments * HD) + blockIdx.y * 16 + e;
+    constexpr int kStride = HD / 4;
+    float L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) {
-        for (int s = 0; s < p.segments; ++s) M = fmaxf(M, ml[s].x);
-        const float base = M == -INFINITY ? 0.f : M;
-        const int step = WIDE ? GROUPS : 1;
-#pragma unroll 4
-        for (int s = WIDE ? g : 0; s < p.segments; s += step) {
-            const float2 x = ml[s];
-            if (x.y == 0.f) continue;   // saw nothing: its O was not written
-            const float w = exp2f(x.x - base);
-            const float4 v = po[static_cast<long long>(s) * LANES];
-            L = fmaf(w, x.y, L);
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
-        }
-    }
+    auto add = [&](float w, const float4& v) {
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
+    };
     if constexpr (WIDE) {
+        const bool mine = threadIdx.x < p.segments;
+        const float2 x = mine ? ml[threadIdx.x] : make_float2(-INFINITY, 0.f);
+        float M = x.x;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+        if (lane == 0) s_red[warp] = M;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) M = fmaxf(M, s_red[i]);
+        const float w = x.y == 0.f ? 0.f : exp2f(x.x - (M == -INFINITY ? 0.f : M));   // l = 0: saw nothing, O not written
+        s_w[threadIdx.x] = w;
+        float t = w * x.y;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) t += __shfl_xor_sync(0xffffffffu, t, i);
+        if (lane == 0) s_l[warp] = t;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) L += s_l[i];
+        for (int s0 = g; s0 < p.segments; s0 += 16 * 8) {
+            float4 v[8];
+            float f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int s = s0 + 16 * u;
+                f[u] = s < p.segments ? s_w[s] : 0.f;
+                // (a weight of NaN has its O)
+                v[u] = s < p.segments && f[u] != 0.f ? po[static_cast<long long>(s) * kStride] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) add(f[u], v[u]);
+        }
         s_o[g][e] = o;
-        if (e == 0) s_l[g] = L;
         __syncthreads();
         if (g != 0) return;
 #pragma unroll
-        for (int i = 1; i < GROUPS; ++i) {
-            const float4 v = s_o[i][e];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
-            L += s_l[i];
+        for (int i = 1; i < 16; ++i) add(1.f, s_o[i][e]);
+    } else if (in) {
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int s = 0; s < p.segments; ++s) M = fmaxf(M, ml[s].x);
+        const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+        for (int s = 0; s < p.segments; ++s) {
+            const float2 x = ml[s];
+            const bool some = x.y != 0.f;
+            const float w = some ? exp2f(x.x - base) : 0.f;
+            const float4 v = some ? po[static_cast<long long>(s) * kStride] : make_float4(0.f, 0.f, 0.f, 0.f);
+            L = fmaf(w, x.y, L);
+            add(w, v);
         }
     }
     if (in) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        uint16_t* out = p.out + token * p.out_stride + (row - static_cast<long long>(token) * p.num_q_heads) * HD + 4 * e;
+        uint16_t* out = p.out + token * p.out_stride + (row - static_cast<long long>(token) * p.num_q_heads) * HD +
+                        blockIdx.y * 64 + 4 * e;
         *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
     }
 }
@@ -1069,13 +1098,13 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     const long long rows = static_cast<long long>(a.b.num_tokens) * a.num_q_heads;
     p.part_ml = reinterpret_cast<float2*>(a.workspace + rows * a.segments * HD);
     p.wait_limit_ns = a.wait_limit_ns;
-    constexpr int kPerCta = 256 / (HD / 4);
     auto join = [&]() {
         if (a.segments == 1) return cudaSuccess;
-        if (rows < 4 * a.num_sms)
-            return launch_kernel(kv_join_kernel<HD, true>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, a.pdl, p);
-        return launch_kernel(kv_join_kernel<HD, false>, dim3(static_cast<unsigned>((rows + kPerCta - 1) / kPerCta)),
-                             dim3(256), 0, stream, a.pdl, p);
+        if (rows < 16 * a.num_sms)
+            return launch_kernel(kv_join_kernel<HD, true>, dim3(static_cast<unsigned>(rows), HD / 64), dim3(256), 0, stream,
+                                 a.pdl, p);
+        return launch_kernel(kv_join_kernel<HD, false>, dim3(static_cast<unsigned>((rows + 15) / 16), HD / 64), dim3(256), 0,
+                             stream, a.pdl, p);
     };
     if (few > 0) {
         const cudaError_t e = launch_few_rows<E4M3, HD>(p, few, a.pdl, stream);

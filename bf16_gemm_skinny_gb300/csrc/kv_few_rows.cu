@@ -56,6 +56,13 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool 
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
+// The aligned 4 bytes that hold the byte at `src`, to shared memory.
+__device__ __forceinline__ void cp_async_word_of(uint32_t dst, const uint8_t* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
+                 "l"(reinterpret_cast<uintptr_t>(src) & ~static_cast<uintptr_t>(3))
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -85,7 +92,8 @@ struct Few {
     static constexpr int kWarpRing = kAhead * (kKeyBytes + kValBytes);
     static constexpr int kRing = kWarps * kWarpRing;
     static constexpr int kOut = kWarps * kRows * HD * 4;   // the warps' O, over the ring
-    static constexpr int kPitch = HD + 8;                   // Q rows, padded against bank conflicts
+    // Q rows, padded so that the 8 lanes of a 16-byte read's quarter meet distinct banks
+    static constexpr int kPitch = HD + (E4M3 ? 8 : 32);
     static constexpr int kBytes = (kRing > kOut ? kRing : kOut) + kRows * kPitch * 2;
 };
 
@@ -101,7 +109,10 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     extern __shared__ __align__(16) uint8_t smem[];
     uint16_t* s_q = reinterpret_cast<uint16_t*>(smem + F::kBytes - F::kRows * kPitch * 2);
     float* s_o = reinterpret_cast<float*>(smem);          // [kWarps][F::kRows][HD], once the ring is done with
-    __shared__ uint32_t s_meta[kWarps][A + 1][32];   // scale bytes, and bit 16: holds a key
+    // per position of the steps on their way: which byte of s_sk / s_sv holds its scale
+    // (bits 0-1, 2-3), and bit 4: it holds a key
+    __shared__ uint32_t s_meta[kWarps][A + 1][32];
+    __shared__ uint32_t s_sk[E4M3 ? kWarps : 1][A + 1][32], s_sv[E4M3 ? kWarps : 1][A + 1][32];
     __shared__ float s_m[kWarps][F::kRows], s_l[kWarps][F::kRows], s_scale[F::kRows];
     __shared__ int s_flag;
 
@@ -155,7 +166,6 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     const long long pitch = static_cast<long long>(p.b.num_kv_heads) * HD * kElem;
     const int mine = lane & (F::kGroup - 1);   // the position of a step whose page this lane looks up
     int entry = -1, row = -1;     // block-table entry of the group looked up last, cache row of the one found last
-    uint32_t kb = 127u, vb = 127u;
     // page and place in it of the group to look up next, stepped from group to group
     const int bs = p.b.block_size;
     const int step_pages = kWarps * F::kGroup / bs, step_slots = kWarps * F::kGroup - step_pages * bs;
@@ -181,20 +191,45 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
             }
         }
     };
-    auto find = [&](int i) {   // the group looked up last
+    auto find = [&](int i) {   // the step looked up last
         row = -1;
-        kb = vb = 127u;
         if (i < keys.end && keys.holds(keys.base(i) + mine)) {
-            if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks)) {
+            if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks))
                 row = entry * bs + entry_off;
-                if constexpr (E4M3) {
-                    kb = p.b.k_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
-                    vb = p.b.v_scales[static_cast<long long>(row) * p.b.num_kv_heads + kvh];
-                }
-            } else {
+            else
                 *reinterpret_cast<volatile int*>(p.b.status) = 0x200;   // kDevErrBadIndex
+        }
+    };
+    const uint8_t* scales_end[2] = {nullptr, nullptr};
+    if constexpr (E4M3) {
+        const long long n_scales = static_cast<long long>(p.b.num_blocks) * bs * p.b.num_kv_heads;
+        scales_end[0] = p.b.k_scales + n_scales;
+        scales_end[1] = p.b.v_scales + n_scales;
+    }
+    // A scale byte on its way to word `w`; returns its place there.  The word around it
+    // is copied where it lies within the scales, else the byte is loaded.
+    auto load_scale = [&](uint32_t* w, const uint8_t* scales, const uint8_t* end, long long i) -> uint32_t {
+        const uint8_t* src = scales + i;
+        const uint32_t b = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) & 3u);
+        if (src - b >= scales && src - b + 4 <= end) {
+            cp_async_word_of(static_cast<uint32_t>(__cvta_generic_to_shared(w)), src);
+            return b;
+        }
+        *w = *src;
+        return 0u;
+    };
+    // the step whose rows `row` holds: its note, and its scales in the next group of copies
+    auto note = [&](int slot) {
+        uint32_t meta = 0u;
+        if (row >= 0) {
+            meta = 16u;
+            if constexpr (E4M3) {
+                const long long at = static_cast<long long>(row) * p.b.num_kv_heads + kvh;
+                meta |= load_scale(&s_sk[warp][slot][lane], p.b.k_scales, scales_end[0], at);
+                meta |= load_scale(&s_sv[warp][slot][lane], p.b.v_scales, scales_end[1], at) << 2;
             }
         }
+        s_meta[warp][slot][lane] = meta;
     };
     uint8_t* ring = smem + warp * F::kWarpRing + lane * 16;   // this lane's 16 bytes of each 512
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
@@ -220,31 +255,17 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         }
         cp_async_commit();
     };
-    // What find() found, for the step's turn: noted two steps later, so that the scale
-    // bytes' loads have that long.
-    uint32_t found_k[2] = {127u, 127u}, found_v[2] = {127u, 127u}, found[2] = {0u, 0u};   // the last, the one before
-    auto keep = [&]() {
-        found_k[1] = found_k[0];
-        found_v[1] = found_v[0];
-        found[1] = found[0];
-        found_k[0] = kb;
-        found_v[0] = vb;
-        found[0] = row >= 0 ? 0x10000u : 0u;
-    };
-    auto note = [&](int slot, int which) { s_meta[warp][slot][lane] = found_k[which] | (found_v[which] << 8) | found[which]; };
-
-    // Steps in turn: copies are issued A steps ahead of their use, rows (and scale
-    // bytes) found one step before that, block-table entries loaded one before that.
+    // Steps in turn: copies are issued A steps ahead of their use, rows found one step
+    // before that, block-table entries loaded one before that.
     const int i0 = keys.begin + warp;
     look_up(i0);
     find(i0);
     look_up(i0 + kWarps);
 #pragma unroll
     for (int a = 0; a < A; ++a) {
+        note(a);
         load_keys(a);
         load_values(a);
-        keep();
-        if (a > 0) note(a - 1, 1);
         find(i0 + (a + 1) * kWarps);
         look_up(i0 + (a + 2) * kWarps);
     }
@@ -305,17 +326,22 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     bool wide = false;
 
 
-    int at = 0, slot = 0, slot_in = A - 1;   // ring place; places of this step's note and of the next one written
+    int at = 0, slot = 0, slot_in = A;   // ring place; places of this step's note and of the next one written
     for (int i = i0; i < keys.end; i += kWarps) {
         const int base = keys.base(i);
-        note(slot_in, 0);   // found two steps ago: `keep` of the step before the one about to be issued
-        if (++slot_in > A) slot_in = 0;
+        cp_async_wait<2 * A - 1>();      // this step's keys and scales
         __syncwarp();
         const uint32_t meta = s_meta[warp][slot][mine];
+        const bool holds = (meta & 16u) != 0;
+        uint32_t kb_now = 127u, vb_now = 127u;
+        if constexpr (E4M3) {
+            if (holds) {
+                kb_now = (s_sk[warp][slot][mine] >> (8 * (meta & 3u))) & 255u;
+                vb_now = (s_sv[warp][slot][mine] >> (8 * ((meta >> 2) & 3u))) & 255u;
+            }
+        }
         if (++slot > A) slot = 0;
-        const uint32_t have = __ballot_sync(0xffffffffu, (meta >> 16) != 0);   // positions that hold a key
-        const uint32_t kb_now = meta & 255u, vb_now = (meta >> 8) & 255u;
-        cp_async_wait<2 * A - 1>();      // this group's keys
+        const uint32_t have = __ballot_sync(0xffffffffu, holds);   // positions that hold a key
         const uint8_t* ks = ring + at * F::kKeyBytes;
         // S^T, 16 positions at a time
         float s[R][SUB][4];
@@ -364,6 +390,8 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                 for (int k = 0; k < 4; ++k) s[n8][b][k] = t[n8][0][k] + t[n8][1][k];
         }
         // a later step's keys on their way to this one's place
+        note(slot_in);
+        if (++slot_in > A) slot_in = 0;
         load_keys(at);
         // weights: lane (g, c) has positions g + 8 k and rows 8 n + 2c, 8 n + 2c + 1
         float grow_e = 1.f, kf[2 * SUB], vf[2 * SUB];
@@ -375,7 +403,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                 vf[k] = __shfl_sync(0xffffffffu, own_v, g + 8 * k);
             }
             // the range of V's exponents, all-zero rows (the least scale) left out
-            const bool h = (meta >> 16) != 0 && vb_now > 10u && vb_now != 255u;
+            const bool h = holds && vb_now > 10u && vb_now != 255u;
             const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
             const int low = __reduce_min_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : 1000);
             if (top > -1000) {
@@ -517,7 +545,6 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         }
         load_values(at);
         if (++at == A) at = 0;
-        keep();
         find(i + (A + 1) * kWarps);
         look_up(i + (A + 2) * kWarps);
     }
