@@ -46,6 +46,7 @@ OPTIONS = {
     "prefetch_kb": 16,
     "k_order": 17,
     "pair_m": 18,
+    "kv_kernel": 19,
 }
 
 # Every symbol include/bsk.h (the C ABI) declares.
@@ -83,6 +84,8 @@ def library_path() -> str:
 def load():
     """Load libbsk.so (raises if it is missing: build it with bf16_gemm_skinny_gb300.build.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -147,11 +150,12 @@ def load():
 def _addr(t) -> int | None:
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
-    if hasattr(t, "data_ptr"):
-        return int(t.data_ptr())
-    return int(t.ctypes.data)   # a NumPy array (host memory)
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        return int(t.ctypes.data)   # a NumPy array (host memory)
 
 
 _torch = None
@@ -171,7 +175,7 @@ def _current_stream_handle() -> int:
         if raw is not None and get_dev is not None:
             _raw_stream = lambda: raw(get_dev())  # noqa: E731
     if _raw_stream is not None:
-        return int(_raw_stream())
+        return _raw_stream()
     return int(_torch.cuda.current_stream().cuda_stream)
 
 

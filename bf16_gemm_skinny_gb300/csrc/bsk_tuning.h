@@ -84,6 +84,9 @@ void bsk_tile_coord(int t, int num_m, int num_n, int group_m, int* pid_m, int* p
  *                            tiles (each CTA stages 256 rows of A; every B slice feeds two
  *                            MMAs; one accumulator, so the epilogue no longer overlaps the
  *                            next tile's MMAs)
+ *   BSK_OPT_KV_KERNEL        kernel of chunk_attention and decode_attention: 0 automatic, 1 the
+ *                            tcgen05 kernel (128 query rows per CTA), 2 the kernel for few rows
+ *                            (8 or 16 per CTA)
  * Returns BSK_ERR_INVALID_ARG for an unknown key or a value out of range.
  */
 enum {
@@ -104,7 +107,8 @@ enum {
     BSK_OPT_SPLIT_K = 15,
     BSK_OPT_PREFETCH_KB = 16,
     BSK_OPT_K_ORDER = 17,
-    BSK_OPT_PAIR_M = 18
+    BSK_OPT_PAIR_M = 18,
+    BSK_OPT_KV_KERNEL = 19
 };
 int bsk_set_option(int key, long long value);
 long long bsk_get_option(int key);

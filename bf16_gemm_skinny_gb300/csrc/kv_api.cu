@@ -227,6 +227,7 @@ int enqueue_attention(bsk::KvAttnLaunch& a, int num_segments, cudaStream_t s)
     const long long limit_us = bsk_get_option(BSK_OPT_WAIT_LIMIT_US);
     if (limit_us > 0) a.wait_limit_ns = static_cast<unsigned long long>(limit_us) * 1000ull;
     a.pdl = bsk_get_option(BSK_OPT_PDL) != 1;
+    a.kernel = static_cast<int>(bsk_get_option(BSK_OPT_KV_KERNEL));
     a.segments = num_segments > 0 ? num_segments : bsk::kv_attention_segments(a);
     Workspace ws(s);
     const size_t bytes = bsk::kv_attention_workspace(a);

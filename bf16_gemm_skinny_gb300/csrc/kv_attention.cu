@@ -532,7 +532,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         // ------------------------------------------------------------------
         constexpr int PL = kTile / 32;
         const int bs = p.b.block_size;
-        const int none = p.b.num_blocks * bs;
+        const int flat = p.b.flat_len > 0 ? seq * p.b.flat_len : -1;   // rows of a flat copy
+        const int none = p.b.flat_len > 0 ? p.b.num_seqs * p.b.flat_len : p.b.num_blocks * bs;
         const int tile_pages = kTile / bs, tile_slots = kTile - tile_pages * bs;
         int page[PL], off[PL];              // of the next tile to look up
         int entry[PL], entry_off[PL];       // looked up: block-table entry and place in the page
@@ -566,10 +567,11 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             bool bad = false;
 #pragma unroll
             for (int u = 0; u < PL; ++u) {
-                const bool h = keys.holds(keys.base(i) + u * 32 + lane);
+                const int t = keys.base(i) + u * 32 + lane;
+                const bool h = keys.holds(t);
                 const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
                 bad = bad || (h && !g);
-                row[u] = h && g ? entry[u] * bs + entry_off[u] : none;
+                row[u] = h && g ? (flat >= 0 ? flat + t : entry[u] * bs + entry_off[u]) : none;
                 have |= (h && g ? 1u : 0u) << u;
                 if constexpr (E4M3) {
                     kb[u] = vb[u] = 127u;
@@ -1061,11 +1063,17 @@ long long most_keys(const KvAttnLaunch& a)
 }
 
 // Rows per CTA of the kernel for few query rows per KV head, or 0: the call takes
-// the other kernel.
+// the other kernel.  An E4M3 cache read for few rows would spend its time in the
+// other kernel's shared memory.  Measured in microseconds, many-row / few-row kernel
+// (32 sequences of up to 4000 tokens): head_dim 256, 8 rows 105 / 87, 32 rows 106 / 143;
+// 128, 8 rows 139 / 75, 32 rows 136 / 143; 64, 8 rows 71 / 44, 32 rows 73 / 72.  On a
+// BF16 cache it does not pay: 8 rows of 256 83 / 130, of 128 91 / 117, of 64 46 / 45.
 int few_rows(const KvAttnLaunch& a)
 {
     const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
-    return rows <= 8 ? 8 : (rows <= 32 ? 16 : 0);
+    const int few = rows <= 8 || a.b.head_dim == 256 ? 8 : 16;
+    if (a.b.type != kCacheE4M3 || a.kernel == 1) return 0;
+    return a.kernel == 2 || rows * a.b.head_dim <= 2048 ? few : 0;
 }
 
 template <bool E4M3, int HD>
@@ -1106,9 +1114,11 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
         return launch_kernel(kv_join_kernel<HD, false>, dim3(static_cast<unsigned>((rows + 15) / 16), HD / 64), dim3(256), 0,
                              stream, a.pdl, p);
     };
-    if (few > 0) {
-        const cudaError_t e = launch_few_rows<E4M3, HD>(p, few, a.pdl, stream);
-        return e != cudaSuccess ? e : join();
+    if constexpr (E4M3) {
+        if (few > 0) {
+            const cudaError_t e = launch_few_rows<HD>(p, few, a.pdl, stream);
+            return e != cudaSuccess ? e : join();
+        }
     }
     KvMaps maps = {};
     TmapEncodeFn enc = tmap_encoder();
@@ -1120,8 +1130,10 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     p.box = 4;
     for (int r = 8; r <= Geo<E4M3, HD>::kTile; r *= 2)
         if (a.b.block_size % r == 0) p.box = r;
+    if (a.b.flat_len > 0) p.box = 16;   // (whole tiles are one box; of the last one, boxes)
     const cuuint64_t width = static_cast<cuuint64_t>(a.b.num_kv_heads) * HD;
-    const cuuint64_t cache_rows = static_cast<cuuint64_t>(a.b.num_blocks) * a.b.block_size;
+    const cuuint64_t cache_rows = a.b.flat_len > 0 ? static_cast<cuuint64_t>(a.b.num_seqs) * a.b.flat_len
+                                                   : static_cast<cuuint64_t>(a.b.num_blocks) * a.b.block_size;
     const cuuint64_t pitch = E4M3 ? width : width * 2;
     const cuuint32_t rows8 = static_cast<cuuint32_t>(p.box);
     const cuuint32_t ones[4] = {1, 1, 1, 1};
@@ -1179,8 +1191,15 @@ int kv_attention_segments(const KvAttnLaunch& a)
     double best = 0;
     int segments = 1;
     for (int s = 1; s <= 256 && (s == 1 || s <= tiles); ++s) {
-        const long long waves = (ctas * s + slots - 1) / slots;
-        double t = static_cast<double>(waves) * (fixed + static_cast<double>((tiles + s - 1) / s));
+        const double each = static_cast<double>((tiles + s - 1) / s);
+        double t;
+        if (a.b.num_seqs == 1) {
+            // equal CTAs: whole waves
+            t = static_cast<double>((ctas * s + slots - 1) / slots) * (fixed + each);
+        } else {
+            // lengths anywhere up to the longest: the average work, and the last CTA's
+            t = static_cast<double>(ctas) * (0.6 * static_cast<double>(tiles) + s * fixed) / static_cast<double>(slots) + each;
+        }
         if (s > 1) t += fixed + rows * s * a.b.head_dim * 8 / 3.5e6;
         if (s == 1 || t < best) {
             best = t;
@@ -1190,14 +1209,50 @@ int kv_attention_segments(const KvAttnLaunch& a)
     return segments;
 }
 
-size_t kv_attention_workspace(const KvAttnLaunch& a)
+namespace {
+
+size_t partial_bytes(const KvAttnLaunch& a)
 {
     if (a.segments <= 1) return 0;
-    return static_cast<size_t>(a.b.num_tokens) * a.num_q_heads * a.segments * (a.b.head_dim + 2) * sizeof(float);
+    const size_t bytes = static_cast<size_t>(a.b.num_tokens) * a.num_q_heads * a.segments * (a.b.head_dim + 2) * sizeof(float);
+    return (bytes + 255) / 256 * 256;
 }
 
-int launch_kv_attention(const KvAttnLaunch& a, cudaStream_t stream, char* msg, size_t msg_len)
+// Rows of a sequence in the flat BF16 copy of an E4M3 cache, or 0: no copy is made.
+// It costs one pass over the positions in sight; without it every 128 query rows
+// convert them again.  Microseconds without / with it, 30000 positions: head_dim 256,
+// 256 rows 84 / 97, 512 rows 143 / 126, 2048 rows 477 / 273; 128, 256 rows 104 / 90,
+// 2048 rows 680 / 274; 64, 256 rows 48 / 46, 2048 rows 267 / 152.
+int flat_rows(const KvAttnLaunch& a)
 {
+    const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
+    if (a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < 2 * (a.b.head_dim > 128 ? 256 : 128)) return 0;
+    const long long len = (a.max_seq_len + 127LL) / 128 * 128;
+    const long long bytes = len * a.b.num_seqs * a.b.num_kv_heads * a.b.head_dim * 4;
+    return len * a.b.num_seqs <= 0x7fffffffLL && bytes <= (2LL << 30) ? static_cast<int>(len) : 0;
+}
+
+}  // namespace
+
+size_t kv_attention_workspace(const KvAttnLaunch& a)
+{
+    return partial_bytes(a) +
+           static_cast<size_t>(flat_rows(a)) * a.b.num_seqs * a.b.num_kv_heads * a.b.head_dim * 2 * sizeof(uint16_t);
+}
+
+int launch_kv_attention(const KvAttnLaunch& launch, cudaStream_t stream, char* msg, size_t msg_len)
+{
+    KvAttnLaunch a = launch;
+    if (const int flat = flat_rows(a); flat > 0) {
+        uint16_t* k = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(a.workspace) + partial_bytes(a));
+        uint16_t* v = k + static_cast<size_t>(flat) * a.b.num_seqs * a.b.num_kv_heads * a.b.head_dim;
+        if (launch_kv_flatten(a.b, k, v, flat, a.max_seq_len, a.window, a.sinks, a.pdl, stream, msg, msg_len)) return 1;
+        a.b.k = k;
+        a.b.v = v;
+        a.b.k_scales = a.b.v_scales = nullptr;
+        a.b.type = kCacheBF16;
+        a.b.flat_len = flat;
+    }
     msg[0] = '\0';
     const bool q = a.b.type == kCacheE4M3;
     cudaError_t e = cudaErrorInvalidValue;

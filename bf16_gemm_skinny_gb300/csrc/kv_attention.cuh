@@ -210,9 +210,9 @@ __device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* tabl
     }
 }
 
-// Launches the kernel for few query rows: `rows` (8 or 16) per CTA, p.tiles of them
-// per sequence and KV head.
-template <bool E4M3, int HD>
+// Launches the kernel for few query rows over an E4M3 cache: `rows` (8, or 16 with
+// HD < 256) per CTA, p.tiles of them per sequence and KV head.
+template <int HD>
 cudaError_t launch_few_rows(const AttnParams& p, int rows, bool pdl, cudaStream_t stream);
 
 }  // namespace kv

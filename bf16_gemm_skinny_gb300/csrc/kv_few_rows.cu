@@ -1,4 +1,4 @@
-// kv_few_rows.cu -- attention over the paged cache for few query rows per KV
+// kv_few_rows.cu -- attention over a paged E4M3 cache for few query rows per KV
 // head: single tokens, and a few drafted ones.
 //
 // The same one-pass sums as kv_attention.cu, but the cache is read once for at
@@ -26,22 +26,15 @@ namespace kv {
 namespace {
 
 
-template <bool E4M3>
+// D (16 x 8, FP32) += A (16 x 16, FP16, row-major) * B (16 x 8, FP16, column-major).
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    if constexpr (E4M3)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
@@ -70,38 +63,36 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 // Sizes.  `kAhead` steps per warp are on their way: the CTAs of an SM have 100 to
 // 200 KB in flight, which the latency times HBM's rate needs (about 45 KB) with
 // room for uneven progress.
-template <bool E4M3, int HD, int R>
+template <int HD, int R>
 struct Few {
     static constexpr int kRows = 8 * R;                 // query rows per CTA (R MMAs of N = 8)
-    static constexpr int kElem = E4M3 ? 1 : 2;
-    static constexpr int kVec = 16 / kElem;             // values in 16 bytes
-    static constexpr int kKeyVecs = HD / (4 * kVec);    // 16-byte pieces of a key's row per lane (4 lanes a row)
-    // values: 8 lanes a row.  With HD = 64 in E4M3 a lane's share is 8 bytes; it takes
-    // the 16 around them and uses its half.
-    static constexpr bool kHalf = E4M3 && HD == 64;
-    static constexpr int kValVecs = kHalf ? 1 : HD / (8 * kVec);
-    static constexpr int kRowBytes = HD * kElem;
-    // A warp's step: 16 positions, or 32 where two steps' copies fit beside each other
-    // (the work per step that does not depend on its size is over half of it).
-    static constexpr int kSub = kRowBytes == 512 ? 1 : 2;
+    static constexpr int kVec = 16;                     // codes in 16 bytes
+    static constexpr int kKeyVecs = HD / 64;            // 16-byte pieces of a key's row per lane (4 lanes a row)
+    // values: 8 lanes a row.  With HD = 64 a lane's share is 8 bytes; it takes the 16
+    // around them and uses its half.
+    static constexpr bool kHalf = HD == 64;
+    static constexpr int kValVecs = kHalf ? 1 : HD / 128;
+    // A warp's step is 32 positions: the work that does not depend on their number is
+    // over half of that of 16.
+    static constexpr int kSub = 2;
     static constexpr int kGroup = 16 * kSub;
-    static constexpr int kWarps = kRowBytes >= 256 ? 3 : 4;
-    static constexpr int kAhead = kRowBytes == 64 ? 3 : 2;
-    static constexpr int kCtas = R > 1 || kRowBytes >= 256 ? 2 : 3;   // of an SM
+    static constexpr int kWarps = HD == 256 ? 3 : 4;
+    static constexpr int kAhead = HD == 64 ? 3 : 2;
+    static constexpr int kCtas = R > 1 || HD == 256 ? 2 : 3;   // of an SM
     static constexpr int kKeyBytes = kSub * 2 * kKeyVecs * 512, kValBytes = kSub * 4 * kValVecs * 512;   // of a step
     static constexpr int kWarpRing = kAhead * (kKeyBytes + kValBytes);
     static constexpr int kRing = kWarps * kWarpRing;
     static constexpr int kOut = kWarps * kRows * HD * 4;   // the warps' O, over the ring
     // Q rows, padded so that the 8 lanes of a 16-byte read's quarter meet distinct banks
-    static constexpr int kPitch = HD + (E4M3 ? 8 : 32);
+    static constexpr int kPitch = HD + 8;
     static constexpr int kBytes = (kRing > kOut ? kRing : kOut) + kRows * kPitch * 2;
 };
 
-template <bool E4M3, int HD, int R>
-__global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R>::kCtas) kv_few_rows_kernel(const __grid_constant__ AttnParams p)
+template <int HD, int R>
+__global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv_few_rows_kernel(const __grid_constant__ AttnParams p)
 {
-    using F = Few<E4M3, HD, R>;
-    constexpr int kWarps = F::kWarps, kElem = F::kElem, kVec = F::kVec, kKeyVecs = F::kKeyVecs, kValVecs = F::kValVecs;
+    using F = Few<HD, R>;
+    constexpr int kWarps = F::kWarps, kVec = F::kVec, kKeyVecs = F::kKeyVecs, kValVecs = F::kValVecs;
     constexpr bool kHalf = F::kHalf;
     constexpr int A = F::kAhead, SUB = F::kSub;
     constexpr int kDim = HD / 16;                // O^T tiles
@@ -112,7 +103,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     // per position of the steps on their way: which byte of s_sk / s_sv holds its scale
     // (bits 0-1, 2-3), and bit 4: it holds a key
     __shared__ uint32_t s_meta[kWarps][A + 1][32];
-    __shared__ uint32_t s_sk[E4M3 ? kWarps : 1][A + 1][32], s_sv[E4M3 ? kWarps : 1][A + 1][32];
+    __shared__ uint32_t s_sk[kWarps][A + 1][32], s_sv[kWarps][A + 1][32];
     __shared__ float s_m[kWarps][F::kRows], s_l[kWarps][F::kRows], s_scale[F::kRows];
     __shared__ int s_flag;
 
@@ -161,9 +152,9 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     }
     const int32_t* table = p.b.block_tables + static_cast<long long>(seq) * p.b.max_blocks;
 
-    const uint8_t* kc = static_cast<const uint8_t*>(p.b.k) + static_cast<long long>(kvh) * HD * kElem;
-    const uint8_t* vc = static_cast<const uint8_t*>(p.b.v) + static_cast<long long>(kvh) * HD * kElem;
-    const long long pitch = static_cast<long long>(p.b.num_kv_heads) * HD * kElem;
+    const uint8_t* kc = static_cast<const uint8_t*>(p.b.k) + static_cast<long long>(kvh) * HD;
+    const uint8_t* vc = static_cast<const uint8_t*>(p.b.v) + static_cast<long long>(kvh) * HD;
+    const long long pitch = static_cast<long long>(p.b.num_kv_heads) * HD;
     const int mine = lane & (F::kGroup - 1);   // the position of a step whose page this lane looks up
     int entry = -1, row = -1;     // block-table entry of the group looked up last, cache row of the one found last
     // page and place in it of the group to look up next, stepped from group to group
@@ -201,11 +192,9 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         }
     };
     const uint8_t* scales_end[2] = {nullptr, nullptr};
-    if constexpr (E4M3) {
-        const long long n_scales = static_cast<long long>(p.b.num_blocks) * bs * p.b.num_kv_heads;
-        scales_end[0] = p.b.k_scales + n_scales;
-        scales_end[1] = p.b.v_scales + n_scales;
-    }
+    const long long n_scales = static_cast<long long>(p.b.num_blocks) * bs * p.b.num_kv_heads;
+    scales_end[0] = p.b.k_scales + n_scales;
+    scales_end[1] = p.b.v_scales + n_scales;
     // A scale byte on its way to word `w`; returns its place there.  The word around it
     // is copied where it lies within the scales, else the byte is loaded.
     auto load_scale = [&](uint32_t* w, const uint8_t* scales, const uint8_t* end, long long i) -> uint32_t {
@@ -223,11 +212,9 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         uint32_t meta = 0u;
         if (row >= 0) {
             meta = 16u;
-            if constexpr (E4M3) {
-                const long long at = static_cast<long long>(row) * p.b.num_kv_heads + kvh;
-                meta |= load_scale(&s_sk[warp][slot][lane], p.b.k_scales, scales_end[0], at);
-                meta |= load_scale(&s_sv[warp][slot][lane], p.b.v_scales, scales_end[1], at) << 2;
-            }
+            const long long at = static_cast<long long>(row) * p.b.num_kv_heads + kvh;
+            meta |= load_scale(&s_sk[warp][slot][lane], p.b.k_scales, scales_end[0], at);
+            meta |= load_scale(&s_sv[warp][slot][lane], p.b.v_scales, scales_end[1], at) << 2;
         }
         s_meta[warp][slot][lane] = meta;
     };
@@ -284,16 +271,14 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
             m = __vmaxu2(m, w[i] & 0x7fff7fffu);
         }
         float scale = p.scale_log2;
-        if constexpr (E4M3) {
-            // times a power of two that brings the row's largest value to [2^14, 2^15)
-            m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-            const int e = max(-126, min(static_cast<int>(m >> 7) - 127 - 14, 113));
-            const float f = exp2f(static_cast<float>(-e));
-            scale *= exp2f(static_cast<float>(e));
+        // times a power of two that brings the row's largest value to [2^14, 2^15)
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        const int e = max(-126, min(static_cast<int>(m >> 7) - 127 - 14, 113));
+        const float f = exp2f(static_cast<float>(-e));
+        scale *= exp2f(static_cast<float>(e));
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i)
-                w[i] = f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-        }
+        for (int i = 0; i < kPairs; ++i)
+            w[i] = f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
         if (lane == 0) s_scale[r] = scale;
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) *reinterpret_cast<uint32_t*>(s_q + r * kPitch + (i * 32 + lane) * 2) = w[i];
@@ -334,11 +319,9 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         const uint32_t meta = s_meta[warp][slot][mine];
         const bool holds = (meta & 16u) != 0;
         uint32_t kb_now = 127u, vb_now = 127u;
-        if constexpr (E4M3) {
-            if (holds) {
-                kb_now = (s_sk[warp][slot][mine] >> (8 * (meta & 3u))) & 255u;
-                vb_now = (s_sv[warp][slot][mine] >> (8 * ((meta >> 2) & 3u))) & 255u;
-            }
+        if (holds) {
+            kb_now = (s_sk[warp][slot][mine] >> (8 * (meta & 3u))) & 255u;
+            vb_now = (s_sv[warp][slot][mine] >> (8 * ((meta >> 2) & 3u))) & 255u;
         }
         if (++slot > A) slot = 0;
         const uint32_t have = __ballot_sync(0xffffffffu, holds);   // positions that hold a key
@@ -358,29 +341,21 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                 const uint4 k1 = *reinterpret_cast<const uint4*>(ks + ((2 * b + 1) * kKeyVecs + v) * 512);
                 const uint32_t x[2][4] = {{k0.x, k0.y, k0.z, k0.w}, {k1.x, k1.y, k1.z, k1.w}};
                 const uint16_t* qs = s_q + g * kPitch + v * 4 * kVec + c * kVec;
-                constexpr int kHalves = E4M3 ? 2 : 1;   // 8 values of each row: two MMAs
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {   // 8 values of each row: two MMAs
                     uint32_t a[2][4];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        if constexpr (E4M3) {
-                            a[u][0] = e4m3x2_f16x2(x[0][2 * h + u]);
-                            a[u][1] = e4m3x2_f16x2(x[1][2 * h + u]);
-                            a[u][2] = e4m3x2_f16x2(x[0][2 * h + u] >> 16);
-                            a[u][3] = e4m3x2_f16x2(x[1][2 * h + u] >> 16);
-                        } else {
-                            a[u][0] = x[0][2 * u];
-                            a[u][1] = x[1][2 * u];
-                            a[u][2] = x[0][2 * u + 1];
-                            a[u][3] = x[1][2 * u + 1];
-                        }
+                        a[u][0] = e4m3x2_f16x2(x[0][2 * h + u]);
+                        a[u][1] = e4m3x2_f16x2(x[1][2 * h + u]);
+                        a[u][2] = e4m3x2_f16x2(x[0][2 * h + u] >> 16);
+                        a[u][3] = e4m3x2_f16x2(x[1][2 * h + u] >> 16);
                     }
 #pragma unroll
                     for (int n8 = 0; n8 < R; ++n8) {
                         const uint4 q = *reinterpret_cast<const uint4*>(qs + n8 * 8 * kPitch + h * 8);
-                        mma16816<E4M3>(t[n8][0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
-                        mma16816<E4M3>(t[n8][1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+                        mma16816(t[n8][0], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+                        mma16816(t[n8][1], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
                     }
                 }
             }
@@ -395,25 +370,23 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         load_keys(at);
         // weights: lane (g, c) has positions g + 8 k and rows 8 n + 2c, 8 n + 2c + 1
         float grow_e = 1.f, kf[2 * SUB], vf[2 * SUB];
-        if constexpr (E4M3) {
-            const float own_k = e8m0_value(kb_now), own_v = e8m0_value(vb_now);
+        const float own_k = e8m0_value(kb_now), own_v = e8m0_value(vb_now);
 #pragma unroll
-            for (int k = 0; k < 2 * SUB; ++k) {
-                kf[k] = __shfl_sync(0xffffffffu, own_k, g + 8 * k);
-                vf[k] = __shfl_sync(0xffffffffu, own_v, g + 8 * k);
+        for (int k = 0; k < 2 * SUB; ++k) {
+            kf[k] = __shfl_sync(0xffffffffu, own_k, g + 8 * k);
+            vf[k] = __shfl_sync(0xffffffffu, own_v, g + 8 * k);
+        }
+        // the range of V's exponents, all-zero rows (the least scale) left out
+        const bool h = holds && vb_now > 10u && vb_now != 255u;
+        const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
+        const int low = __reduce_min_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : 1000);
+        if (top > -1000) {
+            if (low_e == 1000 || top > E + 4) {
+                grow_e = exp2_fast(static_cast<float>(E - top));
+                E = top;
             }
-            // the range of V's exponents, all-zero rows (the least scale) left out
-            const bool h = holds && vb_now > 10u && vb_now != 255u;
-            const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
-            const int low = __reduce_min_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : 1000);
-            if (top > -1000) {
-                if (low_e == 1000 || top > E + 4) {
-                    grow_e = exp2_fast(static_cast<float>(E - top));
-                    E = top;
-                }
-                low_e = min(low_e, low);
-                wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
-            }
+            low_e = min(low_e, low);
+            wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
         }
         const bool masked = have != 0xffffffffu || base + F::kGroup - 1 > pmin ||
                             (base < lo_max && base + F::kGroup > p.sinks);
@@ -426,7 +399,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     x[k][q] = s[n8][k >> 1][2 * (k & 1) + q];
-                    if constexpr (E4M3) x[k][q] *= kf[k];
+                    x[k][q] *= kf[k];
                 }
             if (masked) {
 #pragma unroll
@@ -473,7 +446,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 b[q] = m[n8][q] == -INFINITY ? 0.f : m[n8][q];
-                if constexpr (E4M3) b[q] -= static_cast<float>(3 - E);
+                b[q] -= static_cast<float>(3 - E);
             }
 #pragma unroll
             for (int k = 0; k < 2 * SUB; ++k) {   // positions g + 8 k
@@ -483,10 +456,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                     w[q] = exp2_fast(fmaf(x[k][q], row_scale[n8][q], -b[q]));
                     l[n8][q] += w[q];
                 }
-                if constexpr (E4M3)
-                    pt[n8][k] = transpose8x8(f16x2(w[0] * vf[k], w[1] * vf[k]));
-                else
-                    pt[n8][k] = transpose8x8(bf16x2(w[0], w[1]));
+                pt[n8][k] = transpose8x8(f16x2(w[0] * vf[k], w[1] * vf[k]));
             }
         }
         // O^T
@@ -512,34 +482,23 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
                     }
                 }
                 constexpr int kPairs = kHalf ? 4 : kVec / 2;   // pairs of dimensions a lane has per position
-                if constexpr (E4M3) {
-                    // two positions' codes byte by byte beside each other, four dimensions at a time
+                // two positions' codes byte by byte beside each other, four dimensions at a time
 #pragma unroll
-                    for (int d = 0; d < kPairs; d += 2) {
-                        const uint32_t u0 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x5140);
-                        const uint32_t u1 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x7362);
-                        const uint32_t u2 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x5140);
-                        const uint32_t u3 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x7362);
-                        const uint32_t a[2][4] = {{e4m3x2_f16x2(u0), e4m3x2_f16x2(u0 >> 16), e4m3x2_f16x2(u2),
-                                                   e4m3x2_f16x2(u2 >> 16)},
-                                                  {e4m3x2_f16x2(u1), e4m3x2_f16x2(u1 >> 16), e4m3x2_f16x2(u3),
-                                                   e4m3x2_f16x2(u3 >> 16)}};
+                for (int d = 0; d < kPairs; d += 2) {
+                    const uint32_t u0 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x5140);
+                    const uint32_t u1 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x7362);
+                    const uint32_t u2 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x5140);
+                    const uint32_t u3 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x7362);
+                    const uint32_t a[2][4] = {{e4m3x2_f16x2(u0), e4m3x2_f16x2(u0 >> 16), e4m3x2_f16x2(u2),
+                                               e4m3x2_f16x2(u2 >> 16)},
+                                              {e4m3x2_f16x2(u1), e4m3x2_f16x2(u1 >> 16), e4m3x2_f16x2(u3),
+                                               e4m3x2_f16x2(u3 >> 16)}};
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int n8 = 0; n8 < R; ++n8)
-                                mma16816<true>(o[n8][v * kPairs + d + u], a[u][0], a[u][1], a[u][2], a[u][3],
-                                               pt[n8][2 * b], pt[n8][2 * b + 1]);
-                    }
-                } else {
-#pragma unroll
-                    for (int d = 0; d < kPairs; ++d) {
-                        const uint32_t a0 = __byte_perm(y[0][d], y[1][d], 0x5410), a1 = __byte_perm(y[0][d], y[1][d], 0x7632);
-                        const uint32_t a2 = __byte_perm(y[2][d], y[3][d], 0x5410), a3 = __byte_perm(y[2][d], y[3][d], 0x7632);
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int n8 = 0; n8 < R; ++n8)
-                            mma16816<false>(o[n8][v * kPairs + d], a0, a1, a2, a3, pt[n8][2 * b], pt[n8][2 * b + 1]);
-                    }
+                            mma16816(o[n8][v * kPairs + d + u], a[u][0], a[u][1], a[u][2], a[u][3],
+                                           pt[n8][2 * b], pt[n8][2 * b + 1]);
                 }
             }
         }
@@ -552,7 +511,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
     __syncthreads();   // the ring becomes s_o
 
     // ---- the warps' results ---------------------------------------------------
-    const float plain = E4M3 ? exp2f(static_cast<float>(E - 3)) : 1.f;
+    const float plain = exp2f(static_cast<float>(E - 3));
     constexpr int kPairs = kHalf ? 4 : kVec / 2;
 #pragma unroll
     for (int n8 = 0; n8 < R; ++n8) {
@@ -615,7 +574,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
         for (int r = warp; r < rows; r += kWarps) {
             if (!((s_flag >> r) & 1)) continue;
             const int my = row0 + r;
-            repair_row<E4M3, HD, F::kGroup>(p, table, keys, kvh, first + my / p.group, kvh * p.group + my % p.group,
+            repair_row<true, HD, F::kGroup>(p, table, keys, kvh, first + my / p.group, kvh * p.group + my % p.group,
                                          pos0 + my / p.group, seg);
         }
     }
@@ -623,7 +582,7 @@ __global__ void __launch_bounds__(Few<E4M3, HD, R>::kWarps * 32, Few<E4M3, HD, R
 
 }  // namespace
 
-template <bool E4M3, int HD>
+template <int HD>
 cudaError_t launch_few_rows(const AttnParams& p, int rows, bool pdl, cudaStream_t stream)
 {
     const long long ctas = static_cast<long long>(p.tiles) * p.b.num_kv_heads * p.b.num_seqs * p.segments;
@@ -634,17 +593,15 @@ cudaError_t launch_few_rows(const AttnParams& p, int rows, bool pdl, cudaStream_
         return launch_kernel(kern, dim3(static_cast<unsigned>(ctas)), dim3(threads), bytes, stream, pdl, p);
     };
     static SmemOptIn one, two;
-    if (rows <= 8)
-        return launch(kv_few_rows_kernel<E4M3, HD, 1>, Few<E4M3, HD, 1>::kWarps * 32, Few<E4M3, HD, 1>::kBytes, one);
-    return launch(kv_few_rows_kernel<E4M3, HD, 2>, Few<E4M3, HD, 2>::kWarps * 32, Few<E4M3, HD, 2>::kBytes, two);
+    if constexpr (HD < 256) {
+        if (rows > 8) return launch(kv_few_rows_kernel<HD, 2>, Few<HD, 2>::kWarps * 32, Few<HD, 2>::kBytes, two);
+    }
+    return launch(kv_few_rows_kernel<HD, 1>, Few<HD, 1>::kWarps * 32, Few<HD, 1>::kBytes, one);
 }
 
-template cudaError_t launch_few_rows<false, 64>(const AttnParams&, int, bool, cudaStream_t);
-template cudaError_t launch_few_rows<false, 128>(const AttnParams&, int, bool, cudaStream_t);
-template cudaError_t launch_few_rows<false, 256>(const AttnParams&, int, bool, cudaStream_t);
-template cudaError_t launch_few_rows<true, 64>(const AttnParams&, int, bool, cudaStream_t);
-template cudaError_t launch_few_rows<true, 128>(const AttnParams&, int, bool, cudaStream_t);
-template cudaError_t launch_few_rows<true, 256>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<64>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<128>(const AttnParams&, int, bool, cudaStream_t);
+template cudaError_t launch_few_rows<256>(const AttnParams&, int, bool, cudaStream_t);
 
 }  // namespace kv
 }  // namespace bsk

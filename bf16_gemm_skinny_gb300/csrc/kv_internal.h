@@ -32,6 +32,9 @@ struct KvBatch {
     int type = kCacheBF16;
     int num_seqs = 0, num_tokens = 0;
     int num_kv_heads = 0, head_dim = 0, block_size = 0, max_blocks = 0, num_blocks = 0;
+    // > 0: k and v are not the pages but copies of their positions, position t of
+    // sequence s in row s * flat_len + t (the block table still says which exist)
+    int flat_len = 0;
     int* status = nullptr;
 };
 
@@ -48,6 +51,10 @@ struct KvCopyLaunch {
 };
 int launch_kv_append(const KvCopyLaunch& a, cudaStream_t stream, char* msg, size_t msg_len);
 int launch_kv_gather(const KvCopyLaunch& a, cudaStream_t stream, char* msg, size_t msg_len);
+// The positions of an E4M3 cache that the new tokens see, as BF16 in the layout of
+// KvBatch::flat_len.
+int launch_kv_flatten(const KvBatch& b, uint16_t* k_out, uint16_t* v_out, int flat_len, int max_seq_len, int window,
+                      int sinks, bool pdl, cudaStream_t stream, char* msg, size_t msg_len);
 
 struct KvAttnLaunch {
     KvBatch b;
@@ -59,6 +66,7 @@ struct KvAttnLaunch {
     int max_seq_len = 0;
     float scale = 1.f;
     int window = 0, sinks = 0;     // window 0: every earlier position is visible
+    int kernel = 0;                // 0 automatic, 1 many rows (tcgen05), 2 few rows
     int segments = 1;              // kv_attention_segments()
     float* workspace = nullptr;    // kv_attention_workspace() bytes, or nullptr when that is 0
     int num_sms = 1;
@@ -84,13 +92,15 @@ __device__ __forceinline__ float e8m0_value(uint32_t b)
 }
 
 // Row of the cache that holds position `pos` of the sequence whose block table
-// is `table`: block * block_size + slot, or -1 (and a status code) when the
+// is `table`: block * block_size + slot (or its row in a flat copy), or -1 (and a status code) when the
 // table does not reach that far or its entry is no block.
 __device__ __forceinline__ long long kv_row(const KvBatch& b, const int32_t* table, int pos)
 {
     const int i = pos / b.block_size;
     if (i < b.max_blocks) {
         const int blk = table[i];
+        if (blk >= 0 && blk < b.num_blocks && b.flat_len > 0)
+            return (table - b.block_tables) / b.max_blocks * b.flat_len + pos;
         if (blk >= 0 && blk < b.num_blocks)
             return static_cast<long long>(blk) * b.block_size + (pos - i * b.block_size);
     }
