@@ -12,7 +12,7 @@
 // A CTA has 128 query rows (token x query head, the heads of one KV head side by
 // side, so they share the keys) and walks the keys in tiles of kTile positions:
 //   S = Q K^T   tcgen05.mma, Q from TMEM, K from shared memory, S in TMEM (two buffers)
-//   P = 2^(..)  eight warps, S from TMEM to registers and P back, 16 bits, over S
+//   P = 2^(..)  four or eight warps, S from TMEM to registers and P back, 16 bits, over S
 //   O += P V    tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // The MMAs of S for tile j+1 and of PV for tile j-1 run while the warps work on
 // tile j.  Q lies in TMEM, so that shared memory holds nothing but keys and values
@@ -133,7 +133,6 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, const W
 // Geometry
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128;        // query rows per CTA (the M of the MMAs)
-constexpr int kSoftmaxWarps = 8;  // warps 4..11
 constexpr int kConvertWarps = 4;  // warps 12..15, E4M3 only
 constexpr int kSlots = 8;         // tiles whose cache rows, masks and scales are kept
 
@@ -150,11 +149,23 @@ enum AttnSite : int {
 template <bool E4M3, int HD>
 struct Geo {
     static constexpr int kBlocks = HD / 64;                    // 64-element (128-byte) blocks of a row
-    // Positions per tile.  TMEM's 512 columns hold two S tiles, Q (HD / 2 columns)
-    // and O (HD): with HD = 256 that leaves 2 x 64.
-    static constexpr int kTile = HD == 256 ? 64 : 128;
-    static constexpr int kCols = kTile / 2;                    // S columns per softmax warp
-    static constexpr int kColQ = 2 * kTile, kColO = HD == 64 ? 320 : 512 - HD;   // TMEM columns of Q and O
+    // CTAs per SM.  A CTA alternates between waiting for its own scores and working on
+    // them; a second one fills the gaps, and one's start and end.  With HD = 64 two fit
+    // TMEM with 64-position tiles: a windowed chunk of 4097 tokens takes 82 us with two,
+    // 110 with one of 128-position tiles.  With HD = 128 a second one leaves room for one S
+    // tile only and lost (325 against 276 us for four ragged chunks).
+    static constexpr int kCtas = !E4M3 && HD == 64 ? 2 : 1;
+    // Positions per tile, S tiles in TMEM.  TMEM's columns (512, or 256 for each of two
+    // CTAs) hold the S tiles, Q (HD / 2 columns) and O (HD).
+    static constexpr int kTile = HD == 256 || kCtas == 2 ? 64 : 128;
+    static constexpr int kTmem = 512 / kCtas;
+    // Softmax warps: four have a row per lane; eight, two lanes a row.
+    static constexpr int kHalves = kCtas == 2 ? 1 : 2;
+    static constexpr int kSoftmaxWarps = 4 * kHalves;          // warps 4 ..
+    static constexpr int kCols = kTile / kHalves;              // S columns per softmax warp
+    static constexpr int kColQ = 2 * kTile;               // TMEM columns of Q and O
+    static constexpr int kColO = HD == 64 ? kColQ + 32 : kTmem - HD;
+    static_assert(kColQ + HD / 2 <= kColO && kColO + HD <= kTmem, "TMEM columns of one CTA");
     // A stage: one tile's keys or values in 16 bits, [kTile / 8][kBlocks] swizzle atoms
     // of 8 rows x 128 bytes.  Keys are read as a K-major operand (8-row groups
     // kBlocks * 1024 bytes apart), values as an MN-major one (64-dimension blocks 1024
@@ -163,12 +174,12 @@ struct Geo {
     static constexpr int kStages = E4M3 && HD != 64 ? 2 : 3;   // of keys, and of values
     static constexpr int kRawBytes = E4M3 ? kTile * HD : 0;    // a tile's codes, rows side by side
     static constexpr int kRawStages = E4M3 ? 2 : 0;
-    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kThreads = E4M3 ? 512 : 128 + 32 * kSoftmaxWarps;
     static constexpr int kBars = 4 * kStages + 4 * kRawStages + 2 * kSlots + 8;
     static constexpr int kScaleBytes = E4M3 ? kSlots * (kTile * 8 + 8) : 0;
     static constexpr int kMisc = kScaleBytes + kSlots * (kTile + 36) * 4 + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
     static constexpr int kBytes = 1024 + 2 * kStages * kStageBytes + 2 * kRawStages * kRawBytes + kMisc;
-    static_assert(kBytes <= 232448, "shared memory of one CTA");
+    static_assert(kBytes <= 232448 / kCtas - (kCtas - 1) * 1024, "shared memory of one CTA");
 };
 
 // Tensor maps of the cache.  Gathers see it as [num_blocks * block_size] rows of
@@ -199,7 +210,7 @@ __device__ __forceinline__ int box_state(const uint32_t* mask, int k, int box)
 // The kernel
 // ---------------------------------------------------------------------------
 template <bool E4M3, int HD>
-__global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
+__global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
     kv_attention_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnParams p)
 {
     using G = Geo<E4M3, HD>;
@@ -208,6 +219,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
     constexpr int NB = G::kBlocks;
     constexpr int kTile = G::kTile;
     constexpr int C = G::kCols;
+    constexpr int H = G::kHalves;
     constexpr uint32_t kIdescS = idesc_f16(!E4M3, false, false, kRows, kTile);
     constexpr uint32_t kIdescO = idesc_f16(!E4M3, false, true, kRows, HD);
 
@@ -329,12 +341,12 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(m_full0 + 8 * s, 1);
-            mbar_init(m_empty0 + 8 * s, kSoftmaxWarps + 1);
+            mbar_init(m_empty0 + 8 * s, G::kSoftmaxWarps + 1);
         }
-        mbar_init(q_full, kSoftmaxWarps);
+        mbar_init(q_full, G::kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full0 + 8 * i, 1);
-            mbar_init(p_full0 + 8 * i, kSoftmaxWarps);
+            mbar_init(p_full0 + 8 * i, G::kSoftmaxWarps);
             mbar_init(o_done0 + 8 * i, 1);
         }
         mbar_init(drain, 1);
@@ -342,7 +354,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_alloc(smem_u32(tmem_slot), G::kTmem);
         tmem_relinquish_alloc_permit();
     }
     if (warp >= 4 && warp < 8) s_flag[threadIdx.x - 128] = 0;
@@ -697,7 +709,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         // stay matched, the waits return at once and the output is undefined.
         // ------------------------------------------------------------------
         const int quarter = warp & 3;
-        const int half = (warp - 4) >> 2;
+        const int half = H == 2 ? (warp - 4) >> 2 : 0;
         const int r = quarter * 32 + lane;
         const bool idle = quarter * 32 >= rows;   // the whole warp
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -709,10 +721,11 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         if (!idle) {
             // this half of Q's row: 16-bit pairs, one per TMEM column
             const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + static_cast<long long>(head) * HD +
-                                                              half * (HD / 2));
-            uint32_t w[HD / 4];
+                                                              half * (HD / H));
+            constexpr int QW = HD / 2 / H;   // pairs
+            uint32_t w[QW];
 #pragma unroll
-            for (int c = 0; c < HD / 16; ++c) {
+            for (int c = 0; c < QW / 4; ++c) {
                 const uint4 x = src[c];
                 w[4 * c] = x.x ^ p.q_sign;
                 w[4 * c + 1] = x.y ^ p.q_sign;
@@ -724,7 +737,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                 // value to [2^14, 2^15).  What FP16 then drops is under 2^-39 of the largest.
                 uint32_t m = 0;
 #pragma unroll
-                for (int c = 0; c < HD / 4; ++c) m = __vmaxu2(m, w[c] & 0x7fff7fffu);
+                for (int c = 0; c < QW; ++c) m = __vmaxu2(m, w[c] & 0x7fff7fffu);
                 m = max(m & 0xffffu, m >> 16);
                 uint32_t* sm = reinterpret_cast<uint32_t*>(s_max);
                 sm[half * kRows + r] = m;
@@ -735,14 +748,14 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                 const float f = exp2f(static_cast<float>(-e));
                 row_scale *= exp2f(static_cast<float>(e));
 #pragma unroll
-                for (int c = 0; c < HD / 4; ++c)
+                for (int c = 0; c < QW; ++c)
                     w[c] = f16x2(__uint_as_float(w[c] << 16) * f, __uint_as_float(w[c] & 0xffff0000u) * f);
                 named_barrier(1 + quarter, 64);   // s_max is free again
             }
-            const uint32_t q_addr = lane_addr + G::kColQ + half * (HD / 4);
-            if constexpr (HD >= 128) {
+            const uint32_t q_addr = lane_addr + G::kColQ + half * QW;
+            if constexpr (QW >= 32) {
 #pragma unroll
-                for (int c = 0; c < HD / 128; ++c) {
+                for (int c = 0; c < QW / 32; ++c) {
                     uint32_t t[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) t[i] = w[32 * c + i];
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             wait_long(s_full0 + 8 * buf, (j >> 1) & 1, wc, kSiteKvScores);
             tc_fence_after_sync();
             if (!idle) {
-                const uint32_t s_addr = lane_addr + buf * kTile + half * C;
+                const uint32_t s_addr = lane_addr + (j & 1) * kTile + half * C;
                 float2 x[C / 2];
                 {
                     uint32_t raw[C / 32][32];
@@ -831,11 +844,14 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < C / 2; ++c) mx[c & 3] = max3(mx[c & 3], x[c].x, x[c].y);
                 float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                // the row's other half; also: both warps have read S, P may go over it
-                float* sm = s_max + buf * 2 * kRows;
-                sm[half * kRows + r] = top;
-                named_barrier(1 + quarter, 64);
-                top = fmaxf(top, sm[(half ^ 1) * kRows + r]) * row_scale;
+                if constexpr (H == 2) {
+                    // the row's other half; also: both warps have read S, P may go over it
+                    float* sm = s_max + buf * 2 * kRows;
+                    sm[half * kRows + r] = top;
+                    named_barrier(1 + quarter, 64);
+                    top = fmaxf(top, sm[(half ^ 1) * kRows + r]);
+                }
+                top *= row_scale;
                 const float mn = fmaxf(m, top);
                 if (j == 0) {
                     m = mn;
@@ -850,8 +866,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                     tc_fence_after_sync();
                     // this half of the row's O, 16 columns at a time (beside x in registers)
 #pragma unroll 1
-                    for (int c = 0; c < HD / 32; ++c) {
-                        const uint32_t o_addr = lane_addr + G::kColO + half * (HD / 2) + c * 16;
+                    for (int c = 0; c < HD / H / 16; ++c) {
+                        const uint32_t o_addr = lane_addr + G::kColO + half * (HD / H) + c * 16;
                         uint32_t o[16];
                         tmem_ld_32x32b_x16(o_addr, o);
                         tmem_ld_wait();
@@ -863,7 +879,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
                 float base = m == -INFINITY ? 0.f : m;
                 if constexpr (E4M3) base -= static_cast<float>(3 - E);
                 const float2 sc = make_float2(row_scale, row_scale), nb = make_float2(-base, -base);
-                const uint32_t p_addr = lane_addr + buf * kTile + half * (C / 2);
+                const uint32_t p_addr = lane_addr + (j & 1) * kTile + half * (C / 2);
 #pragma unroll
                 for (int g = 0; g < C / 32; ++g) {   // 32 columns, 16 of P, at a time
                     uint32_t w[16];
@@ -904,17 +920,19 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
         tc_fence_after_sync();
         if (!idle) {
             float l = l2.x + l2.y;
-            float* sm = s_max + (nt & 1) * 2 * kRows;
-            sm[half * kRows + r] = l;
-            named_barrier(1 + quarter, 64);
-            l = sm[r] + sm[kRows + r];   // the same order for both halves
+            if constexpr (H == 2) {
+                float* sm = s_max + (nt & 1) * 2 * kRows;
+                sm[half * kRows + r] = l;
+                named_barrier(1 + quarter, 64);
+                l = sm[r] + sm[kRows + r];   // the same order for both halves
+            }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long at = (static_cast<long long>(token) * p.num_q_heads + head) * p.segments + seg;
             // a split row's partial sums leave out E4M3's 2^(3 - E)
             const float plain = E4M3 ? exp2f(static_cast<float>(E - 3)) : 1.f;
             float odd = 0.f;   // NaN once a value is not finite
-            for (int c = 0; c < HD / 64; ++c) {
-                const int d0 = half * (HD / 2) + c * 32;
+            for (int c = 0; c < HD / H / 32; ++c) {
+                const int d0 = half * (HD / H) + c * 32;
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(lane_addr + G::kColO + d0, o);
                 tmem_ld_wait();
@@ -943,8 +961,11 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
             }
             if (p.segments > 1 && half == 0 && r < rows) p.part_ml[at] = make_float2(m, l * plain);
             if (((odd != 0.f && l - l == 0.f) || wide) && r < rows) s_flag[r] = 1;   // odd is NaN, l is finite
-            named_barrier(1 + quarter, 64);
-            for (int i = half; i < 32; i += 2) {
+            if constexpr (H == 2)
+                named_barrier(1 + quarter, 64);
+            else
+                __syncwarp();
+            for (int i = half; i < 32; i += H) {
                 const int rr = quarter * 32 + i;
                 if (rr < rows && s_flag[rr]) {
                     const int row = row0 + rr;
@@ -958,7 +979,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, 1)
     __syncthreads();
     if (warp == kWarpMma) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, G::kTmem);
     }
 }
 
@@ -1172,43 +1193,6 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
 
 }  // namespace
 
-int kv_attention_segments(const KvAttnLaunch& a)
-{
-    const int few = few_rows(a);
-    const int cta_rows = few ? few : kRows;
-    const int tile = few ? 64 : (a.b.head_dim == 256 ? 64 : 128);
-    const long long group = a.num_q_heads / a.b.num_kv_heads;
-    const long long per_seq = (static_cast<long long>(a.max_chunk) * group + cta_rows - 1) / cta_rows;
-    long long row_tiles = (static_cast<long long>(a.b.num_tokens) * group + cta_rows - 1) / cta_rows + a.b.num_seqs - 1;
-    if (row_tiles > per_seq * a.b.num_seqs) row_tiles = per_seq * a.b.num_seqs;
-    const long long ctas = row_tiles * a.b.num_kv_heads;
-    const long long tiles = (most_keys(a) + tile - 1) / tile;
-    const double rows = static_cast<double>(a.b.num_tokens) * a.num_q_heads;
-    // Time in units of one tile's work on one CTA: a CTA starts and ends in about
-    // `fixed`, a join costs about as much and the traffic of the partial rows.
-    const double fixed = few ? 4 : (tile == 64 ? 6 : 3);
-    const long long slots = few ? 2LL * a.num_sms : a.num_sms;
-    double best = 0;
-    int segments = 1;
-    for (int s = 1; s <= 256 && (s == 1 || s <= tiles); ++s) {
-        const double each = static_cast<double>((tiles + s - 1) / s);
-        double t;
-        if (a.b.num_seqs == 1) {
-            // equal CTAs: whole waves
-            t = static_cast<double>((ctas * s + slots - 1) / slots) * (fixed + each);
-        } else {
-            // lengths anywhere up to the longest: the average work, and the last CTA's
-            t = static_cast<double>(ctas) * (0.6 * static_cast<double>(tiles) + s * fixed) / static_cast<double>(slots) + each;
-        }
-        if (s > 1) t += fixed + rows * s * a.b.head_dim * 8 / 3.5e6;
-        if (s == 1 || t < best) {
-            best = t;
-            segments = s;
-        }
-    }
-    return segments;
-}
-
 namespace {
 
 size_t partial_bytes(const KvAttnLaunch& a)
@@ -1233,6 +1217,44 @@ int flat_rows(const KvAttnLaunch& a)
 }
 
 }  // namespace
+
+int kv_attention_segments(const KvAttnLaunch& a)
+{
+    const int few = few_rows(a);
+    const int cta_rows = few ? few : kRows;
+    const bool two = a.b.head_dim == 64 && (a.b.type == kCacheBF16 || flat_rows(a) > 0);   // CTAs per SM
+    const int tile = few || two || a.b.head_dim == 256 ? 64 : 128;
+    const long long group = a.num_q_heads / a.b.num_kv_heads;
+    const long long per_seq = (static_cast<long long>(a.max_chunk) * group + cta_rows - 1) / cta_rows;
+    long long row_tiles = (static_cast<long long>(a.b.num_tokens) * group + cta_rows - 1) / cta_rows + a.b.num_seqs - 1;
+    if (row_tiles > per_seq * a.b.num_seqs) row_tiles = per_seq * a.b.num_seqs;
+    const long long ctas = row_tiles * a.b.num_kv_heads;
+    const long long tiles = (most_keys(a) + tile - 1) / tile;
+    const double rows = static_cast<double>(a.b.num_tokens) * a.num_q_heads;
+    // Time in units of one tile's work on one CTA: a CTA starts and ends in about
+    // `fixed`, a join costs about as much and the traffic of the partial rows.
+    const double fixed = few ? 4 : (tile == 64 ? 6 : 3);
+    const long long slots = few || two ? 2LL * a.num_sms : a.num_sms;
+    double best = 0;
+    int segments = 1;
+    for (int s = 1; s <= 256 && (s == 1 || s <= tiles); ++s) {
+        const double each = static_cast<double>((tiles + s - 1) / s);
+        double t;
+        if (a.b.num_seqs == 1 || a.window > 0) {
+            // equal CTAs: whole waves
+            t = static_cast<double>((ctas * s + slots - 1) / slots) * (fixed + each);
+        } else {
+            // lengths anywhere up to the longest: the average work, and the last CTA's
+            t = static_cast<double>(ctas) * (0.6 * static_cast<double>(tiles) + s * fixed) / static_cast<double>(slots) + each;
+        }
+        if (s > 1) t += fixed + rows * s * a.b.head_dim * 8 / 3.5e6;
+        if (s == 1 || t < best) {
+            best = t;
+            segments = s;
+        }
+    }
+    return segments;
+}
 
 size_t kv_attention_workspace(const KvAttnLaunch& a)
 {
