@@ -575,12 +575,14 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         };
         auto fetch = [&](int i) {           // the tile looked up last
             if (i >= keys.end) return;
+            const int base = keys.base(i);
+            const bool inside = keys.all(base, kTile);   // the usual case: all positions in sight
             have = 0;
             bool bad = false;
 #pragma unroll
             for (int u = 0; u < PL; ++u) {
-                const int t = keys.base(i) + u * 32 + lane;
-                const bool h = keys.holds(t);
+                const int t = base + u * 32 + lane;
+                const bool h = inside || keys.holds(t);
                 const bool g = static_cast<unsigned>(entry[u]) < static_cast<unsigned>(p.b.num_blocks);
                 bad = bad || (h && !g);
                 row[u] = h && g ? (flat >= 0 ? flat + t : entry[u] * bs + entry_off[u]) : none;
@@ -596,6 +598,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
             }
             if (bad) *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
         };
+        const int box_shift = 31 - __clz(p.box);
         look_up(keys.begin);
         fetch(keys.begin);
         look_up(keys.begin + 1);
@@ -604,42 +607,44 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
             const int slot = j % kSlots;
             ok = __all_sync(0xffffffffu, wait_long(m_empty0 + 8 * slot, ((j / kSlots) & 1) ^ 1, wc, kSiteKvMeta));
             if (!ok) break;
-            int top = 0, low = 255;   // E4M3: the range of V's exponents, all-zero rows (the least scale) left out
+            const bool full = __all_sync(0xffffffffu, have == (1u << PL) - 1u);
+            const int row0 = __shfl_sync(0xffffffffu, row[0], 0);
+            bool run = full && p.tile_rows > 0 && row0 + kTile <= p.tile_rows && (E4M3 || HD == 64 || (row0 & 7) == 0);
 #pragma unroll
-            for (int u = 0; u < PL; ++u) {
-                const bool h = ((have >> u) & 1u) != 0;
-                s_row[slot * kTile + u * 32 + lane] = row[u];
-                const uint32_t word = __ballot_sync(0xffffffffu, h);
-                if (lane == 0) s_mask[slot * 4 + u] = word;
-                if constexpr (E4M3) {
+            for (int u = 0; u < PL; ++u) run = run && row[u] == row0 + u * 32 + lane;
+            run = __all_sync(0xffffffffu, run);
+            int kind = kLoadTile;
+            if (run) {
+                if (lane < PL) s_mask[slot * 4 + lane] = 0xffffffffu;
+                if (lane == 0) s_box[slot * 32] = row0;
+            } else {
+#pragma unroll
+                for (int u = 0; u < PL; ++u) {
+                    const uint32_t word = __ballot_sync(0xffffffffu, (have >> u) & 1u);
+                    if (lane == 0) s_mask[slot * 4 + u] = word;
+                    const int k = u * 32 + lane;
+                    s_row[slot * kTile + k] = row[u];
+                    if ((k & (p.box - 1)) == 0) s_box[slot * 32 + (k >> box_shift)] = row[u];
+                }
+                __syncwarp();
+                const bool mixed = !full && lane * p.box < kTile && box_state(s_mask + slot * 4, lane * p.box, p.box) == 2;
+                kind = p.box >= 8 && !__any_sync(0xffffffffu, mixed) ? kLoadBoxes : kLoadRows;
+            }
+            if (lane == 0) s_kind[slot * 4] = kind;
+            if constexpr (E4M3) {
+                int top = 0, low = 255;   // the range of V's exponents, all-zero rows (the least scale) left out
+#pragma unroll
+                for (int u = 0; u < PL; ++u) {
                     s_kf[slot * kTile + u * 32 + lane] = e8m0_value(kb[u]);
                     s_vf[slot * kTile + u * 32 + lane] = e8m0_value(vb[u]);
-                    if (h && vb[u] > 10u && vb[u] != 255u) {
+                    if (((have >> u) & 1u) != 0 && vb[u] > 10u && vb[u] != 255u) {
                         top = max(top, static_cast<int>(vb[u]));
                         low = min(low, static_cast<int>(vb[u]));
                     }
                 }
-            }
-            if constexpr (E4M3) {
                 top = __reduce_max_sync(0xffffffffu, top);
                 low = __reduce_min_sync(0xffffffffu, low);
                 if (lane == 0) s_exp[slot] = make_int2(top, low);
-            }
-            __syncwarp();
-            {
-                // lane's box (pages of an odd size: four positions, gathers only unless the tile is one box)
-                const int k = lane * p.box;
-                const bool in = k < kTile;
-                const int state = in ? box_state(s_mask + slot * 4, k, p.box) : 0;
-                const int first_row = s_row[slot * kTile + (in ? k : 0)];
-                const int row0 = __shfl_sync(0xffffffffu, first_row, 0);
-                const bool run = !in || (state == 1 && first_row == row0 + k &&
-                                         (p.box >= 8 || s_row[slot * kTile + k + 3] == first_row + 3));
-                const bool tiled = __all_sync(0xffffffffu, run) && p.tile_rows > 0 && row0 + kTile <= p.tile_rows &&
-                                   (E4M3 || HD == 64 || (row0 & 7) == 0);
-                const bool boxed = p.box >= 8 && __all_sync(0xffffffffu, state != 2);
-                if (in) s_box[slot * 32 + lane] = first_row;
-                if (lane == 0) s_kind[slot * 4] = tiled ? kLoadTile : (boxed ? kLoadBoxes : kLoadRows);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(m_full0 + 8 * slot);
