@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
     const int kvh = idx % p.b.num_kv_heads;
     idx /= p.b.num_kv_heads;
     const int seq = idx % p.b.num_seqs;
-    const int seg = idx / p.b.num_seqs;
+    const int seg = p.segments - 1 - idx / p.b.num_seqs;   // what only long sequences have, first
     int first = seq, n = 1;
     if (p.b.cu_tokens != nullptr) {
         first = p.b.cu_tokens[seq];

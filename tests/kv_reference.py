@@ -163,3 +163,29 @@ class Problem:
 
     def shape(self):
         return self.heads, self.dim, self.page, self.max_blocks, self.num_blocks
+
+
+def attention_on_gpu(q, k, v, tables, cu, lens, heads, page, scale, window=0, sinks=0):
+    """attention() for long sequences: the same definition in 64 bits, by whole sequences on the GPU.
+    Every page is good and every query position exists."""
+    T, hq, D = q.shape
+    out = torch.zeros(T, hq, D, dtype=torch.float64, device="cuda")
+    spread, reach = torch.zeros_like(out), torch.zeros(T, hq, dtype=torch.float64, device="cuda")
+    q, k, v = q.cuda().double(), k.cuda().reshape(-1, heads, D), v.cuda().reshape(-1, heads, D)
+    for s, n in enumerate(lens):
+        a, b = cu[s], cu[s + 1]
+        if a == b:
+            continue
+        at = torch.tensor([tables[s][t // page] * page + t % page for t in range(n)], device="cuda")
+        t = torch.arange(n, device="cuda")
+        p = torch.arange(n - (b - a), n, device="cuda")[:, None]
+        seen = t <= p
+        if window:
+            seen &= (t > p - window) | (t < sinks)
+        for h in range(hq):
+            kk, vv = k[at, h // (hq // heads)], v[at, h // (hq // heads)]
+            x = (q[a:b, h] @ kk.T * scale).masked_fill(~seen, -math.inf)
+            w = torch.softmax(x, -1)
+            out[a:b, h], spread[a:b, h] = w @ vv, w @ vv.abs()
+            reach[a:b, h] = (q[a:b, h].abs() @ kk.abs().T).masked_fill(~seen, 0).amax(-1)
+    return out.cpu(), spread.cpu(), reach.cpu()

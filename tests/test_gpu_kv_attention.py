@@ -236,3 +236,152 @@ def test_append_then_attend(e4m3):
         if d[n] is not None:
             setattr(p, n, d[n].cpu())
     check(p, got)
+
+
+# ---------------------------------------------------------------------------
+# Each kernel by itself: the automatic choice goes by the cache's type and the
+# number of query rows, these tests make it.
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def kernel():
+    """Sets the kernel: 1 many rows (an E4M3 cache converted tile by tile), 2 few rows."""
+    yield lambda k: bsk.set_option("kv_kernel", k)
+    bsk.set_option("kv_kernel", 0)
+
+
+@pytest.mark.parametrize("which", [1, 2])
+@pytest.mark.parametrize("lens,new,heads,group,dim,page", CHUNKS)
+def test_kernels_on_a_quantised_cache(kernel, which, lens, new, heads, group, dim, page):
+    p = ref.Problem(31, lens, new, heads, group, dim, page, True)
+    kernel(which)
+    check(p, run(p))
+    check(p, run(p, 40, 3), 40, 3)
+    check(p, run(p, segments=3))
+
+
+@pytest.mark.parametrize("heads,group,dim,page,lens,new,window,sinks", [
+    (2, 4, 256, 784, [3000], [130], 0, 0),
+    (2, 2, 128, 16, [1500, 700, 2049], [128, 5, 300], 0, 0),
+    (1, 8, 64, 31, [1800], [257], 0, 0),
+    (2, 4, 128, 64, [2500, 300], [200, 300], 500, 7),
+    (1, 4, 256, 16, [2000], [512], 0, 0),
+    (1, 8, 64, 128, [4097], [600], 1024, 130),
+])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_long_chunks(heads, group, dim, page, lens, new, window, sinks, e4m3):
+    """Enough rows for the flat copy of a quantised cache, many tiles, pages that end inside tiles."""
+    p = ref.Problem(32, lens, new, heads, group, dim, page, e4m3)
+    k, v = p.values()
+    scale = 1 / math.sqrt(dim)
+    out, spread, reach = ref.attention_on_gpu(p.q, k, v, p.tables, p.cu, p.lens, heads, page, scale, window, sinks)
+    bound = ref.attention_bound(out, spread, reach, scale, dim, max(lens))
+    for segments in (0, 1, 4):
+        got = run(p, window, sinks, segments=segments)
+        bad = ~((got.double() - out).abs() <= bound)
+        assert not bad.any(), (segments, int(bad.sum()), bad.nonzero()[0].tolist())
+
+
+@pytest.mark.parametrize("heads,group,dim,page,lens", [
+    (4, 4, 256, 784, [9000]), (2, 8, 128, 16, [5000, 17, 3001]), (1, 8, 64, 7, [6000, 6001])])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_long_decode(heads, group, dim, page, lens, e4m3):
+    p = ref.Problem(33, lens, [1] * len(lens), heads, group, dim, page, e4m3)
+    k, v = p.values()
+    scale = 1 / math.sqrt(dim)
+    for window, sinks in ((0, 0), (1000, 4)):
+        out, spread, reach = ref.attention_on_gpu(p.q, k, v, p.tables, p.cu, p.lens, heads, page, scale, window, sinks)
+        bound = ref.attention_bound(out, spread, reach, scale, dim, max(lens))
+        got = run(p, window, sinks, decode=True)
+        assert ((got.double() - out).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("new", [4, 130])
+def test_value_scales_far_apart(kernel, which, new):
+    """Rows of V from 2^-60 to 2^60 in one sequence, some of them zero: each token's output to its own precision."""
+    p = ref.Problem(34, [260], [new], 1, 2, 128, 16, True)
+    g = torch.Generator().manual_seed(3)
+    for t in range(260):
+        b, o = p.tables[0][t // 16], t % 16
+        x = torch.randn(1, 128, generator=g).bfloat16()
+        x = x * (0.0 if t % 7 == 3 else 2.0 ** (60 - t * 120 // 259))
+        p.v[b, o], p.vs[b, o] = ref.quantise(x)
+    kernel(which)
+    check(p, run(p))
+    check(p, run(p, 3, 0), 3, 0)       # a window of rows of much the same size
+    check(p, run(p, segments=2))
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_all_zero_and_tiny_values(kernel, which):
+    p = ref.Problem(35, [200], [3], 1, 2, 64, 16, True)
+    zero = torch.zeros(1, 64).bfloat16()
+    for t in range(200):
+        p.v[p.tables[0][t // 16], t % 16], p.vs[p.tables[0][t // 16], t % 16] = ref.quantise(zero)
+    kernel(which)
+    assert not run(p).any()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("big", [2.0 ** 40, 2.0 ** -100])
+def test_queries_of_any_size(e4m3, big):
+    """Queries far from 1 with a scale that brings the scores back: FP16 beside E4M3 keys loses nothing."""
+    p = ref.Problem(36, [150], [2], 1, 4, 64, 16, e4m3)
+    p.fused[:, :256] = (p.fused[:, :256].float() * big).bfloat16()
+    p.q = p.fused[:2, :256].reshape(2, 4, 64)
+    check(p, run(p, scale=0.125 / big), scale=0.125 / big)
+
+
+@pytest.mark.parametrize("new", [100, 300])
+def test_nans_in_a_quantised_cache_stay_with_the_tokens_that_see_them(new):
+    """As above, with few and with many rows (the flat copy)."""
+    p = ref.Problem(37, [400], [new], 1, 4, 128, 16, True)
+    for t in (390, 250):
+        p.v[p.tables[0][t // 16], t % 16], p.vs[p.tables[0][t // 16], t % 16] = 0x7F, 255
+    got = run(p, 40, 0)
+    first = 400 - new
+    seen = [any(q - 40 < t <= q for t in (390, 250)) for q in range(first, 400)]
+    nan = torch.isnan(got).all(-1).all(-1)
+    assert nan.tolist() == seen and torch.isfinite(got[~nan]).all()
+    clean = ref.Problem(37, [400], [new], 1, 4, 128, 16, True)
+    want = run(clean, 40, 0)[~nan].double()
+    assert (got[~nan].double() - want).abs().max() <= 2.0 ** -6 * want.abs().max()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_bad_pages_under_many_rows(e4m3):
+    p = ref.Problem(38, [600], [300], 1, 2, 64, 16, e4m3)
+    p.tables[0][5], p.tables[0][30] = -1, p.num_blocks + 3
+    d = p.device()
+    with pytest.raises(bsk.BskError):
+        run(p, d=d)
+    out = torch.full((300, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    bsk.chunk_attention_enqueue(int(e4m3), d["k"], d["v"], d["ks"], d["vs"], d["fused"], p.stride, out, 128, d["cu"],
+                                d["tables"], d["lens"], 1, 300, 300, 2, *p.shape(), 600, 0.125)
+    with pytest.raises(bsk.BskError):
+        bsk.stream_check()
+    check(p, out.reshape(300, 2, 64).cpu(), num_blocks=p.num_blocks)
+
+
+def test_attention_past_32_bits():
+    """A cache of over 2^31 rows' bytes: the pages at its end are read where they are."""
+    heads, dim, page = 8, 256, 1024
+    for kind in (bsk.CACHE_BF16, bsk.CACHE_E4M3):
+        blocks = 2 ** 32 // (heads * dim * page) + 2
+        dt = torch.bfloat16 if kind == bsk.CACHE_BF16 else torch.uint8
+        k = torch.zeros(blocks, page, heads, dim, dtype=dt, device="cuda")
+        v = torch.zeros(blocks, page, heads, dim, dtype=dt, device="cuda")
+        s = [None, None] if dt == torch.bfloat16 else [torch.full((blocks, page, heads), 127, dtype=torch.uint8, device="cuda")
+                                                       for _ in range(2)]
+        one = 1.0 if dt == torch.bfloat16 else 0x38        # E4M3 1.0
+        v[-1, :, 5] = one
+        tables = torch.tensor([[blocks - 1]], dtype=torch.int32, device="cuda")
+        lens = torch.tensor([page], dtype=torch.int32, device="cuda")
+        for new in (1, 300):
+            cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+            q = torch.randn(new, heads * dim, device="cuda").bfloat16()
+            out = torch.full((new, heads * dim), math.nan, dtype=torch.bfloat16, device="cuda")
+            bsk.chunk_attention(kind, k, v, *s, q, heads * dim, out, heads * dim, cu, tables, lens, 1, new, new, heads,
+                                heads, dim, page, 1, blocks, page, 1 / 16)
+            o = out.reshape(new, heads, dim)
+            assert (o[:, 5] == 1).all() and not o[:, :5].any() and not o[:, 6:].any()
