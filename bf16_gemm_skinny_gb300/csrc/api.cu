@@ -1113,6 +1113,8 @@ int api_prepare(int* sms, int** status)
 
 int api_sync_and_check(cudaStream_t s) { return sync_and_check(s); }
 
+int api_pool(cudaMemPool_t* pool) { return host_pool(pool); }
+
 void record_error(const char* msg)
 {
     snprintf(t_err, sizeof(t_err), "%s", msg);

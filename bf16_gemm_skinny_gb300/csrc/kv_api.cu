@@ -25,7 +25,10 @@ int fail(int status, const char* fmt, ...)
     return status;
 }
 
-// Stream-ordered workspace, freed in stream order after use.
+// Stream-ordered workspace, freed in stream order after use.  From the library's
+// pool: the default one gives its memory back at every synchronisation, and a
+// blocking call would map it anew each time (some 200 us).  A capturing stream
+// takes the default pool, whose allocations become nodes of the graph.
 struct Workspace {
     void* ptr = nullptr;
     cudaStream_t s;
@@ -38,7 +41,15 @@ struct Workspace {
     }
     cudaError_t take(size_t bytes)
     {
-        const cudaError_t e = cudaMallocAsync(&ptr, bytes, s);
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(s, &capture);
+        cudaMemPool_t pool = nullptr;
+        if (e == cudaSuccess) {
+            if (capture != cudaStreamCaptureStatusNone || bsk::api_pool(&pool) != BSK_OK)
+                e = cudaMallocAsync(&ptr, bytes, s);
+            else
+                e = cudaMallocFromPoolAsync(&ptr, bytes, pool, s);
+        }
         if (e != cudaSuccess) {
             cudaGetLastError();
             ptr = nullptr;

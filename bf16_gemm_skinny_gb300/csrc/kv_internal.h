@@ -82,6 +82,9 @@ int launch_kv_attention(const KvAttnLaunch& a, cudaStream_t stream, char* msg, s
 // the SM count and the device status word), the status of a finished stream.
 int api_prepare(int* sms, int** status);
 int api_sync_and_check(cudaStream_t s);
+// The library's own memory pool of the current device, which keeps its memory
+// mapped when a stream is synchronised (up to 2 GiB).
+int api_pool(cudaMemPool_t* pool);
 
 #ifdef __CUDACC__
 
