@@ -151,7 +151,7 @@ struct Geo {
     static constexpr int kBlocks = HD / 64;                    // 64-element (128-byte) blocks of a row
     // CTAs per SM.  A CTA alternates between waiting for its own scores and working on
     // them; a second one fills the gaps, and one's start and end.  With HD = 64 two fit
-    // TMEM with 64-position tiles: a windowed chunk of 4097 tokens takes 82 us with two,
+    // TMEM with 64-position tiles: a windowed chunk of 4097 tokens takes 76 us with two,
     // 110 with one of 128-position tiles.  With HD = 128 a second one leaves room for one S
     // tile only and lost (325 against 276 us for four ragged chunks).
     static constexpr int kCtas = !E4M3 && HD == 64 ? 2 : 1;
@@ -1091,15 +1091,16 @@ long long most_keys(const KvAttnLaunch& a)
 // Rows per CTA of the kernel for few query rows per KV head, or 0: the call takes
 // the other kernel.  An E4M3 cache read for few rows would spend its time in the
 // other kernel's shared memory.  Measured in microseconds, many-row / few-row kernel
-// (32 sequences of up to 4000 tokens): head_dim 256, 8 rows 105 / 87, 32 rows 106 / 143;
-// 128, 8 rows 139 / 75, 32 rows 136 / 143; 64, 8 rows 71 / 44, 32 rows 73 / 72.  On a
-// BF16 cache it does not pay: 8 rows of 256 83 / 130, of 128 91 / 117, of 64 46 / 45.
+// (32 sequences of up to 4000 tokens; one of 30000): head_dim 256, 8 rows 111 / 79, 35 / 29,
+// 16 rows 118 / 125, 35 / 42; 128, 32 rows 163 / 137, 50 / 44, 64 rows 151 / 241; 64, 32 rows
+// 72 / 67, 25 / 25, 64 rows 73 / 115.  On a BF16 cache it did not pay: 8 rows of 256 83 / 130,
+// of 128 91 / 117, of 64 46 / 45.
 int few_rows(const KvAttnLaunch& a)
 {
     const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
     const int few = rows <= 8 || a.b.head_dim == 256 ? 8 : 16;
     if (a.b.type != kCacheE4M3 || a.kernel == 1) return 0;
-    return a.kernel == 2 || rows * a.b.head_dim <= 2048 ? few : 0;
+    return a.kernel == 2 || rows <= (a.b.head_dim == 256 ? 8 : 32) ? few : 0;
 }
 
 template <bool E4M3, int HD>
@@ -1218,7 +1219,7 @@ int flat_rows(const KvAttnLaunch& a)
     if (a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < 2 * (a.b.head_dim > 128 ? 256 : 128)) return 0;
     const long long len = (a.max_seq_len + 127LL) / 128 * 128;
     const long long bytes = len * a.b.num_seqs * a.b.num_kv_heads * a.b.head_dim * 4;
-    return len * a.b.num_seqs <= 0x7fffffffLL && bytes <= (2LL << 30) ? static_cast<int>(len) : 0;
+    return a.b.num_seqs <= 65535 && len * a.b.num_seqs <= 0x7fffffffLL && bytes <= (2LL << 30) ? static_cast<int>(len) : 0;
 }
 
 }  // namespace
@@ -1238,19 +1239,24 @@ int kv_attention_segments(const KvAttnLaunch& a)
     const double rows = static_cast<double>(a.b.num_tokens) * a.num_q_heads;
     // Time in units of one tile's work on one CTA: a CTA starts and ends in about
     // `fixed`, a join costs about as much and the traffic of the partial rows.
-    const double fixed = few ? 4 : (tile == 64 ? 6 : 3);
+    const double fixed = few ? 4 : (tile == 64 ? 8 : 3);
     const long long slots = few || two ? 2LL * a.num_sms : a.num_sms;
     double best = 0;
     int segments = 1;
     for (int s = 1; s <= 256 && (s == 1 || s <= tiles); ++s) {
         const double each = static_cast<double>((tiles + s - 1) / s);
         double t;
+        const double full = static_cast<double>((ctas * s + slots - 1) / slots) * (fixed + each);   // whole waves
         if (a.b.num_seqs == 1 || a.window > 0) {
-            // equal CTAs: whole waves
-            t = static_cast<double>((ctas * s + slots - 1) / slots) * (fixed + each);
+            t = full;   // equal CTAs
         } else {
-            // lengths anywhere up to the longest: the average work, and the last CTA's
-            t = static_cast<double>(ctas) * (0.6 * static_cast<double>(tiles) + s * fixed) / static_cast<double>(slots) + each;
+            // Lengths anywhere up to the longest: 0.6 of it on average.  Fewer CTAs than
+            // slots end together; else it is the average work, and the last CTA's.  The
+            // kernel for many rows has few CTAs, so that one wave more or less counts:
+            // there, against the chance that all are as long as the longest.
+            const double n = s > 1 ? static_cast<double>(ctas) * (0.6 * s + 0.5) : static_cast<double>(ctas);
+            const double spread = (static_cast<double>(ctas) * 0.6 * static_cast<double>(tiles) + n * fixed) / static_cast<double>(slots) + each;
+            t = few ? spread : 0.6 * (n <= static_cast<double>(slots) ? fixed + each : spread) + 0.4 * full;
         }
         if (s > 1) t += fixed + rows * s * a.b.head_dim * 8 / 3.5e6;
         if (s == 1 || t < best) {
