@@ -1,4 +1,5 @@
-"""ctypes binding of libbsk (argument marshalling only).
+"""Binding of libbsk (argument marshalling only), by ctypes; the calls on the
+paged cache, of which a decode step makes several per layer, by a small extension.
 
 Each function takes CUDA tensors (any 16-bit dtype; only ``data_ptr()`` is
 used) or raw device addresses as ints, plus an optional stream (a
@@ -10,6 +11,8 @@ been built, the call raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -110,20 +113,6 @@ def load():
             getattr(lib, name).restype = i
         for name in ("decode_attention_bf16", "bsk_decode_attention_bf16_enqueue"):
             getattr(lib, name).argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, i, i, ctypes.c_float, i, p]
-            getattr(lib, name).restype = i
-        for name in ("kv_cache_append", "bsk_kv_cache_append_enqueue"):
-            getattr(lib, name).argtypes = [i, p, p, p, p, p, i, p, i, p, p, p, i, i, i, i, i, i, i, p]
-            getattr(lib, name).restype = i
-        for name in ("kv_cache_gather", "bsk_kv_cache_gather_enqueue"):
-            getattr(lib, name).argtypes = [i, p, p, p, p, p, p, p, p, p, i, i, i, i, i, i, i, p]
-            getattr(lib, name).restype = i
-        for name in ("chunk_attention", "bsk_chunk_attention_enqueue"):
-            getattr(lib, name).argtypes = [i, p, p, p, p, p, i, p, i, p, p, p, i, i, i, i, i, i, i, i, i, i,
-                                           ctypes.c_float, i, i, i, p]
-            getattr(lib, name).restype = i
-        for name in ("decode_attention", "bsk_decode_attention_enqueue"):
-            getattr(lib, name).argtypes = [i, p, p, p, p, p, i, p, i, p, p, i, i, i, i, i, i, i, i,
-                                           ctypes.c_float, i, i, i, p]
             getattr(lib, name).restype = i
         lib.bsk_stream_check.argtypes = [p]
         lib.bsk_stream_check.restype = i
@@ -285,15 +274,34 @@ def decode_attention_bf16_enqueue(q, k_cache, v_cache, block_tables, seq_lens, o
         num_segments, _stream(stream)))
 
 
+_calls = None
+
+
+def _load_calls():
+    """The extension module with the calls on the paged cache (raises if it is not built)."""
+    global _calls
+    load()
+    path = _build.CALLS_PATH
+    if not os.path.exists(path):
+        raise RuntimeError(f"_calls.so not built ({path}); run bf16_gemm_skinny_gb300.build.build()")
+    with _lock:
+        if _calls is None:
+            loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+            loader.exec_module(module)
+            _calls = module
+    return _calls
+
+
 def kv_cache_append(cache_type: int, k_cache, v_cache, k_scales, v_scales, k, k_stride: int, v, v_stride: int,
                     cu_tokens, block_tables, seq_lens, num_seqs: int, num_tokens: int, num_kv_heads: int,
                     head_dim: int, block_size: int, max_blocks: int, num_blocks: int, stream=None) -> None:
     """New tokens' keys and values into a paged cache, BF16 or quantised to E4M3 with a power-of-two scale per row
     (see include/bsk.h); blocks until done."""
-    _check(load().kv_cache_append(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
-                                  _addr(k), k_stride, _addr(v), v_stride, _addr(cu_tokens), _addr(block_tables),
-                                  _addr(seq_lens), num_seqs, num_tokens, num_kv_heads, head_dim, block_size,
-                                  max_blocks, num_blocks, _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.kv_cache_append(cache_type, k_cache, v_cache, k_scales, v_scales, k, k_stride, v, v_stride, cu_tokens,
+                                 block_tables, seq_lens, num_seqs, num_tokens, num_kv_heads, head_dim, block_size,
+                                 max_blocks, num_blocks, _stream(stream)))
 
 
 def kv_cache_append_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, k, k_stride: int, v,
@@ -301,31 +309,31 @@ def kv_cache_append_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scale
                             num_kv_heads: int, head_dim: int, block_size: int, max_blocks: int, num_blocks: int,
                             stream=None) -> None:
     """Asynchronous variant of kv_cache_append (check with stream_check)."""
-    _check(load().bsk_kv_cache_append_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
-                                              _addr(v_scales), _addr(k), k_stride, _addr(v), v_stride,
-                                              _addr(cu_tokens), _addr(block_tables), _addr(seq_lens), num_seqs,
-                                              num_tokens, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
-                                              _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.bsk_kv_cache_append_enqueue(cache_type, k_cache, v_cache, k_scales, v_scales, k, k_stride, v,
+                                             v_stride, cu_tokens, block_tables, seq_lens, num_seqs, num_tokens,
+                                             num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
+                                             _stream(stream)))
 
 
 def kv_cache_gather(cache_type: int, k_cache, v_cache, k_scales, v_scales, k_out, v_out, cu_tokens, block_tables,
                     seq_lens, num_seqs: int, num_tokens: int, num_kv_heads: int, head_dim: int, block_size: int,
                     max_blocks: int, num_blocks: int, stream=None) -> None:
     """The last tokens of each sequence read back from the cache as BF16; blocks until done."""
-    _check(load().kv_cache_gather(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
-                                  _addr(k_out), _addr(v_out), _addr(cu_tokens), _addr(block_tables), _addr(seq_lens),
-                                  num_seqs, num_tokens, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
-                                  _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.kv_cache_gather(cache_type, k_cache, v_cache, k_scales, v_scales, k_out, v_out, cu_tokens,
+                                 block_tables, seq_lens, num_seqs, num_tokens, num_kv_heads, head_dim, block_size,
+                                 max_blocks, num_blocks, _stream(stream)))
 
 
 def kv_cache_gather_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, k_out, v_out, cu_tokens,
                             block_tables, seq_lens, num_seqs: int, num_tokens: int, num_kv_heads: int, head_dim: int,
                             block_size: int, max_blocks: int, num_blocks: int, stream=None) -> None:
     """Asynchronous variant of kv_cache_gather (check with stream_check)."""
-    _check(load().bsk_kv_cache_gather_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
-                                              _addr(v_scales), _addr(k_out), _addr(v_out), _addr(cu_tokens),
-                                              _addr(block_tables), _addr(seq_lens), num_seqs, num_tokens, num_kv_heads,
-                                              head_dim, block_size, max_blocks, num_blocks, _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.bsk_kv_cache_gather_enqueue(cache_type, k_cache, v_cache, k_scales, v_scales, k_out, v_out, cu_tokens,
+                                             block_tables, seq_lens, num_seqs, num_tokens, num_kv_heads, head_dim,
+                                             block_size, max_blocks, num_blocks, _stream(stream)))
 
 
 def chunk_attention(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out, out_stride: int,
@@ -335,11 +343,11 @@ def chunk_attention(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_
                     num_segments: int = 0, stream=None) -> None:
     """Attention of a chunk of new tokens per sequence over a paged cache, causal, with an optional sliding window and
     sinks (see include/bsk.h); blocks until done."""
-    _check(load().chunk_attention(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
-                                  _addr(q), q_stride, _addr(out), out_stride, _addr(cu_tokens), _addr(block_tables),
-                                  _addr(seq_lens), num_seqs, num_tokens, max_chunk, num_q_heads, num_kv_heads,
-                                  head_dim, block_size, max_blocks, num_blocks, max_seq_len, softmax_scale, window,
-                                  sinks, num_segments, _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.chunk_attention(cache_type, k_cache, v_cache, k_scales, v_scales, q, q_stride, out, out_stride,
+                                 cu_tokens, block_tables, seq_lens, num_seqs, num_tokens, max_chunk, num_q_heads,
+                                 num_kv_heads, head_dim, block_size, max_blocks, num_blocks, max_seq_len,
+                                 softmax_scale, window, sinks, num_segments, _stream(stream)))
 
 
 def chunk_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out,
@@ -348,12 +356,12 @@ def chunk_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scale
                             max_blocks: int, num_blocks: int, max_seq_len: int, softmax_scale: float,
                             window: int = 0, sinks: int = 0, num_segments: int = 0, stream=None) -> None:
     """Asynchronous variant of chunk_attention (check with stream_check)."""
-    _check(load().bsk_chunk_attention_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
-                                              _addr(v_scales), _addr(q), q_stride, _addr(out), out_stride,
-                                              _addr(cu_tokens), _addr(block_tables), _addr(seq_lens), num_seqs,
-                                              num_tokens, max_chunk, num_q_heads, num_kv_heads, head_dim, block_size,
-                                              max_blocks, num_blocks, max_seq_len, softmax_scale, window, sinks,
-                                              num_segments, _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.bsk_chunk_attention_enqueue(cache_type, k_cache, v_cache, k_scales, v_scales, q, q_stride, out,
+                                             out_stride, cu_tokens, block_tables, seq_lens, num_seqs, num_tokens,
+                                             max_chunk, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks,
+                                             num_blocks, max_seq_len, softmax_scale, window, sinks, num_segments,
+                                             _stream(stream)))
 
 
 def decode_attention(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out, out_stride: int,
@@ -362,10 +370,11 @@ def decode_attention(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q
                      window: int = 0, sinks: int = 0, num_segments: int = 0, stream=None) -> None:
     """Attention of one new token per sequence over a paged cache (chunk_attention's form for single tokens); blocks
     until done."""
-    _check(load().decode_attention(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales), _addr(v_scales),
-                                   _addr(q), q_stride, _addr(out), out_stride, _addr(block_tables), _addr(seq_lens),
-                                   num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks, num_blocks,
-                                   max_seq_len, softmax_scale, window, sinks, num_segments, _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.decode_attention(cache_type, k_cache, v_cache, k_scales, v_scales, q, q_stride, out, out_stride,
+                                  block_tables, seq_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                  max_blocks, num_blocks, max_seq_len, softmax_scale, window, sinks, num_segments,
+                                  _stream(stream)))
 
 
 def decode_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scales, q, q_stride: int, out,
@@ -374,11 +383,11 @@ def decode_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scal
                              max_seq_len: int, softmax_scale: float, window: int = 0, sinks: int = 0,
                              num_segments: int = 0, stream=None) -> None:
     """Asynchronous variant of decode_attention (check with stream_check)."""
-    _check(load().bsk_decode_attention_enqueue(cache_type, _addr(k_cache), _addr(v_cache), _addr(k_scales),
-                                               _addr(v_scales), _addr(q), q_stride, _addr(out), out_stride,
-                                               _addr(block_tables), _addr(seq_lens), num_seqs, num_q_heads,
-                                               num_kv_heads, head_dim, block_size, max_blocks, num_blocks, max_seq_len,
-                                               softmax_scale, window, sinks, num_segments, _stream(stream)))
+    calls = _calls or _load_calls()
+    _check(calls.bsk_decode_attention_enqueue(cache_type, k_cache, v_cache, k_scales, v_scales, q, q_stride, out,
+                                              out_stride, block_tables, seq_lens, num_seqs, num_q_heads, num_kv_heads,
+                                              head_dim, block_size, max_blocks, num_blocks, max_seq_len, softmax_scale,
+                                              window, sinks, num_segments, _stream(stream)))
 
 
 def stream_check(stream=None) -> None:

@@ -1,8 +1,9 @@
 """Build libbsk.so in-tree from csrc/ with nvcc for sm_103a.
 
 The translation units compile in parallel (one nvcc per file), then link into
-``bf16_gemm_skinny_gb300/_build/libbsk.so``.  Rebuilds only when a source or
-header is newer than the library.
+``bf16_gemm_skinny_gb300/_build/libbsk.so``.  ``_calls.so`` beside it is the Python
+module that calls some of its entry points.  Rebuilds only when a source or header
+is newer than either.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libbsk.so")
+CALLS_PATH = os.path.join(BUILD_DIR, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "py_calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", f"-I{INCLUDE}", "-Xptxas", "-v"]
 
@@ -34,29 +38,31 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + [CALLS_SOURCE] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libbsk.so; returns its path."""
+    """Compile and link libbsk.so and _calls.so; returns the library's path."""
     if not force and not is_stale():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
 
     def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
+        name = os.path.splitext(os.path.basename(src))[0]
+        obj = os.path.join(BUILD_DIR, name + ".o")
+        python = [f"-I{sysconfig.get_paths()['include']}"] if src == CALLS_SOURCE else []
+        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *python, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
-        log = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".ptxas.log")
+        log = os.path.join(BUILD_DIR, name + ".ptxas.log")
         with open(log, "w") as f:
             f.write(r.stdout + r.stderr)
         if r.returncode != 0:
@@ -64,12 +70,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(compile_one, _sources()))
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stderr[-4000:])
-    os.replace(tmp, LIB_PATH)
+        *objs, calls = ex.map(compile_one, _sources() + [CALLS_SOURCE])
+
+    def link(path, args):
+        tmp = path + f".tmp{os.getpid()}"
+        r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *args], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stderr[-4000:])
+        os.replace(tmp, path)
+
+    link(LIB_PATH, [*objs, "-lcudart"])
+    link(CALLS_PATH, [calls, "-cudart", "none", f"-L{BUILD_DIR}", "-lbsk", "-Xlinker", "-rpath,$ORIGIN"])
     if verbose:
         print(f"built {LIB_PATH}")
     return LIB_PATH
