@@ -209,6 +209,14 @@ __device__ __forceinline__ int box_state(const uint32_t* mask, int k, int box)
     return all == bits ? 1 : (any == 0u ? 0 : 2);
 }
 
+// Where 16-byte piece c of row r goes, of rows of N pieces one after the other: piece
+// c ^ row_swizzle(r), so that 8 neighbouring rows' same pieces meet distinct banks.
+template <int N>
+__device__ __forceinline__ int row_swizzle(int r)
+{
+    return N >= 8 ? r & 7 : (r >> 1) & 3;
+}
+
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
@@ -387,7 +395,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         const uint32_t full0 = E4M3 ? (is_k ? rk_full0 : rv_full0) : (is_k ? k_full0 : v_full0);
         const uint32_t empty0 = E4M3 ? (is_k ? rk_empty0 : rv_empty0) : (is_k ? k_empty0 : v_empty0);
         const uint32_t dst0 = smem_u32(E4M3 ? (is_k ? r_k : r_v) : (is_k ? s_k : s_v));
-        const int box = p.box;
+        const int box = p.box, pad = max(box, 16);
         // the rows from `row` on, as positions k .. of a tile
         auto load_box = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int k, int row) {
             if constexpr (!E4M3 && HD > 64) {
@@ -410,29 +418,33 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
             const int slot = j % kSlots;
             ok = wait_long(m_full0 + 8 * slot, (j / kSlots) & 1, wc, kSiteKvMeta) &&
                  wait_long(empty0 + 8 * stage, phase ^ 1u, wc, kSiteKvEmpty);
+            if (!E4M3 && j == S - 1) ok = ok && wait_long(q_full, 0, wc, kSiteKvQ);   // Q came through this stage
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ++issued;
+            // Positions past the last key, to the next group of 16 (or box), are not loaded:
+            // their scores are masked, and PV leaves their groups out.
+            const int upto = min(kTile, (keys.kv_end - keys.base(keys.begin + j) + pad - 1) & -pad);
             if (elect_one()) {
                 const uint32_t bar = full0 + 8 * stage;
                 const uint32_t dst = dst0 + stage * kBytes;
                 const int kind = s_kind[slot * 4];
                 const int4* boxes = reinterpret_cast<const int4*>(s_box + slot * 32);
-                mbar_arrive_expect_tx(bar, kBytes);
+                mbar_arrive_expect_tx(bar, kBytes / kTile * upto);
                 if (kind == kLoadTile) {
                     load_box(dst, tile_map, bar, 0, boxes[0].x);
                 } else if (kind == kLoadBoxes) {
-                    for (int k = 0; k < kTile; k += 4 * box) {
+                    for (int k = 0; k < upto; k += 4 * box) {
                         const int4 r = boxes[k / box >> 2];
                         load_box(dst, box_map, bar, k, r.x);
-                        if (k + box < kTile) load_box(dst, box_map, bar, k + box, r.y);
-                        if (k + 2 * box < kTile) load_box(dst, box_map, bar, k + 2 * box, r.z);
-                        if (k + 3 * box < kTile) load_box(dst, box_map, bar, k + 3 * box, r.w);
+                        if (k + box < upto) load_box(dst, box_map, bar, k + box, r.y);
+                        if (k + 2 * box < upto) load_box(dst, box_map, bar, k + 2 * box, r.z);
+                        if (k + 3 * box < upto) load_box(dst, box_map, bar, k + 3 * box, r.w);
                     }
                 } else {
                     const int* rows_of = s_row + slot * kTile;
                     const uint32_t* mask = s_mask + slot * 4;
-                    for (int k = 0; k < kTile; k += box) {
+                    for (int k = 0; k < upto; k += box) {
                         if (box >= 8 && box_state(mask, k, box) != 2) {
                             load_box(dst, box_map, bar, k, rows_of[k]);
                             continue;
@@ -680,6 +692,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                     x[u] = *reinterpret_cast<const uint4*>(raw + line + c * 16);
                 }
                 wait_long((v ? v_empty0 : k_empty0) + 8 * ss, ((j / S) & 1) ^ 1, wc, kSiteKvEmpty);
+                if (j == S - 1) wait_long(q_full, 0, wc, kSiteKvQ);   // Q came through this stage
 #pragma unroll
                 for (int u = 0; u < kChunks; ++u) {
                     const int ch = u * (32 * kConvertWarps) + tid;
@@ -723,25 +736,45 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         const int pos = pos0 + my / p.group;
         float row_scale = p.scale_log2;
         if (!idle) {
-            // this half of Q's row: 16-bit pairs, one per TMEM column
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_stride + static_cast<long long>(head) * HD +
-                                                              half * (HD / H));
+            // This half of Q's row: 16-bit pairs, one per TMEM column.  Neighbouring lanes load
+            // neighbouring 16 bytes, and the rows go to their lanes through the last stages
+            // of keys and values (a lane loading its own row takes 32 cache lines an
+            // instruction, and the look-ups queue behind them: 2000 to 5000 clocks).
             constexpr int QW = HD / 2 / H;   // pairs
-            uint32_t w[QW];
+            constexpr int LPR = QW / 4;      // lanes per row
+            constexpr int kMine = 32 * QW * 4;
+            static_assert(4 * H * kMine <= 2 * G::kStageBytes, "Q's rows in two stages");
+            const int at = (quarter * H + half) * kMine;
+            uint4* mine = reinterpret_cast<uint4*>((at < G::kStageBytes ? s_k : s_v - G::kStageBytes) +
+                                                   (S - 1) * G::kStageBytes + at);
+            const long long q_row = token * p.q_stride + static_cast<long long>(head) * HD + half * (HD / H);
+            constexpr int kRound = E4M3 && LPR > 8 ? 8 : LPR;   // loads at a time (as registers allow)
+#pragma unroll 1
+            for (int c0 = 0; c0 < LPR; c0 += kRound) {
+                uint4 x[kRound];
 #pragma unroll
-            for (int c = 0; c < QW / 4; ++c) {
-                const uint4 x = src[c];
-                w[4 * c] = x.x ^ p.q_sign;
-                w[4 * c + 1] = x.y ^ p.q_sign;
-                w[4 * c + 2] = x.z ^ p.q_sign;
-                w[4 * c + 3] = x.w ^ p.q_sign;
+                for (int c = 0; c < kRound; ++c) {
+                    const int i = (c0 + c) * 32 + lane;
+                    x[c] = *reinterpret_cast<const uint4*>(p.q + __shfl_sync(0xffffffffu, q_row, i / LPR) + i % LPR * 8);
+                }
+#pragma unroll
+                for (int c = 0; c < kRound; ++c) {
+                    const int i = (c0 + c) * 32 + lane;
+                    mine[i / LPR * LPR + (i % LPR ^ row_swizzle<LPR>(i / LPR))] = x[c];
+                }
             }
+            __syncwarp();
+            float f = 1.f;
             if constexpr (E4M3) {
                 // FP16 beside FP16 keys: the row times a power of two that brings its largest
                 // value to [2^14, 2^15).  What FP16 then drops is under 2^-39 of the largest.
                 uint32_t m = 0;
 #pragma unroll
-                for (int c = 0; c < QW; ++c) m = __vmaxu2(m, w[c] & 0x7fff7fffu);
+                for (int c = 0; c < LPR; ++c) {
+                    const uint4 x = mine[lane * LPR + (c ^ row_swizzle<LPR>(lane))];
+                    m = __vmaxu2(__vmaxu2(m, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+                    m = __vmaxu2(__vmaxu2(m, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
+                }
                 m = max(m & 0xffffu, m >> 16);
                 uint32_t* sm = reinterpret_cast<uint32_t*>(s_max);
                 sm[half * kRows + r] = m;
@@ -749,28 +782,34 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 m = max(m, sm[(half ^ 1) * kRows + r]);
                 int e = static_cast<int>(m >> 7) - 127 - 14;               // q * 2^-e
                 e = max(-126, min(e, 113));
-                const float f = exp2f(static_cast<float>(-e));
+                f = exp2f(static_cast<float>(-e));
                 row_scale *= exp2f(static_cast<float>(e));
-#pragma unroll
-                for (int c = 0; c < QW; ++c)
-                    w[c] = f16x2(__uint_as_float(w[c] << 16) * f, __uint_as_float(w[c] & 0xffff0000u) * f);
                 named_barrier(1 + quarter, 64);   // s_max is free again
             }
-            const uint32_t q_addr = lane_addr + G::kColQ + half * QW;
-            if constexpr (QW >= 32) {
+            constexpr int kPart = QW < 32 ? 16 : 32;   // columns at a time
 #pragma unroll
-                for (int c = 0; c < QW / 32; ++c) {
-                    uint32_t t[32];
+            for (int c0 = 0; c0 < QW; c0 += kPart) {
+                uint32_t t[kPart];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) t[i] = w[32 * c + i];
-                    tmem_st_32x32b_x32(q_addr + 32 * c, t);
+                for (int c = 0; c < kPart; c += 4) {
+                    const uint4 x = mine[lane * LPR + ((c0 + c) / 4 ^ row_swizzle<LPR>(lane))];
+                    t[c] = x.x ^ p.q_sign;
+                    t[c + 1] = x.y ^ p.q_sign;
+                    t[c + 2] = x.z ^ p.q_sign;
+                    t[c + 3] = x.w ^ p.q_sign;
                 }
-            } else {
-                uint32_t t[16];
+                if constexpr (E4M3) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) t[i] = w[i];
-                tmem_st_32x32b_x16(q_addr, t);
+                    for (int c = 0; c < kPart; ++c)
+                        t[c] = f16x2(__uint_as_float(t[c] << 16) * f, __uint_as_float(t[c] & 0xffff0000u) * f);
+                }
+                const uint32_t q_addr = lane_addr + G::kColQ + half * QW + c0;
+                if constexpr (kPart == 32)
+                    tmem_st_32x32b_x32(q_addr, t);
+                else
+                    tmem_st_32x32b_x16(q_addr, t);
             }
+            fence_proxy_async_smem();   // the stage is the TMA unit's from here on
             tmem_st_wait();
             tc_fence_before_sync();
         }
@@ -934,6 +973,9 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
             const long long at = (static_cast<long long>(token) * p.num_q_heads + head) * p.segments + seg;
             // a split row's partial sums leave out E4M3's 2^(3 - E)
             const float plain = E4M3 ? exp2f(static_cast<float>(E - 3)) : 1.f;
+            const long long out_at = p.segments == 1 ? token * p.out_stride + static_cast<long long>(head) * HD : at * HD;
+            uint4* stage = reinterpret_cast<uint4*>(s_k + (warp - 4) * 4096);
+            static_assert(2 * S * G::kStageBytes >= 4 * H * 4096, "rows of 32 FP32 in the stages");
             float odd = 0.f;   // NaN once a value is not finite
             for (int c = 0; c < HD / H / 32; ++c) {
                 const int d0 = half * (HD / H) + c * 32;
@@ -942,24 +984,43 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(o[i]), 0.f, odd);
-                if (r < rows) {
-                    if (p.segments == 1) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + token * p.out_stride +
-                                                              static_cast<long long>(head) * HD + d0);
+                // through shared memory (the stages are done with), so that neighbouring
+                // lanes write neighbouring 16 bytes
+                __syncwarp();
+                if (p.segments == 1) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t h[4];
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                h[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                    } else {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + d0);
+                        for (int k = 0; k < 4; ++k)
+                            h[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                        stage[lane * 4 + (i ^ row_swizzle<4>(lane))] = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                    __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(o[4 * i]) * plain, __uint_as_float(o[4 * i + 1]) * plain,
-                                                 __uint_as_float(o[4 * i + 2]) * plain, __uint_as_float(o[4 * i + 3]) * plain);
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = i * 8 + (lane >> 2);
+                        const long long to = __shfl_sync(0xffffffffu, out_at, rr);
+                        if (quarter * 32 + rr < rows)
+                            *reinterpret_cast<uint4*>(p.out + to + d0 + (lane & 3) * 8) =
+                                stage[rr * 4 + ((lane & 3) ^ row_swizzle<4>(rr))];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        stage[lane * 8 + (i ^ row_swizzle<8>(lane))] =
+                            make_uint4(__float_as_uint(__uint_as_float(o[4 * i]) * plain),
+                                       __float_as_uint(__uint_as_float(o[4 * i + 1]) * plain),
+                                       __float_as_uint(__uint_as_float(o[4 * i + 2]) * plain),
+                                       __float_as_uint(__uint_as_float(o[4 * i + 3]) * plain));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + (lane >> 3);
+                        const long long to = __shfl_sync(0xffffffffu, out_at, rr);
+                        if (quarter * 32 + rr < rows)
+                            *reinterpret_cast<uint4*>(p.part_o + to + d0 + (lane & 7) * 4) =
+                                stage[rr * 8 + ((lane & 7) ^ row_swizzle<8>(rr))];
                     }
                 }
             }
@@ -969,13 +1030,11 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 named_barrier(1 + quarter, 64);
             else
                 __syncwarp();
-            for (int i = half; i < 32; i += H) {
-                const int rr = quarter * 32 + i;
-                if (rr < rows && s_flag[rr]) {
-                    const int row = row0 + rr;
-                    repair_row<E4M3, HD, kTile>(p, table, keys, kvh, first + row / p.group, kvh * p.group + row % p.group,
-                                         pos0 + row / p.group, seg);
-                }
+            for (uint32_t left = __ballot_sync(0xffffffffu, s_flag[r] != 0); left != 0; left &= left - 1) {
+                const int rr = quarter * 32 + __ffs(left) - 1, row = row0 + rr;
+                if (H == 2 && (rr & 1) != half) continue;
+                repair_row<E4M3, HD, kTile>(p, table, keys, kvh, first + row / p.group, kvh * p.group + row % p.group,
+                                            pos0 + row / p.group, seg);
             }
         }
         tc_fence_before_sync();
