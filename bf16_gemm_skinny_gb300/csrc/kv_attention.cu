@@ -16,7 +16,16 @@
 //   O += P V    tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // The MMAs of S for tile j+1 and of PV for tile j-1 run while the warps work on
 // tile j.  Q lies in TMEM, so that shared memory holds nothing but keys and values
-// on their way and an MMA reads one operand from it.
+// on their way and an MMA reads one operand from it (with Q there too, head_dim 256
+// took 1040 us where this took 927).
+//
+// Bound, long chunks: shared memory.  A tile is 1024 clocks of MMAs (head_dim 128 and
+// 256); in them shared memory takes its 64 KB of keys and values from the TMA unit (57
+// bytes a clock at best) and gives the MMAs 64 KB.  Measured about 1850 clocks a tile:
+// 2048 tokens over 30720 (16 query heads, 4 KV heads of 256, BF16) 858 us, 1240 TFLOP/s,
+// 0.67 of the tensor cores' measured rate.  head_dim 64: the exponentials (a windowed
+// chunk of 4097 tokens, 32 heads, 72 us, 420 TFLOP/s).  Few rows: HBM and a CTA's start
+// and end, some 6 us (8 sequences decoded through a window of 4096, BF16: 31 us, 4.3 TB/s).
 #include <cmath>
 #include <cstdio>
 
@@ -154,8 +163,8 @@ struct Geo {
     static constexpr int kBlocks = HD / 64;                    // 64-element (128-byte) blocks of a row
     // CTAs per SM.  A CTA alternates between waiting for its own scores and working on
     // them; a second one fills the gaps, and one's start and end.  With HD = 64 two fit
-    // TMEM with 64-position tiles: a windowed chunk of 4097 tokens takes 76 us with two,
-    // 110 with one of 128-position tiles.  With HD = 128 a second one leaves room for one S
+    // TMEM with 64-position tiles: a windowed chunk of 4097 tokens took 76 us with two
+    // (72 now), 110 with one of 128-position tiles.  With HD = 128 a second one leaves room for one S
     // tile only and lost (325 against 276 us for four ragged chunks).
     static constexpr int kCtas = !E4M3 && HD == 64 ? 2 : 1;
     // Positions per tile, S tiles in TMEM.  TMEM's columns (512, or 256 for each of two
@@ -1051,7 +1060,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
 // sum_s l_s 2^(m_s - M), in a fixed order.  256 threads have 64 dimensions of one
 // row (WIDE: few rows, up to 256 segments; 16 groups of 16 threads share the
 // segments) or of 16 rows (a group each).  Latency is what counts: the loads of
-// (m, l) are one round, those of O as many as the registers allow.
+// (m, l) are one round, those of O as many as the registers allow.  One row of 256 by
+// 74 segments: some 3 us between the attention's last store and the next call.
 // ---------------------------------------------------------------------------
 template <int HD, bool WIDE>
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ AttnParams p)
@@ -1149,16 +1159,16 @@ long long most_keys(const KvAttnLaunch& a)
 // Rows per CTA of the kernel for few query rows per KV head, or 0: the call takes
 // the other kernel.  An E4M3 cache read for few rows would spend its time in the
 // other kernel's shared memory.  Measured in microseconds, many-row / few-row kernel
-// (32 sequences of up to 4000 tokens; one of 30000): head_dim 256, 8 rows 111 / 79, 35 / 29,
-// 16 rows 118 / 125, 35 / 42; 128, 32 rows 163 / 137, 50 / 44, 64 rows 151 / 241; 64, 32 rows
-// 72 / 67, 25 / 25, 64 rows 73 / 115.  On a BF16 cache it did not pay: 8 rows of 256 83 / 130,
-// of 128 91 / 117, of 64 46 / 45.
+// (32 sequences of up to 4000 tokens; one of 30000): head_dim 256, 8 rows 78 / 77, 31 / 29,
+// 16 rows 79 / 125, 32 / 42; 128, 8 rows 132 / 69, 41 / 25, 16 rows 123 / 82, 42 / 31, 24 rows
+// 123 / 133, 42 / 45; 64, 16 rows 63 / 48, 23 / 19, 24 rows 63 / 70, 24 / 25.  On a BF16 cache
+// it did not pay: 8 rows of 256 83 / 130, of 128 91 / 117, of 64 46 / 45.
 int few_rows(const KvAttnLaunch& a)
 {
     const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
     const int few = rows <= 8 || a.b.head_dim == 256 ? 8 : 16;
     if (a.b.type != kCacheE4M3 || a.kernel == 1) return 0;
-    return a.kernel == 2 || rows <= (a.b.head_dim == 256 ? 8 : 32) ? few : 0;
+    return a.kernel == 2 || rows <= (a.b.head_dim == 256 ? 8 : 16) ? few : 0;
 }
 
 template <bool E4M3, int HD>
@@ -1269,12 +1279,12 @@ size_t partial_bytes(const KvAttnLaunch& a)
 // Rows of a sequence in the flat BF16 copy of an E4M3 cache, or 0: no copy is made.
 // It costs one pass over the positions in sight; without it every 128 query rows
 // convert them again.  Microseconds without / with it, 30000 positions: head_dim 256,
-// 256 rows 84 / 97, 512 rows 143 / 126, 2048 rows 477 / 273; 128, 256 rows 104 / 90,
-// 2048 rows 680 / 274; 64, 256 rows 48 / 46, 2048 rows 267 / 152.
+// 512 rows 94 / 105, 1024 rows 156 / 148, 2048 rows 301 / 256; 128, 256 rows 78 / 75,
+// 512 rows 139 / 99, 2048 rows 502 / 264; 64, 256 rows 37 / 36, 2048 rows 223 / 114.
 int flat_rows(const KvAttnLaunch& a)
 {
     const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
-    if (a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < 2 * (a.b.head_dim > 128 ? 256 : 128)) return 0;
+    if (a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < (a.b.head_dim == 256 ? 1024 : 256)) return 0;
     const long long len = (a.max_seq_len + 127LL) / 128 * 128;
     const long long bytes = len * a.b.num_seqs * a.b.num_kv_heads * a.b.head_dim * 4;
     return len * a.b.num_seqs <= 0x7fffffffLL && bytes <= (2LL << 30) ? static_cast<int>(len) : 0;

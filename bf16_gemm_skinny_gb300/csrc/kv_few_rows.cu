@@ -14,8 +14,15 @@
 // of P^T by movmatrix.  E4M3 codes become FP16 pairs by one instruction each
 // (exact), and Q, scaled by a power of two per row, FP16 too.
 //
-// The warps of a CTA take the groups of 16 or 32 positions of its segment in turn.  They
-// are joined in shared memory, the segments by kv_join_kernel.
+// The warps of a CTA take the 32-position steps of its segment in turn.  They are
+// joined in shared memory, the segments by kv_join_kernel.
+//
+// Bound: the latency of a warp's step (some 700 instructions, 8 to 11 warps per SM);
+// without its MMAs, or on a few pages read over and over, it is under 4% faster.
+// Measured: 64 sequences of up to 8000 tokens, 64 heads over 8 KV heads of 128: 155 us,
+// 3.6 TB/s (0.53 of the measured copy rate; 231 us with loads into registers, 181 with
+// 16 positions a step); one of 32768, 16 heads over 4 of 256: 27 us, 2.5 TB/s, of
+// which 19 us do not depend on the length.
 #include <cstdio>
 
 #include "bsk_internal.h"
@@ -24,7 +31,6 @@
 namespace bsk {
 namespace kv {
 namespace {
-
 
 // D (16 x 8, FP32) += A (16 x 16, FP16, row-major) * B (16 x 8, FP16, column-major).
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
             if (static_cast<unsigned>(entry) < static_cast<unsigned>(p.b.num_blocks))
                 row = entry * bs + entry_off;
             else
-                *reinterpret_cast<volatile int*>(p.b.status) = 0x200;   // kDevErrBadIndex
+                *reinterpret_cast<volatile int*>(p.b.status) = kDevErrBadIndex;
         }
     };
     const uint8_t* scales_end[2] = {nullptr, nullptr};
@@ -309,7 +315,6 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
     int E = 0, low_e = 1000;
     bool wide = false;
 
-
     int at = 0, slot = 0, slot_in = A;   // ring place; places of this step's note and of the next one written
     for (int i = i0; i < keys.end; i += kWarps) {
         const int base = keys.base(i);
@@ -340,7 +345,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
                 const uint4 k1 = *reinterpret_cast<const uint4*>(ks + ((2 * b + 1) * kKeyVecs + v) * 512);
                 const uint32_t x[2][4] = {{k0.x, k0.y, k0.z, k0.w}, {k1.x, k1.y, k1.z, k1.w}};
                 const uint16_t* qs = s_q + g * kPitch + v * 4 * kVec + c * kVec;
-                #pragma unroll
+#pragma unroll
                 for (int h = 0; h < 2; ++h) {   // 8 values of each row: two MMAs
                     uint32_t a[2][4];
 #pragma unroll
