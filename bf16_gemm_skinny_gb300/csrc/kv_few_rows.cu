@@ -17,10 +17,10 @@
 // The warps of a CTA take the 32-position steps of its segment in turn.  They are
 // joined in shared memory, the segments by kv_join_kernel.
 //
-// Bound: the latency of a warp's step (some 700 instructions, 8 to 11 warps per SM);
+// Bound: the latency of a warp's step (some 700 instructions, 6 to 16 warps per SM);
 // without its MMAs, or on a few pages read over and over, it is under 4% faster.
-// Measured: 64 sequences of up to 8000 tokens, 64 heads over 8 KV heads of 128: 155 us,
-// 3.6 TB/s (0.53 of the measured copy rate; 231 us with loads into registers, 181 with
+// Measured: 64 sequences of up to 8000 tokens, 64 heads over 8 KV heads of 128: 149 us,
+// 3.7 TB/s (0.55 of the measured copy rate; 231 us with loads into registers, 181 with
 // 16 positions a step); one of 32768, 16 heads over 4 of 256: 27 us, 2.5 TB/s, of
 // which 19 us do not depend on the length.
 #include <cstdio>
@@ -65,9 +65,12 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Sizes.  `kAhead` steps per warp are on their way: the CTAs of an SM have 100 to
-// 200 KB in flight, which the latency times HBM's rate needs (about 45 KB) with
-// room for uneven progress.
+// Sizes.  `kAhead` steps per warp are on their way: the CTAs of an SM have 64 to
+// 200 KB in flight; the latency times HBM's rate needs about 45 KB.  More warps count
+// for more than more steps ahead.  Microseconds with 4 CTAs of one step ahead / 3 of
+// two (head_dim 64: three): 64 sequences of up to 8000 tokens, head_dim 128, 149 / 156;
+// 32 of up to 4000, head_dim 64, 27 / 37; 5 or 6 CTAs spill (167; 33).  With head_dim 256
+// twice the warps at one step ahead are the same (27.1 / 27.4, one sequence of 32768).
 template <int HD, int R>
 struct Few {
     static constexpr int kRows = 8 * R;                 // query rows per CTA (R MMAs of N = 8)
@@ -82,8 +85,8 @@ struct Few {
     static constexpr int kSub = 2;
     static constexpr int kGroup = 16 * kSub;
     static constexpr int kWarps = HD == 256 ? 3 : 4;
-    static constexpr int kAhead = HD == 64 ? 3 : 2;
-    static constexpr int kCtas = R > 1 || HD == 256 ? 2 : 3;   // of an SM
+    static constexpr int kAhead = HD == 256 ? 2 : 1;
+    static constexpr int kCtas = R > 1 || HD == 256 ? 2 : 4;   // of an SM
     static constexpr int kKeyBytes = kSub * 2 * kKeyVecs * 512, kValBytes = kSub * 4 * kValVecs * 512;   // of a step
     static constexpr int kWarpRing = kAhead * (kKeyBytes + kValBytes);
     static constexpr int kRing = kWarps * kWarpRing;
