@@ -85,8 +85,8 @@ void bsk_tile_coord(int t, int num_m, int num_n, int group_m, int* pid_m, int* p
  *                            MMAs; one accumulator, so the epilogue no longer overlaps the
  *                            next tile's MMAs)
  *   BSK_OPT_KV_KERNEL        kernel of chunk_attention and decode_attention: 0 automatic, 1 the
- *                            tcgen05 kernel (128 query rows per CTA), 2 the kernel for few rows
- *                            (8 or 16 per CTA)
+ *                            tcgen05 kernel (128 query rows per CTA) on the cache as it is, 2 for
+ *                            an E4M3 cache the kernel for few rows (8 or 16 per CTA)
  * Returns BSK_ERR_INVALID_ARG for an unknown key or a value out of range.
  */
 enum {

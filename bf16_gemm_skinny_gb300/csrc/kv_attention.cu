@@ -1160,8 +1160,8 @@ long long most_keys(const KvAttnLaunch& a)
 // the other kernel.  An E4M3 cache read for few rows would spend its time in the
 // other kernel's shared memory.  Measured in microseconds, many-row / few-row kernel
 // (32 sequences of up to 4000 tokens; one of 30000): head_dim 256, 8 rows 78 / 77, 31 / 29,
-// 16 rows 79 / 125, 32 / 42; 128, 8 rows 132 / 69, 41 / 25, 16 rows 123 / 82, 42 / 31, 24 rows
-// 123 / 133, 42 / 45; 64, 16 rows 63 / 48, 23 / 19, 24 rows 63 / 70, 24 / 25.  On a BF16 cache
+// 16 rows 78 / 125, 31 / 42; 128, 8 rows 132 / 67, 41 / 25, 16 rows 123 / 78, 42 / 29, 24 rows
+// 122 / 127, 42 / 42; 64, 16 rows 63 / 44, 23 / 18, 32 rows 63 / 66, 24 / 23.  On a BF16 cache
 // it did not pay: 8 rows of 256 83 / 130, of 128 91 / 117, of 64 46 / 45.
 int few_rows(const KvAttnLaunch& a)
 {
