@@ -385,3 +385,25 @@ def test_attention_past_32_bits():
                                 heads, dim, page, 1, blocks, page, 1 / 16)
             o = out.reshape(new, heads, dim)
             assert (o[:, 5] == 1).all() and not o[:, :5].any() and not o[:, 6:].any()
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,group,dim,page", [(1, 4, 64, 8), (2, 2, 128, 64), (1, 2, 256, 31), (2, 4, 128, 16)])
+def test_lengths_around_a_tile_after_a_cache_of_nans(kernel, which, heads, group, dim, page, e4m3):
+    """Tiles with few keys: what an earlier call left in shared memory (NaN here) is no part of them."""
+    lens = [1, 15, 16, 17, 33, 63, 64, 65, 79, 127, 128, 129, 145, 193]
+    new = [1, 15, 3, 17, 33, 60, 64, 2, 79, 127, 128, 120, 1, 190]
+    nan = ref.Problem(41, [700], [200], heads, group, dim, page, e4m3)
+    d = nan.device()
+    if e4m3:
+        d["ks"].fill_(255), d["vs"].fill_(255)
+        d["k"].fill_(127), d["v"].fill_(127)
+    else:
+        d["k"].fill_(math.nan), d["v"].fill_(math.nan)
+    p = ref.Problem(42, lens, new, heads, group, dim, page, e4m3)
+    kernel(which)
+    for window, sinks in ((0, 0), (40, 3)):
+        for _ in range(3):
+            assert torch.isnan(run(nan, d=d)).all()
+        check(p, run(p, window, sinks), window, sinks)
