@@ -46,6 +46,7 @@ __device__ __forceinline__ long long token_row(const KvBatch& b, int t)
 {
     const int s = kv_sequence_of(b, t);
     if (s >= b.num_seqs) return -2;
+    if (b.cu_tokens != nullptr && t < b.cu_tokens[s]) return -2;   // before the first sequence's rows
     const int end = b.cu_tokens != nullptr ? b.cu_tokens[s + 1] : t + 1;
     const long long pos = static_cast<long long>(b.seq_lens[s]) - (static_cast<long long>(end) - t);
     if (pos < 0 || pos > 0x7fffffffLL) return -1;   // more new tokens than the sequence is long

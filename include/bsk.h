@@ -225,7 +225,8 @@ typedef enum bsk_cache_type {
  * [0, num_blocks) that a call needs, or a position past max_blocks blocks, is
  * skipped and reported as BSK_ERR_INVALID_ARG by the blocking call (or the next
  * bsk_stream_check); entries that no token needs are not read.  Token rows
- * outside every sequence (past cu_tokens[num_seqs]) are left alone.
+ * outside every sequence (before cu_tokens[0], from cu_tokens[num_seqs] on) are
+ * left alone, so that cu_tokens may be a part of a larger batch's.
  */
 
 /*

@@ -1,0 +1,94 @@
+"""GPU parity of the paged-cache calls where a number format, a range or a
+bound ends: token arrays whose first rows belong to no sequence, scales of a
+quantised cache far apart or at their least, softmax scales and scores at the
+ends of FP32, loose bounds.  Against the definition in 64 bits, within the bound of
+kv_reference.attention_bound unless a test says otherwise."""
+import math
+
+import pytest
+import torch
+
+import kv_reference as ref
+import test_gpu_kv_attention as att
+from bf16_gemm_skinny_gb300 import _native as bsk
+from bf16_gemm_skinny_gb300 import build as bsk_build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    import oracle
+
+    bsk_build.build()
+    oracle.build()
+    torch.cuda.init()
+    yield bsk.load()
+
+
+@pytest.fixture
+def kernel():
+    """Sets the kernel: 1 many rows (an E4M3 cache converted tile by tile), 2 few rows."""
+    yield lambda k: bsk.set_option("kv_kernel", k)
+    bsk.set_option("kv_kernel", 0)
+
+
+def bits(t):
+    return t.cpu().view(torch.int16) if t.dtype == torch.bfloat16 else t.cpu()
+
+
+# ---------------------------------------------------------------------------
+# Token rows before cu_tokens[0]
+# ---------------------------------------------------------------------------
+def leading(e4m3, first=3):
+    """Two sequences with 2 and 4 new tokens, whose rows begin at `first`."""
+    p = ref.Problem(51, [20, 9], [2, 4], heads=2, group=2, dim=64, page=16, e4m3=e4m3)
+    g = torch.Generator().manual_seed(1)
+    p.cu = [c + first for c in p.cu]
+    p.tokens += first
+    p.fused = torch.randn(p.tokens, p.stride, generator=g).bfloat16()
+    p.q = p.fused[:, :p.hq * p.dim].reshape(p.tokens, p.hq, p.dim)
+    return p
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_leaves_rows_before_the_first_sequence_alone(e4m3):
+    p = leading(e4m3)
+    want = [x if x is None else x.clone() for x in (p.k, p.v, p.ks, p.vs)]
+    for r, s, pos in ref.new_positions(p.cu, p.lens):
+        at = p.tables[s][pos // p.page], pos % p.page
+        for i, col in ((0, p.hq), (1, p.hq + p.heads)):
+            x = p.fused[r, col * p.dim:(col + p.heads) * p.dim].reshape(p.heads, p.dim)
+            if e4m3:
+                want[i][at], want[i + 2][at] = ref.quantise(x)
+            else:
+                want[i][at] = x
+    d = p.device()
+    k, v = d["fused"][:, p.hq * p.dim:], d["fused"][:, (p.hq + p.heads) * p.dim:]
+    bsk.kv_cache_append(int(e4m3), d["k"], d["v"], d["ks"], d["vs"], k, p.stride, v, p.stride, d["cu"], d["tables"],
+                        d["lens"], 2, p.tokens, *p.shape())
+    for name, w in zip(("k", "v", "ks", "vs"), want):
+        assert w is None or torch.equal(bits(d[name]), bits(w)), name
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_gather_leaves_rows_before_the_first_sequence_alone(e4m3):
+    p = leading(e4m3)
+    d = p.device()
+    out = [torch.full((p.tokens, p.heads, p.dim), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    bsk.kv_cache_gather(int(e4m3), d["k"], d["v"], d["ks"], d["vs"], *out, d["cu"], d["tables"], d["lens"], 2, p.tokens,
+                        *p.shape())
+    for o, x in zip(out, p.values()):
+        want = torch.full((p.tokens, p.heads, p.dim), 7.0, dtype=torch.bfloat16)
+        for r, s, pos in ref.new_positions(p.cu, p.lens):
+            want[r] = x[p.tables[s][pos // p.page], pos % p.page].bfloat16()
+        assert torch.equal(bits(o), bits(want))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_leaves_rows_before_the_first_sequence_alone(e4m3):
+    p = leading(e4m3)
+    got = att.run(p)
+    assert torch.isnan(got[:3]).all()
+    got[:3] = 0
+    att.check(p, got)
