@@ -63,7 +63,8 @@ EXPORTS = (
 )
 # Tuning options and test hooks (csrc/bsk_tuning.h): exported for the tests and
 # the benchmark, not part of the C ABI.
-TUNING_EXPORTS = ("bsk_tile_coord", "bsk_set_option", "bsk_get_option", "bsk_test_wait_timeout", "bsk_plan_gemm")
+TUNING_EXPORTS = ("bsk_tile_coord", "bsk_set_option", "bsk_get_option", "bsk_test_wait_timeout", "bsk_plan_gemm",
+                  "bsk_plan_kv_attention")
 
 COL_MAJOR, ROW_MAJOR = 0, 1
 BIAS_NONE, BIAS_ROW, BIAS_COLUMN = 0, 1, 2
@@ -132,6 +133,8 @@ def load():
         lib.bsk_test_wait_timeout.restype = i
         lib.bsk_plan_gemm.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(i)]
         lib.bsk_plan_gemm.restype = i
+        lib.bsk_plan_kv_attention.argtypes = [i] * 13 + [ctypes.POINTER(i)]
+        lib.bsk_plan_kv_attention.restype = i
         _lib = lib
         return lib
 
@@ -406,6 +409,16 @@ def plan_gemm(M: int, N: int, K: int, a_mn_major: bool = True, b_mn_major: bool 
     out = (ctypes.c_int * 7)()
     _check(load().bsk_plan_gemm(M, N, K, int(a_mn_major), int(b_mn_major), int(fp8), sms, out))
     return dict(zip(("block_n", "block_m", "pair", "stream_k", "split_k", "pair_m", "dyn"), list(out)))
+
+
+def plan_kv_attention(cache_type: int, num_seqs: int, num_tokens: int, max_chunk: int, num_q_heads: int,
+                      num_kv_heads: int, head_dim: int, max_seq_len: int, window: int = 0, sinks: int = 0,
+                      num_segments: int = 0, one_token_each: bool = False, sms: int = 152) -> dict:
+    """What chunk_attention would launch for a batch of these sizes (test hook; launches nothing)."""
+    out = (ctypes.c_int * 4)()
+    _check(load().bsk_plan_kv_attention(cache_type, int(one_token_each), num_seqs, num_tokens, max_chunk, num_q_heads,
+                                        num_kv_heads, head_dim, max_seq_len, window, sinks, num_segments, sms, out))
+    return dict(zip(("cta_rows", "tiles", "segments", "flat_rows"), list(out)))
 
 
 def set_option(name: str, value: int) -> None:

@@ -126,6 +126,16 @@ long long bsk_get_option(int key);
 int bsk_plan_gemm(int M, int N, int K, int a_mn_major, int b_mn_major, int fp8, int sms, int* plan);
 
 /*
+ * Test hook: what chunk_attention (one_token_each nonzero: without cu_tokens) would
+ * launch for a batch of these sizes on `sms` SMs under the current options, written
+ * to plan[0..3]: query rows per CTA, row tiles per sequence and KV head, segments of
+ * the keys, rows per sequence of the BF16 copy of an E4M3 cache (0 = none).
+ */
+int bsk_plan_kv_attention(int cache_type, int one_token_each, int num_seqs, int num_tokens, int max_chunk,
+                          int num_q_heads, int num_kv_heads, int head_dim, int max_seq_len, int window, int sinks,
+                          int num_segments, int sms, int* plan);
+
+/*
  * Test hook for the watchdog: launches one CTA that waits on a barrier that
  * nothing completes, using the GEMM's bounded wait with a limit of
  * `limit_us` microseconds (1 .. 10,000,000).  Returns BSK_ERR_TIMEOUT when the

@@ -206,6 +206,13 @@ int enqueue_gather(bsk::KvCopyLaunch& a, cudaStream_t s)
     return BSK_OK;
 }
 
+void plan_attention(bsk::KvAttnLaunch& a, int num_segments)
+{
+    bsk::kv_attention_limit(a);
+    a.kernel = static_cast<int>(bsk_get_option(BSK_OPT_KV_KERNEL));
+    a.segments = num_segments > 0 ? num_segments : bsk::kv_attention_segments(a);
+}
+
 int enqueue_attention(bsk::KvAttnLaunch& a, int num_segments, cudaStream_t s)
 {
     bool empty = false;
@@ -238,8 +245,7 @@ int enqueue_attention(bsk::KvAttnLaunch& a, int num_segments, cudaStream_t s)
     const long long limit_us = bsk_get_option(BSK_OPT_WAIT_LIMIT_US);
     if (limit_us > 0) a.wait_limit_ns = static_cast<unsigned long long>(limit_us) * 1000ull;
     a.pdl = bsk_get_option(BSK_OPT_PDL) != 1;
-    a.kernel = static_cast<int>(bsk_get_option(BSK_OPT_KV_KERNEL));
-    a.segments = num_segments > 0 ? num_segments : bsk::kv_attention_segments(a);
+    plan_attention(a, num_segments);
     Workspace ws(s);
     const size_t bytes = bsk::kv_attention_workspace(a);
     if (bytes > 0) {
@@ -375,6 +381,33 @@ int decode_attention(int cache_type, const void* k_cache, const void* v_cache, c
                            block_tables, seq_lens, num_seqs, num_seqs, 1, num_q_heads, num_kv_heads, head_dim,
                            block_size, max_blocks, num_blocks, max_seq_len, softmax_scale, window, sinks,
                            num_segments, stream);
+}
+
+int bsk_plan_kv_attention(int cache_type, int one_token_each, int num_seqs, int num_tokens, int max_chunk,
+                          int num_q_heads, int num_kv_heads, int head_dim, int max_seq_len, int window, int sinks,
+                          int num_segments, int sms, int* plan)
+{
+    if (plan == nullptr || num_seqs < 1 || num_tokens < 1 || max_chunk < 1 || num_kv_heads < 1 ||
+        num_q_heads < num_kv_heads || head_dim < 1 || max_seq_len < 0 || window < 0 || sinks < 0 || num_segments < 0 ||
+        sms < 1)
+        return fail(BSK_ERR_INVALID_ARG, "plan query: sizes and SM count must be positive, plan non-NULL");
+    static const int32_t some = 0;   // stands for a prefix sum; not read
+    bsk::KvAttnLaunch a;
+    a.b = make_batch(cache_type, nullptr, nullptr, nullptr, nullptr, one_token_each ? nullptr : &some, nullptr, nullptr,
+                     num_seqs, num_tokens, num_kv_heads, head_dim, 1, 1, 1);
+    a.max_chunk = max_chunk;
+    a.num_q_heads = num_q_heads;
+    a.max_seq_len = max_seq_len;
+    a.window = window;
+    a.sinks = sinks;
+    a.num_sms = sms;
+    plan_attention(a, num_segments);
+    const bsk::KvAttnPlan p = bsk::kv_attention_plan(a);
+    plan[0] = p.cta_rows;
+    plan[1] = p.tiles;
+    plan[2] = p.segments;
+    plan[3] = p.flat_rows;
+    return BSK_OK;
 }
 
 }  // extern "C"

@@ -1171,6 +1171,20 @@ int few_rows(const KvAttnLaunch& a)
     return a.kernel == 2 || rows <= (a.b.head_dim == 256 ? 8 : 16) ? few : 0;
 }
 
+int cta_rows_of(const KvAttnLaunch& a)
+{
+    const int few = few_rows(a);
+    return few > 0 ? few : kRows;
+}
+
+// Row tiles per sequence and KV head: at most num_tokens * num_q_heads (kv_attention_limit).
+int row_tiles_of(const KvAttnLaunch& a)
+{
+    const int cta_rows = cta_rows_of(a);
+    const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
+    return static_cast<int>((rows + cta_rows - 1) / cta_rows);
+}
+
 template <bool E4M3, int HD>
 cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, size_t msg_len)
 {
@@ -1184,10 +1198,8 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     p.group = a.num_q_heads / a.b.num_kv_heads;
     p.max_chunk = a.max_chunk;
     p.max_seq_len = a.max_seq_len;
-    const long long max_rows = static_cast<long long>(a.max_chunk) * p.group;
     const int few = few_rows(a);
-    const int cta_rows = few > 0 ? few : kRows;
-    p.tiles = static_cast<int>((max_rows + cta_rows - 1) / cta_rows);
+    p.tiles = row_tiles_of(a);
     p.segments = a.segments;
     // Segments are as many positions for short sequences as for long ones, so that
     // CTAs have equal work in a batch of uneven lengths.
@@ -1295,7 +1307,7 @@ int flat_rows(const KvAttnLaunch& a)
 int kv_attention_segments(const KvAttnLaunch& a)
 {
     const int few = few_rows(a);
-    const int cta_rows = few ? few : kRows;
+    const int cta_rows = cta_rows_of(a);
     const bool two = a.b.head_dim == 64 && (a.b.type == kCacheBF16 || flat_rows(a) > 0);   // CTAs per SM
     const int tile = few || two || a.b.head_dim == 256 ? 64 : 128;
     const long long group = a.num_q_heads / a.b.num_kv_heads;
@@ -1333,6 +1345,22 @@ int kv_attention_segments(const KvAttnLaunch& a)
         }
     }
     return segments;
+}
+
+void kv_attention_limit(KvAttnLaunch& a)
+{
+    const int most = a.b.cu_tokens != nullptr ? a.b.num_tokens : 1;
+    if (a.max_chunk > most) a.max_chunk = most;
+}
+
+KvAttnPlan kv_attention_plan(const KvAttnLaunch& a)
+{
+    KvAttnPlan plan;
+    plan.cta_rows = cta_rows_of(a);
+    plan.tiles = row_tiles_of(a);
+    plan.segments = a.segments;
+    plan.flat_rows = flat_rows(a);
+    return plan;
 }
 
 size_t kv_attention_workspace(const KvAttnLaunch& a)

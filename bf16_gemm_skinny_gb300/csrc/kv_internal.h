@@ -73,6 +73,19 @@ struct KvAttnLaunch {
     unsigned long long wait_limit_ns = 2000000000ull;
     bool pdl = true;
 };
+// The caller's bounds as far as the batch can reach: a sequence brings no more new
+// tokens than there are (without cu_tokens: one).  max_chunk decides the kernel, the
+// grid and the flat copy, and row numbers up to max_chunk * (query heads per KV head)
+// are 32-bit in the kernels; num_tokens * num_q_heads is known to fit.
+void kv_attention_limit(KvAttnLaunch& a);
+// What the call launches (for the planner hook).
+struct KvAttnPlan {
+    int cta_rows = 0;    // query rows per CTA
+    int tiles = 0;       // CTAs' row tiles per sequence and KV head
+    int segments = 1;
+    int flat_rows = 0;   // rows per sequence of the flat copy, or 0
+};
+KvAttnPlan kv_attention_plan(const KvAttnLaunch& a);
 // Segments that a call without a choice of its own splits the keys into (>= 1).
 int kv_attention_segments(const KvAttnLaunch& a);
 size_t kv_attention_workspace(const KvAttnLaunch& a);

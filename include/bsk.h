@@ -270,8 +270,9 @@ int kv_cache_gather(int cache_type, const void* k_cache, const void* v_cache, co
  *
  *   q    [num_tokens, num_q_heads, head_dim] BF16, q_stride elements between tokens
  *   out  the same shape, BF16, out_stride elements between tokens
- *   max_chunk     an upper bound of the new tokens per sequence (host side; a longer
- *                 one is reported like a bad block-table entry, its output undefined)
+ *   max_chunk     an upper bound of the new tokens per sequence (host side, any; above
+ *                 num_tokens it counts as num_tokens; a sequence with more is reported
+ *                 like a bad block-table entry, its output undefined)
  *   max_seq_len   an upper bound of seq_lens (longer ones count as max_seq_len)
  *   softmax_scale finite; 1/sqrt(head_dim) is usual
  *   num_segments  parts that the visible positions are split into when one call has

@@ -92,3 +92,18 @@ def test_attention_leaves_rows_before_the_first_sequence_alone(e4m3):
     assert torch.isnan(got[:3]).all()
     got[:3] = 0
     att.check(p, got)
+
+
+# ---------------------------------------------------------------------------
+# Bounds
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new,group", [([1], 2), ([5, 0, 140], 8), ([300], 2)])
+def test_a_loose_bound_of_new_tokens(e4m3, new, group):
+    """max_chunk far above the tokens there are: as with the exact bound."""
+    lens = [n + 40 for n in new]
+    p = ref.Problem(82, lens, new, 1, group, 64, 16, e4m3)
+    want = att.run(p, max_chunk=sum(new))
+    att.check(p, want)
+    for loose in (2 ** 31 - 1, 2 ** 30 + 5, sum(new) + 1):
+        assert torch.equal(att.run(p, max_chunk=loose), want)

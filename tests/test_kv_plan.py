@@ -1,0 +1,34 @@
+"""What the attention over the paged cache launches, by the planner hook (no GPU)."""
+import pytest
+
+from bf16_gemm_skinny_gb300 import _native as bsk
+from bf16_gemm_skinny_gb300 import build as bsk_build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    bsk_build.build()
+    return bsk.load()
+
+
+BOTH = [bsk.CACHE_BF16, bsk.CACHE_E4M3]
+
+
+@pytest.mark.parametrize("cache", BOTH)
+@pytest.mark.parametrize("group", [1, 2, 8])
+@pytest.mark.parametrize("tokens", [1, 7, 300])
+@pytest.mark.parametrize("loose", [301, 2 ** 20, 2 ** 31 - 1])
+def test_a_loose_bound_of_new_tokens_plans_as_the_number_of_tokens(cache, group, tokens, loose):
+    """max_chunk decides the kernel, the grid and the flat copy; rows up to max_chunk * group are 32-bit numbers."""
+    shape = dict(num_q_heads=2 * group, num_kv_heads=2, head_dim=128, max_seq_len=4000)
+    want = bsk.plan_kv_attention(cache, 1, tokens, tokens, **shape)
+    assert want["tiles"] == -(-tokens * group // want["cta_rows"])
+    assert bsk.plan_kv_attention(cache, 1, tokens, loose, **shape) == want
+
+
+@pytest.mark.parametrize("cache", BOTH)
+def test_one_token_each_plans_as_chunks_of_one(cache):
+    shape = dict(num_q_heads=16, num_kv_heads=4, head_dim=256, max_seq_len=9000)
+    want = bsk.plan_kv_attention(cache, 40, 40, 1, one_token_each=True, **shape)
+    assert want["tiles"] == 1
+    assert bsk.plan_kv_attention(cache, 40, 40, 2 ** 31 - 1, one_token_each=True, **shape) == want
