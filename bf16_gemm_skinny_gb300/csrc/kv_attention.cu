@@ -28,6 +28,7 @@
 // and end, some 6 us (8 sequences decoded through a window of 4096, BF16: 31 us, 4.3 TB/s).
 #include <cmath>
 #include <cstdio>
+#include <limits>
 
 #include "bsk_internal.h"
 #include "kv_attention.cuh"
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 int e = static_cast<int>(m >> 7) - 127 - 14;               // q * 2^-e
                 e = max(-126, min(e, 113));
                 f = exp2f(static_cast<float>(-e));
-                row_scale *= exp2f(static_cast<float>(e));
+                row_scale = row_factor(p.scale_log2, e);
                 named_barrier(1 + quarter, 64);   // s_max is free again
             }
             constexpr int kPart = QW < 32 ? 16 : 32;   // columns at a time
@@ -1205,7 +1206,7 @@ cudaError_t launch_hd(const KvAttnLaunch& a, cudaStream_t stream, char* msg, siz
     // CTAs have equal work in a batch of uneven lengths.
     p.segment_keys = static_cast<int>((most_keys(a) + a.segments * 128LL - 1) / (a.segments * 128LL) * 128);
     // a zero scale still has to keep -inf (a position not seen) at -inf
-    p.scale_log2 = a.scale == 0.f ? 1e-37f : std::fabs(a.scale) * 1.4426950408889634f;
+    p.scale_log2 = a.scale == 0.f ? std::numeric_limits<float>::denorm_min() : std::fabs(a.scale) * 1.4426950408889634f;
     p.q_sign = a.scale < 0.f ? 0x80008000u : 0u;
     p.window = a.window;
     p.sinks = a.sinks;

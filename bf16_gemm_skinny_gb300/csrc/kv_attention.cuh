@@ -79,6 +79,13 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t two)
         : "r"(h));
     return f;
 }
+// The score factor of a query row that was multiplied by 2^-e: never 0, since it also
+// multiplies the -inf of a position out of sight.  FP32's least number stands for what
+// is smaller: scores up to FP32's largest times it are within 2^-21 of 0.
+__device__ __forceinline__ float row_factor(float scale_log2, int e)
+{
+    return fmaxf(scale_log2 * exp2f(static_cast<float>(e)), __uint_as_float(1u));
+}
 struct AttnParams {
     KvBatch b;
     const uint16_t* q;
@@ -89,7 +96,7 @@ struct AttnParams {
     int segment_keys;             // positions of a segment, a multiple of 128 (the last one takes the rest)
     int box;                      // rows per TMA box, or 4: pages of an odd size, gathers only
     int tile_rows;                // cache rows that boxes of a tile's rows may cover
-    float scale_log2;             // |softmax scale| * log2(e), > 0
+    float scale_log2;             // |softmax scale| * log2(e), > 0 (a scale of 0: FP32's least number)
     uint32_t q_sign;              // 0x80008000 for a negative scale
     int window, sinks;
     float* part_o;                // [rows][segments][HD] unnormalised O

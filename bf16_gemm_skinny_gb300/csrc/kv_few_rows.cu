@@ -278,16 +278,14 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
             w[i] = r < rows ? src[i * 32 + lane] ^ p.q_sign : 0u;
             m = __vmaxu2(m, w[i] & 0x7fff7fffu);
         }
-        float scale = p.scale_log2;
         // times a power of two that brings the row's largest value to [2^14, 2^15)
         m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
         const int e = max(-126, min(static_cast<int>(m >> 7) - 127 - 14, 113));
         const float f = exp2f(static_cast<float>(-e));
-        scale *= exp2f(static_cast<float>(e));
 #pragma unroll
         for (int i = 0; i < kPairs; ++i)
             w[i] = f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
-        if (lane == 0) s_scale[r] = scale;
+        if (lane == 0) s_scale[r] = row_factor(p.scale_log2, e);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) *reinterpret_cast<uint32_t*>(s_q + r * kPitch + (i * 32 + lane) * 2) = w[i];
     }

@@ -107,3 +107,19 @@ def test_a_loose_bound_of_new_tokens(e4m3, new, group):
     att.check(p, want)
     for loose in (2 ** 31 - 1, 2 ** 30 + 5, sum(new) + 1):
         assert torch.equal(att.run(p, max_chunk=loose), want)
+
+
+# ---------------------------------------------------------------------------
+# Softmax scales and scores at the ends of FP32
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("which,new", [(0, 5), (1, 5), (2, 5), (1, 70), (0, 200)])
+@pytest.mark.parametrize("scale", [0.0, 1e-45, 1e-38, 1e-30, -1e-8, 0.125])
+def test_small_scales_with_small_queries(kernel, which, new, scale):
+    """Rows of queries that are zero, 2^-40, 2^-110 or as usual: with no scale to speak of, the mean of what they see."""
+    p = ref.Problem(71, [330], [new], 1, 2, 64, 16, True)
+    for r in range(new):
+        p.fused[r, :128] = (p.fused[r, :128].float() * (0.0, 2.0 ** -40, 1.0, 2.0 ** -110)[r % 4]).bfloat16()
+    p.q = p.fused[:new, :128].reshape(new, 2, 64)
+    kernel(which)
+    att.check(p, att.run(p, scale=scale), scale=scale)
+    att.check(p, att.run(p, 17, 2, scale=scale), 17, 2, scale=scale)
