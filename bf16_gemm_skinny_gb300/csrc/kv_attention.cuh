@@ -80,11 +80,12 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t two)
     return f;
 }
 // The score factor of a query row that was multiplied by 2^-e: never 0, since it also
-// multiplies the -inf of a position out of sight.  FP32's least number stands for what
-// is smaller: scores up to FP32's largest times it are within 2^-21 of 0.
+// multiplies the -inf of a position out of sight, and never infinite, since it also
+// multiplies scores of 0.  FP32's least number stands for what is smaller (scores up to
+// FP32's largest times it are within 2^-21 of 0), its largest for what is larger.
 __device__ __forceinline__ float row_factor(float scale_log2, int e)
 {
-    return fmaxf(scale_log2 * exp2f(static_cast<float>(e)), __uint_as_float(1u));
+    return fminf(fmaxf(scale_log2 * exp2f(static_cast<float>(e)), __uint_as_float(1u)), __uint_as_float(0x7f7fffffu));
 }
 struct AttnParams {
     KvBatch b;

@@ -123,3 +123,18 @@ def test_small_scales_with_small_queries(kernel, which, new, scale):
     kernel(which)
     att.check(p, att.run(p, scale=scale), scale=scale)
     att.check(p, att.run(p, 17, 2, scale=scale), 17, 2, scale=scale)
+
+
+@pytest.mark.parametrize("which,new", [(0, 3), (1, 3), (2, 3), (1, 70), (0, 200)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_large_scales_with_large_queries_on_zero_keys(kernel, e4m3, which, new):
+    """Scores of 0 however large scale and query are: the mean of what a token sees."""
+    p = ref.Problem(72, [230], [new], 1, 2, 64, 16, e4m3)
+    p.k[p.used] = 0
+    if e4m3:
+        p.ks[p.used] = 127
+    p.fused[:, :128] = (p.fused[:, :128].float() * 2.0 ** 100).bfloat16()
+    p.q = p.fused[:new, :128].reshape(new, 2, 64)
+    kernel(which)
+    for scale in (2.3e38, 2.0 ** 60, -1.0):
+        att.check(p, att.run(p, scale=scale), scale=scale)

@@ -32,3 +32,10 @@ def test_one_token_each_plans_as_chunks_of_one(cache):
     want = bsk.plan_kv_attention(cache, 40, 40, 1, one_token_each=True, **shape)
     assert want["tiles"] == 1
     assert bsk.plan_kv_attention(cache, 40, 40, 2 ** 31 - 1, one_token_each=True, **shape) == want
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_a_scale_whose_product_with_log2_e_is_infinite_is_refused(scale):
+    with pytest.raises(bsk.BskError, match="softmax_scale"):
+        bsk.decode_attention_enqueue(bsk.CACHE_BF16, 4096, 1 << 20, None, None, 16, 256, 1 << 25, 256, 64, 64, 1, 4, 4, 64, 16,
+                                     8, 8, 128, scale, stream=0)
