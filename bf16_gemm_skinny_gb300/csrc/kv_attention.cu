@@ -189,7 +189,7 @@ struct Geo {
     static constexpr int kRawStages = E4M3 ? 2 : 0;
     static constexpr int kThreads = E4M3 ? 384 + 64 * kConvertWarps : 128 + 32 * kSoftmaxWarps;
     static constexpr int kBars = 4 * kStages + 4 * kRawStages + 2 * kSlots + 8;
-    static constexpr int kScaleBytes = E4M3 ? kSlots * (kTile * 8 + 8) : 0;
+    static constexpr int kScaleBytes = E4M3 ? kSlots * (kTile * 8 + 4) : 0;
     static constexpr int kMisc = kScaleBytes + kSlots * (kTile + 36) * 4 + kSlots * 16 + 2 * 2 * kRows * 4 + kRows * 4 + kBars * 8 + 16;
     static constexpr int kBytes = 1024 + 2 * kStages * kStageBytes + 2 * kRawStages * kRawBytes + kMisc;
     static_assert(kBytes <= 232448 / kCtas - (kCtas - 1) * 1024, "shared memory of one CTA");
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
     uint8_t* r_k = s_v + S * G::kStageBytes;                        // E4M3: [RS] keys' codes
     uint8_t* r_v = r_k + G::kRawStages * G::kRawBytes;              //       [RS] values' codes
     float* s_kf = reinterpret_cast<float*>(r_v + G::kRawStages * G::kRawBytes);   // E4M3: [kSlots][kTile] K scales
-    float* s_vf = s_kf + (E4M3 ? kSlots * kTile : 0);               //       V scales
-    int2* s_exp = reinterpret_cast<int2*>(s_vf + (E4M3 ? kSlots * kTile : 0));    // [kSlots] V scales' range
+    uint32_t* s_vf = reinterpret_cast<uint32_t*>(s_kf + (E4M3 ? kSlots * kTile : 0));   //       V rows' FP16 factors, twice
+    int* s_exp = reinterpret_cast<int*>(s_vf + (E4M3 ? kSlots * kTile : 0));    // [kSlots] V scales' E
     int* s_row = reinterpret_cast<int*>(s_exp + (E4M3 ? kSlots : 0));   // [kSlots][kTile] cache row of each position
     int* s_box = s_row + kSlots * kTile;                            // [kSlots][32] cache row of each box
     int* s_kind = s_box + kSlots * 32;                              // [kSlots][4] (first used) LoadKind of the tile
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
     uint64_t* bars = reinterpret_cast<uint64_t*>(s_flag + kRows);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::kBars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint32_t* s_wide = tmem_slot + 2;              // E4M3: a V scale is out of range
     const uint32_t k_full0 = smem_u32(bars);                // S: a tile's keys are there
     const uint32_t k_empty0 = k_full0 + 8 * S;              // S: ... and read
     const uint32_t v_full0 = k_empty0 + 8 * S;
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(m_full0 + 8 * s, 1);
-            mbar_init(m_empty0 + 8 * s, G::kSoftmaxWarps + 1);
+            mbar_init(m_empty0 + 8 * s, G::kSoftmaxWarps + 1 + (E4M3 ? kConvertWarps : 0));
         }
         mbar_init(q_full, G::kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
@@ -372,6 +373,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         }
         mbar_init(drain, 1);
         *abort_flag = 0u;
+        *s_wide = 0u;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -576,6 +578,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         int entry[PL], entry_off[PL];       // looked up: block-table entry and place in the page
         int row[PL];                        // of the next tile to publish
         uint32_t kb[PL], vb[PL], have = 0;
+        ScaleRange scales;
         auto look_up = [&](int i) {         // tiles in turn
             if (i >= keys.end) return;
             if (i == keys.begin || i == keys.sink_tiles) {
@@ -657,19 +660,27 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
             }
             if (lane == 0) s_kind[slot * 4] = kind;
             if constexpr (E4M3) {
-                int top = 0, low = 255;   // the range of V's exponents, all-zero rows (the least scale) left out
+                // the range of V's exponents, the least scale (that of all-zero rows) left out
+                int top = -1000, low = 1000;
 #pragma unroll
                 for (int u = 0; u < PL; ++u) {
                     s_kf[slot * kTile + u * 32 + lane] = e8m0_value(kb[u]);
-                    s_vf[slot * kTile + u * 32 + lane] = e8m0_value(vb[u]);
                     if (((have >> u) & 1u) != 0 && vb[u] > 10u && vb[u] != 255u) {
-                        top = max(top, static_cast<int>(vb[u]));
-                        low = min(low, static_cast<int>(vb[u]));
+                        top = max(top, static_cast<int>(vb[u]) - 127);
+                        low = min(low, static_cast<int>(vb[u]) - 127);
                     }
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
                 low = __reduce_min_sync(0xffffffffu, low);
-                if (lane == 0) s_exp[slot] = make_int2(top, low);
+                const bool wide = scales.take(top, low);
+#pragma unroll
+                for (int u = 0; u < PL; ++u)
+                    s_vf[slot * kTile + u * 32 + lane] =
+                        0x10001u * (((have >> u) & 1u) != 0 ? scales.factor(vb[u]) : 0x3c00u);
+                if (lane == 0) {
+                    s_exp[slot] = scales.E;
+                    if (wide) *s_wide = 1u;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(m_full0 + 8 * slot);
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
     } else if (warp >= 12) {
         if constexpr (E4M3) {
             // ----------------------------------------------------------------
-            // Codes -> FP16, where the MMAs read them.
+            // Codes -> FP16, where the MMAs read them; values times their row's factor.
             // A failed wait does not leave the loop (see the softmax warps).
             // ----------------------------------------------------------------
             const int tid = (threadIdx.x - 384) % (32 * kConvertWarps);
@@ -708,9 +719,12 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                     const int ch = u * (32 * kConvertWarps) + tid;
                     const int r = ch / CPR, e = ch % CPR;
                     const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                    const uint32_t factor = v ? s_vf[(j % kSlots) * kTile + r] : 0x3c003c00u;
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) o[k] = e4m3x2_f16x2(w[k >> 1] >> (16 * (k & 1)));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], factor);
                     uint8_t* d = dst + ((r >> 3) * NB + (e >> 2)) * 1024 + (r & 7) * 128;
                     // 16-byte chunks permuted by the row; lanes of odd blocks write the later one
                     // first, so that a row's lanes meet distinct banks
@@ -724,6 +738,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 if (lane == 0) {
                     mbar_arrive((v ? rv_empty0 : rk_empty0) + 8 * rs);
                     mbar_arrive((v ? v_full0 : k_full0) + 8 * ss);
+                    if (v) mbar_arrive(m_empty0 + 8 * (j % kSlots));
                 }
             };
             for (int j = 0; j < nt; ++j) convert(j, warp >= 12 + kConvertWarps);
@@ -829,12 +844,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         const int lo_max = p.window > 0 ? pmax - p.window + 1 : 0;                        // the last row's
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
-        // E4M3: O and l hold 2^(3 - E) of their values, E the V scales' largest exponent so
-        // far or up to 4 less, so that weight x scale stays below FP16's 65504 and
-        // loses at most 2^-27 of the largest.  Scales too far apart for that, or far
-        // from 1, set `wide`: then the rows are computed one by one (repair_row).
-        int E = 0, low_e = 1000;
-        bool wide = false;
+        // E4M3 (ScaleRange): O holds 2^(5 - E) of its values, and weights, O and l 2^7 more.
+        int E = 0;
         for (int j = 0; j < nt; ++j) {
             const int buf = j & 1;
             const int slot = j % kSlots;
@@ -854,7 +865,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                         x[c] = make_float2(__uint_as_float(raw[c >> 4][(2 * c) & 31]),
                                            __uint_as_float(raw[c >> 4][(2 * c + 1) & 31]));
                 }
-                float grow_e = 1.f;   // E4M3: factor of O and l for a new E
+                float grow_e = 1.f;   // E4M3: factor of O for a new E
                 if constexpr (E4M3) {
                     const float4* kf = reinterpret_cast<const float4*>(s_kf + slot * kTile + half * C);
 #pragma unroll
@@ -864,16 +875,9 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                         x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(f.z, f.w));
                         if (c % 4 == 3) asm volatile("" ::: "memory");   // no more loads ahead: registers
                     }
-                    const int2 range = s_exp[slot];
-                    if (range.x > 0) {
-                        const int top = range.x - 127;
-                        if (low_e == 1000 || top > E + 4) {   // the first scales, or larger ones
-                            grow_e = exp2_fast(static_cast<float>(E - top));
-                            E = top;
-                        }
-                        low_e = min(low_e, range.y - 127);
-                        wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
-                    }
+                    const int now = s_exp[slot];
+                    if (j > 0) grow_e = exp2_fast(static_cast<float>(E - now));
+                    E = now;
                 }
                 // positions that hold no key, or that this row does not see
                 const int t0 = keys.base(keys.begin + j) + half * C;
@@ -909,12 +913,13 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 if (j == 0) {
                     m = mn;
                 } else if (__any_sync(0xffffffffu, mn > m + 8.f) || (E4M3 && grow_e != 1.f)) {
-                    float f = grow_e;
+                    float f = 1.f;
                     if (mn > m + 8.f) {
-                        f *= exp2_fast(m - mn);
+                        f = exp2_fast(m - mn);
                         m = mn;
                     }
                     l2 = mul2(l2, make_float2(f, f));
+                    f *= grow_e;
                     wait_long(o_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, wc, kSiteKvOutput);   // PV of j - 1
                     tc_fence_after_sync();
                     // this half of the row's O, 16 columns at a time (beside x in registers)
@@ -930,7 +935,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                     }
                 }
                 float base = m == -INFINITY ? 0.f : m;
-                if constexpr (E4M3) base -= static_cast<float>(3 - E);
+                if constexpr (E4M3) base -= kWeightLog2;
                 const float2 sc = make_float2(row_scale, row_scale), nb = make_float2(-base, -base);
                 const uint32_t p_addr = lane_addr + (j & 1) * kTile + half * (C / 2);
 #pragma unroll
@@ -945,13 +950,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                         e1.y = exp2_fast(e1.y);
                         l2 = add2(l2, add2(e0, e1));
                         if constexpr (E4M3) {
-                            const float4 f =
-                                *reinterpret_cast<const float4*>(s_vf + slot * kTile + half * C + 32 * g + 2 * c);
-                            e0 = mul2(e0, make_float2(f.x, f.y));
-                            e1 = mul2(e1, make_float2(f.z, f.w));
                             w[c] = f16x2(e0.x, e0.y);
                             w[c + 1] = f16x2(e1.x, e1.y);
-                            if (c % 8 == 6) asm volatile("" ::: "memory");
                         } else {
                             w[c] = bf16x2(e0.x, e0.y);
                             w[c + 1] = bf16x2(e1.x, e1.y);
@@ -981,8 +981,10 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const long long at = (static_cast<long long>(token) * p.num_q_heads + head) * p.segments + seg;
-            // a split row's partial sums leave out E4M3's 2^(3 - E)
-            const float plain = E4M3 ? exp2f(static_cast<float>(E - 3)) : 1.f;
+            // E4M3: out of the weighted mean, O / l; a split row's partial sums leave out 2^7 too
+            const float mean = E4M3 ? exp2f(static_cast<float>(E - 5)) : 1.f;
+            const float plain = E4M3 ? exp2f(static_cast<float>(E - 5) - kWeightLog2) : 1.f;
+            const bool wide = E4M3 && *s_wide != 0u;
             const long long out_at = p.segments == 1 ? token * p.out_stride + static_cast<long long>(head) * HD : at * HD;
             uint4* stage = reinterpret_cast<uint4*>(s_k + (warp - 4) * 4096);
             static_assert(2 * S * G::kStageBytes >= 4 * H * 4096, "rows of 32 FP32 in the stages");
@@ -1003,7 +1005,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                         uint32_t h[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            h[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                            h[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv * mean,
+                                          __uint_as_float(o[8 * i + 2 * k + 1]) * inv * mean);
                         stage[lane * 4 + (i ^ row_swizzle<4>(lane))] = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                     __syncwarp();
@@ -1034,7 +1037,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                     }
                 }
             }
-            if (p.segments > 1 && half == 0 && r < rows) p.part_ml[at] = make_float2(m, l * plain);
+            if (p.segments > 1 && half == 0 && r < rows) p.part_ml[at] = make_float2(m, E4M3 ? l * exp2f(-kWeightLog2) : l);
             if (((odd != 0.f && l - l == 0.f) || wide) && r < rows) s_flag[r] = 1;   // odd is NaN, l is finite
             if constexpr (H == 2)
                 named_barrier(1 + quarter, 64);

@@ -87,6 +87,40 @@ __device__ __forceinline__ float row_factor(float scale_log2, int e)
 {
     return fminf(fmaxf(scale_log2 * exp2f(static_cast<float>(e)), __uint_as_float(1u)), __uint_as_float(0x7f7fffffu));
 }
+// Scales of E4M3 values.  A row's scale 2^s goes into its FP16 values, not into the
+// weights: a value is code * 2^(s - E + 5), which FP16 holds exactly for s - E from -20
+// (E4M3's least step 2^-9 becomes 2^-24) to 2 (448 becomes 57344), and O is multiplied
+// by 2^(E' - E'') when E moves.  E follows the largest scale in sight, from -40 up, in
+// steps of more than 2.  Weights are stored times 2^7: at most 2^15 (the running maximum
+// may lag by 2^8), exact to FP16's 2^-12 of themselves down to 2^-21 of the row's largest
+// and to 2^-32 of it below.  (The scale in the weights instead, w * 2^(s - E) in FP16, lost
+// the weights of ordinary rows beside one large value that no row attends to.)
+// A row further below E, or one whose O would shrink past FP32, makes the CTA's rows
+// be computed one by one (repair_row).
+struct ScaleRange {
+    int E = -40, low = 1000;
+    // New rows' largest and least exponent (-1000, 1000: none); true: out of range
+    __device__ __forceinline__ bool take(int top, int least)
+    {
+        if (top > E + 2) E = top;
+        low = min(low, least);
+        return least < E - 20 || low < E - 90;
+    }
+    // 2^(s - E + 5) in FP16 for the scale byte b of a row in sight; 0 when that is too small
+    __device__ __forceinline__ uint32_t factor(uint32_t b) const
+    {
+        const int g = static_cast<int>(b) - 127 - E + 5;
+        if (b == 255u) return 0x7e00u;
+        return g >= -14 ? static_cast<uint32_t>(g + 15) << 10 : (g == -15 ? 0x0200u : 0u);
+    }
+};
+constexpr float kWeightLog2 = 7.f;   // weights are stored times 2^this
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 struct AttnParams {
     KvBatch b;
     const uint16_t* q;

@@ -12,7 +12,8 @@
 // (Q is read in the same order); a value's row likewise, two positions' values
 // put side by side with byte permutations.  P goes from the layout of S^T to that
 // of P^T by movmatrix.  E4M3 codes become FP16 pairs by one instruction each
-// (exact), and Q, scaled by a power of two per row, FP16 too.
+// (exact), the values by a second one times their row's scale (ScaleRange, exact), and
+// Q, scaled by a power of two per row, FP16 too.
 //
 // The warps of a CTA take the 32-position steps of its segment in turn.  They are
 // joined in shared memory, the segments by kv_join_kernel.
@@ -312,8 +313,8 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
             for (int i = 0; i < 4; ++i) o[n8][d][i] = 0.f;
     }
     const int lo_max = p.window > 0 ? pmax - p.window + 1 : 0;
-    // E4M3 (as in kv_attention.cu): o and l hold 2^(3 - E) of their values
-    int E = 0, low_e = 1000;
+    // o holds 2^(5 - E) of its values (ScaleRange), and weights, o and l 2^7 more
+    ScaleRange scales;
     bool wide = false;
 
     int at = 0, slot = 0, slot_in = A;   // ring place; places of this step's note and of the next one written
@@ -374,24 +375,24 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
         if (++slot_in > A) slot_in = 0;
         load_keys(at);
         // weights: lane (g, c) has positions g + 8 k and rows 8 n + 2c, 8 n + 2c + 1
-        float grow_e = 1.f, kf[2 * SUB], vf[2 * SUB];
-        const float own_k = e8m0_value(kb_now), own_v = e8m0_value(vb_now);
+        float kf[2 * SUB];
+        const float own_k = e8m0_value(kb_now);
 #pragma unroll
-        for (int k = 0; k < 2 * SUB; ++k) {
-            kf[k] = __shfl_sync(0xffffffffu, own_k, g + 8 * k);
-            vf[k] = __shfl_sync(0xffffffffu, own_v, g + 8 * k);
-        }
-        // the range of V's exponents, all-zero rows (the least scale) left out
+        for (int k = 0; k < 2 * SUB; ++k) kf[k] = __shfl_sync(0xffffffffu, own_k, g + 8 * k);
+        // the range of V's exponents, the least scale (that of all-zero rows) left out
         const bool h = holds && vb_now > 10u && vb_now != 255u;
         const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
         const int low = __reduce_min_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : 1000);
-        if (top > -1000) {
-            if (low_e == 1000 || top > E + 4) {
-                grow_e = exp2_fast(static_cast<float>(E - top));
-                E = top;
-            }
-            low_e = min(low_e, low);
-            wide = wide || E - low_e > 20 || top > 60 || low_e < -60;
+        const int before = scales.E;
+        wide = scales.take(top, low) || wide;
+        const float grow_e = exp2_fast(static_cast<float>(before - scales.E));
+        // this lane's values: positions 2c + 8k and 2c + 8k + 1
+        uint32_t vf[2 * SUB];
+        {
+            uint32_t pair = holds ? scales.factor(vb_now) : 0x3c00u;
+            pair |= __shfl_down_sync(0xffffffffu, pair, 1) << 16;
+#pragma unroll
+            for (int k = 0; k < 2 * SUB; ++k) vf[k] = __shfl_sync(0xffffffffu, pair, 2 * c + 8 * k);
         }
         const bool masked = have != 0xffffffffu || base + F::kGroup - 1 > pmin ||
                             (base < lo_max && base + F::kGroup > p.sinks);
@@ -427,17 +428,18 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
                 mn[q] = fmaxf(m[n8][q], t * row_scale[n8][q]);
             }
-            // O and l move to a new maximum only once it is 2^8 larger (or E changes)
+            // O and l move to a new maximum only once it is 2^8 larger (O also with E)
             if (__any_sync(0xffffffffu, mn[0] > m[n8][0] + 8.f || mn[1] > m[n8][1] + 8.f) || grow_e != 1.f) {
                 float f[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    f[k] = grow_e;
+                    f[k] = 1.f;
                     if (mn[k] > m[n8][k] + 8.f) {
-                        f[k] *= exp2_fast(m[n8][k] - mn[k]);
+                        f[k] = exp2_fast(m[n8][k] - mn[k]);
                         m[n8][k] = mn[k];
                     }
                     l[n8][k] *= f[k];
+                    f[k] *= grow_e;
                 }
 #pragma unroll
                 for (int d = 0; d < kDim; ++d) {
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 b[q] = m[n8][q] == -INFINITY ? 0.f : m[n8][q];
-                b[q] -= static_cast<float>(3 - E);
+                b[q] -= kWeightLog2;
             }
 #pragma unroll
             for (int k = 0; k < 2 * SUB; ++k) {   // positions g + 8 k
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
                     w[q] = exp2_fast(fmaf(x[k][q], row_scale[n8][q], -b[q]));
                     l[n8][q] += w[q];
                 }
-                pt[n8][k] = transpose8x8(f16x2(w[0] * vf[k], w[1] * vf[k]));
+                pt[n8][k] = transpose8x8(f16x2(w[0], w[1]));
             }
         }
         // O^T
@@ -494,10 +496,12 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
                     const uint32_t u1 = __byte_perm(y[0][d >> 1], y[1][d >> 1], 0x7362);
                     const uint32_t u2 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x5140);
                     const uint32_t u3 = __byte_perm(y[2][d >> 1], y[3][d >> 1], 0x7362);
-                    const uint32_t a[2][4] = {{e4m3x2_f16x2(u0), e4m3x2_f16x2(u0 >> 16), e4m3x2_f16x2(u2),
-                                               e4m3x2_f16x2(u2 >> 16)},
-                                              {e4m3x2_f16x2(u1), e4m3x2_f16x2(u1 >> 16), e4m3x2_f16x2(u3),
-                                               e4m3x2_f16x2(u3 >> 16)}};
+                    const uint32_t f0 = vf[2 * b], f1 = vf[2 * b + 1];
+                    const uint32_t a[2][4] = {
+                        {mul_f16x2(e4m3x2_f16x2(u0), f0), mul_f16x2(e4m3x2_f16x2(u0 >> 16), f0),
+                         mul_f16x2(e4m3x2_f16x2(u2), f1), mul_f16x2(e4m3x2_f16x2(u2 >> 16), f1)},
+                        {mul_f16x2(e4m3x2_f16x2(u1), f0), mul_f16x2(e4m3x2_f16x2(u1 >> 16), f0),
+                         mul_f16x2(e4m3x2_f16x2(u3), f1), mul_f16x2(e4m3x2_f16x2(u3 >> 16), f1)}};
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
     __syncthreads();   // the ring becomes s_o
 
     // ---- the warps' results ---------------------------------------------------
-    const float plain = exp2f(static_cast<float>(E - 3));
+    const float plain = exp2f(static_cast<float>(scales.E - 5) - kWeightLog2);
     constexpr int kPairs = kHalf ? 4 : kVec / 2;
 #pragma unroll
     for (int n8 = 0; n8 < R; ++n8) {
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
             t += __shfl_xor_sync(0xffffffffu, t, 16);
             if (g == 0) {
                 s_m[warp][8 * n8 + 2 * c + k] = m[n8][k];
-                s_l[warp][8 * n8 + 2 * c + k] = t * plain;
+                s_l[warp][8 * n8 + 2 * c + k] = t * exp2f(-kWeightLog2);
             }
         }
 #pragma unroll

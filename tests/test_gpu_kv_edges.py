@@ -138,3 +138,83 @@ def test_large_scales_with_large_queries_on_zero_keys(kernel, e4m3, which, new):
     kernel(which)
     for scale in (2.3e38, 2.0 ** 60, -1.0):
         att.check(p, att.run(p, scale=scale), scale=scale)
+
+
+# ---------------------------------------------------------------------------
+# Scales of a quantised cache's values
+# ---------------------------------------------------------------------------
+def put(p, t, x=None, y=None):
+    """Position t of sequence 0: keys x, values y."""
+    b, o = p.tables[0][t // p.page], t % p.page
+    if x is not None:
+        p.k[b, o], p.ks[b, o] = ref.quantise(x.bfloat16())
+    if y is not None:
+        p.v[b, o], p.vs[b, o] = ref.quantise(y.bfloat16())
+
+
+def flat_tail(n, new, group, dim, tail, spread, where, peak_value=1.0):
+    """One sequence of n positions whose scores are the same but for two: one key with 2^tail times the others' weight,
+    and one whose value is 2^spread times as large and either has no weight or is seen by the last token only."""
+    p = ref.Problem(61, [n], [new], 1, group, dim, 16)
+    g = torch.Generator().manual_seed(62)
+    p.e4m3 = True
+    p.k = torch.zeros(p.k.shape, dtype=torch.uint8)
+    p.v = torch.randint(0x28, 0x7f, p.v.shape, generator=g, dtype=torch.uint8)     # 0.25 .. 448, all positive
+    p.ks = torch.full(p.k.shape[:-1], 127, dtype=torch.uint8)
+    p.vs = p.ks.clone()
+    p.fused[:, :group * dim] = 1.0
+    p.q = p.fused[:, :group * dim].reshape(new, group, dim)
+    one = torch.ones(1, dim)
+    score = 1 / (dim * (1 / math.sqrt(dim)))                                       # a constant key's value per unit of score
+    put(p, 3, one * (tail * math.log(2) * score), None if peak_value else 0 * one)
+    t = n - 1 if where == "unseen" else 7
+    if where == "weightless":
+        put(p, t, one * (-100 * score))
+    if spread:
+        p.vs[p.tables[0][t // 16], t % 16] = 127 + spread
+    return p
+
+
+TAILS = [(4, 2000, 10), (9, 2000, 10), (12, 4000, 11), (14, 4000, 11), (16, 4000, 10), (20, 200, 7.5), (20, 4000, 9)]
+
+
+@pytest.mark.parametrize("where", ["weightless", "unseen"])
+@pytest.mark.parametrize("which,new,dim", [(0, 4, 128), (2, 4, 64), (2, 4, 256), (1, 4, 128), (1, 70, 64), (1, 70, 256), (0, 300, 128)])
+@pytest.mark.parametrize("spread,n,tail", TAILS)
+def test_a_large_value_of_no_weight_costs_the_others_nothing(kernel, spread, n, tail, which, new, dim, where):
+    p = flat_tail(max(n, new), new, 2, dim, tail, spread, where)
+    kernel(which)
+    att.check(p, att.run(p))
+    att.check(p, att.run(p, segments=3))
+
+
+@pytest.mark.parametrize("which,new", [(0, 2), (1, 2), (2, 40)])
+def test_a_flat_tail_beside_a_key_without_value(kernel, which, new):
+    """Weights of 2^-22 of the row's largest, whose own value is zero: FP16 weights beside E4M3 values hold them to 2^-10."""
+    p = flat_tail(4000, new, 2, 128, 22, 0, "weightless", peak_value=0.0)
+    kernel(which)
+    att.check(p, att.run(p))
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("spread,tail", [(14, 14), (12, 16.5), (8, 18)])
+def test_long_flat_tails(kernel, which, spread, tail):
+    p = flat_tail(30000, 2, 2, 64, tail, spread, "weightless")
+    k, v = p.values()
+    out, span, reach = ref.attention_on_gpu(p.q, k, v, p.tables, p.cu, p.lens, 1, 16, 1 / 8)
+    kernel(which)
+    assert ((att.run(p).double() - out).abs() <= ref.attention_bound(out, span, reach, 1 / 8, 64, 30000)).all()
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("step", [3, -3, 17, -17])
+def test_scales_that_rise_and_fall(kernel, which, step):
+    """Scales from 2^-40 to 2^40 in steps along the sequence; windows of like and of unlike rows."""
+    n = 400
+    p = ref.Problem(63, [n], [60], 1, 2, 64, 16, True)
+    for t in range(n):
+        e = (t // 20 * step) % 81 - 40
+        p.vs[p.tables[0][t // 16], t % 16] = 127 + e
+    kernel(which)
+    for window, sinks in ((0, 0), (15, 0), (40, 2)):
+        att.check(p, att.run(p, window, sinks), window, sinks)
