@@ -701,37 +701,48 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 const uint8_t* raw = (v ? r_v : r_k) + rs * G::kRawBytes;
                 uint8_t* dst = (v ? s_v : s_k) + ss * G::kStageBytes;
                 wait_long((v ? rv_full0 : rk_full0) + 8 * rs, (j / RS) & 1, wc, kSiteKvRaw);
-                uint4 x[kChunks];
-#pragma unroll
-                for (int u = 0; u < kChunks; ++u) {
+                auto codes = [&](int u) {
                     const int ch = u * (32 * kConvertWarps) + tid;
                     const int r = ch / CPR, e = ch % CPR;
                     // the line (128 bytes; 64 with HD = 64) of row r's codes, and the chunk in it,
                     // swizzled by the line's place
                     const int line = ((e >> 3) * kTile + r) * (HD == 64 ? 64 : 128);
                     const int c = (e & 7) ^ ((line >> 7) & (HD == 64 ? 3 : 7));
-                    x[u] = *reinterpret_cast<const uint4*>(raw + line + c * 16);
-                }
+                    return *reinterpret_cast<const uint4*>(raw + line + c * 16);
+                };
                 wait_long((v ? v_empty0 : k_empty0) + 8 * ss, ((j / S) & 1) ^ 1, wc, kSiteKvEmpty);
                 if (j == S - 1) wait_long(q_full, 0, wc, kSiteKvQ);   // Q came through this stage
+                // Two chunks at a time: the warps of a CTA run six different loops, and more code
+                // here costs them all (chunks of a few tokens over 2000 to 9000, head_dim 256: 53.8 us
+                // with two, 56.4 with four, 63.4 with all eight).
+                constexpr int kAtOnce = 2;
+#pragma unroll 1
+                for (int u0 = 0; u0 < kChunks; u0 += kAtOnce) {
+                    uint4 x[kAtOnce];
+                    uint32_t factor[kAtOnce];
 #pragma unroll
-                for (int u = 0; u < kChunks; ++u) {
-                    const int ch = u * (32 * kConvertWarps) + tid;
-                    const int r = ch / CPR, e = ch % CPR;
-                    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                    const uint32_t factor = v ? s_vf[(j % kSlots) * kTile + r] : 0x3c003c00u;
-                    uint32_t o[8];
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        x[u] = codes(u0 + u);
+                        factor[u] = v ? s_vf[(j % kSlots) * kTile + ((u0 + u) * (32 * kConvertWarps) + tid) / CPR] : 0x3c003c00u;
+                    }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = e4m3x2_f16x2(w[k >> 1] >> (16 * (k & 1)));
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        const int ch = (u0 + u) * (32 * kConvertWarps) + tid;
+                        const int r = ch / CPR, e = ch % CPR;
+                        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                        // factor 0, the least scale: all zeros, or a code whose value this sum leaves out?
+                        if (factor[u] == 0u && ((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) != 0u) *s_wide = 1u;
+                        uint32_t o[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], factor);
-                    uint8_t* d = dst + ((r >> 3) * NB + (e >> 2)) * 1024 + (r & 7) * 128;
-                    // 16-byte chunks permuted by the row; lanes of odd blocks write the later one
-                    // first, so that a row's lanes meet distinct banks
-                    const int c16 = (e & 3) * 2, flip = (e >> 2) & 1;
-                    const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-                    *reinterpret_cast<uint4*>(d + (((c16 + flip) ^ (r & 7)) << 4)) = flip ? b : a;
-                    *reinterpret_cast<uint4*>(d + (((c16 + 1 - flip) ^ (r & 7)) << 4)) = flip ? a : b;
+                        for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(e4m3x2_f16x2(w[k >> 1] >> (16 * (k & 1))), factor[u]);
+                        uint8_t* d = dst + ((r >> 3) * NB + (e >> 2)) * 1024 + (r & 7) * 128;
+                        // 16-byte chunks permuted by the row; lanes of odd blocks write the later one
+                        // first, so that a row's lanes meet distinct banks
+                        const int c16 = (e & 3) * 2, flip = (e >> 2) & 1;
+                        const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4*>(d + (((c16 + flip) ^ (r & 7)) << 4)) = flip ? b : a;
+                        *reinterpret_cast<uint4*>(d + (((c16 + 1 - flip) ^ (r & 7)) << 4)) = flip ? a : b;
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();

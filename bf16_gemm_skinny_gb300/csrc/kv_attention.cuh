@@ -96,7 +96,9 @@ __device__ __forceinline__ float row_factor(float scale_log2, int e)
 // and to 2^-32 of it below.  (The scale in the weights instead, w * 2^(s - E) in FP16, lost
 // the weights of ordinary rows beside one large value that no row attends to.)
 // A row further below E, or one whose O would shrink past FP32, makes the CTA's rows
-// be computed one by one (repair_row).
+// be computed one by one (repair_row).  Rows at the least scale, 2^-117, may be zeros,
+// which mind no factor: they stay out of the range, their factor is 0 (E is -40 at
+// least), and the first code among them that is not 0 does the same.
 struct ScaleRange {
     int E = -40, low = 1000;
     // New rows' largest and least exponent (-1000, 1000: none); true: out of range

@@ -469,6 +469,18 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
         // O^T
         cp_async_wait<2 * A - 1>();      // this group's values
         const uint8_t* vs = ring + A * F::kKeyBytes + at * F::kValBytes;
+        if (__any_sync(0xffffffffu, holds && vb_now <= 10u)) {
+            // rows at the least scale: all zeros, or a code whose value this sum leaves out?
+#pragma unroll
+            for (int k = 0; k < 4 * SUB; ++k) {
+                const bool none = ((k & 1) != 0 ? vf[k >> 1] >> 16 : vf[k >> 1] & 0xffffu) == 0u;
+#pragma unroll
+                for (int v = 0; v < kValVecs; ++v) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(vs + (k * kValVecs + v) * 512);
+                    wide = wide || (none && ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0u);
+                }
+            }
+        }
 #pragma unroll
         for (int b = 0; b < SUB; ++b) {
 #pragma unroll
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
                     make_float2(o[n8][d][k] * plain, o[n8][d][2 + k] * plain);
         }
     }
-    if (wide && lane == 0) atomicOr(&s_flag, 0xffff);
+    if (__any_sync(0xffffffffu, wide) && lane == 0) atomicOr(&s_flag, 0xffff);
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (HD / 4); i += kWarps * 32) {
         const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;

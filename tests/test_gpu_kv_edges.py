@@ -218,3 +218,40 @@ def test_scales_that_rise_and_fall(kernel, which, step):
     kernel(which)
     for window, sinks in ((0, 0), (15, 0), (40, 2)):
         att.check(p, att.run(p, window, sinks), window, sinks)
+
+
+# ---------------------------------------------------------------------------
+# The least scale (2^-117)
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("which,new", [(0, 3), (1, 3), (2, 3), (1, 90), (0, 200)])
+@pytest.mark.parametrize("others", ["none", "zero", "large"])
+def test_values_under_the_least_scale(kernel, which, new, others):
+    """Values of 2^-112 to 2^-122 (their scale is held at 2^-117), alone, beside rows of zeros, and beside rows of
+    ordinary size that most tokens do not see."""
+    n = 300
+    p = ref.Problem(64, [n], [new], 1, 2, 64, 16, True)
+    g = torch.Generator().manual_seed(65)
+    for t in range(n):
+        x = torch.randn(1, 64, generator=g) * 2.0 ** (-112 - t % 11)
+        if others == "zero" and t % 3 == 1:
+            x = x * 0
+        if others == "large" and t in (n - 1, n - 101):
+            x = x.sign()
+        put(p, t, None, x)
+    kernel(which)
+    assert int(p.vs.min()) == 10
+    for window, sinks in ((0, 0), (20, 0)):
+        att.check(p, att.run(p, window, sinks), window, sinks)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_rows_of_zeros_among_ordinary_values(kernel, which):
+    """Zero rows have the least scale: whole tiles of them, before, between and after others."""
+    n = 500
+    p = ref.Problem(66, [n], [6], 1, 2, 64, 16, True)
+    for t in range(n):
+        if t < 130 or t % 5 == 0 or t > 400:
+            put(p, t, None, torch.zeros(1, 64))
+    kernel(which)
+    for window, sinks in ((0, 0), (60, 3), (480, 0)):
+        att.check(p, att.run(p, window, sinks), window, sinks)
