@@ -669,6 +669,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                         top = max(top, static_cast<int>(vb[u]) - 127);
                         low = min(low, static_cast<int>(vb[u]) - 127);
                     }
+                    if (k_scale_too_large(kb[u])) low = -1000;   // out of any range
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
                 low = __reduce_min_sync(0xffffffffu, low);

@@ -196,12 +196,12 @@ __device__ __forceinline__ void row_add(const KvBatch& b, const int32_t* table, 
         float k[EPL], v[EPL];
         load_slice<E4M3, EPL>(b.k, hr * HD + lane * EPL, k);
         load_slice<E4M3, EPL>(b.v, hr * HD + lane * EPL, v);
+        const float ks = E4M3 ? e8m0_value(b.k_scales[hr]) : 1.f;
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s = fmaf(q[i], k[i], s);
+        for (int i = 0; i < EPL; ++i) s = fmaf(q[i], k[i] * ks, s);
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-        if constexpr (E4M3) s *= e8m0_value(b.k_scales[hr]);
         s *= scale_log2;
         const float vs = E4M3 ? e8m0_value(b.v_scales[hr]) : 1.f;
         const float mn = fmaxf(m, s);
@@ -253,6 +253,11 @@ __device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* tabl
         if (lane == 0) p.part_ml[at] = make_float2(m, l);
     }
 }
+
+// A score is (sum of 2^-e q * code) * K scale * row_factor, and the sum up to 2^32 (q up to
+// 2^15, codes to 448, 256 of them), so that beside a K scale above 2^95 it may pass FP32
+// although q.k does not: such a key in sight makes the CTA's rows be computed one by one.
+__device__ __forceinline__ bool k_scale_too_large(uint32_t b) { return b - 223u < 32u; }
 
 // Launches the kernel for few query rows over an E4M3 cache: `rows` (8, or 16 with
 // HD < 256) per CTA, p.tiles of them per sequence and KV head.

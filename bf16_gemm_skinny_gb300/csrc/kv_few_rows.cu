@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
         // the range of V's exponents, the least scale (that of all-zero rows) left out
         const bool h = holds && vb_now > 10u && vb_now != 255u;
         const int top = __reduce_max_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : -1000);
-        const int low = __reduce_min_sync(0xffffffffu, h ? static_cast<int>(vb_now) - 127 : 1000);
+        const bool far = holds && k_scale_too_large(kb_now);   // out of any range
+        const int low = __reduce_min_sync(0xffffffffu, far ? -1000 : (h ? static_cast<int>(vb_now) - 127 : 1000));
         const int before = scales.E;
         wide = scales.take(top, low) || wide;
         const float grow_e = exp2_fast(static_cast<float>(before - scales.E));

@@ -255,3 +255,18 @@ def test_rows_of_zeros_among_ordinary_values(kernel, which):
     kernel(which)
     for window, sinks in ((0, 0), (60, 3), (480, 0)):
         att.check(p, att.run(p, window, sinks), window, sinks)
+
+
+# ---------------------------------------------------------------------------
+# Scales of a quantised cache's keys
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("which,new", [(0, 2), (1, 2), (2, 2), (1, 70)])
+@pytest.mark.parametrize("e", [80, 100, 112, 119])
+def test_large_keys_with_small_queries(kernel, which, new, e):
+    """Keys about 2^e beside queries about 2^-e: ordinary scores."""
+    p = ref.Problem(73, [200], [new], 1, 2, 64, 16, True)
+    p.ks = (p.ks.int() + e).clamp(max=247).to(torch.uint8)
+    p.fused[:, :128] = (p.fused[:, :128].float() * 2.0 ** -e).bfloat16()
+    p.q = p.fused[:new, :128].reshape(new, 2, 64)
+    kernel(which)
+    att.check(p, att.run(p))
