@@ -50,6 +50,7 @@ OPTIONS = {
     "k_order": 17,
     "pair_m": 18,
     "kv_kernel": 19,
+    "kv_workspace_kb": 20,
 }
 
 # Every symbol include/bsk.h (the C ABI) declares.

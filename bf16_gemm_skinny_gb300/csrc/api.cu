@@ -47,7 +47,7 @@ int fail_cuda(cudaError_t e, const char* what)
 // ----------------------------------------------------------------------------
 // options
 // ----------------------------------------------------------------------------
-constexpr int kNumOpts = 20;
+constexpr int kNumOpts = 21;
 std::atomic<long long> g_opt[kNumOpts];
 
 long long opt_or(int key, long long dflt)
@@ -1305,6 +1305,7 @@ int bsk_set_option(int key, long long value)
     case BSK_OPT_K_ORDER: ok = value == 0 || value == 1; break;
     case BSK_OPT_PAIR_M: ok = value >= 0 && value <= 2; break;
     case BSK_OPT_KV_KERNEL: ok = value >= 0 && value <= 2; break;
+    case BSK_OPT_KV_WORKSPACE_KB: ok = value >= 0 && value <= 1LL << 40; break;
     case BSK_OPT_WAIT_LIMIT_US: ok = value >= 0 && value <= 60000000; break;
     case BSK_OPT_NUM_SMS: ok = value >= 0 && value <= 100000; break;
     default: ok = false;

@@ -87,6 +87,8 @@ void bsk_tile_coord(int t, int num_m, int num_n, int group_m, int* pid_m, int* p
  *   BSK_OPT_KV_KERNEL        kernel of chunk_attention and decode_attention: 0 automatic, 1 the
  *                            tcgen05 kernel (128 query rows per CTA) on the cache as it is, 2 for
  *                            an E4M3 cache the kernel for few rows (8 or 16 per CTA)
+ *   BSK_OPT_KV_WORKSPACE_KB  test hook: workspaces of chunk_attention and decode_attention larger
+ *                            than this many KiB count as failed allocations (0: none do)
  * Returns BSK_ERR_INVALID_ARG for an unknown key or a value out of range.
  */
 enum {
@@ -108,7 +110,8 @@ enum {
     BSK_OPT_PREFETCH_KB = 16,
     BSK_OPT_K_ORDER = 17,
     BSK_OPT_PAIR_M = 18,
-    BSK_OPT_KV_KERNEL = 19
+    BSK_OPT_KV_KERNEL = 19,
+    BSK_OPT_KV_WORKSPACE_KB = 20
 };
 int bsk_set_option(int key, long long value);
 long long bsk_get_option(int key);

@@ -41,6 +41,8 @@ struct Workspace {
     }
     cudaError_t take(size_t bytes)
     {
+        const long long limit_kb = bsk_get_option(BSK_OPT_KV_WORKSPACE_KB);
+        if (limit_kb > 0 && bytes > static_cast<unsigned long long>(limit_kb) * 1024ull) return cudaErrorMemoryAllocation;
         cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
         cudaError_t e = cudaStreamIsCapturing(s, &capture);
         cudaMemPool_t pool = nullptr;
@@ -248,14 +250,25 @@ int enqueue_attention(bsk::KvAttnLaunch& a, int num_segments, cudaStream_t s)
     a.pdl = bsk_get_option(BSK_OPT_PDL) != 1;
     plan_attention(a, num_segments);
     Workspace ws(s);
-    const size_t bytes = bsk::kv_attention_workspace(a);
-    if (bytes > 0) {
-        const cudaError_t e = ws.take(bytes);
-        if (e != cudaSuccess)
-            return fail(BSK_ERR_NO_MEMORY, "cudaMallocAsync(%zu bytes) for a workspace failed: %s", bytes,
-                        cudaGetErrorString(e));
-        a.workspace = static_cast<float*>(ws.ptr);
+    size_t bytes = bsk::kv_attention_workspace(a);
+    cudaError_t e = bytes > 0 ? ws.take(bytes) : cudaSuccess;
+    // The flat copy and segments of the library's own choice are for speed: without room
+    // for them the cache is converted tile by tile, and read in one segment.
+    if (e == cudaErrorMemoryAllocation && bsk::kv_attention_plan(a).flat_rows > 0) {
+        a.flat_copy = false;
+        plan_attention(a, num_segments);
+        bytes = bsk::kv_attention_workspace(a);
+        e = bytes > 0 ? ws.take(bytes) : cudaSuccess;
     }
+    if (e == cudaErrorMemoryAllocation && num_segments == 0) {
+        a.segments = 1;
+        bytes = 0;
+        e = cudaSuccess;
+    }
+    if (e != cudaSuccess)
+        return fail(BSK_ERR_NO_MEMORY, "cudaMallocAsync(%zu bytes) for a workspace failed: %s", bytes,
+                    cudaGetErrorString(e));
+    a.workspace = static_cast<float*>(ws.ptr);
     char msg[512] = "";
     if (bsk::launch_kv_attention(a, s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
     return BSK_OK;

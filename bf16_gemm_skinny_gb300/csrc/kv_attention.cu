@@ -1312,7 +1312,7 @@ size_t partial_bytes(const KvAttnLaunch& a)
 int flat_rows(const KvAttnLaunch& a)
 {
     const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
-    if (a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < (a.b.head_dim == 256 ? 1024 : 256)) return 0;
+    if (!a.flat_copy || a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < (a.b.head_dim == 256 ? 1024 : 256)) return 0;
     const long long len = (a.max_seq_len + 127LL) / 128 * 128;
     const long long bytes = len * a.b.num_seqs * a.b.num_kv_heads * a.b.head_dim * 4;
     return len * a.b.num_seqs <= 0x7fffffffLL && bytes <= (2LL << 30) ? static_cast<int>(len) : 0;

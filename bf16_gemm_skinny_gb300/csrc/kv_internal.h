@@ -68,6 +68,7 @@ struct KvAttnLaunch {
     int window = 0, sinks = 0;     // window 0: every earlier position is visible
     int kernel = 0;                // 0 automatic, 1 many rows (tcgen05), 2 few rows
     int segments = 1;              // kv_attention_segments()
+    bool flat_copy = true;         // false: no flat copy of an E4M3 cache (no memory for it)
     float* workspace = nullptr;    // kv_attention_workspace() bytes, or nullptr when that is 0
     int num_sms = 1;
     unsigned long long wait_limit_ns = 2000000000ull;

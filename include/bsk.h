@@ -286,7 +286,8 @@ int kv_cache_gather(int cache_type, const void* k_cache, const void* v_cache, co
  * E4M3 cache that at least 256 query rows per KV head (1024 with head_dim 256; rows
  * are max_chunk * num_q_heads / num_kv_heads) are to read, its positions as BF16, if
  * num_seqs * max_seq_len * num_kv_heads * head_dim * 4 bytes are at most 2 GiB (a
- * larger one is converted tile by tile).  Blocking; the _enqueue forms only launch.
+ * larger one, or one that there is no memory for, is converted tile by tile; without
+ * memory for automatic segments there is one).  Blocking; the _enqueue forms only launch.
  * decode_attention is the form for one new token per sequence (q and out have
  * num_seqs rows).
  */

@@ -270,3 +270,48 @@ def test_large_keys_with_small_queries(kernel, which, new, e):
     p.q = p.fused[:new, :128].reshape(new, 2, 64)
     kernel(which)
     att.check(p, att.run(p))
+
+
+# ---------------------------------------------------------------------------
+# Workspaces
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def workspace_kb():
+    yield lambda kb: bsk.set_option("kv_workspace_kb", kb)
+    bsk.set_option("kv_workspace_kb", 0)
+
+
+@pytest.mark.parametrize("segments", [0, 1, 3])
+def test_no_memory_for_the_flat_copy(workspace_kb, segments):
+    """A quantised cache read by many rows is converted tile by tile where its BF16 copy finds no room."""
+    p = ref.Problem(91, [900, 700], [300, 150], 2, 2, 128, 16, True)
+    plan = bsk.plan_kv_attention(bsk.CACHE_E4M3, 2, 450, 300, 4, 2, 128, 900, num_segments=segments)
+    copy = plan["flat_rows"] * 2 * 2 * 128 * 4
+    assert copy > 0
+    att.check(p, att.run(p, segments=segments))
+    workspace_kb(copy // 1024 - 1)
+    if segments == 3 and 450 * 4 * 3 * 130 * 4 > (copy // 1024 - 1) * 1024:
+        with pytest.raises(bsk.BskError) as exc:   # the segments' own workspace does not fit either
+            att.run(p, segments=segments)
+        assert exc.value.status == 5
+        return
+    att.check(p, att.run(p, segments=segments))
+    att.check(p, att.run(p, 100, 3, segments=segments), 100, 3)
+
+
+def test_no_memory_for_the_segments(workspace_kb):
+    p = ref.Problem(92, [900], [1], 2, 2, 128, 16, True)
+    workspace_kb(1)
+    with pytest.raises(bsk.BskError) as exc:
+        att.run(p, segments=8)
+    assert exc.value.status == 5 and "workspace" in str(exc.value)
+    workspace_kb(0)
+    att.check(p, att.run(p, segments=8))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_no_memory_for_segments_of_its_own_choice(workspace_kb, e4m3):
+    p = ref.Problem(93, [3000], [1], 1, 2, 128, 16, e4m3)
+    assert bsk.plan_kv_attention(int(e4m3), 1, 1, 1, 2, 1, 128, 3000)["segments"] > 1
+    workspace_kb(1)
+    att.check(p, att.run(p))
