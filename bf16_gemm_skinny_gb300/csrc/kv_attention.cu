@@ -1309,8 +1309,16 @@ size_t partial_bytes(const KvAttnLaunch& a)
 // convert them again.  Microseconds without / with it, 30000 positions: head_dim 256,
 // 512 rows 94 / 105, 1024 rows 156 / 148, 2048 rows 301 / 256; 128, 256 rows 78 / 75,
 // 512 rows 139 / 99, 2048 rows 502 / 264; 64, 256 rows 37 / 36, 2048 rows 223 / 114.
+// In a batch of prompts and single tokens it also passes over the sequences that few
+// rows read, so the rows per sequence count too, on average.  8000 positions, one
+// prompt among single tokens (4 among 12 for the last of 256), 8 rows a token (256: 4):
+// head_dim 256, 19 rows on average 352 / 829, 131 332 / 501, 515 741 / 791, 1026 621 / 573;
+// 128, 39 rows 799 / 884, 135 591 / 525, 519 1368 / 934; 64, 39 rows 753 / 592.
 int flat_rows(const KvAttnLaunch& a)
 {
+    const long long all_rows = static_cast<long long>(a.b.num_tokens) * (a.num_q_heads / a.b.num_kv_heads);
+    const int average = a.b.head_dim == 256 ? 1024 : (a.b.head_dim == 128 ? 96 : 32);
+    if (all_rows < static_cast<long long>(average) * a.b.num_seqs) return 0;
     const long long rows = static_cast<long long>(a.max_chunk) * (a.num_q_heads / a.b.num_kv_heads);
     if (!a.flat_copy || a.b.type != kCacheE4M3 || few_rows(a) > 0 || a.kernel == 1 || rows < (a.b.head_dim == 256 ? 1024 : 256)) return 0;
     const long long len = (a.max_seq_len + 127LL) / 128 * 128;

@@ -284,7 +284,8 @@ int kv_cache_gather(int cache_type, const void* k_cache, const void* v_cache, co
  * nearest even.  A workspace is allocated in stream order: with more than one
  * segment num_tokens * num_q_heads * segments * (head_dim + 2) floats, and for an
  * E4M3 cache that at least 256 query rows per KV head (1024 with head_dim 256; rows
- * are max_chunk * num_q_heads / num_kv_heads) are to read, its positions as BF16, if
+ * are max_chunk * num_q_heads / num_kv_heads) are to read, and 32, 96 or 1024 (head_dim
+ * 64, 128, 256) on average over the sequences, its positions as BF16, if
  * num_seqs * max_seq_len * num_kv_heads * head_dim * 4 bytes are at most 2 GiB (a
  * larger one, or one that there is no memory for, is converted tile by tile; without
  * memory for automatic segments there is one).  Blocking; the _enqueue forms only launch.

@@ -39,3 +39,15 @@ def test_a_scale_whose_product_with_log2_e_is_infinite_is_refused(scale):
     with pytest.raises(bsk.BskError, match="softmax_scale"):
         bsk.decode_attention_enqueue(bsk.CACHE_BF16, 4096, 1 << 20, None, None, 16, 256, 1 << 25, 256, 64, 64, 1, 4, 4, 64, 16,
                                      8, 8, 128, scale, stream=0)
+
+
+@pytest.mark.parametrize("dim,heads,group,chunk,singles,copied", [
+    (128, 8, 8, 256, 63, False), (128, 8, 8, 512, 31, True), (128, 8, 8, 4096, 31, True), (128, 8, 8, 256, 0, True),
+    (64, 8, 8, 256, 63, True), (64, 8, 8, 256, 100, False),
+    (256, 4, 4, 256, 63, False), (256, 4, 4, 2048, 31, False), (256, 4, 4, 2048, 3, True), (256, 4, 4, 256, 0, True),
+])
+def test_one_prompt_among_single_tokens_has_the_whole_cache_copied_only_where_it_pays(dim, heads, group, chunk, singles,
+                                                                                      copied):
+    """The BF16 copy of a quantised cache goes by the rows that read a sequence on average, not by the longest chunk's."""
+    plan = bsk.plan_kv_attention(bsk.CACHE_E4M3, singles + 1, singles + chunk, chunk, heads * group, heads, dim, 8000 if singles < 64 else 4000)
+    assert (plan["flat_rows"] > 0) == copied
