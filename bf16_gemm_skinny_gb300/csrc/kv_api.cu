@@ -227,6 +227,8 @@ int enqueue_attention(bsk::KvAttnLaunch& a, int num_segments, cudaStream_t s)
     if (a.max_chunk <= 0 && !empty) return fail(BSK_ERR_INVALID_ARG, "max_chunk must be positive (got %d)", a.max_chunk);
     if (a.max_seq_len < 0 || static_cast<long long>(a.max_seq_len) > static_cast<long long>(b.max_blocks) * b.block_size)
         return fail(BSK_ERR_INVALID_ARG, "max_seq_len %d is negative or exceeds max_blocks * block_size", a.max_seq_len);
+    if (a.max_seq_len > INT_MAX - 255)   // whole tiles of positions are counted in 32 bits
+        return fail(BSK_ERR_INVALID_ARG, "max_seq_len %d exceeds 2^31 - 256", a.max_seq_len);
     if (!std::isfinite(a.scale * 1.4426950408889634f))   // the kernels' factor, for powers of two
         return fail(BSK_ERR_INVALID_ARG, "softmax_scale must be finite, and so must softmax_scale * log2(e)");
     if (a.window < 0 || a.sinks < 0)

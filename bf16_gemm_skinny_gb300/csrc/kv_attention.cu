@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
     const int pmin = pos0 + row0 / p.group, pmax = pos0 + (row0 + rows - 1) / p.group;
     Keys<kTile> keys;
     keys.kv_end = max(pmax + 1, 0);
-    keys.lo = p.window > 0 && pmin - p.window + 1 > 0 ? pmin - p.window + 1 : 0;
+    keys.lo = window_start(pmin, p.window);
     keys.sink_end = min(p.sinks, keys.lo);
     keys.lo_tile = keys.lo / kTile;
     keys.sink_tiles = min((keys.sink_end + kTile - 1) / kTile, keys.lo_tile);
@@ -852,8 +852,8 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
-        const int lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;   // this row's window
-        const int lo_max = p.window > 0 ? pmax - p.window + 1 : 0;                        // the last row's
+        const int lo = window_start(pos, p.window);        // this row's
+        const int lo_max = window_start(pmax, p.window);   // the last row's
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         // E4M3 (ScaleRange): O holds 2^(5 - E) of its values, and weights, O and l 2^7 more.

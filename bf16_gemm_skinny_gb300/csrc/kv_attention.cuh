@@ -141,6 +141,13 @@ struct AttnParams {
     unsigned long long wait_limit_ns;
 };
 
+// The first position in the window of a query at `pos` (which may be negative, and the
+// window up to 2^31 - 1); no window: 0.
+__device__ __forceinline__ int window_start(int pos, int window)
+{
+    return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 // The key tiles that some row of a CTA sees: those of the sinks, then those from
 // the window's first on.  A position holds a key when it is below kv_end and not
 // between sink_end and lo.
@@ -231,7 +238,7 @@ __device__ __noinline__ void repair_row(const AttnParams& p, const int32_t* tabl
         o[i] = 0.f;
     }
     float m = -INFINITY, l = 0.f;
-    const int lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+    const int lo = window_start(pos, p.window);
     const int sinks = min(p.sinks, lo);
     for (int part = 0; part < 2; ++part) {   // the segment's sink tiles, then its window tiles
         const int i0 = part == 0 ? keys.begin : max(keys.begin, keys.sink_tiles);

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
     const int pmin = pos0 + row0 / p.group, pmax = pos0 + (row0 + rows - 1) / p.group;
     Keys<F::kGroup> keys;
     keys.kv_end = max(pmax + 1, 0);
-    keys.lo = p.window > 0 && pmin - p.window + 1 > 0 ? pmin - p.window + 1 : 0;
+    keys.lo = window_start(pmin, p.window);
     keys.sink_end = min(p.sinks, keys.lo);
     keys.lo_tile = keys.lo / F::kGroup;
     keys.sink_tiles = min((keys.sink_end + F::kGroup - 1) / F::kGroup, keys.lo_tile);
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
             const int r = 8 * n8 + 2 * c + i;
             row_scale[n8][i] = s_scale[r];
             row_pos[n8][i] = r < rows ? pos0 + (row0 + r) / p.group : -1;
-            row_lo[n8][i] = p.window > 0 && row_pos[n8][i] - p.window + 1 > 0 ? row_pos[n8][i] - p.window + 1 : 0;
+            row_lo[n8][i] = window_start(row_pos[n8][i], p.window);
             m[n8][i] = -INFINITY;
             l[n8][i] = 0.f;
         }
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(Few<HD, R>::kWarps * 32, Few<HD, R>::kCtas) kv
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n8][d][i] = 0.f;
     }
-    const int lo_max = p.window > 0 ? pmax - p.window + 1 : 0;
+    const int lo_max = window_start(pmax, p.window);
     // o holds 2^(5 - E) of its values (ScaleRange), and weights, o and l 2^7 more
     ScaleRange scales;
     bool wide = false;

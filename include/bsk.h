@@ -273,7 +273,8 @@ int kv_cache_gather(int cache_type, const void* k_cache, const void* v_cache, co
  *   max_chunk     an upper bound of the new tokens per sequence (host side, any; above
  *                 num_tokens it counts as num_tokens; a sequence with more is reported
  *                 like a bad block-table entry, its output undefined)
- *   max_seq_len   an upper bound of seq_lens (longer ones count as max_seq_len)
+ *   max_seq_len   an upper bound of seq_lens (longer ones count as max_seq_len), at
+ *                 most max_blocks * block_size and 2^31 - 256
  *   softmax_scale at most 2.35e38 in magnitude; 1/sqrt(head_dim) is usual.  Scores
  *                 q.k_t and scale * q.k_t within FP32's range are meant
  *   num_segments  parts that the visible positions are split into when one call has

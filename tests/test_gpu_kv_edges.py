@@ -315,3 +315,55 @@ def test_no_memory_for_segments_of_its_own_choice(workspace_kb, e4m3):
     assert bsk.plan_kv_attention(int(e4m3), 1, 1, 1, 2, 1, 128, 3000)["segments"] > 1
     workspace_kb(1)
     att.check(p, att.run(p))
+
+
+# ---------------------------------------------------------------------------
+# Positions at the ends of 32 bits
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new", [25, 200])
+def test_a_window_of_any_size_beside_positions_below_zero(e4m3, new):
+    """More new tokens than positions, and windows up to 2^31 - 1."""
+    p = ref.Problem(81, [10, 30], [new, 5], 2, 2, 64, 16, e4m3)
+    for window in (2 ** 31 - 1, 2 ** 31 - 8, 1000, 4):
+        got = att.run(p, window, 0, max_len=32)
+        assert not got[:new - 10].any()
+        att.check(p, got, window, 0)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new", [1, 40])
+def test_the_longest_sequence(e4m3, new):
+    """2^31 - 256 positions in pages of 2^20 that all share two blocks, seen through a window with sinks."""
+    page, blocks, dim, n = 2 ** 20, 2, 64, 2 ** 31 - 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    k, v = (torch.randint(0x20, 0x40, (blocks, page, 1, dim), generator=g, device="cuda", dtype=torch.uint8) if e4m3 else
+            torch.randn(blocks, page, 1, dim, generator=g, device="cuda", dtype=torch.float32).bfloat16() for _ in range(2))
+    s = [torch.full((blocks, page, 1), 127, dtype=torch.uint8, device="cuda") if e4m3 else None for _ in range(2)]
+    assert k.dtype == dt
+    tables = (torch.arange(2048, dtype=torch.int32, device="cuda") % 2).reshape(1, -1)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    q = torch.randn(new, 2 * dim, generator=g, device="cuda").bfloat16()
+    window, sinks = 200, 70
+    def values(c, sc):
+        at = torch.cat([torch.arange(sinks), torch.arange(n - new - window, n)])
+        rows = ((at // page) % 2 * page + at % page).cuda()
+        x = c.reshape(-1, dim)[rows]
+        return at, (ref.dequantise(x.cpu(), torch.full((len(at),), 127, dtype=torch.uint8)) if e4m3 else x.cpu().double())
+    at, kk = values(k, s[0])
+    _, vv = values(v, s[1])
+    out = torch.full((new, 2 * dim), math.nan, dtype=torch.bfloat16, device="cuda")
+    bsk.chunk_attention(int(e4m3), k, v, *s, q, 2 * dim, out, 2 * dim, cu, tables, lens, 1, new, new, 2, 1, dim, page, 2048,
+                        blocks, n, 1 / 8, window, sinks)
+    got = out.cpu().reshape(new, 2, dim).double()
+    for i in range(new):
+        p = n - new + i
+        seen = (at <= p) & ((at > p - window) | (at < sinks))
+        for h in range(2):
+            qq = q[i, h * dim:(h + 1) * dim].cpu().double()
+            w = torch.softmax((kk @ qq / 8).masked_fill(~seen, -math.inf), 0)
+            want, spread = w @ vv, w @ vv.abs()
+            bound = ref.attention_bound(want, spread, (kk.abs() @ qq.abs()).max(), 1 / 8, dim, int(seen.sum()))
+            assert ((got[i, h] - want).abs() <= bound).all(), (i, h)

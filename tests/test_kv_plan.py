@@ -51,3 +51,10 @@ def test_one_prompt_among_single_tokens_has_the_whole_cache_copied_only_where_it
     """The BF16 copy of a quantised cache goes by the rows that read a sequence on average, not by the longest chunk's."""
     plan = bsk.plan_kv_attention(bsk.CACHE_E4M3, singles + 1, singles + chunk, chunk, heads * group, heads, dim, 8000 if singles < 64 else 4000)
     assert (plan["flat_rows"] > 0) == copied
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 255, 2 ** 31 - 1])
+def test_lengths_whose_whole_tiles_pass_32_bits_are_refused(length):
+    with pytest.raises(bsk.BskError, match="max_seq_len"):
+        bsk.decode_attention_enqueue(bsk.CACHE_BF16, 4096, 1 << 30, None, None, 16, 256, 1 << 40, 256, 64, 64, 1, 4, 4, 64, 1 << 20,
+                                     2048, 2, length, 0.125, 100, 0, stream=0)
