@@ -287,7 +287,8 @@ def _load_calls():
     load()
     path = _build.CALLS_PATH
     if not os.path.exists(path):
-        raise RuntimeError(f"_calls.so not built ({path}); run bf16_gemm_skinny_gb300.build.build()")
+        raise RuntimeError(f"the module _calls is not built for this interpreter ({path}): run "
+                           "bf16_gemm_skinny_gb300.build.build(), which needs the interpreter's headers (Python.h)")
     with _lock:
         if _calls is None:
             loader = importlib.machinery.ExtensionFileLoader("_calls", path)
