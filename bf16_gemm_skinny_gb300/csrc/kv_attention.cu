@@ -713,10 +713,11 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                 };
                 wait_long((v ? v_empty0 : k_empty0) + 8 * ss, ((j / S) & 1) ^ 1, wc, kSiteKvEmpty);
                 if (j == S - 1) wait_long(q_full, 0, wc, kSiteKvQ);   // Q came through this stage
-                // Two chunks at a time: the warps of a CTA run six different loops, and more code
-                // here costs them all (chunks of a few tokens over 2000 to 9000, head_dim 256: 53.8 us
-                // with two, 56.4 with four, 63.4 with all eight).
-                constexpr int kAtOnce = 2;
+                // One or two chunks at a time: the warps of a CTA run six different loops, and more
+                // code here costs them all.  Chunks of a few tokens over 2000 to 9000, head_dim 256:
+                // 56.5 us with one, 53.5 with two, 56.4 with four, 63.4 with all eight; 2048 rows over
+                // 30000 positions without the flat copy, head_dim 64: 221 us with one, 244 with two.
+                constexpr int kAtOnce = HD == 256 ? 2 : 1;
 #pragma unroll 1
                 for (int u0 = 0; u0 < kChunks; u0 += kAtOnce) {
                     uint4 x[kAtOnce];
@@ -735,7 +736,11 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                         if (factor[u] == 0u && ((w[0] | w[1] | w[2] | w[3]) & 0x7f7f7f7fu) != 0u) *s_wide = 1u;
                         uint32_t o[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(e4m3x2_f16x2(w[k >> 1] >> (16 * (k & 1))), factor[u]);
+                        for (int k = 0; k < 8; ++k) o[k] = e4m3x2_f16x2(w[k >> 1] >> (16 * (k & 1)));
+                        if (v) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] = mul_f16x2(o[k], factor[u]);
+                        }
                         uint8_t* d = dst + ((r >> 3) * NB + (e >> 2)) * 1024 + (r & 7) * 128;
                         // 16-byte chunks permuted by the row; lanes of odd blocks write the later one
                         // first, so that a row's lanes meet distinct banks
