@@ -19,13 +19,15 @@
 // on their way and an MMA reads one operand from it (with Q there too, head_dim 256
 // took 1040 us where this took 927).
 //
-// Bound, long chunks: shared memory.  A tile is 1024 clocks of MMAs (head_dim 128 and
-// 256); in them shared memory takes its 64 KB of keys and values from the TMA unit (57
-// bytes a clock at best) and gives the MMAs 64 KB.  Measured about 1850 clocks a tile:
-// 2048 tokens over 30720 (16 query heads, 4 KV heads of 256, BF16) 858 us, 1240 TFLOP/s,
-// 0.67 of the tensor cores' measured rate.  head_dim 64: the exponentials (a windowed
-// chunk of 4097 tokens, 32 heads, 72 us, 420 TFLOP/s).  Few rows: HBM and a CTA's start
-// and end, some 6 us (8 sequences decoded through a window of 4096, BF16: 31 us, 4.3 TB/s).
+// Bound, long chunks: a tile is 1024 clocks of MMAs (head_dim 128 and 256) and takes about
+// 1850.  Its 64 KB of keys and values come from the TMA unit in 1150 (57 bytes a clock at
+// best); the rest is one set of softmax warps that takes tile after tile (load S,
+// exchange the maximum, exponentials, store P).  2048 tokens over 30720 (16 query heads,
+// 4 KV heads of 256, BF16): 856 to 883 us by box, 1200 to 1240 TFLOP/s, 0.63 to 0.65 of
+// the tensor cores' measured rate.  head_dim 64: the same per tile, and the start and end
+// of a CTA, some 6 us each over 3.5 waves of CTAs (a windowed chunk of 4097 tokens, 32
+// heads, 73 us, of which the exponentials alone would be 25).  Few rows: HBM and a CTA's
+// start and end (8 sequences decoded through a window of 4096, BF16: 31 us, 4.3 TB/s).
 #include <cmath>
 #include <cstdio>
 #include <limits>
@@ -145,7 +147,7 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, const W
 constexpr int kRows = 128;        // query rows per CTA (the M of the MMAs)
 // Warps 12 .. convert E4M3 codes, four of them keys and four values.  32 sequences of
 // up to 4000 tokens, 16 rows of head_dim 256: 105 us with four warps for both in turn,
-// 89 with eight, 77 with four for each.
+// 89 with eight, 77 with four for each (78 now).
 constexpr int kConvertWarps = 4;
 constexpr int kSlots = 8;         // tiles whose cache rows, masks and scales are kept
 
@@ -970,6 +972,9 @@ __global__ void __launch_bounds__(Geo<E4M3, HD>::kThreads, Geo<E4M3, HD>::kCtas)
                             w[c] = f16x2(e0.x, e0.y);
                             w[c + 1] = f16x2(e1.x, e1.y);
                         } else {
+                            // BF16, since an MMA's operands have one type and FP16 does not hold BF16
+                            // values: 2^-8 of a weight at most (outputs are 0.0023 off in the mean,
+                            // where weights in FP32 give 0.0017, the output's own rounding)
                             w[c] = bf16x2(e0.x, e0.y);
                             w[c + 1] = bf16x2(e1.x, e1.y);
                         }
@@ -1180,9 +1185,9 @@ long long most_keys(const KvAttnLaunch& a)
 // Rows per CTA of the kernel for few query rows per KV head, or 0: the call takes
 // the other kernel.  An E4M3 cache read for few rows would spend its time in the
 // other kernel's shared memory.  Measured in microseconds, many-row / few-row kernel
-// (32 sequences of up to 4000 tokens; one of 30000): head_dim 256, 8 rows 78 / 77, 31 / 29,
-// 16 rows 78 / 125, 31 / 42; 128, 8 rows 132 / 67, 41 / 25, 16 rows 123 / 78, 42 / 29, 24 rows
-// 122 / 127, 42 / 42; 64, 16 rows 63 / 44, 23 / 18, 32 rows 63 / 66, 24 / 23.  On a BF16 cache
+// (32 sequences of up to 4000 tokens; one of 30000): head_dim 256, 8 rows 79 / 79, 31 / 30,
+// 16 rows 78 / 129, 31 / 43; 128, 8 rows 135 / 68, 42 / 25, 16 rows 123 / 80, 42 / 30, 24 rows
+// 123 / 131, 43 / 43; 64, 16 rows 62 / 45, 22 / 18, 32 rows 63 / 68, 24 / 23.  On a BF16 cache
 // it did not pay: 8 rows of 256 83 / 130, of 128 91 / 117, of 64 46 / 45.
 int few_rows(const KvAttnLaunch& a)
 {
@@ -1312,13 +1317,13 @@ size_t partial_bytes(const KvAttnLaunch& a)
 // Rows of a sequence in the flat BF16 copy of an E4M3 cache, or 0: no copy is made.
 // It costs one pass over the positions in sight; without it every 128 query rows
 // convert them again.  Microseconds without / with it, 30000 positions: head_dim 256,
-// 512 rows 94 / 105, 1024 rows 156 / 148, 2048 rows 301 / 256; 128, 256 rows 78 / 75,
-// 512 rows 139 / 99, 2048 rows 502 / 264; 64, 256 rows 37 / 36, 2048 rows 223 / 114.
+// 512 rows 94 / 105, 1024 rows 159 / 150, 2048 rows 304 / 257; 128, 256 rows 79 / 75,
+// 512 rows 142 / 99, 2048 rows 521 / 261; 64, 256 rows 37 / 36, 2048 rows 217 / 114.
 // In a batch of prompts and single tokens it also passes over the sequences that few
 // rows read, so the rows per sequence count too, on average.  8000 positions, one
 // prompt among single tokens (4 among 12 for the last of 256), 8 rows a token (256: 4):
-// head_dim 256, 19 rows on average 352 / 829, 131 332 / 501, 515 741 / 791, 1026 621 / 573;
-// 128, 39 rows 799 / 884, 135 591 / 525, 519 1368 / 934; 64, 39 rows 753 / 592.
+// head_dim 256, 19 rows on average 353 / 829, 131 330 / 501, 515 735 / 791, 1026 607 / 573;
+// 128, 39 rows 774 / 884, 135 572 / 526, 519 1332 / 934; 64, 39 rows 686 / 589.
 int flat_rows(const KvAttnLaunch& a)
 {
     const long long all_rows = static_cast<long long>(a.b.num_tokens) * (a.num_q_heads / a.b.num_kv_heads);
@@ -1333,6 +1338,12 @@ int flat_rows(const KvAttnLaunch& a)
 
 }  // namespace
 
+// An estimate: it counts tiles of 64 or 128 positions, while a segment's positions are
+// rounded to 128 (so that the last of many segments may be empty: 10 of 74 for one
+// sequence of 32768), and two CTAs of the few-row kernel per SM, which has four below
+// head_dim 256.  One sequence of 32768, E4M3, head_dim 256: 607 us in one segment, 116 in
+// 6, 34 in 32, 28 in the 74 it takes; 8 chunks of 1-6 tokens over 2000-9000: 160, 46,
+// 74, and 53 in its 7; three chunks of 300 tokens over 9000, BF16: 136 (its choice), 167, 353.
 int kv_attention_segments(const KvAttnLaunch& a)
 {
     const int few = few_rows(a);

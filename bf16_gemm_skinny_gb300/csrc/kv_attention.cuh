@@ -92,9 +92,9 @@ __device__ __forceinline__ float row_factor(float scale_log2, int e)
 // (E4M3's least step 2^-9 becomes 2^-24) to 2 (448 becomes 57344), and O is multiplied
 // by 2^(E' - E'') when E moves.  E follows the largest scale in sight, from -40 up, in
 // steps of more than 2.  Weights are stored times 2^7: at most 2^15 (the running maximum
-// may lag by 2^8), exact to FP16's 2^-12 of themselves down to 2^-21 of the row's largest
-// and to 2^-32 of it below.  (The scale in the weights instead, w * 2^(s - E) in FP16, lost
-// the weights of ordinary rows beside one large value that no row attends to.)
+// may lag by 2^8), off by 2^-11 of themselves at most down to 2^-21 of the row's largest
+// and by 2^-32 of it below that.  (The scale in the weights instead, w * 2^(s - E) in
+// FP16, lost the weights of ordinary rows beside one large value that no row attends to.)
 // A row further below E, or one whose O would shrink past FP32, makes the CTA's rows
 // be computed one by one (repair_row).  Rows at the least scale, 2^-117, may be zeros,
 // which mind no factor: they stay out of the range, their factor is 0 (E is -40 at

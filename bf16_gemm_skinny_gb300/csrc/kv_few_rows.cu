@@ -18,12 +18,12 @@
 // The warps of a CTA take the 32-position steps of its segment in turn.  They are
 // joined in shared memory, the segments by kv_join_kernel.
 //
-// Bound: the latency of a warp's step (some 700 instructions, 6 to 16 warps per SM);
-// without its MMAs, or on a few pages read over and over, it is under 4% faster.
-// Measured: 64 sequences of up to 8000 tokens, 64 heads over 8 KV heads of 128: 149 us,
-// 3.7 TB/s (0.55 of the measured copy rate; 231 us with loads into registers, 181 with
-// 16 positions a step); one of 32768, 16 heads over 4 of 256: 27 us, 2.5 TB/s, of
-// which 19 us do not depend on the length.
+// Bound: the latency of a warp's step (some 750 instructions, 6 to 16 warps per SM);
+// without its MMAs, or on a few pages read over and over, it was under 4% faster.
+// Measured: 64 sequences of up to 8000 tokens, 64 heads over 8 KV heads of 128: 148 to
+// 150 us, 3.7 TB/s (0.55 of the measured copy rate; 231 us with loads into registers, 181
+// with 16 positions a step); one of 32768, 16 heads over 4 of 256: 28 us, 2.4 TB/s, of
+// which some 19 us do not depend on the length.
 #include <cstdio>
 
 #include "bsk_internal.h"

@@ -280,18 +280,33 @@ int kv_cache_gather(int cache_type, const void* k_cache, const void* v_cache, co
  *   num_segments  parts that the visible positions are split into when one call has
  *                 too few tokens to fill the GPU, 1..256; 0 = automatic
  *
- * FP32 scores, statistics and sums; the weights are rounded to BF16 (beside E4M3
- * values, which become FP16, to FP16) for the tensor cores, the output once, to
- * nearest even.  A workspace is allocated in stream order: with more than one
- * segment num_tokens * num_q_heads * segments * (head_dim + 2) floats, and for an
- * E4M3 cache that at least 256 query rows per KV head (1024 with head_dim 256; rows
- * are max_chunk * num_q_heads / num_kv_heads) are to read, and 32, 96 or 1024 (head_dim
- * 64, 128, 256) on average over the sequences, its positions as BF16, if
- * num_seqs * max_seq_len * num_kv_heads * head_dim * 4 bytes are at most 2 GiB (a
- * larger one, or one that there is no memory for, is converted tile by tile; without
- * memory for automatic segments there is one).  Blocking; the _enqueue forms only launch.
- * decode_attention is the form for one new token per sequence (q and out have
- * num_seqs rows).
+ * FP32 scores, statistics and sums; the weights are rounded for the tensor cores,
+ * the output once, to nearest even.  Beside BF16 values, those of the copy below
+ * among them, weights become BF16 (2^-8 of themselves at most).  Beside E4M3 values
+ * taken as they are, values become FP16, exactly, and weights FP16: 2^-11 of
+ * themselves at most down to 2^-21 of the row's largest, below that 2^-32 of the
+ * largest.  So a token's output over an E4M3 cache may differ in its last bits with
+ * the batch it is in.  decode_attention_bf16 keeps its weights in FP32 (mean error
+ * 0.0017 against 64 bits, the output's rounding; decode_attention over BF16 0.0023)
+ * and takes 1.1 to 2.4 times as long: take it where those bits count.
+ *
+ * Some contents take a path that computes one row after the other, with the same
+ * results but 16 to 230 times as slow: values that are not finite where a token does
+ * not see them, and, over an E4M3 cache that is not copied, keys with scales above
+ * 2^95 and values, not all zeros, with scales more than 2^20 below the largest in
+ * sight or below 2^-60.
+ *
+ * A workspace is allocated in stream order, from a pool of the library's own that
+ * keeps up to 2 GiB mapped for later calls (in a stream that is being captured, from
+ * the default pool).  With more than one segment it is num_tokens * num_q_heads *
+ * segments * (head_dim + 2) floats.  An E4M3 cache that many query rows per KV head
+ * read has its positions copied as BF16 first: at least 256 rows (1024 with head_dim
+ * 256; rows are max_chunk * num_q_heads / num_kv_heads) and 32, 96 or 1024 (head_dim
+ * 64, 128, 256) on average over the sequences, if num_seqs * max_seq_len *
+ * num_kv_heads * head_dim * 4 bytes are at most 2 GiB (a larger one, or one that there
+ * is no memory for, is converted tile by tile; without memory for automatic segments
+ * there is one).  Blocking; the _enqueue forms only launch.  decode_attention is the
+ * form for one new token per sequence (q and out have num_seqs rows).
  */
 int chunk_attention(int cache_type, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
                     const uint8_t* v_scales, const uint16_t* q, int q_stride, uint16_t* out, int out_stride,
