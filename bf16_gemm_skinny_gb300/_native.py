@@ -1,5 +1,6 @@
 """Binding of libbsk (argument marshalling only), by ctypes; the calls on the
-paged cache, of which a decode step makes several per layer, by a small extension.
+paged cache and of the feed-forward layers, of which a decode step makes several
+per layer, by a small extension.
 
 Each function takes CUDA tensors (any 16-bit dtype; only ``data_ptr()`` is
 used) or raw device addresses as ints, plus an optional stream (a
@@ -51,6 +52,8 @@ OPTIONS = {
     "pair_m": 18,
     "kv_kernel": 19,
     "kv_workspace_kb": 20,
+    "linear_kernel": 21,
+    "linear_tile": 22,
 }
 
 # Every symbol include/bsk.h (the C ABI) declares.
@@ -61,6 +64,9 @@ EXPORTS = (
     "gemm_fp8", "bsk_gemm_fp8_enqueue", "gemm_f16_colmajor_host", "gemv_bf16_host",
     "kv_cache_append", "bsk_kv_cache_append_enqueue", "kv_cache_gather", "bsk_kv_cache_gather_enqueue",
     "chunk_attention", "bsk_chunk_attention_enqueue", "decode_attention", "bsk_decode_attention_enqueue",
+    "linear_act", "bsk_linear_act_enqueue", "gated_linear", "bsk_gated_linear_enqueue",
+    "linear_act_backward", "bsk_linear_act_backward_enqueue", "gated_linear_backward",
+    "bsk_gated_linear_backward_enqueue",
 )
 # Tuning options and test hooks (csrc/bsk_tuning.h): exported for the tests and
 # the benchmark, not part of the C ABI.
@@ -72,6 +78,9 @@ BIAS_NONE, BIAS_ROW, BIAS_COLUMN = 0, 1, 2
 FP8_E4M3, FP8_E5M2 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 CACHE_BF16, CACHE_E4M3 = 0, 1
+TYPE_BF16, TYPE_F16 = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+GRAD_F32, GRAD_16 = 0, 1
 
 
 class BskError(RuntimeError):
@@ -393,6 +402,84 @@ def decode_attention_enqueue(cache_type: int, k_cache, v_cache, k_scales, v_scal
                                               out_stride, block_tables, seq_lens, num_seqs, num_q_heads, num_kv_heads,
                                               head_dim, block_size, max_blocks, num_blocks, max_seq_len, softmax_scale,
                                               window, sinks, num_segments, _stream(stream)))
+
+
+def linear_act(type: int, W, w_stride: int, x, x_stride: int, bias, residual, residual_stride: int, y, y_stride: int,
+               z, z_stride: int, M: int, K: int, n: int, activation: int, stream=None) -> None:
+    """y = act(x W^T + bias) + residual, and z = x W^T + bias where it is kept (see include/bsk.h);
+    blocks until done."""
+    calls = _calls or _load_calls()
+    _check(calls.linear_act(type, W, w_stride, x, x_stride, bias, residual, residual_stride, y, y_stride, z,
+                            z_stride, M, K, n, activation, _stream(stream)))
+
+
+def linear_act_enqueue(type: int, W, w_stride: int, x, x_stride: int, bias, residual, residual_stride: int, y,
+                       y_stride: int, z, z_stride: int, M: int, K: int, n: int, activation: int,
+                       stream=None) -> None:
+    """Asynchronous variant of linear_act (check with stream_check)."""
+    calls = _calls or _load_calls()
+    _check(calls.bsk_linear_act_enqueue(type, W, w_stride, x, x_stride, bias, residual, residual_stride, y, y_stride,
+                                        z, z_stride, M, K, n, activation, _stream(stream)))
+
+
+def gated_linear(type: int, Wg, Wu, w_stride: int, x, x_stride: int, bias_g, bias_u, h, h_stride: int, g, u,
+                 gu_stride: int, M: int, K: int, n: int, activation: int, stream=None) -> None:
+    """h = act(x Wg^T + bias_g) * (x Wu^T + bias_u), and both factors where they are kept (see include/bsk.h);
+    blocks until done."""
+    calls = _calls or _load_calls()
+    _check(calls.gated_linear(type, Wg, Wu, w_stride, x, x_stride, bias_g, bias_u, h, h_stride, g, u, gu_stride, M,
+                              K, n, activation, _stream(stream)))
+
+
+def gated_linear_enqueue(type: int, Wg, Wu, w_stride: int, x, x_stride: int, bias_g, bias_u, h, h_stride: int, g, u,
+                         gu_stride: int, M: int, K: int, n: int, activation: int, stream=None) -> None:
+    """Asynchronous variant of gated_linear (check with stream_check)."""
+    calls = _calls or _load_calls()
+    _check(calls.bsk_gated_linear_enqueue(type, Wg, Wu, w_stride, x, x_stride, bias_g, bias_u, h, h_stride, g, u,
+                                          gu_stride, M, K, n, activation, _stream(stream)))
+
+
+def linear_act_backward(type: int, W, w_stride: int, x, x_stride: int, z, z_stride: int, dy, dy_stride: int, dx,
+                        dx_stride: int, dW, dw_stride: int, dbias, grad_type: int, accumulate: int, M: int, K: int,
+                        n: int, activation: int, stream=None) -> None:
+    """Gradients of linear_act: dx, dW and dbias, each where it is wanted (see include/bsk.h);
+    blocks until done."""
+    calls = _calls or _load_calls()
+    _check(calls.linear_act_backward(type, W, w_stride, x, x_stride, z, z_stride, dy, dy_stride, dx, dx_stride, dW,
+                                     dw_stride, dbias, grad_type, accumulate, M, K, n, activation, _stream(stream)))
+
+
+def linear_act_backward_enqueue(type: int, W, w_stride: int, x, x_stride: int, z, z_stride: int, dy, dy_stride: int,
+                                dx, dx_stride: int, dW, dw_stride: int, dbias, grad_type: int, accumulate: int,
+                                M: int, K: int, n: int, activation: int, stream=None) -> None:
+    """Asynchronous variant of linear_act_backward (check with stream_check)."""
+    calls = _calls or _load_calls()
+    _check(calls.bsk_linear_act_backward_enqueue(type, W, w_stride, x, x_stride, z, z_stride, dy, dy_stride, dx,
+                                                 dx_stride, dW, dw_stride, dbias, grad_type, accumulate, M, K, n,
+                                                 activation, _stream(stream)))
+
+
+def gated_linear_backward(type: int, Wg, Wu, w_stride: int, x, x_stride: int, g, u, gu_stride: int, dh,
+                          dh_stride: int, dx, dx_stride: int, dWg, dWu, dw_stride: int, dbias_g, dbias_u,
+                          grad_type: int, accumulate: int, M: int, K: int, n: int, activation: int,
+                          stream=None) -> None:
+    """Gradients of gated_linear: dx, dWg and dWu, dbias_g and dbias_u, each where it is wanted (see include/bsk.h);
+    blocks until done."""
+    calls = _calls or _load_calls()
+    _check(calls.gated_linear_backward(type, Wg, Wu, w_stride, x, x_stride, g, u, gu_stride, dh, dh_stride, dx,
+                                       dx_stride, dWg, dWu, dw_stride, dbias_g, dbias_u, grad_type, accumulate, M, K,
+                                       n, activation, _stream(stream)))
+
+
+def gated_linear_backward_enqueue(type: int, Wg, Wu, w_stride: int, x, x_stride: int, g, u, gu_stride: int, dh,
+                                  dh_stride: int, dx, dx_stride: int, dWg, dWu, dw_stride: int, dbias_g, dbias_u,
+                                  grad_type: int, accumulate: int, M: int, K: int, n: int, activation: int,
+                                  stream=None) -> None:
+    """Asynchronous variant of gated_linear_backward (check with stream_check)."""
+    calls = _calls or _load_calls()
+    _check(calls.bsk_gated_linear_backward_enqueue(type, Wg, Wu, w_stride, x, x_stride, g, u, gu_stride, dh,
+                                                   dh_stride, dx, dx_stride, dWg, dWu, dw_stride, dbias_g, dbias_u,
+                                                   grad_type, accumulate, M, K, n, activation, _stream(stream)))
 
 
 def stream_check(stream=None) -> None:

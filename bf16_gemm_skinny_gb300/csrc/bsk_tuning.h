@@ -89,6 +89,11 @@ void bsk_tile_coord(int t, int num_m, int num_n, int group_m, int* pid_m, int* p
  *                            an E4M3 cache the kernel for few rows (8 or 16 per CTA)
  *   BSK_OPT_KV_WORKSPACE_KB  test hook: workspaces of chunk_attention and decode_attention larger
  *                            than this many KiB count as failed allocations (0: none do)
+ *   BSK_OPT_LINEAR_KERNEL    kernel of the feed-forward layers' products: 0 automatic, 1 one CTA
+ *                            per tile, 2 CTA pairs, 3 the CUDA-core kernel (forward, few tokens)
+ *   BSK_OPT_LINEAR_TILE      their accumulator columns per tile: 0 automatic, else a multiple of
+ *                            16 up to 256 (taken where the kernel allows it); BSK_OPT_SPLIT_K
+ *                            sets the CTAs that share a tile's k loop
  * Returns BSK_ERR_INVALID_ARG for an unknown key or a value out of range.
  */
 enum {
@@ -111,7 +116,9 @@ enum {
     BSK_OPT_K_ORDER = 17,
     BSK_OPT_PAIR_M = 18,
     BSK_OPT_KV_KERNEL = 19,
-    BSK_OPT_KV_WORKSPACE_KB = 20
+    BSK_OPT_KV_WORKSPACE_KB = 20,
+    BSK_OPT_LINEAR_KERNEL = 21,
+    BSK_OPT_LINEAR_TILE = 22
 };
 int bsk_set_option(int key, long long value);
 long long bsk_get_option(int key);

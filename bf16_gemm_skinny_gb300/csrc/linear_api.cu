@@ -1,0 +1,660 @@
+// linear_api.cu -- the C entry points of the feed-forward layer calls: argument
+// checks, plan, workspace, launches.  No compute here.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdarg>
+#include <cstdio>
+
+#include "bsk.h"
+#include "bsk_internal.h"
+#include "bsk_tuning.h"
+#include "kv_internal.h"
+#include "linear_internal.h"
+
+namespace {
+
+int fail(int status, const char* fmt, ...)
+{
+    char msg[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(msg, sizeof(msg), fmt, ap);
+    va_end(ap);
+    bsk::record_error(msg);
+    return status;
+}
+
+int fail_cuda(cudaError_t e, const char* what)
+{
+    return fail(BSK_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+// Stream-ordered workspace in 256-byte aligned parts, freed in stream order after
+// use.  From the library's pool, whose memory stays mapped; a capturing stream
+// takes the default pool, whose allocations become nodes of the graph.
+class Workspace {
+  public:
+    explicit Workspace(cudaStream_t stream) : s_(stream) {}
+    Workspace(const Workspace&) = delete;
+    Workspace& operator=(const Workspace&) = delete;
+    ~Workspace()
+    {
+        if (ptr_ != nullptr) cudaFreeAsync(ptr_, s_);
+    }
+    // Notes a part; its offset.
+    size_t part(size_t bytes)
+    {
+        const size_t at = bytes_;
+        bytes_ += (bytes + 255) / 256 * 256;
+        return at;
+    }
+    int take()
+    {
+        if (bytes_ == 0) return BSK_OK;
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(s_, &capture);
+        cudaMemPool_t pool = nullptr;
+        if (e == cudaSuccess) {
+            if (capture != cudaStreamCaptureStatusNone || bsk::api_pool(&pool) != BSK_OK)
+                e = cudaMallocAsync(&ptr_, bytes_, s_);
+            else
+                e = cudaMallocFromPoolAsync(&ptr_, bytes_, pool, s_);
+        }
+        if (e == cudaSuccess) return BSK_OK;
+        cudaGetLastError();
+        ptr_ = nullptr;
+        return fail(BSK_ERR_NO_MEMORY, "cudaMallocAsync(%zu bytes) for a workspace failed: %s", bytes_,
+                    cudaGetErrorString(e));
+    }
+    uint8_t* at(size_t offset) const { return static_cast<uint8_t*>(ptr_) + offset; }
+
+  private:
+    void* ptr_ = nullptr;
+    size_t bytes_ = 0;
+    cudaStream_t s_;
+};
+
+// A matrix argument: `rows` rows of `width` elements of `size` bytes, `ld` elements apart.
+struct Matrix {
+    const char* name;
+    const void* p;
+    long long rows, width, ld;
+    int size;
+
+    long long bytes() const { return p != nullptr && rows > 0 && width > 0 ? ((rows - 1) * ld + width) * size : 0; }
+};
+
+bool overlap(const Matrix& a, const Matrix& b)
+{
+    const long long ab = a.bytes(), bb = b.bytes();
+    if (ab <= 0 || bb <= 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    return a0 < b0 + static_cast<uintptr_t>(bb) && b0 < a0 + static_cast<uintptr_t>(ab);
+}
+
+// Outputs overlap neither an input nor each other.  `same`: an input that may be
+// the first output itself (same address and stride), or nullptr.
+int check_overlaps(const Matrix* out, int outs, const Matrix* in, int ins, const void* same = nullptr)
+{
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < ins; ++j) {
+            if (i == 0 && same != nullptr && in[j].p == same && out[0].p == same && in[j].ld == out[0].ld) continue;
+            if (overlap(out[i], in[j])) return fail(BSK_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, in[j].name);
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return fail(BSK_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return BSK_OK;
+}
+
+// Alignment to the element, and a stride that holds a row.
+int check_matrix(const Matrix& m)
+{
+    if (m.p == nullptr) return BSK_OK;
+    if (reinterpret_cast<uintptr_t>(m.p) % static_cast<unsigned>(m.size) != 0)
+        return fail(BSK_ERR_INVALID_ARG, "%s is not aligned to its elements (%d bytes)", m.name, m.size);
+    if (m.ld < (m.width > 1 ? m.width : 1))
+        return fail(BSK_ERR_INVALID_ARG, "the stride of %s (%lld) must be at least %lld", m.name, m.ld,
+                    m.width > 1 ? m.width : 1LL);
+    return BSK_OK;
+}
+
+int check_common(int type, int activation, int M, int K, int n)
+{
+    if (type != BSK_TYPE_BF16 && type != BSK_TYPE_F16)
+        return fail(BSK_ERR_INVALID_ARG, "type must be BSK_TYPE_BF16 or BSK_TYPE_F16 (got %d)", type);
+    if (activation < BSK_ACT_NONE || activation > BSK_ACT_SILU)
+        return fail(BSK_ERR_INVALID_ARG, "unknown activation %d", activation);
+    if (M < 0 || K < 0 || n < 0) return fail(BSK_ERR_INVALID_ARG, "negative size (M=%d K=%d n=%d)", M, K, n);
+    const long long big = 0x7FFFFC00LL;   // tile coordinates stay in 32 bits
+    if (M > big || K > big || n > big) return fail(BSK_ERR_INVALID_ARG, "sizes must be at most 2^31 - 1024");
+    return BSK_OK;
+}
+
+bool direct(const void* p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+
+// Operands that the TMA unit cannot read where they are (base not 16-byte
+// aligned, or rows not a multiple of 16 bytes apart), to be copied to padded rows.
+class Packer {
+  public:
+    explicit Packer(Workspace& ws) : ws_(ws) {}
+    // Before take(): plans the copy of an operand, if it needs one.
+    void plan(const void** p, long long* ld, long long rows, long long width)
+    {
+        if (!direct(*p, *ld)) force(p, ld, rows, width);
+    }
+    // Plans the copy of an operand, whether or not it needs one.
+    void force(const void** p, long long* ld, long long rows, long long width)
+    {
+        Item& i = items_[n_++];
+        i.p = p;
+        i.ld = ld;
+        i.rows = rows;
+        i.width = width;
+        i.padded = (width + 63) / 64 * 64;
+        i.offset = ws_.part(static_cast<size_t>(rows) * static_cast<size_t>(i.padded) * 2);
+    }
+    // After take(): enqueues the copies and points the operands at them.
+    int run(int sms, bool pdl, int* status, unsigned long long limit_ns, cudaStream_t s)
+    {
+        char msg[256] = "";
+        for (int i = 0; i < n_; i += 2) {
+            bsk::PackCopy c[2];
+            const int n = n_ - i < 2 ? 1 : 2;
+            for (int j = 0; j < n; ++j) {
+                const Item& t = items_[i + j];
+                c[j] = {*t.p, *t.ld * 2, ws_.at(t.offset), t.padded * 2, t.width * 2, t.rows};
+            }
+            if (bsk::launch_pack(c, n, sms, pdl, status, limit_ns, s, msg, sizeof(msg)))
+                return fail(BSK_ERR_CUDA, "%s", msg);
+            for (int j = 0; j < n; ++j) {
+                const Item& t = items_[i + j];
+                *t.p = ws_.at(t.offset);
+            }
+        }
+        for (int i = 0; i < n_; ++i) *items_[i].ld = items_[i].padded;   // (weights share one stride: set last)
+        return BSK_OK;
+    }
+
+  private:
+    struct Item {
+        const void** p;
+        long long* ld;
+        long long rows, width, padded;
+        size_t offset;
+    };
+    Workspace& ws_;
+    Item items_[4];
+    int n_ = 0;
+};
+
+// What every launch of a call needs from the device and the options.
+struct Context {
+    int sms = 0;
+    int* status = nullptr;
+    unsigned long long limit_ns = 2000000000ull;
+    bool pdl = true;
+    cudaStream_t s = nullptr;
+
+    int prepare(void* stream)
+    {
+        s = static_cast<cudaStream_t>(stream);
+        const int st = bsk::api_prepare(&sms, &status);
+        if (st != BSK_OK) return st;
+        const long long us = bsk_get_option(BSK_OPT_WAIT_LIMIT_US);
+        if (us > 0) limit_ns = static_cast<unsigned long long>(us) * 1000ull;
+        pdl = bsk_get_option(BSK_OPT_PDL) != 1;
+        return BSK_OK;
+    }
+    int run(bsk::LinearLaunch& g) const
+    {
+        g.num_sms = sms;
+        g.status = status;
+        g.wait_limit_ns = limit_ns;
+        g.pdl = pdl;
+        bsk::plan_linear(g);
+        char msg[512] = "";
+        if (bsk::launch_linear(g, s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
+        return BSK_OK;
+    }
+};
+
+struct ForwardArgs {
+    int type;
+    bool gated;
+    const uint16_t* W[2];
+    long long w_stride;
+    const uint16_t* x;
+    long long x_stride;
+    const uint16_t* bias[2];
+    const uint16_t* residual;
+    long long r_stride;
+    uint16_t* out;
+    long long out_stride;
+    uint16_t* keep[2];
+    long long keep_stride;
+    int M, K, n, activation;
+};
+
+// *launched: the stream has work of this call.
+int enqueue_forward(const ForwardArgs& a, void* stream, bool* launched)
+{
+    *launched = false;
+    int st = check_common(a.type, a.activation, a.M, a.K, a.n);
+    if (st != BSK_OK) return st;
+    const int parts = a.gated ? 2 : 1;
+    const Matrix out[3] = {{a.gated ? "h" : "y", a.out, a.n, a.M, a.out_stride, 2},
+                           {a.gated ? "g" : "z", a.keep[0], a.n, a.M, a.keep_stride, 2},
+                           {"u", a.gated ? a.keep[1] : nullptr, a.n, a.M, a.keep_stride, 2}};
+    const Matrix in[6] = {{"x", a.x, a.n, a.K, a.x_stride, 2},
+                          {a.gated ? "Wg" : "W", a.W[0], a.M, a.K, a.w_stride, 2},
+                          {"Wu", a.gated ? a.W[1] : nullptr, a.M, a.K, a.w_stride, 2},
+                          {a.gated ? "bias_g" : "bias", a.bias[0], 1, a.M, a.M + 1LL, 2},
+                          {"bias_u", a.gated ? a.bias[1] : nullptr, 1, a.M, a.M + 1LL, 2},
+                          {"residual", a.residual, a.n, a.M, a.r_stride, 2}};
+    for (const Matrix& m : out)
+        if ((st = check_matrix(m)) != BSK_OK) return st;
+    for (const Matrix& m : in)
+        if ((st = check_matrix(m)) != BSK_OK) return st;
+    if (a.M == 0 || a.n == 0) return BSK_OK;
+    if (a.out == nullptr) return fail(BSK_ERR_INVALID_ARG, "%s is NULL", out[0].name);
+    if (a.K > 0)
+        for (int i = 0; i < parts + 1; ++i)
+            if (in[i].p == nullptr) return fail(BSK_ERR_INVALID_ARG, "%s is NULL", in[i].name);
+    if (a.gated && (a.keep[0] == nullptr) != (a.keep[1] == nullptr))
+        return fail(BSK_ERR_INVALID_ARG, "g and u are kept together: pass both or neither");
+    if ((st = check_overlaps(out, 3, in, 6, a.residual)) != BSK_OK) return st;
+    if (((a.M + 15LL) / 16) * ((a.n + 127LL) / 128) > INT_MAX) return fail(BSK_ERR_INVALID_ARG, "problem too large");
+
+    Context ctx;
+    if ((st = ctx.prepare(stream)) != BSK_OK) return st;
+    *launched = true;
+    bsk::LinearLaunch g;
+    g.mode = a.gated ? bsk::kModeGated : bsk::kModeLinear;
+    g.type = a.type;
+    g.A[0] = a.x;
+    g.lda = a.x_stride;
+    g.B[0] = a.W[0];
+    g.B[1] = a.gated ? a.W[1] : nullptr;
+    g.ldb = a.w_stride;
+    g.rows = a.n;
+    g.cols = a.M;
+    g.k = a.K;
+    g.out[0] = a.out;
+    g.ldo = a.out_stride;
+    g.act = a.activation;
+    g.residual = a.residual;
+    g.ldr = a.r_stride;
+    g.ldk = a.keep_stride;
+    for (int i = 0; i < parts; ++i) {
+        g.bias[i] = a.bias[i];
+        g.keep[i] = a.keep[i];
+    }
+    Workspace ws(ctx.s);
+    if (a.K == 0) {
+        // an empty sum: the same product over 8 zeros
+        const size_t bytes = static_cast<size_t>(a.n > a.M ? a.n : a.M) * 16;
+        const size_t at = ws.part(bytes);
+        if ((st = ws.take()) != BSK_OK) return st;
+        const cudaError_t e = cudaMemsetAsync(ws.at(at), 0, bytes, ctx.s);
+        if (e != cudaSuccess) return fail_cuda(e, "cudaMemsetAsync");
+        g.A[0] = g.B[0] = ws.at(at);
+        if (a.gated) g.B[1] = g.B[0];
+        g.lda = g.ldb = g.k = 8;
+        return ctx.run(g);
+    }
+    Packer pack(ws);
+    pack.plan(&g.A[0], &g.lda, a.n, a.K);
+    // the weights share a stride: if one needs a copy, both get one
+    const bool w_direct = direct(g.B[0], g.ldb) && (!a.gated || direct(g.B[1], g.ldb));
+    if (!w_direct)
+        for (int i = 0; i < parts; ++i) pack.force(&g.B[i], &g.ldb, a.M, a.K);
+    if ((st = ws.take()) != BSK_OK) return st;
+    if ((st = pack.run(ctx.sms, ctx.pdl, ctx.status, ctx.limit_ns, ctx.s)) != BSK_OK) return st;
+    return ctx.run(g);
+}
+
+struct BackwardArgs {
+    int type;
+    bool gated;
+    const uint16_t* W[2];
+    long long w_stride;
+    const uint16_t* x;
+    long long x_stride;
+    const uint16_t* z[2];
+    long long z_stride;
+    const uint16_t* dy;
+    long long dy_stride;
+    uint16_t* dx;
+    long long dx_stride;
+    void* dW[2];
+    long long dw_stride;
+    void* db[2];
+    int grad_type, accumulate, M, K, n, activation;
+};
+
+int enqueue_backward(const BackwardArgs& a, void* stream, bool* launched)
+{
+    *launched = false;
+    int st = check_common(a.type, a.activation, a.M, a.K, a.n);
+    if (st != BSK_OK) return st;
+    if (a.grad_type != BSK_GRAD_F32 && a.grad_type != BSK_GRAD_16)
+        return fail(BSK_ERR_INVALID_ARG, "grad_type must be BSK_GRAD_F32 or BSK_GRAD_16 (got %d)", a.grad_type);
+    if (a.accumulate != 0 && a.accumulate != 1)
+        return fail(BSK_ERR_INVALID_ARG, "accumulate must be 0 or 1 (got %d)", a.accumulate);
+    const int parts = a.gated ? 2 : 1;
+    const int gs = a.grad_type == BSK_GRAD_F32 ? 4 : 2;
+    const Matrix out[5] = {{"dx", a.dx, a.n, a.K, a.dx_stride, 2},
+                           {a.gated ? "dWg" : "dW", a.dW[0], a.M, a.K, a.dw_stride, gs},
+                           {"dWu", a.dW[1], a.M, a.K, a.dw_stride, gs},
+                           {a.gated ? "dbias_g" : "dbias", a.db[0], 1, a.M, a.M + 1LL, gs},
+                           {"dbias_u", a.db[1], 1, a.M, a.M + 1LL, gs}};
+    const Matrix in[6] = {{a.gated ? "Wg" : "W", a.W[0], a.M, a.K, a.w_stride, 2},
+                          {"Wu", a.W[1], a.M, a.K, a.w_stride, 2},
+                          {"x", a.x, a.n, a.K, a.x_stride, 2},
+                          {a.gated ? "g" : "z", a.z[0], a.n, a.M, a.z_stride, 2},
+                          {"u", a.z[1], a.n, a.M, a.z_stride, 2},
+                          {a.gated ? "dh" : "dy", a.dy, a.n, a.M, a.dy_stride, 2}};
+    for (const Matrix& m : out)
+        if ((st = check_matrix(m)) != BSK_OK) return st;
+    for (const Matrix& m : in)
+        if ((st = check_matrix(m)) != BSK_OK) return st;
+    if (a.gated && (a.dW[0] == nullptr) != (a.dW[1] == nullptr))
+        return fail(BSK_ERR_INVALID_ARG, "dWg and dWu are computed together: pass both or neither");
+    const bool want_dx = a.dx != nullptr && a.n > 0 && a.K > 0;
+    const bool want_dw = a.dW[0] != nullptr && a.M > 0 && a.K > 0;
+    const bool want_db = (a.db[0] != nullptr || a.db[1] != nullptr) && a.M > 0;
+    if (!want_dx && !want_dw && !want_db) return BSK_OK;
+    const bool need_z = a.gated || a.activation != BSK_ACT_NONE;
+    if (a.n > 0 && a.M > 0) {
+        if (a.dy == nullptr) return fail(BSK_ERR_INVALID_ARG, "%s is NULL", in[5].name);
+        if (need_z && a.z[0] == nullptr) return fail(BSK_ERR_INVALID_ARG, "%s is NULL", in[3].name);
+        if (a.gated && a.z[1] == nullptr) return fail(BSK_ERR_INVALID_ARG, "u is NULL");
+        if (want_dx && (a.W[0] == nullptr || (a.gated && a.W[1] == nullptr)))
+            return fail(BSK_ERR_INVALID_ARG, "%s is NULL", a.W[0] == nullptr ? in[0].name : "Wu");
+        if (want_dw && a.x == nullptr) return fail(BSK_ERR_INVALID_ARG, "x is NULL");
+    }
+    if ((st = check_overlaps(out, 5, in, 6)) != BSK_OK) return st;
+    const long long most_tiles = 0x7FFFFFFFLL;
+    if (((a.n + 127LL) / 128) * ((a.K + 63LL) / 64) > most_tiles || 2 * ((a.M + 127LL) / 128) * ((a.K + 63LL) / 64) > most_tiles)
+        return fail(BSK_ERR_INVALID_ARG, "problem too large");
+
+    Context ctx;
+    if ((st = ctx.prepare(stream)) != BSK_OK) return st;
+    *launched = true;
+    cudaError_t e = cudaSuccess;
+    if (a.M == 0) {   // dx is an empty sum
+        e = cudaMemset2DAsync(a.dx, static_cast<size_t>(a.dx_stride) * 2, 0, static_cast<size_t>(a.K) * 2, a.n, ctx.s);
+        return e == cudaSuccess ? BSK_OK : fail_cuda(e, "cudaMemset2DAsync");
+    }
+    if (a.n == 0) {   // so are the weights' and biases' gradients
+        for (int i = 0; i < parts && a.accumulate == 0 && e == cudaSuccess; ++i) {
+            if (want_dw)
+                e = cudaMemset2DAsync(a.dW[i], static_cast<size_t>(a.dw_stride) * gs, 0, static_cast<size_t>(a.K) * gs, a.M, ctx.s);
+            if (a.db[i] != nullptr && e == cudaSuccess) e = cudaMemsetAsync(a.db[i], 0, static_cast<size_t>(a.M) * gs, ctx.s);
+        }
+        return e == cudaSuccess ? BSK_OK : fail_cuda(e, "cudaMemsetAsync");
+    }
+
+    // dz: dy itself without an activation, else computed into the workspace
+    Workspace ws(ctx.s);
+    const bool products = want_dx || want_dw;
+    const bool make_dz = need_z && products;
+    const void* dz[2] = {a.dy, nullptr};
+    long long ld_dz = a.dy_stride;
+    size_t dz_at[2] = {0, 0};
+    if (make_dz) {
+        ld_dz = (a.M + 63LL) / 64 * 64;
+        for (int i = 0; i < parts; ++i) dz_at[i] = ws.part(static_cast<size_t>(a.n) * static_cast<size_t>(ld_dz) * 2);
+    }
+    const int chunks = bsk::act_backward_chunks(a.n, a.M, ctx.sms);
+    const size_t partial_at = want_db ? ws.part(static_cast<size_t>(chunks) * parts * static_cast<size_t>(a.M) * 4) : 0;
+    const void* x = a.x;
+    long long ldx = a.x_stride;
+    const void* W[2] = {a.W[0], a.W[1]};
+    long long ldw = a.w_stride;
+    Packer pack(ws);
+    if (want_dw) pack.plan(&x, &ldx, a.n, a.K);
+    if (want_dx && (!direct(W[0], ldw) || (a.gated && !direct(W[1], ldw))))
+        for (int i = 0; i < parts; ++i) pack.force(&W[i], &ldw, a.M, a.K);
+    if (!make_dz && products) pack.plan(&dz[0], &ld_dz, a.n, a.M);
+    if ((st = ws.take()) != BSK_OK) return st;
+    char msg[512] = "";
+    if (make_dz || want_db) {
+        bsk::ActBackwardLaunch l;
+        l.type = a.type;
+        l.gated = a.gated;
+        l.act = a.activation;
+        l.n = a.n;
+        l.M = a.M;
+        l.ldz = a.z_stride;
+        l.dy = a.dy;
+        l.ld_dy = a.dy_stride;
+        l.ld_dz = ld_dz;
+        for (int i = 0; i < parts; ++i) {
+            l.z[i] = need_z ? a.z[i] : nullptr;
+            if (make_dz) dz[i] = l.dz[i] = ws.at(dz_at[i]);
+        }
+        l.partial = want_db ? reinterpret_cast<float*>(ws.at(partial_at)) : nullptr;
+        l.chunks = chunks;
+        l.pdl = ctx.pdl;
+        if (bsk::launch_act_backward(l, ctx.s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
+        if (want_db) {
+            bsk::BiasGradLaunch b;
+            b.type = a.type;
+            b.parts = parts;
+            b.M = a.M;
+            b.chunks = chunks;
+            b.partial = l.partial;
+            b.db[0] = a.db[0];
+            b.db[1] = a.db[1];
+            b.f32 = gs == 4;
+            b.accumulate = a.accumulate != 0;
+            b.pdl = ctx.pdl;
+            if (bsk::launch_bias_grad(b, ctx.s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
+        }
+    }
+    if ((st = pack.run(ctx.sms, ctx.pdl, ctx.status, ctx.limit_ns, ctx.s)) != BSK_OK) return st;
+    if (want_dx) {
+        bsk::LinearLaunch g;
+        g.mode = bsk::kModeGradInput;
+        g.type = a.type;
+        g.sources = parts;
+        g.lda = ld_dz;
+        g.ldb = ldw;
+        for (int i = 0; i < parts; ++i) {
+            g.A[i] = dz[i];
+            g.B[i] = W[i];
+        }
+        g.rows = a.n;
+        g.cols = a.K;
+        g.k = a.M;
+        g.out[0] = a.dx;
+        g.ldo = a.dx_stride;
+        if ((st = ctx.run(g)) != BSK_OK) return st;
+    }
+    if (want_dw) {
+        bsk::LinearLaunch g;
+        g.mode = bsk::kModeGradWeight;
+        g.type = a.type;
+        g.sources = parts;
+        g.lda = ld_dz;
+        g.B[0] = x;
+        g.ldb = ldx;
+        for (int i = 0; i < parts; ++i) {
+            g.A[i] = dz[i];
+            g.out[i] = a.dW[i];
+        }
+        g.rows = a.M;
+        g.cols = a.K;
+        g.k = a.n;
+        g.ldo = a.dw_stride;
+        g.out_f32 = gs == 4;
+        g.accumulate = a.accumulate != 0;
+        if ((st = ctx.run(g)) != BSK_OK) return st;
+    }
+    return BSK_OK;
+}
+
+// The blocking form of a call: the stream's work is done, its errors reported.
+template <typename Args>
+int blocking(int (*enqueue)(const Args&, void*, bool*), const Args& a, void* stream)
+{
+    bool launched = false;
+    const int st = enqueue(a, stream, &launched);
+    return st != BSK_OK || !launched ? st : bsk::api_sync_and_check(static_cast<cudaStream_t>(stream));
+}
+template <typename Args>
+int only_enqueue(int (*enqueue)(const Args&, void*, bool*), const Args& a, void* stream)
+{
+    bool launched = false;
+    return enqueue(a, stream, &launched);
+}
+
+}  // namespace
+
+namespace bsk {
+
+// The tile, the kernel and the split of a product: the least estimated time.
+void plan_linear(LinearLaunch& g)
+{
+    const bool b_mn = g.mode == kModeGradInput || g.mode == kModeGradWeight;
+    const bool gated = g.mode == kModeGated;
+    const long long kb = (g.k + 63LL) / 64 * (g.mode == kModeGradInput ? g.sources : 1);
+    const long long row_sources = g.mode == kModeGradWeight ? g.sources : 1;
+    const long long opt_kernel = bsk_get_option(BSK_OPT_LINEAR_KERNEL);
+    const long long opt_tile = bsk_get_option(BSK_OPT_LINEAR_TILE);
+    const long long opt_split = bsk_get_option(BSK_OPT_SPLIT_K);
+    double best = -1.0;
+    for (int pair = 0; pair < 2; ++pair) {
+        if ((opt_kernel == 1 && pair) || (opt_kernel == 2 && !pair)) continue;
+        const int unit = pair ? (b_mn ? 128 : 64) : gated ? 32 : b_mn ? 64 : 16;
+        const long long rows_per = pair ? 256 : 128;
+        const long long slots = pair ? (g.num_sms > 1 ? g.num_sms / 2 : 1) : g.num_sms;
+        const long long m_tiles = (g.rows + rows_per - 1) / rows_per * row_sources;
+        for (int bn = unit; bn <= 256; bn += unit) {
+            if (opt_tile > 0 && bn != opt_tile && opt_tile % unit == 0) continue;
+            const long long wcols = gated ? bn / 2 : bn;
+            const long long tiles = m_tiles * ((g.cols + wcols - 1) / wcols);
+            for (int split = 1; split <= (pair ? 1 : 8); split *= 2) {
+                if (opt_split > 0 && split != opt_split && !pair && opt_split <= 8) continue;
+                if (split > 1 && (kb < 2 * split || opt_split == 1)) break;
+                const long long waves = (tiles * split + slots - 1) / slots;
+                const long long a_rows = !pair && !b_mn && g.rows < 128 ? (g.rows + 7) / 8 * 8 : 128;
+                const double per_kb = pair ? 150.0 + 0.7 * bn : 100.0 + 1.1 * static_cast<double>(a_rows / 4 + bn);
+                const double est = 5000.0 + (split > 1 ? 1500.0 : 0.0) +
+                                   static_cast<double>(waves) * (static_cast<double>((kb + split - 1) / split) * per_kb + 4.0 * bn);
+                if (best < 0.0 || est < best) {
+                    best = est;
+                    g.pair = pair != 0;
+                    g.bn = bn;
+                    g.split = split;
+                }
+            }
+        }
+    }
+    const long long opt_group = bsk_get_option(BSK_OPT_GROUP_M);
+    g.group_m = opt_group > 0 ? static_cast<int>(opt_group) : 8;
+}
+
+int launch_linear(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len)
+{
+    return g.type == kTypeBF16 ? launch_linear_bf16(g, stream, msg, msg_len) : launch_linear_f16(g, stream, msg, msg_len);
+}
+
+}  // namespace bsk
+
+extern "C" {
+
+int bsk_linear_act_enqueue(
+    int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride, const uint16_t* bias,
+    const uint16_t* residual, int residual_stride, uint16_t* y, int y_stride, uint16_t* z, int z_stride, int M, int K, int n,
+    int activation, void* stream)
+{
+    return only_enqueue<ForwardArgs>(enqueue_forward,
+                         {type, false, {W, nullptr}, w_stride, x, x_stride, {bias, nullptr}, residual, residual_stride, y,
+                         y_stride, {z, nullptr}, z_stride, M, K, n, activation},
+                         stream);
+}
+
+int linear_act(
+    int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride, const uint16_t* bias,
+    const uint16_t* residual, int residual_stride, uint16_t* y, int y_stride, uint16_t* z, int z_stride, int M, int K, int n,
+    int activation, void* stream)
+{
+    return blocking<ForwardArgs>(enqueue_forward,
+                         {type, false, {W, nullptr}, w_stride, x, x_stride, {bias, nullptr}, residual, residual_stride, y,
+                         y_stride, {z, nullptr}, z_stride, M, K, n, activation},
+                         stream);
+}
+
+int bsk_gated_linear_enqueue(
+    int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x, int x_stride,
+    const uint16_t* bias_g, const uint16_t* bias_u, uint16_t* h, int h_stride, uint16_t* g, uint16_t* u, int gu_stride, int M,
+    int K, int n, int activation, void* stream)
+{
+    return only_enqueue<ForwardArgs>(enqueue_forward,
+                         {type, true, {Wg, Wu}, w_stride, x, x_stride, {bias_g, bias_u}, nullptr, 0, h, h_stride, {g, u},
+                         gu_stride, M, K, n, activation},
+                         stream);
+}
+
+int gated_linear(
+    int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x, int x_stride,
+    const uint16_t* bias_g, const uint16_t* bias_u, uint16_t* h, int h_stride, uint16_t* g, uint16_t* u, int gu_stride, int M,
+    int K, int n, int activation, void* stream)
+{
+    return blocking<ForwardArgs>(enqueue_forward,
+                         {type, true, {Wg, Wu}, w_stride, x, x_stride, {bias_g, bias_u}, nullptr, 0, h, h_stride, {g, u},
+                         gu_stride, M, K, n, activation},
+                         stream);
+}
+
+int bsk_linear_act_backward_enqueue(
+    int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride, const uint16_t* z,
+    int z_stride, const uint16_t* dy, int dy_stride, uint16_t* dx, int dx_stride, void* dW, int dw_stride, void* dbias,
+    int grad_type, int accumulate, int M, int K, int n, int activation, void* stream)
+{
+    return only_enqueue<BackwardArgs>(enqueue_backward,
+                         {type, false, {W, nullptr}, w_stride, x, x_stride, {z, nullptr}, z_stride, dy, dy_stride, dx, dx_stride,
+                          {dW, nullptr}, dw_stride, {dbias, nullptr}, grad_type, accumulate, M, K, n, activation},
+                         stream);
+}
+
+int linear_act_backward(
+    int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride, const uint16_t* z,
+    int z_stride, const uint16_t* dy, int dy_stride, uint16_t* dx, int dx_stride, void* dW, int dw_stride, void* dbias,
+    int grad_type, int accumulate, int M, int K, int n, int activation, void* stream)
+{
+    return blocking<BackwardArgs>(enqueue_backward,
+                         {type, false, {W, nullptr}, w_stride, x, x_stride, {z, nullptr}, z_stride, dy, dy_stride, dx, dx_stride,
+                          {dW, nullptr}, dw_stride, {dbias, nullptr}, grad_type, accumulate, M, K, n, activation},
+                         stream);
+}
+
+int bsk_gated_linear_backward_enqueue(
+    int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x, int x_stride,
+    const uint16_t* g, const uint16_t* u, int gu_stride, const uint16_t* dh, int dh_stride, uint16_t* dx, int dx_stride,
+    void* dWg, void* dWu, int dw_stride, void* dbias_g, void* dbias_u, int grad_type, int accumulate, int M, int K, int n,
+    int activation, void* stream)
+{
+    return only_enqueue<BackwardArgs>(enqueue_backward,
+                         {type, true, {Wg, Wu}, w_stride, x, x_stride, {g, u}, gu_stride, dh, dh_stride, dx, dx_stride,
+                          {dWg, dWu}, dw_stride, {dbias_g, dbias_u}, grad_type, accumulate, M, K, n, activation},
+                         stream);
+}
+
+int gated_linear_backward(
+    int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x, int x_stride,
+    const uint16_t* g, const uint16_t* u, int gu_stride, const uint16_t* dh, int dh_stride, uint16_t* dx, int dx_stride,
+    void* dWg, void* dWu, int dw_stride, void* dbias_g, void* dbias_u, int grad_type, int accumulate, int M, int K, int n,
+    int activation, void* stream)
+{
+    return blocking<BackwardArgs>(enqueue_backward,
+                         {type, true, {Wg, Wu}, w_stride, x, x_stride, {g, u}, gu_stride, dh, dh_stride, dx, dx_stride,
+                          {dWg, dWu}, dw_stride, {dbias_g, dbias_u}, grad_type, accumulate, M, K, n, activation},
+                         stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,100 @@
+// linear_internal.h -- the products of the feed-forward layer calls as their
+// kernels see them, and the launchers of the linear_*.cu files (not part of the
+// C ABI).
+//
+// Every product here leaves a row-major result: rows along the accumulator's
+// TMEM lanes, columns along its registers.
+//   linear   out[t, j] = act(sum_k x[t, k] W[j, k] + b[j]) + r[t, j]
+//   gated    out[t, j] = act(g) * u,  g and u two such sums (Wg and Wu)
+//   input gradient    dx[t, k] = sum over the sources s and features j of dz_s[t, j] W_s[j, k]
+//   weight gradient   dW_s[j, k] (+)= sum_t dz_s[t, j] x[t, k]
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace bsk {
+
+enum ValueType : int { kTypeBF16 = 0, kTypeF16 = 1 };
+enum Activation : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+enum LinearMode : int { kModeLinear = 0, kModeGated = 1, kModeGradInput = 2, kModeGradWeight = 3 };
+
+// One product.  Operands are 16-bit, 16-byte aligned, with leading dimensions
+// (elements) that are multiples of 8.
+//   mode          rows x cols   k (per source)  A[s]               B[s]
+//   linear        n x M         K               x [n, K]           W [M, K]
+//   gated         n x M         K               x [n, K]           Wg, Wu [M, K]
+//   input grad.   n x K         M, sources      dz_s [n, M]        W_s [M, K] (read along M)
+//   weight grad.  M x K, sources  n             dz_s [n, M] (read along n)   x [n, K] (read along n)
+struct LinearLaunch {
+    int mode = kModeLinear;
+    int type = kTypeBF16;
+    int sources = 1;               // gradients: 1 or 2
+    const void* A[2] = {nullptr, nullptr};
+    long long lda = 0;
+    const void* B[2] = {nullptr, nullptr};
+    long long ldb = 0;
+    int rows = 0, cols = 0, k = 0;
+    void* out[2] = {nullptr, nullptr};   // [1]: the second source's weight gradient
+    long long ldo = 0;
+    bool out_f32 = false;          // weight gradients in FP32
+    bool accumulate = false;       // weight gradients added to what is there
+    int act = kActNone;
+    const void* bias[2] = {nullptr, nullptr};
+    const void* residual = nullptr;
+    long long ldr = 0;
+    void* keep[2] = {nullptr, nullptr};  // pre-activations, rounded
+    long long ldk = 0;
+    int num_sms = 1;
+    int* status = nullptr;
+    unsigned long long wait_limit_ns = 2000000000ull;
+    bool pdl = true;
+    // plan_linear()'s choice
+    bool pair = false;             // 256-row tiles on CTA pairs, else 128-row tiles
+    int bn = 128;                  // accumulator columns per tile (gated: both halves)
+    int split = 1;                 // one-CTA tiles: CTAs of a cluster that share a tile's k loop
+    int group_m = 8;
+};
+
+// Fills in the plan (tile width, kernel, split) from the sizes; options override it.
+void plan_linear(LinearLaunch& g);
+int launch_linear(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len);
+int launch_linear_bf16(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len);
+int launch_linear_f16(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len);
+
+// The element-wise part of the backward passes, and the sums over the tokens:
+//   gated:  dz[0] = dy * u * act'(g),  dz[1] = dy * act(g)   (z[0] = g, z[1] = u)
+//   else:   dz[0] = dy * act'(z[0])
+// rounded to the type ([n, M], ld_dz apart; NULL: not stored).  With `partial`
+// (chunks x parts x M floats) the columns' FP32 sums over each chunk of tokens
+// go there.
+struct ActBackwardLaunch {
+    int type = kTypeBF16;
+    bool gated = false;
+    int act = kActNone;
+    int n = 0, M = 0;
+    const void* z[2] = {nullptr, nullptr};
+    long long ldz = 0;
+    const void* dy = nullptr;
+    long long ld_dy = 0;
+    void* dz[2] = {nullptr, nullptr};
+    long long ld_dz = 0;
+    float* partial = nullptr;
+    int chunks = 1;
+    bool pdl = true;
+};
+int act_backward_chunks(int n, int M, int num_sms);
+int launch_act_backward(const ActBackwardLaunch& a, cudaStream_t stream, char* msg, size_t msg_len);
+
+// db[p][j] (+)= sum over the chunks, in order, of partial[chunk][p][j].
+struct BiasGradLaunch {
+    int type = kTypeBF16;
+    int parts = 1, M = 0, chunks = 1;
+    const float* partial = nullptr;
+    void* db[2] = {nullptr, nullptr};
+    bool f32 = false, accumulate = false, pdl = true;
+};
+int launch_bias_grad(const BiasGradLaunch& a, cudaStream_t stream, char* msg, size_t msg_len);
+
+}  // namespace bsk

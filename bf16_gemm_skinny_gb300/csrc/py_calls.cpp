@@ -1,4 +1,5 @@
-// py_calls.cpp -- the cache entry points as Python calls (module _calls).
+// py_calls.cpp -- the entry points of the cache and of the feed-forward layers as
+// Python calls (module _calls).
 //
 // A decode step makes these calls for every layer, on kernels of a few
 // microseconds, so the call itself counts.  With some twenty arguments ctypes
@@ -111,6 +112,14 @@ PyMethodDef g_methods[] = {
     method<bsk_chunk_attention_enqueue>("bsk_chunk_attention_enqueue"),
     method<decode_attention>("decode_attention"),
     method<bsk_decode_attention_enqueue>("bsk_decode_attention_enqueue"),
+    method<linear_act>("linear_act"),
+    method<bsk_linear_act_enqueue>("bsk_linear_act_enqueue"),
+    method<gated_linear>("gated_linear"),
+    method<bsk_gated_linear_enqueue>("bsk_gated_linear_enqueue"),
+    method<linear_act_backward>("linear_act_backward"),
+    method<bsk_linear_act_backward_enqueue>("bsk_linear_act_backward_enqueue"),
+    method<gated_linear_backward>("gated_linear_backward"),
+    method<bsk_gated_linear_backward_enqueue>("bsk_gated_linear_backward_enqueue"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -13,7 +13,10 @@
  *   kv_cache_append    new tokens' keys and values into a paged cache, in BF16 or
  *                      quantised to E4M3; kv_cache_gather reads them back;
  *   chunk_attention    attention of a chunk of new tokens over such a cache, and
- *   decode_attention   of single tokens, with an optional sliding window and sinks.
+ *   decode_attention   of single tokens, with an optional sliding window and sinks;
+ *   linear_act         linear layer with bias, activation and residual, BF16 or FP16,
+ *   gated_linear       the gated pair of linear layers of a feed-forward block, and
+ *                      linear_act_backward, gated_linear_backward, their gradients.
  *
  * Conventions shared by every call:
  *  - Matrix pointers are DEVICE pointers (cudaMalloc / torch CUDA tensors) to
@@ -320,6 +323,86 @@ int decode_attention(int cache_type, const void* k_cache, const void* v_cache, c
                      int num_kv_heads, int head_dim, int block_size, int max_blocks, int num_blocks,
                      int max_seq_len, float softmax_scale, int window, int sinks, int num_segments, void* stream);
 
+/* 16-bit type of the feed-forward calls' activations and weights. */
+typedef enum bsk_value_type {
+    BSK_TYPE_BF16 = 0,
+    BSK_TYPE_F16 = 1 /* IEEE binary16 */
+} bsk_value_type;
+
+typedef enum bsk_activation {
+    BSK_ACT_NONE = 0,
+    BSK_ACT_RELU = 1,
+    BSK_ACT_GELU = 2,      /* z Phi(z), the normal distribution function (the erf form) */
+    BSK_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    BSK_ACT_SILU = 4       /* z / (1 + e^-z) */
+} bsk_activation;
+
+/* Type of the gradients of weights and biases. */
+typedef enum bsk_grad_type {
+    BSK_GRAD_F32 = 0,
+    BSK_GRAD_16 = 1 /* the call's 16-bit type */
+} bsk_grad_type;
+
+/*
+ * The layers of a feed-forward block, beside gemv_bf16: a linear layer with bias,
+ * activation and residual in one kernel, the gated pair of linear layers, and the
+ * backward pass of each.  With n tokens, M output and K input features:
+ *
+ *   linear_act             z = x W^T + bias;  y = act(z) + residual
+ *   gated_linear           g = x Wg^T + bias_g;  u = x Wu^T + bias_u;  h = act(g) * u
+ *   linear_act_backward    dz = dy * act'(z);  dx = dz W;  dW = dz^T x;  dbias = sum over the tokens of dz
+ *   gated_linear_backward  dg = dh * u * act'(g);  du = dh * act(g);  dx = dg Wg + du Wu;
+ *                          dWg = dg^T x;  dWu = du^T x;  dbias_g, dbias_u the sums of dg and du
+ *
+ *   type             bsk_value_type of every matrix and vector below, but for the
+ *                    gradients of weights and biases
+ *   W, Wg, Wu        [M, K], w_stride elements between rows
+ *   x, dx            [n, K];  residual, y, z, h, g, u, dy, dh  [n, M];  their own strides.
+ *                    Strides are at least the row's length; only rows' elements are
+ *                    read and written, so that a matrix may be a part of wider rows
+ *   bias...          [M], NULL: none
+ *   residual         NULL: none.  It may be y itself (same address and stride)
+ *   z; g, u          forward: where to keep them for a backward pass (rounded), NULL:
+ *                    not kept; backward: what was kept (z is not read, and may be NULL,
+ *                    with BSK_ACT_NONE)
+ *   dx, dW..., dbias...  gradients wanted; NULL: not computed.  dWg and dWu go together.
+ *                    The residual's gradient is dy
+ *   dW..., dbias...  [M, K] with dw_stride, and [M], of grad_type; with accumulate 1
+ *                    they are added to what is there
+ *
+ * Sums are FP32.  The activation works on the unrounded FP32 z (g, u), and every
+ * output is rounded once, to nearest even.  dz (dg, du) is rounded to `type` before
+ * its products with W and x (without an activation dz is dy and nothing is
+ * rounded); the sums for dbias take it unrounded.  An addition to 16-bit gradients is
+ * made in FP32 and rounded.  The same call gives the same bits, but another number of
+ * tokens may sum in another order.
+ *
+ * A stride or an address that is not a multiple of 16 bytes costs a copy of the
+ * operand into a workspace (x, W..., dy without an activation).  The backward calls
+ * take a workspace of 2 n M bytes for each dz and 4 M bytes for each bias and about
+ * 4 chunks of tokens per SM.  Workspaces are allocated in stream order, from a pool of
+ * the library's own that keeps up to 2 GiB mapped for later calls (in a stream that is
+ * being captured, from the default pool).  Outputs overlap neither inputs (but for the
+ * residual above) nor each other (BSK_ERR_INVALID_ARG).  Sizes are at most 2^31 - 1024.
+ * K = 0 is an empty sum, n = 0 gives zero gradients of weights and biases (or adds
+ * nothing), M = 0 a dx of zeros.  Blocking; the _enqueue forms only launch.
+ */
+int linear_act(int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride, const uint16_t* bias,
+               const uint16_t* residual, int residual_stride, uint16_t* y, int y_stride, uint16_t* z, int z_stride,
+               int M, int K, int n, int activation, void* stream);
+int gated_linear(int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x, int x_stride,
+                 const uint16_t* bias_g, const uint16_t* bias_u, uint16_t* h, int h_stride, uint16_t* g, uint16_t* u,
+                 int gu_stride, int M, int K, int n, int activation, void* stream);
+int linear_act_backward(int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride,
+                        const uint16_t* z, int z_stride, const uint16_t* dy, int dy_stride, uint16_t* dx,
+                        int dx_stride, void* dW, int dw_stride, void* dbias, int grad_type, int accumulate, int M,
+                        int K, int n, int activation, void* stream);
+int gated_linear_backward(int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x,
+                          int x_stride, const uint16_t* g, const uint16_t* u, int gu_stride, const uint16_t* dh,
+                          int dh_stride, uint16_t* dx, int dx_stride, void* dWg, void* dWu, int dw_stride,
+                          void* dbias_g, void* dbias_u, int grad_type, int accumulate, int M, int K, int n,
+                          int activation, void* stream);
+
 /*
  * gemm_f16_colmajor for callers that cannot allocate device memory during a
  * call (for example a serving process whose own allocator reserved all free
@@ -420,6 +503,25 @@ int bsk_decode_attention_enqueue(int cache_type, const void* k_cache, const void
                                  const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
                                  int head_dim, int block_size, int max_blocks, int num_blocks, int max_seq_len,
                                  float softmax_scale, int window, int sinks, int num_segments, void* stream);
+
+int bsk_linear_act_enqueue(int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride,
+                           const uint16_t* bias, const uint16_t* residual, int residual_stride, uint16_t* y,
+                           int y_stride, uint16_t* z, int z_stride, int M, int K, int n, int activation,
+                           void* stream);
+int bsk_gated_linear_enqueue(int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride, const uint16_t* x,
+                             int x_stride, const uint16_t* bias_g, const uint16_t* bias_u, uint16_t* h, int h_stride,
+                             uint16_t* g, uint16_t* u, int gu_stride, int M, int K, int n, int activation,
+                             void* stream);
+int bsk_linear_act_backward_enqueue(int type, const uint16_t* W, int w_stride, const uint16_t* x, int x_stride,
+                                    const uint16_t* z, int z_stride, const uint16_t* dy, int dy_stride, uint16_t* dx,
+                                    int dx_stride, void* dW, int dw_stride, void* dbias, int grad_type,
+                                    int accumulate, int M, int K, int n, int activation, void* stream);
+int bsk_gated_linear_backward_enqueue(int type, const uint16_t* Wg, const uint16_t* Wu, int w_stride,
+                                      const uint16_t* x, int x_stride, const uint16_t* g, const uint16_t* u,
+                                      int gu_stride, const uint16_t* dh, int dh_stride, uint16_t* dx, int dx_stride,
+                                      void* dWg, void* dWu, int dw_stride, void* dbias_g, void* dbias_u,
+                                      int grad_type, int accumulate, int M, int K, int n, int activation,
+                                      void* stream);
 
 /* Synchronise `stream`, then report BSK_ERR_CUDA for a pending CUDA error or
  * BSK_ERR_TIMEOUT if a device-side wait gave up since the last check. */
