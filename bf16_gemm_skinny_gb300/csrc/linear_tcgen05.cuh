@@ -18,8 +18,8 @@
 // Two k sources (dx = dg Wg + du Wu): one k loop over both, one accumulator, so
 // that dx is rounded once.
 //
-// Roles (192 threads): warp 0 loads by TMA into a ring of k slices, warp 1 issues
-// the MMAs, warps 2..5 are the epilogue, overlapped with the next tile's loop by a
+// Roles (320 threads): warp 0 loads by TMA into a ring of k slices, warp 1 issues
+// the MMAs, warps 2..9 are the epilogue, overlapped with the next tile's loop by a
 // second accumulator.  Tile sizes are run-time values (TMA boxes, instruction
 // descriptor, ring depth): with few rows only those are staged -- the MMA reads
 // on into whatever follows in shared memory, and those rows are not stored.
@@ -39,8 +39,8 @@
 namespace bsk {
 namespace {
 
-constexpr int kLinThreads = 192;
-constexpr int kLinEpiWarps = 4;
+constexpr int kLinEpiWarps = 8;                  // two per quarter of the TMEM lanes: every other kCh columns
+constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
 constexpr int kLinBK = 64;                       // k values per stage: one 128-byte swizzle row
 constexpr int kLinBarBytes = 512;
 constexpr int kLinSmemBytes = 232448;            // all of it: one CTA per SM, so that 512 TMEM columns are free
@@ -48,6 +48,13 @@ constexpr int kLinRingBytes = kLinSmemBytes - 1024 - kLinBarBytes;
 constexpr int kLinMaxStages = 24;
 constexpr int kLinAccCols = 256;                 // TMEM columns of one accumulator (two of them)
 constexpr int kCh = 16;                          // columns per epilogue step: 32 bytes of 16-bit values
+constexpr int kStagePitch = 9;                   // words per row of a warp's staging buffer (odd: no bank conflicts)
+constexpr int kStageBytes = kLinEpiWarps * 32 * kStagePitch * 4;
+// FP32 weight gradients: k-blocks summed in an accumulator before they are added to
+// FP32 registers.  A tensor-core accumulation cuts each of its sums (toward zero), so
+// an error grows with their number: dW over 8192 tokens came out 2e-5 off, in segments of 256
+// tokens 1e-6, as much as FP32 arithmetic gives.
+constexpr int kSegmentKb = 16;
 
 enum LinearWaitSite {
     kSiteLinEmpty = 0x30,
@@ -66,6 +73,8 @@ struct LinearParams {
     int bn;                   // accumulator columns per tile
     int wcols;                // result columns per tile: bn, gated bn / 2
     int stages, a_bytes, b_bytes;
+    int seg_kb;               // weight gradient: k-blocks per segment
+    int stage_out;            // rows that no 16-byte accesses reach go through the staging buffers
     int split;                // CTAs that share a tile's k loop (a cluster); 1: none
     uint32_t idesc;
     void* out[2];
@@ -111,51 +120,152 @@ __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, const Wa
 }
 
 // ---------------------------------------------------------------------------
-// Epilogue arithmetic on one row's kCh columns, c0 .. c0 + n - 1 of them there.
+// Epilogue arithmetic on CH columns of one row per lane, c0 .. c0 + n - 1 of them there.
+//
+// Where rows cannot be read or written 16 bytes at a time (odd strides), a
+// whole warp exchanges its 32 rows through its staging buffer, so that neighbouring lanes
+// touch neighbouring elements; `stage` is that buffer, or NULL (each lane by itself).
 // ---------------------------------------------------------------------------
-template <int TYPE>
-__device__ __forceinline__ void load_row(float (&v)[kCh], const uint16_t* p, int n, bool vec)
+template <int TYPE, int CH>
+__device__ __forceinline__ void load_row(float (&v)[CH], const uint16_t* p, int n, bool vec)
 {
-    if (vec && n == kCh) {
-        uint4 w[2];
-        w[0] = *reinterpret_cast<const uint4*>(p);
-        w[1] = *reinterpret_cast<const uint4*>(p + 8);
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if (vec && n == CH) {
 #pragma unroll
-        for (int i = 0; i < kCh / 2; ++i) {
-            const float2 f = unpack2<TYPE>(u[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+        for (int i = 0; i < CH; i += 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + i);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack2<TYPE>(u[k]);
+                v[i + 2 * k] = f.x;
+                v[i + 2 * k + 1] = f.y;
+            }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kCh; ++i) v[i] = i < n ? to_f32<TYPE>(p[i]) : 0.f;
+        for (int i = 0; i < CH; ++i) v[i] = i < n ? to_f32<TYPE>(p[i]) : 0.f;
     }
 }
 
-template <int TYPE>
-__device__ __forceinline__ void store_row16(uint16_t* p, const float (&v)[kCh], int n, bool vec)
+// Rows row - lane .. of a matrix with stride ld (base at column c0), one per lane of a
+// converged warp; lanes with `valid` have a row.
+template <int TYPE, int CH>
+__device__ __forceinline__ void load_rows(float (&v)[CH], const uint16_t* base, long long ld, long long row, int n,
+                                          bool vec, bool valid, uint32_t* stage)
 {
-    uint32_t w[kCh / 2];
+    if (stage == nullptr || vec) {
+        if (valid) load_row<TYPE, CH>(v, base + row * ld, n, vec);
+    } else if constexpr (CH == 16) {
+        const int lane = threadIdx.x & 31;
+        const int rows = __popc(__ballot_sync(0xffffffffu, valid));   // the first lanes'
+        const int r0 = lane >> 4, c = lane & 15;
+        const long long first = row - lane;
+        uint16_t* st = reinterpret_cast<uint16_t*>(stage);
+#pragma unroll 4
+        for (int i = 0; i < 32; i += 2) {
+            const int r = i + r0;
+            if (r < rows && c < n) st[r * (2 * kStagePitch) + c] = base[(first + r) * ld + c];
+        }
+        __syncwarp();
+        load_row<TYPE, CH>(v, st + lane * (2 * kStagePitch), valid ? n : 0, false);
+        __syncwarp();
+    }
+}
+
+template <int TYPE, int CH>
+__device__ __forceinline__ void store_rows16(uint16_t* base, long long ld, long long row, const float (&v)[CH], int n,
+                                             bool vec, bool valid, uint32_t* stage)
+{
+    uint32_t w[CH / 2];
 #pragma unroll
-    for (int i = 0; i < kCh / 2; ++i) w[i] = pack2<TYPE>(v[2 * i], v[2 * i + 1]);
-    if (vec && n == kCh) {
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int i = 0; i < CH / 2; ++i) w[i] = pack2<TYPE>(v[2 * i], v[2 * i + 1]);
+    if (vec && n == CH) {
+        if (valid) {
+            uint4* p = reinterpret_cast<uint4*>(base + row * ld);
+#pragma unroll
+            for (int i = 0; i < CH / 8; ++i) p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    } else if (CH != 16 || stage == nullptr || vec) {
+        if (valid) {
+            uint16_t* p = base + row * ld;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                if (i < n) p[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+        }
+    } else if constexpr (CH == 16) {
+        const int lane = threadIdx.x & 31;
+        const int rows = __popc(__ballot_sync(0xffffffffu, valid));
+        const int r0 = lane >> 4, c = lane & 15;
+        const long long first = row - lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) stage[lane * kStagePitch + i] = w[i];
+        __syncwarp();
+        const uint16_t* st = reinterpret_cast<const uint16_t*>(stage);
+#pragma unroll 4
+        for (int i = 0; i < 32; i += 2) {
+            const int r = i + r0;
+            if (r < rows && c < n) base[(first + r) * ld + c] = st[r * (2 * kStagePitch) + c];
+        }
+        __syncwarp();
+    }
+}
+
+template <int CH>
+__device__ __forceinline__ void store_rows32(float* base, long long ld, long long row, const float (&v)[CH], int n,
+                                             bool vec, bool accumulate, bool valid, uint32_t* stage)
+{
+    if (vec && n == CH) {
+        if (valid) {
+            float* p = base + row * ld;
+#pragma unroll
+            for (int i = 0; i < CH; i += 4) {
+                float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                if (accumulate) {
+                    const float4 w = *reinterpret_cast<const float4*>(p + i);
+                    t = make_float4(t.x + w.x, t.y + w.y, t.z + w.z, t.w + w.w);
+                }
+                *reinterpret_cast<float4*>(p + i) = t;
+            }
+        }
+    } else if (stage == nullptr || vec) {
+        if (valid) {
+            float* p = base + row * ld;
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+                if (i < n) p[i] = accumulate ? p[i] + v[i] : v[i];
+        }
     } else {
+        const int lane = threadIdx.x & 31;
+        const int rows = __popc(__ballot_sync(0xffffffffu, valid));
+        const int r0 = lane >> 3, c = lane & 7;
+        const long long first = row - lane;
 #pragma unroll
-        for (int i = 0; i < kCh; ++i)
-            if (i < n) p[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+        for (int h = 0; h < CH; h += 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) stage[lane * kStagePitch + i] = __float_as_uint(v[h + i]);
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < 32; i += 4) {
+                const int r = i + r0;
+                if (r < rows && h + c < n) {
+                    float* p = base + (first + r) * ld + h + c;
+                    const float t = __uint_as_float(stage[r * kStagePitch + c]);
+                    *p = accumulate ? *p + t : t;
+                }
+            }
+            __syncwarp();
+        }
     }
 }
 
-template <int ACT>
-__device__ __forceinline__ void act_all(float (&v)[kCh])
+template <int ACT, int CH>
+__device__ __forceinline__ void act_all(float (&v)[CH])
 {
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) v[i] = act_value<ACT>(v[i]);
+    for (int i = 0; i < CH; ++i) v[i] = act_value<ACT>(v[i]);
 }
-__device__ __forceinline__ void act_switch(float (&v)[kCh], int act)
+template <int CH>
+__device__ __forceinline__ void act_switch(float (&v)[CH], int act)
 {
     if (act == kActSilu) act_all<kActSilu>(v);
     else if (act == kActGeluTanh) act_all<kActGeluTanh>(v);
@@ -164,70 +274,53 @@ __device__ __forceinline__ void act_switch(float (&v)[kCh], int act)
 }
 
 // a (and b, gated: u) hold the sums of `row`, columns c0 .. c0 + n - 1 of source `src`.
-template <int TYPE, int MODE>
-__device__ __forceinline__ void finish_row(const LinearParams& p, float (&a)[kCh], float (&b)[kCh], int src,
-                                           long long row, int c0, int n)
+// With `stage`, all lanes of a converged warp hold consecutive rows.
+template <int TYPE, int MODE, int CH>
+__device__ __forceinline__ void finish_rows(const LinearParams& p, float (&a)[CH], float (&b)[CH], int src, long long row,
+                                            int c0, int n, bool valid, uint32_t* stage)
 {
     if constexpr (MODE == kModeLinear || MODE == kModeGated) {
         if (p.bias[0] != nullptr) {
-            float t[kCh];
-            load_row<TYPE>(t, p.bias[0] + c0, n, p.vec_bias);
+            float t[CH];
+            load_row<TYPE, CH>(t, p.bias[0] + c0, n, p.vec_bias);
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) a[i] += t[i];
+            for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
         if (MODE == kModeGated && p.bias[1] != nullptr) {
-            float t[kCh];
-            load_row<TYPE>(t, p.bias[1] + c0, n, p.vec_bias);
+            float t[CH];
+            load_row<TYPE, CH>(t, p.bias[1] + c0, n, p.vec_bias);
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) b[i] += t[i];
+            for (int i = 0; i < CH; ++i) b[i] += t[i];
         }
-        if (p.keep[0] != nullptr) store_row16<TYPE>(p.keep[0] + row * p.ldk + c0, a, n, p.vec_keep);
-        if (MODE == kModeGated && p.keep[1] != nullptr) store_row16<TYPE>(p.keep[1] + row * p.ldk + c0, b, n, p.vec_keep);
-        act_switch(a, p.act);
+        if (p.keep[0] != nullptr) {
+            store_rows16<TYPE, CH>(p.keep[0] + c0, p.ldk, row, a, n, p.vec_keep, valid, stage);
+            if (MODE == kModeGated) store_rows16<TYPE, CH>(p.keep[1] + c0, p.ldk, row, b, n, p.vec_keep, valid, stage);
+        }
+        act_switch<CH>(a, p.act);
         if constexpr (MODE == kModeGated) {
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) a[i] *= b[i];
+            for (int i = 0; i < CH; ++i) a[i] *= b[i];
         }
         if (MODE == kModeLinear && p.residual != nullptr) {
-            float t[kCh];
-            load_row<TYPE>(t, p.residual + row * p.ldr + c0, n, p.vec_res);
+            float t[CH] = {};
+            load_rows<TYPE, CH>(t, p.residual + c0, p.ldr, row, n, p.vec_res, valid, stage);
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) a[i] += t[i];
+            for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
-        store_row16<TYPE>(static_cast<uint16_t*>(p.out[0]) + row * p.ldo + c0, a, n, p.vec_out);
+        store_rows16<TYPE, CH>(static_cast<uint16_t*>(p.out[0]) + c0, p.ldo, row, a, n, p.vec_out, valid, stage);
     } else if constexpr (MODE == kModeGradInput) {
-        store_row16<TYPE>(static_cast<uint16_t*>(p.out[0]) + row * p.ldo + c0, a, n, p.vec_out);
+        store_rows16<TYPE, CH>(static_cast<uint16_t*>(p.out[0]) + c0, p.ldo, row, a, n, p.vec_out, valid, stage);
+    } else if (p.out_f32) {
+        store_rows32<CH>(static_cast<float*>(p.out[src]) + c0, p.ldo, row, a, n, p.vec_out, p.accumulate != 0, valid, stage);
     } else {
-        if (p.out_f32) {
-            float* o = static_cast<float*>(p.out[src]) + row * p.ldo + c0;
-            if (p.vec_out && n == kCh) {
+        uint16_t* o = static_cast<uint16_t*>(p.out[src]) + c0;
+        if (p.accumulate) {
+            float t[CH] = {};
+            load_rows<TYPE, CH>(t, o, p.ldo, row, n, p.vec_out, valid, stage);
 #pragma unroll
-                for (int i = 0; i < kCh; i += 4) {
-                    float4 v = make_float4(a[i], a[i + 1], a[i + 2], a[i + 3]);
-                    if (p.accumulate) {
-                        const float4 w = *reinterpret_cast<const float4*>(o + i);
-                        v.x += w.x;
-                        v.y += w.y;
-                        v.z += w.z;
-                        v.w += w.w;
-                    }
-                    *reinterpret_cast<float4*>(o + i) = v;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kCh; ++i)
-                    if (i < n) o[i] = p.accumulate ? o[i] + a[i] : a[i];
-            }
-        } else {
-            uint16_t* o = static_cast<uint16_t*>(p.out[src]) + row * p.ldo + c0;
-            if (p.accumulate) {
-                float t[kCh];
-                load_row<TYPE>(t, o, n, p.vec_out);
-#pragma unroll
-                for (int i = 0; i < kCh; ++i) a[i] += t[i];
-            }
-            store_row16<TYPE>(o, a, n, p.vec_out);
+            for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
+        store_rows16<TYPE, CH>(o, p.ldo, row, a, n, p.vec_out, valid, stage);
     }
 }
 
@@ -391,50 +484,54 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = true;
             bool issued_any = false;
             int it = 0;
-            for (int tile = unit; ok && tile < p.num_tiles; tile += units, ++it) {
-                const int acc = it & 1;
-                const uint32_t aph = static_cast<uint32_t>(it >> 1) & 1u;
-                ok = PAIR ? mbar_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty)
-                          : mbar_wait(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kLinAccCols);
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    ok = lin_wait(full0 + 8 * stage, phase, wc, kSiteLinFull);
+            const int seg_kb = MODE == kModeGradWeight ? p.seg_kb : kb_end - kb_begin;
+            for (int tile = unit; ok && tile < p.num_tiles; tile += units) {
+                for (int seg = kb_begin; ok && seg < kb_end; seg += seg_kb, ++it) {
+                    const int acc = it & 1;
+                    const uint32_t aph = static_cast<uint32_t>(it >> 1) & 1u;
+                    ok = PAIR ? mbar_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty)
+                              : mbar_wait(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty);
+                    ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t a = sA + static_cast<uint32_t>(stage * p.a_bytes);
-                    const uint32_t b = sB + static_cast<uint32_t>(stage * p.b_bytes);
-                    if (lin_elect()) {
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kLinAccCols);
+                    const int seg_end = kb_end - seg < seg_kb ? kb_end : seg + seg_kb;
+                    for (int kb = seg; kb < seg_end; ++kb) {
+                        ok = lin_wait(full0 + 8 * stage, phase, wc, kSiteLinFull);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t a = sA + static_cast<uint32_t>(stage * p.a_bytes);
+                        const uint32_t b = sB + static_cast<uint32_t>(stage * p.b_bytes);
+                        if (lin_elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            // read along k: 32 bytes of every 128-byte row; read along rows
-                            // (columns): 16 k rows of 128 bytes, 64-element blocks 8 KB apart
-                            const uint64_t ad = kAMn ? smem_desc_sw128(a + kk * 2048, 8192, 1024)
-                                                     : smem_desc_sw128(a + kk * 32, 16, 1024);
-                            const uint64_t bd = kBMn ? smem_desc_sw128(b + kk * 2048, 8192, 1024)
-                                                     : smem_desc_sw128(b + kk * 32, 16, 1024);
-                            const uint32_t more = kb != kb_begin || kk != 0 ? 1u : 0u;
-                            if constexpr (PAIR) mma_f16_pair(d, ad, bd, p.idesc, more);
-                            else mma_f16(d, ad, bd, p.idesc, more);
+                            for (int kk = 0; kk < 4; ++kk) {
+                                // read along k: 32 bytes of every 128-byte row; read along rows
+                                // (columns): 16 k rows of 128 bytes, 64-element blocks 8 KB apart
+                                const uint64_t ad = kAMn ? smem_desc_sw128(a + kk * 2048, 8192, 1024)
+                                                         : smem_desc_sw128(a + kk * 32, 16, 1024);
+                                const uint64_t bd = kBMn ? smem_desc_sw128(b + kk * 2048, 8192, 1024)
+                                                         : smem_desc_sw128(b + kk * 32, 16, 1024);
+                                const uint32_t more = kb != seg || kk != 0 ? 1u : 0u;
+                                if constexpr (PAIR) mma_f16_pair(d, ad, bd, p.idesc, more);
+                                else mma_f16(d, ad, bd, p.idesc, more);
+                            }
+                            if constexpr (PAIR) mma_commit_pair_multicast(empty0 + 8 * stage, 0x3);
+                            else mma_commit(empty0 + 8 * stage);
                         }
-                        if constexpr (PAIR) mma_commit_pair_multicast(empty0 + 8 * stage, 0x3);
-                        else mma_commit(empty0 + 8 * stage);
+                        __syncwarp();
+                        issued_any = true;
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    if (lin_elect()) {
+                        if constexpr (PAIR) mma_commit_pair_multicast(tfull0 + 8 * acc, 0x3);
+                        else mma_commit(tfull0 + 8 * acc);
                     }
                     __syncwarp();
-                    issued_any = true;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
-                if (!ok) break;
-                if (lin_elect()) {
-                    if constexpr (PAIR) mma_commit_pair_multicast(tfull0 + 8 * acc, 0x3);
-                    else mma_commit(tfull0 + 8 * acc);
-                }
-                __syncwarp();
             }
             if (!ok && issued_any) {
                 // abort: every MMA issued so far finishes before TMEM is freed
@@ -449,66 +546,122 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------------
-        // epilogue: 32 rows a warp (the TMEM lanes it may read)
+        // epilogue: 32 rows a warp (the TMEM lanes it may read), every other kCh columns
         // ------------------------------------------------------------------
         const int quarter = warp & 3;
+        const int half = (warp - 2) >> 2;
         const uint32_t lead_tempty0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
+        uint32_t* stage = p.stage_out
+                              ? reinterpret_cast<uint32_t*>(smem + kLinRingBytes - kStageBytes) + (warp - 2) * 32 * kStagePitch
+                              : nullptr;
+        auto hand_back = [&](int acc) {   // this warp has read its part of the accumulator
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_remote(lead_tempty0 + 8 * acc);
+                else mbar_arrive(tempty0 + 8 * acc);
+            }
+        };
+        bool ok = true;
         int it = 0;
-        for (int tile = unit; tile < p.num_tiles; tile += units, ++it) {
-            const int acc = it & 1;
-            const uint32_t aph = static_cast<uint32_t>(it >> 1) & 1u;
-            if (!lin_wait(tfull0 + 8 * acc, aph, wc, kSiteLinTmemFull)) break;
-            tc_fence_after_sync();
+        for (int tile = unit; ok && tile < p.num_tiles; tile += units) {
             int pm, pn;
             tile_coord(tile, p.num_m, p.num_n, p.group_m, &pm, &pn);
             const int src = MODE == kModeGradWeight && pm >= p.num_m1 ? 1 : 0;
             const int m0 = (pm - src * p.num_m1) * kTileRows + (PAIR ? rank * 128 : 0) + quarter * 32;
             const int n0 = pn * p.wcols;
             const int row = m0 + lane;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * kLinAccCols);
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
             const bool any = m0 < p.rows;   // rows of this warp's to store
-            if (any && p.split == 1) {
-                const int left = p.cols - n0;
-                const int width = left < p.wcols ? left : p.wcols;
-#pragma unroll 1
-                for (int c = 0; c < width; c += kCh) {
-                    uint32_t ra[kCh], rb[kCh];
-                    lin_tmem_ld16(t_row + c, ra);
-                    if constexpr (kGated) lin_tmem_ld16(t_row + p.wcols + c, rb);
-                    tmem_ld_wait();
-                    float a[kCh], b[kCh];
+            const bool valid = row < p.rows;
+            const int left = p.cols - n0;
+            const int width = left < p.wcols ? left : p.wcols;
+            // split k: partials stay in this CTA's shared memory, over the ring (whose stages the
+            // MMAs have finished reading), bn + 4 floats a row
+            float* part = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * (p.bn + 4);
+            if constexpr (MODE == kModeGradWeight) {
+                float sum[8][kCh];
 #pragma unroll
-                    for (int i = 0; i < kCh; ++i) {
-                        a[i] = __uint_as_float(ra[i]);
-                        b[i] = kGated ? __uint_as_float(rb[i]) : 0.f;
-                    }
-                    if (row < p.rows)
-                        finish_row<TYPE, MODE>(p, a, b, src, row, n0 + c, width - c < kCh ? width - c : kCh);
-                }
-            } else if (any) {
-                // split k: the partial stays in this CTA's shared memory, over the ring (whose
-                // stages the MMAs have finished reading), bn + 4 floats a row
-                fence_proxy_async_smem();
-                float* part = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * (p.bn + 4);
-#pragma unroll 1
-                for (int c = 0; c < p.bn; c += kCh) {
-                    uint32_t r[kCh];
-                    lin_tmem_ld16(t_row + c, r);
-                    tmem_ld_wait();
-                    if (row < p.rows) {
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-                        for (int i = 0; i < kCh; i += 4)
-                            *reinterpret_cast<uint4*>(part + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                    for (int i = 0; i < kCh; ++i) sum[j][i] = 0.f;
+                for (int seg = kb_begin; seg < kb_end; seg += p.seg_kb, ++it) {
+                    const int acc = it & 1;
+                    ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (any) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int c = (2 * j + half) * kCh;
+                            if (c < p.bn) {
+                                uint32_t r[kCh];
+                                lin_tmem_ld16(t_row + acc * kLinAccCols + c, r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < kCh; ++i) sum[j][i] += __uint_as_float(r[i]);
+                            }
+                        }
+                    }
+                    hand_back(acc);
+                }
+                if (!ok) break;
+                if (any) {
+                    if (p.split > 1) fence_proxy_async_smem();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int c = (2 * j + half) * kCh;
+                        if (p.split > 1) {
+                            if (c < p.bn && valid) {
+#pragma unroll
+                                for (int i = 0; i < kCh; i += 4)
+                                    *reinterpret_cast<float4*>(part + c + i) =
+                                        make_float4(sum[j][i], sum[j][i + 1], sum[j][i + 2], sum[j][i + 3]);
+                            }
+                        } else if (c < width) {
+                            finish_rows<TYPE, MODE, kCh>(p, sum[j], sum[j], src, row, n0 + c,
+                                                         width - c < kCh ? width - c : kCh, valid, stage);
+                        }
                     }
                 }
-            }
-            // all of this accumulator is read: back to the MMA warp
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_remote(lead_tempty0 + 8 * acc);
-                else mbar_arrive(tempty0 + 8 * acc);
+            } else {
+                const int acc = it & 1;
+                ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
+                if (!ok) break;
+                ++it;
+                tc_fence_after_sync();
+                const uint32_t t_acc = t_row + static_cast<uint32_t>(acc * kLinAccCols);
+                if (any && p.split == 1) {
+#pragma unroll 1
+                    for (int c = half * kCh; c < width; c += 2 * kCh) {
+                        uint32_t ra[kCh], rb[kCh];
+                        lin_tmem_ld16(t_acc + c, ra);
+                        if constexpr (kGated) lin_tmem_ld16(t_acc + p.wcols + c, rb);
+                        tmem_ld_wait();
+                        float a[kCh], b[kCh];
+#pragma unroll
+                        for (int i = 0; i < kCh; ++i) {
+                            a[i] = __uint_as_float(ra[i]);
+                            b[i] = kGated ? __uint_as_float(rb[i]) : 0.f;
+                        }
+                        finish_rows<TYPE, MODE, kCh>(p, a, b, src, row, n0 + c, width - c < kCh ? width - c : kCh, valid,
+                                                     stage);
+                    }
+                } else if (any) {
+                    fence_proxy_async_smem();
+#pragma unroll 1
+                    for (int c = half * kCh; c < p.bn; c += 2 * kCh) {
+                        uint32_t r[kCh];
+                        lin_tmem_ld16(t_acc + c, r);
+                        tmem_ld_wait();
+                        if (valid) {
+#pragma unroll
+                            for (int i = 0; i < kCh; i += 4)
+                                *reinterpret_cast<uint4*>(part + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                        }
+                    }
+                }
+                hand_back(acc);
             }
         }
         __syncwarp();
@@ -519,6 +672,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             // One tile per cluster.  Barrier 1: every CTA's partial is in its shared memory.
             cluster_sync();
             if (warp >= 2) {
+                // This CTA's columns of the tile (a multiple of 8, so that 16-byte accesses stay
+                // aligned), 8 columns of a row per thread and turn, neighbouring threads on
+                // neighbouring rows.
+                constexpr int kW = 8;
                 int pm, pn;
                 tile_coord(unit, p.num_m, p.num_n, p.group_m, &pm, &pn);
                 const int src = MODE == kModeGradWeight && pm >= p.num_m1 ? 1 : 0;
@@ -526,40 +683,51 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 const int n0 = pn * p.wcols;
                 const int left = p.cols - n0;
                 const int width = left < p.wcols ? left : p.wcols;
-                const int lrow = (warp & 3) * 32 + lane;
-                const int slice = ((width + p.split - 1) / p.split + 7) & ~7;   // 16-byte accesses stay aligned
-                const int c_end = (rank + 1) * slice < width ? (rank + 1) * slice : width;
-                const uint32_t base = sA + static_cast<uint32_t>(lrow * (p.bn + 4) * 4);
-                if (r0 + lrow < p.rows) {
-#pragma unroll 1
-                    for (int c = rank * slice; c < c_end; c += kCh) {
-                        float a[kCh], b[kCh];
+                const int rows = p.rows - r0 < 128 ? p.rows - r0 : 128;
+                const int slice = ((width + p.split - 1) / p.split + kW - 1) / kW * kW;
+                const int c_begin = rank * slice;
+                const int c_end = c_begin + slice < width ? c_begin + slice : width;
+                const int items = c_begin < c_end ? (c_end - c_begin + kW - 1) / kW * rows : 0;
+                for (int e = static_cast<int>(threadIdx.x) - 64; e < items; e += 32 * kLinEpiWarps) {
+                    const int lrow = e % rows;
+                    const int c = c_begin + e / rows * kW;
+                    const uint32_t base = sA + static_cast<uint32_t>((lrow * (p.bn + 4) + c) * 4);
+                    float a[kW] = {}, b[kW] = {};
+                    // four partials' loads in flight; summed in rank order
+                    for (int q0 = 0; q0 < p.split; q0 += 4) {
+                        float4 v[4][2], w[4][2];
 #pragma unroll
-                        for (int i = 0; i < kCh; ++i) a[i] = b[i] = 0.f;
-#pragma unroll 1
-                        for (int q = 0; q < p.split; ++q) {
-                            const uint32_t peer = mapa_shared(base, static_cast<uint32_t>(q));
+                        for (int q = 0; q < 4; ++q) {
+                            if (q0 + q < p.split) {
+                                const uint32_t peer = mapa_shared(base, static_cast<uint32_t>(q0 + q));
 #pragma unroll
-                            for (int i = 0; i < kCh; i += 4) {
-                                if (c + i < c_end) {
-                                    const float4 v = ld_shared_cluster_v4(peer + static_cast<uint32_t>(c + i) * 4u);
-                                    a[i] += v.x;
-                                    a[i + 1] += v.y;
-                                    a[i + 2] += v.z;
-                                    a[i + 3] += v.w;
+                                for (int i = 0; i < 2; ++i) {
+                                    v[q][i] = ld_shared_cluster_v4(peer + 16u * i);
+                                    if constexpr (kGated) w[q][i] = ld_shared_cluster_v4(peer + static_cast<uint32_t>(p.wcols) * 4u + 16u * i);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (q0 + q < p.split) {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    a[4 * i] += v[q][i].x;
+                                    a[4 * i + 1] += v[q][i].y;
+                                    a[4 * i + 2] += v[q][i].z;
+                                    a[4 * i + 3] += v[q][i].w;
                                     if constexpr (kGated) {
-                                        const float4 w = ld_shared_cluster_v4(
-                                            peer + static_cast<uint32_t>(p.wcols + c + i) * 4u);
-                                        b[i] += w.x;
-                                        b[i + 1] += w.y;
-                                        b[i + 2] += w.z;
-                                        b[i + 3] += w.w;
+                                        b[4 * i] += w[q][i].x;
+                                        b[4 * i + 1] += w[q][i].y;
+                                        b[4 * i + 2] += w[q][i].z;
+                                        b[4 * i + 3] += w[q][i].w;
                                     }
                                 }
                             }
                         }
-                        finish_row<TYPE, MODE>(p, a, b, src, r0 + lrow, n0 + c, c_end - c < kCh ? c_end - c : kCh);
                     }
+                    finish_rows<TYPE, MODE, kW>(p, a, b, src, r0 + lrow, n0 + c, c_end - c < kW ? c_end - c : kW, true,
+                                                nullptr);
                 }
             }
             // Barrier 2: no CTA leaves while a peer may still read its shared memory.
@@ -635,11 +803,18 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     p.a_bytes = p.a_rows * 128;
     const int b_rows = PAIR ? g.bn / 2 : g.bn;
     p.b_bytes = b_rows * 128;
+    const int ob = g.out_f32 ? 4 : 2;
+    p.vec_out = lin_aligned16(g.out[0], g.ldo * ob) && lin_aligned16(g.out[1], 0);
+    p.vec_res = lin_aligned16(g.residual, g.ldr * 2);
+    p.vec_keep = lin_aligned16(g.keep[0], g.ldk * 2) && lin_aligned16(g.keep[1], 0);
+    p.vec_bias = lin_aligned16(g.bias[0], 0) && lin_aligned16(g.bias[1], 0);
+    p.stage_out = !(p.vec_out && (p.vec_res || g.residual == nullptr) && (p.vec_keep || g.keep[0] == nullptr));
     // (with few rows the MMA reads up to 16 KB from the start of the last stage's A, into B's stages)
-    p.stages = kLinRingBytes / (p.a_bytes + p.b_bytes);
+    p.stages = (kLinRingBytes - (p.stage_out ? kStageBytes : 0)) / (p.a_bytes + p.b_bytes);
     if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
     p.split = PAIR || g.split < 2 ? 1 : g.split;
     while (p.split > p.kbs * p.k_sources) p.split /= 2;   // every CTA of a cluster has a k-block
+    p.seg_kb = g.out_f32 ? kSegmentKb : p.kbs * p.k_sources;
     p.idesc = idesc_f16(TYPE == kTypeBF16, kAMn, kBMn, kTileRows, g.bn);
     for (int i = 0; i < 2; ++i) {
         p.out[i] = g.out[i];
@@ -653,11 +828,6 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     p.act = g.act;
     p.out_f32 = g.out_f32;
     p.accumulate = g.accumulate;
-    const int ob = g.out_f32 ? 4 : 2;
-    p.vec_out = lin_aligned16(g.out[0], g.ldo * ob) && lin_aligned16(g.out[1], 0);
-    p.vec_res = lin_aligned16(g.residual, g.ldr * 2);
-    p.vec_keep = lin_aligned16(g.keep[0], g.ldk * 2) && lin_aligned16(g.keep[1], 0);
-    p.vec_bias = lin_aligned16(g.bias[0], 0) && lin_aligned16(g.bias[1], 0);
     p.status = g.status;
     p.wait_limit_ns = g.wait_limit_ns;
 
