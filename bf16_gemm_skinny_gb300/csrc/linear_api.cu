@@ -273,21 +273,21 @@ int enqueue_forward(const ForwardArgs& a, void* stream, bool* launched)
     bsk::LinearLaunch g;
     g.mode = a.gated ? bsk::kModeGated : bsk::kModeLinear;
     g.type = a.type;
-    g.A[0] = a.x;
-    g.lda = a.x_stride;
-    g.B[0] = a.W[0];
-    g.B[1] = a.gated ? a.W[1] : nullptr;
-    g.ldb = a.w_stride;
-    g.rows = a.n;
-    g.cols = a.M;
-    g.k = a.K;
-    g.out[0] = a.out;
+    g.parts = parts;
+    g.n = a.n;
+    g.M = a.M;
+    g.K = a.K;
+    g.x = a.x;
+    g.ldx = a.x_stride;
+    g.ldw = a.w_stride;
+    g.out = a.out;
     g.ldo = a.out_stride;
     g.act = a.activation;
     g.residual = a.residual;
     g.ldr = a.r_stride;
     g.ldk = a.keep_stride;
     for (int i = 0; i < parts; ++i) {
+        g.W[i] = a.W[i];
         g.bias[i] = a.bias[i];
         g.keep[i] = a.keep[i];
     }
@@ -299,17 +299,17 @@ int enqueue_forward(const ForwardArgs& a, void* stream, bool* launched)
         if ((st = ws.take()) != BSK_OK) return st;
         const cudaError_t e = cudaMemsetAsync(ws.at(at), 0, bytes, ctx.s);
         if (e != cudaSuccess) return fail_cuda(e, "cudaMemsetAsync");
-        g.A[0] = g.B[0] = ws.at(at);
-        if (a.gated) g.B[1] = g.B[0];
-        g.lda = g.ldb = g.k = 8;
+        g.x = g.W[0] = ws.at(at);
+        if (a.gated) g.W[1] = g.W[0];
+        g.ldx = g.ldw = g.K = 8;
         return ctx.run(g);
     }
     Packer pack(ws);
-    pack.plan(&g.A[0], &g.lda, a.n, a.K);
+    pack.plan(&g.x, &g.ldx, a.n, a.K);
     // the weights share a stride: if one needs a copy, both get one
-    const bool w_direct = direct(g.B[0], g.ldb) && (!a.gated || direct(g.B[1], g.ldb));
+    const bool w_direct = direct(g.W[0], g.ldw) && (!a.gated || direct(g.W[1], g.ldw));
     if (!w_direct)
-        for (int i = 0; i < parts; ++i) pack.force(&g.B[i], &g.ldb, a.M, a.K);
+        for (int i = 0; i < parts; ++i) pack.force(&g.W[i], &g.ldw, a.M, a.K);
     if ((st = ws.take()) != BSK_OK) return st;
     if ((st = pack.run(ctx.sms, ctx.pdl, ctx.status, ctx.limit_ns, ctx.s)) != BSK_OK) return st;
     return ctx.run(g);
@@ -440,60 +440,49 @@ int enqueue_backward(const BackwardArgs& a, void* stream, bool* launched)
         l.chunks = chunks;
         l.pdl = ctx.pdl;
         if (bsk::launch_act_backward(l, ctx.s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
-        if (want_db) {
-            bsk::BiasGradLaunch b;
-            b.type = a.type;
-            b.parts = parts;
-            b.M = a.M;
-            b.chunks = chunks;
-            b.partial = l.partial;
-            b.db[0] = a.db[0];
-            b.db[1] = a.db[1];
-            b.f32 = gs == 4;
-            b.accumulate = a.accumulate != 0;
-            b.pdl = ctx.pdl;
-            if (bsk::launch_bias_grad(b, ctx.s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
-        }
+    }
+    const float* partial = want_db ? reinterpret_cast<const float*>(ws.at(partial_at)) : nullptr;
+    if (!products) {   // the bias gradients alone
+        bsk::BiasGradLaunch b;
+        b.type = a.type;
+        b.parts = parts;
+        b.M = a.M;
+        b.chunks = chunks;
+        b.partial = partial;
+        b.db[0] = a.db[0];
+        b.db[1] = a.db[1];
+        b.f32 = gs == 4;
+        b.accumulate = a.accumulate != 0;
+        b.pdl = ctx.pdl;
+        if (bsk::launch_bias_grad(b, ctx.s, msg, sizeof(msg))) return fail(BSK_ERR_CUDA, "%s", msg);
+        return BSK_OK;
     }
     if ((st = pack.run(ctx.sms, ctx.pdl, ctx.status, ctx.limit_ns, ctx.s)) != BSK_OK) return st;
-    if (want_dx) {
-        bsk::LinearLaunch g;
-        g.mode = bsk::kModeGradInput;
-        g.type = a.type;
-        g.sources = parts;
-        g.lda = ld_dz;
-        g.ldb = ldw;
-        for (int i = 0; i < parts; ++i) {
-            g.A[i] = dz[i];
-            g.B[i] = W[i];
-        }
-        g.rows = a.n;
-        g.cols = a.K;
-        g.k = a.M;
-        g.out[0] = a.dx;
-        g.ldo = a.dx_stride;
-        if ((st = ctx.run(g)) != BSK_OK) return st;
+    bsk::LinearLaunch g;
+    g.mode = bsk::kModeGrad;
+    g.type = a.type;
+    g.parts = parts;
+    g.n = a.n;
+    g.M = a.M;
+    g.K = a.K;
+    g.x = x;
+    g.ldx = ldx;
+    g.ldw = ldw;
+    g.ldz = ld_dz;
+    g.dx = want_dx ? a.dx : nullptr;
+    g.ld_dx = a.dx_stride;
+    g.ld_dw = a.dw_stride;
+    g.grad_f32 = gs == 4;
+    g.accumulate = a.accumulate != 0;
+    g.db_partial = partial;
+    g.db_chunks = chunks;
+    for (int i = 0; i < parts; ++i) {
+        g.W[i] = W[i];
+        g.dz[i] = dz[i];
+        g.dW[i] = want_dw ? a.dW[i] : nullptr;
+        g.db[i] = a.db[i];
     }
-    if (want_dw) {
-        bsk::LinearLaunch g;
-        g.mode = bsk::kModeGradWeight;
-        g.type = a.type;
-        g.sources = parts;
-        g.lda = ld_dz;
-        g.B[0] = x;
-        g.ldb = ldx;
-        for (int i = 0; i < parts; ++i) {
-            g.A[i] = dz[i];
-            g.out[i] = a.dW[i];
-        }
-        g.rows = a.M;
-        g.cols = a.K;
-        g.k = a.n;
-        g.ldo = a.dw_stride;
-        g.out_f32 = gs == 4;
-        g.accumulate = a.accumulate != 0;
-        if ((st = ctx.run(g)) != BSK_OK) return st;
-    }
+    if ((st = ctx.run(g)) != BSK_OK) return st;
     return BSK_OK;
 }
 
@@ -516,35 +505,58 @@ int only_enqueue(int (*enqueue)(const Args&, void*, bool*), const Args& a, void*
 
 namespace bsk {
 
-// The tile, the kernel and the split of a product: the least estimated time.
+// The tile, the kernel and the split of a launch: the least estimated time.
 void plan_linear(LinearLaunch& g)
 {
-    const bool b_mn = g.mode == kModeGradInput || g.mode == kModeGradWeight;
+    const bool grad = g.mode == kModeGrad;
     const bool gated = g.mode == kModeGated;
-    const long long kb = (g.k + 63LL) / 64 * (g.mode == kModeGradInput ? g.sources : 1);
-    const long long row_sources = g.mode == kModeGradWeight ? g.sources : 1;
     const long long opt_kernel = bsk_get_option(BSK_OPT_LINEAR_KERNEL);
     const long long opt_tile = bsk_get_option(BSK_OPT_LINEAR_TILE);
     const long long opt_split = bsk_get_option(BSK_OPT_SPLIT_K);
+    auto up = [](long long a, long long b) { return (a + b - 1) / b; };
     double best = -1.0;
     for (int pair = 0; pair < 2; ++pair) {
         if ((opt_kernel == 1 && pair) || (opt_kernel == 2 && !pair)) continue;
-        const int unit = pair ? (b_mn ? 128 : 64) : gated ? 32 : b_mn ? 64 : 16;
-        const long long rows_per = pair ? 256 : 128;
+        const int unit = pair ? (grad ? 128 : 64) : grad ? 64 : gated ? 32 : 16;
+        const long long tile_rows = pair ? 256 : 128;
         const long long slots = pair ? (g.num_sms > 1 ? g.num_sms / 2 : 1) : g.num_sms;
-        const long long m_tiles = (g.rows + rows_per - 1) / rows_per * row_sources;
+        const long long a_rows = !pair && !grad && g.n < 128 ? up(g.n, 8) * 8 : 128;
         for (int bn = unit; bn <= 256; bn += unit) {
             if (opt_tile > 0 && bn != opt_tile && opt_tile % unit == 0) continue;
             const long long wcols = gated ? bn / 2 : bn;
-            const long long tiles = m_tiles * ((g.cols + wcols - 1) / wcols);
+            // tiles and k-blocks of the launch's products
+            long long tiles[2] = {0, 0}, kb[2] = {0, 0};
+            if (!grad) {
+                tiles[0] = up(g.n, tile_rows) * up(g.M, wcols);
+                kb[0] = up(g.K, 64);
+            } else {
+                if (g.dx != nullptr) {
+                    tiles[0] = up(g.n, tile_rows) * up(g.K, wcols);
+                    kb[0] = up(g.M, 64) * g.parts;
+                }
+                if (g.dW[0] != nullptr) {
+                    tiles[1] = up(g.M, tile_rows) * g.parts * up(g.K, wcols);
+                    kb[1] = up(g.n, 64);
+                }
+            }
+            const int longer = kb[1] > kb[0] ? 1 : 0;
+            const long long t0 = tiles[longer], t1 = tiles[1 - longer], k0 = kb[longer], k1 = kb[1 - longer];
             for (int split = 1; split <= (pair ? 1 : 8); split *= 2) {
                 if (opt_split > 0 && split != opt_split && !pair && opt_split <= 8) continue;
-                if (split > 1 && (kb < 2 * split || opt_split == 1)) break;
-                const long long waves = (tiles * split + slots - 1) / slots;
-                const long long a_rows = !pair && !b_mn && g.rows < 128 ? (g.rows + 7) / 8 * 8 : 128;
-                const double per_kb = pair ? 150.0 + 0.7 * bn : 100.0 + 1.1 * static_cast<double>(a_rows / 4 + bn);
-                const double est = 5000.0 + (split > 1 ? 1500.0 : 0.0) +
-                                   static_cast<double>(waves) * (static_cast<double>((kb + split - 1) / split) * per_kb + 4.0 * bn);
+                if (split > 1 && (k0 < 2 * split || opt_split == 1)) break;
+                const long long fit = split == 1 ? slots : split == 2 ? slots : split == 4 ? slots * 36 / 38 : slots * 30 / 38;
+                if (split > 1 && t1 > 0 && t0 * split > fit) break;
+                const double per_kb = pair ? 130.0 + 0.65 * bn : 90.0 + 0.8 * static_cast<double>(a_rows / 4 + bn);
+                double work;   // of the fullest unit, in k-blocks
+                if (t1 == 0) {
+                    work = static_cast<double>(up(t0 * split, fit) * up(k0, split));
+                } else {
+                    const double mean = static_cast<double>(t0 * k0 + t1 * k1) / static_cast<double>(fit) + 0.5 * static_cast<double>(k1);
+                    const double longest = static_cast<double>(up(k0, split));
+                    work = mean > longest ? mean : longest;
+                }
+                work *= per_kb;
+                const double est = 4000.0 + (split > 1 ? 800.0 + 4.0 * bn : 0.0) + work + 4.0 * bn;
                 if (best < 0.0 || est < best) {
                     best = est;
                     g.pair = pair != 0;
@@ -555,7 +567,7 @@ void plan_linear(LinearLaunch& g)
         }
     }
     const long long opt_group = bsk_get_option(BSK_OPT_GROUP_M);
-    g.group_m = opt_group > 0 ? static_cast<int>(opt_group) : 8;
+    g.group_m = opt_group > 0 ? static_cast<int>(opt_group) : 16;
 }
 
 int launch_linear(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len)

@@ -33,78 +33,112 @@ struct ActBackwardParams {
     uint16_t* dz[2];
     long long ld_dz;
     float* partial;
-    int act;
-    int vec;   // 16-byte accesses allowed everywhere
 };
 
-template <int TYPE>
-__device__ __forceinline__ void grad_load(float (&v)[kGradCols], const uint16_t* p, int n, bool vec)
+// A thread's 8 columns of a block's 256: VEC: side by side (16-byte accesses), else 32
+// apart, so that a warp's 2-byte accesses are to neighbouring addresses whatever the alignment.
+struct GradValues {
+    uint4 w;   // 8 values
+};
+template <bool VEC>
+__device__ __forceinline__ GradValues grad_load(const uint16_t* p, int n)
 {
-    if (vec && n == kGradCols) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    GradValues v;
+    if (VEC && n == kGradCols) {
+        v.w = *reinterpret_cast<const uint4*>(p);
+    } else {
+        uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2<TYPE>(u[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+            const uint32_t lo = 2 * i < n ? p[VEC ? 2 * i : 64 * i] : 0u;
+            const uint32_t hi = 2 * i + 1 < n ? p[VEC ? 2 * i + 1 : 64 * i + 32] : 0u;
+            u[i] = lo | hi << 16;
         }
-    } else {
+        v.w = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    return v;
+}
+template <int TYPE>
+__device__ __forceinline__ void grad_unpack(float (&f)[kGradCols], const GradValues& v)
+{
+    const uint32_t u[4] = {v.w.x, v.w.y, v.w.z, v.w.w};
 #pragma unroll
-        for (int i = 0; i < kGradCols; ++i) v[i] = i < n ? to_f32<TYPE>(p[i]) : 0.f;
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = unpack2<TYPE>(u[i]);
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
     }
 }
 
-template <int TYPE>
-__device__ __forceinline__ void grad_store(uint16_t* p, const float (&v)[kGradCols], int n, bool vec)
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void grad_store(uint16_t* p, const float (&v)[kGradCols], int n)
 {
-    if (vec && n == kGradCols) {
+    if (VEC && n == kGradCols) {
         *reinterpret_cast<uint4*>(p) = make_uint4(pack2<TYPE>(v[0], v[1]), pack2<TYPE>(v[2], v[3]),
                                                   pack2<TYPE>(v[4], v[5]), pack2<TYPE>(v[6], v[7]));
     } else {
 #pragma unroll
         for (int i = 0; i < kGradCols; ++i)
-            if (i < n) p[i] = to_16<TYPE>(v[i]);
+            if (i < n) p[VEC ? i : 32 * i] = to_16<TYPE>(v[i]);
     }
 }
 
-template <int TYPE, bool GATED, int ACT>
+template <int TYPE, bool GATED, int ACT, bool VEC>
 __global__ void __launch_bounds__(kGradThreads) act_backward_kernel(const ActBackwardParams p)
 {
     constexpr int kParts = GATED ? 2 : 1;
+    constexpr bool kNeedZ = ACT != kActNone || GATED;
     __shared__ float sums[kParts][kGradRowThreads][kGradTileCols];
     griddep_wait();
     griddep_launch_dependents();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int c0 = blockIdx.x * kGradTileCols + tx * kGradCols;
-    const int n = p.M - c0 < kGradCols ? p.M - c0 : kGradCols;
+    const int first = blockIdx.x * kGradTileCols;
+    const int c0 = first + (VEC ? tx * kGradCols : tx);
+    const int left = p.M - c0;
+    const int n = VEC ? (left < kGradCols ? left : kGradCols) : (left + 31) / 32 < kGradCols ? (left + 31) / 32 : kGradCols;
     const long long r0 = static_cast<long long>(blockIdx.y) * p.rows_per_chunk;
     const long long r1 = r0 + p.rows_per_chunk < p.n ? r0 + p.rows_per_chunk : p.n;
-    const bool vec = p.vec != 0;
     float sum[kParts][kGradCols] = {};
-    if (n > 0) {
-#pragma unroll 2
-        for (long long r = r0 + ty; r < r1; r += kGradRowThreads) {
-            float dy[kGradCols], z[kGradCols], u[kGradCols];
-            grad_load<TYPE>(dy, p.dy + r * p.ld_dy + c0, n, vec);
-            if (ACT != kActNone || GATED) grad_load<TYPE>(z, p.z[0] + r * p.ldz + c0, n, vec);
-            if (GATED) grad_load<TYPE>(u, p.z[1] + r * p.ldz + c0, n, vec);
-            float d0[kGradCols], d1[kGradCols];
+    if (left > 0) {
+        // kAhead rows' values are loaded before the first of them is worked on: three loads a thread
+        // in flight left HBM at half its rate.
+        constexpr int kAhead = 3;
+        for (long long r = r0 + ty; r < r1; r += kAhead * kGradRowThreads) {
+            GradValues vy[kAhead], vz[kAhead], vu[kAhead];
 #pragma unroll
-            for (int i = 0; i < kGradCols; ++i) {
-                const float2 f = ACT != kActNone || GATED ? act_value_slope<ACT>(z[i]) : make_float2(0.f, 1.f);
-                d0[i] = GATED ? dy[i] * u[i] * f.y : dy[i] * f.y;
-                d1[i] = GATED ? dy[i] * f.x : 0.f;
-                sum[0][i] += d0[i];
-                if (GATED) sum[kParts - 1][i] += d1[i];
+            for (int a = 0; a < kAhead; ++a) {
+                const long long q = r + a * kGradRowThreads;
+                if (q < r1) {
+                    vy[a] = grad_load<VEC>(p.dy + q * p.ld_dy + c0, n);
+                    if (kNeedZ) vz[a] = grad_load<VEC>(p.z[0] + q * p.ldz + c0, n);
+                    if (GATED) vu[a] = grad_load<VEC>(p.z[1] + q * p.ldz + c0, n);
+                }
             }
-            if (p.dz[0] != nullptr) {
-                grad_store<TYPE>(p.dz[0] + r * p.ld_dz + c0, d0, n, vec);
-                if (GATED) grad_store<TYPE>(p.dz[1] + r * p.ld_dz + c0, d1, n, vec);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const long long q = r + a * kGradRowThreads;
+                if (q >= r1) break;
+                float dy[kGradCols], z[kGradCols], u[kGradCols], d0[kGradCols], d1[kGradCols];
+                grad_unpack<TYPE>(dy, vy[a]);
+                if (kNeedZ) grad_unpack<TYPE>(z, vz[a]);
+                if (GATED) grad_unpack<TYPE>(u, vu[a]);
+#pragma unroll
+                for (int i = 0; i < kGradCols; ++i) {
+                    const float2 f = kNeedZ ? act_value_slope<ACT>(z[i]) : make_float2(0.f, 1.f);
+                    d0[i] = GATED ? dy[i] * u[i] * f.y : dy[i] * f.y;
+                    d1[i] = GATED ? dy[i] * f.x : 0.f;
+                    sum[0][i] += d0[i];
+                    if (GATED) sum[kParts - 1][i] += d1[i];
+                }
+                if (p.dz[0] != nullptr) {
+                    grad_store<TYPE, VEC>(p.dz[0] + q * p.ld_dz + c0, d0, n);
+                    if (GATED) grad_store<TYPE, VEC>(p.dz[1] + q * p.ld_dz + c0, d1, n);
+                }
             }
         }
     }
     if (p.partial != nullptr) {
+        // column e of the block's at [e % 8 or e / 32][...]: a thread's i-th column at i * 32 + tx
 #pragma unroll
         for (int q = 0; q < kParts; ++q)
 #pragma unroll
@@ -112,12 +146,12 @@ __global__ void __launch_bounds__(kGradThreads) act_backward_kernel(const ActBac
         __syncthreads();
         for (int e = threadIdx.x; e < kParts * kGradTileCols; e += kGradThreads) {
             const int q = e / kGradTileCols, c = e % kGradTileCols;
-            const int col = blockIdx.x * kGradTileCols + c;
-            if (col >= p.M) continue;
+            if (first + c >= p.M) continue;
+            const int at = VEC ? (c % kGradCols) * 32 + c / kGradCols : c;
             float v = 0.f;
 #pragma unroll
-            for (int y = 0; y < kGradRowThreads; ++y) v += sums[q][y][(c % kGradCols) * 32 + c / kGradCols];
-            p.partial[(static_cast<long long>(blockIdx.y) * kParts + q) * p.M + col] = v;
+            for (int y = 0; y < kGradRowThreads; ++y) v += sums[q][y][at];
+            p.partial[(static_cast<long long>(blockIdx.y) * kParts + q) * p.M + first + c] = v;
         }
     }
 }
@@ -148,21 +182,22 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int TYPE, bool GATED, int ACT>
-cudaError_t launch_act(const ActBackwardLaunch& a, const ActBackwardParams& p, cudaStream_t stream)
+cudaError_t launch_act(const ActBackwardLaunch& a, const ActBackwardParams& p, bool vec, cudaStream_t stream)
 {
     const dim3 grid((a.M + kGradTileCols - 1) / kGradTileCols, a.chunks);
-    return launch_kernel(act_backward_kernel<TYPE, GATED, ACT>, grid, dim3(kGradThreads), 0, stream, a.pdl, p);
+    auto kern = vec ? act_backward_kernel<TYPE, GATED, ACT, true> : act_backward_kernel<TYPE, GATED, ACT, false>;
+    return launch_kernel(kern, grid, dim3(kGradThreads), 0, stream, a.pdl, p);
 }
 
 template <int TYPE, bool GATED>
-cudaError_t launch_act_switch(const ActBackwardLaunch& a, const ActBackwardParams& p, cudaStream_t stream)
+cudaError_t launch_act_switch(const ActBackwardLaunch& a, const ActBackwardParams& p, bool vec, cudaStream_t stream)
 {
     switch (a.act) {
-    case kActRelu: return launch_act<TYPE, GATED, kActRelu>(a, p, stream);
-    case kActGelu: return launch_act<TYPE, GATED, kActGelu>(a, p, stream);
-    case kActGeluTanh: return launch_act<TYPE, GATED, kActGeluTanh>(a, p, stream);
-    case kActSilu: return launch_act<TYPE, GATED, kActSilu>(a, p, stream);
-    default: return launch_act<TYPE, GATED, kActNone>(a, p, stream);
+    case kActRelu: return launch_act<TYPE, GATED, kActRelu>(a, p, vec, stream);
+    case kActGelu: return launch_act<TYPE, GATED, kActGelu>(a, p, vec, stream);
+    case kActGeluTanh: return launch_act<TYPE, GATED, kActGeluTanh>(a, p, vec, stream);
+    case kActSilu: return launch_act<TYPE, GATED, kActSilu>(a, p, vec, stream);
+    default: return launch_act<TYPE, GATED, kActNone>(a, p, vec, stream);
     }
 }
 
@@ -173,14 +208,16 @@ bool aligned(const void* p, long long ld)
 
 }  // namespace
 
-// Chunks of tokens: about four blocks per SM, each with a row per thread at least.
+// Chunks of tokens (a row of blocks each): some 24 blocks per SM, so that the last wave counts for
+// little, and at least 16 tokens a block.  4096 x 17408 gated: 244 us with 4 blocks per SM, of which 3
+// fit at once.
 int act_backward_chunks(int n, int M, int num_sms)
 {
     const long long cols = (M + kGradTileCols - 1) / kGradTileCols;
-    long long chunks = (4LL * num_sms + cols - 1) / cols;
-    const long long most = (n + kGradRowThreads - 1LL) / kGradRowThreads;
+    long long chunks = (24LL * num_sms + cols - 1) / cols;
+    const long long most = (n + 2LL * kGradRowThreads - 1) / (2LL * kGradRowThreads);
     if (chunks > most) chunks = most;
-    if (chunks > 65535) chunks = 65535;
+    if (chunks > 512) chunks = 512;
     return static_cast<int>(chunks < 1 ? 1 : chunks);
 }
 
@@ -190,7 +227,6 @@ int launch_act_backward(const ActBackwardLaunch& a, cudaStream_t stream, char* m
     p.n = a.n;
     p.M = a.M;
     p.rows_per_chunk = (a.n + a.chunks - 1) / a.chunks;
-    p.act = a.act;
     p.ldz = a.ldz;
     p.dy = static_cast<const uint16_t*>(a.dy);
     p.ld_dy = a.ld_dy;
@@ -203,12 +239,11 @@ int launch_act_backward(const ActBackwardLaunch& a, cudaStream_t stream, char* m
         if (a.z[i] != nullptr) vec = vec && aligned(a.z[i], a.ldz);
         if (a.dz[i] != nullptr) vec = vec && aligned(a.dz[i], a.ld_dz);
     }
-    p.vec = vec;
     cudaError_t e;
     if (a.type == kTypeBF16)
-        e = a.gated ? launch_act_switch<kTypeBF16, true>(a, p, stream) : launch_act_switch<kTypeBF16, false>(a, p, stream);
+        e = a.gated ? launch_act_switch<kTypeBF16, true>(a, p, vec, stream) : launch_act_switch<kTypeBF16, false>(a, p, vec, stream);
     else
-        e = a.gated ? launch_act_switch<kTypeF16, true>(a, p, stream) : launch_act_switch<kTypeF16, false>(a, p, stream);
+        e = a.gated ? launch_act_switch<kTypeF16, true>(a, p, vec, stream) : launch_act_switch<kTypeF16, false>(a, p, vec, stream);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "element-wise backward launch failed: %s", cudaGetErrorString(e));
         return 1;

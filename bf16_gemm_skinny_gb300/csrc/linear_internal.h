@@ -6,8 +6,8 @@
 // TMEM lanes, columns along its registers.
 //   linear   out[t, j] = act(sum_k x[t, k] W[j, k] + b[j]) + r[t, j]
 //   gated    out[t, j] = act(g) * u,  g and u two such sums (Wg and Wu)
-//   input gradient    dx[t, k] = sum over the sources s and features j of dz_s[t, j] W_s[j, k]
-//   weight gradient   dW_s[j, k] (+)= sum_t dz_s[t, j] x[t, k]
+//   gradients         dx[t, k] = sum over the sources s and features j of dz_s[t, j] W_s[j, k],
+//                     dW_s[j, k] (+)= sum_t dz_s[t, j] x[t, k],  one launch for both
 #pragma once
 
 #include <cstddef>
@@ -18,34 +18,40 @@ namespace bsk {
 
 enum ValueType : int { kTypeBF16 = 0, kTypeF16 = 1 };
 enum Activation : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
-enum LinearMode : int { kModeLinear = 0, kModeGated = 1, kModeGradInput = 2, kModeGradWeight = 3 };
+enum LinearMode : int { kModeLinear = 0, kModeGated = 1, kModeGrad = 2 };
 
-// One product.  Operands are 16-bit, 16-byte aligned, with leading dimensions
+// One launch.  Operands are 16-bit, 16-byte aligned, with leading dimensions
 // (elements) that are multiples of 8.
-//   mode          rows x cols   k (per source)  A[s]               B[s]
-//   linear        n x M         K               x [n, K]           W [M, K]
-//   gated         n x M         K               x [n, K]           Wg, Wu [M, K]
-//   input grad.   n x K         M, sources      dz_s [n, M]        W_s [M, K] (read along M)
-//   weight grad.  M x K, sources  n             dz_s [n, M] (read along n)   x [n, K] (read along n)
 struct LinearLaunch {
     int mode = kModeLinear;
     int type = kTypeBF16;
-    int sources = 1;               // gradients: 1 or 2
-    const void* A[2] = {nullptr, nullptr};
-    long long lda = 0;
-    const void* B[2] = {nullptr, nullptr};
-    long long ldb = 0;
-    int rows = 0, cols = 0, k = 0;
-    void* out[2] = {nullptr, nullptr};   // [1]: the second source's weight gradient
+    int parts = 1;                 // sources: 2 in gated layers
+    int n = 0, M = 0, K = 0;       // tokens, output and input features
+    const void* x = nullptr;       // [n, K]
+    long long ldx = 0;
+    const void* W[2] = {nullptr, nullptr};   // [M, K]
+    long long ldw = 0;
+    // forward
+    void* out = nullptr;           // [n, M]
     long long ldo = 0;
-    bool out_f32 = false;          // weight gradients in FP32
-    bool accumulate = false;       // weight gradients added to what is there
     int act = kActNone;
     const void* bias[2] = {nullptr, nullptr};
     const void* residual = nullptr;
     long long ldr = 0;
-    void* keep[2] = {nullptr, nullptr};  // pre-activations, rounded
+    void* keep[2] = {nullptr, nullptr};   // pre-activations, rounded
     long long ldk = 0;
+    // gradients
+    const void* dz[2] = {nullptr, nullptr};   // [n, M]
+    long long ldz = 0;
+    void* dx = nullptr;            // [n, K], NULL: not wanted
+    long long ld_dx = 0;
+    void* dW[2] = {nullptr, nullptr};   // [M, K], NULL: not wanted
+    long long ld_dw = 0;
+    bool grad_f32 = false, accumulate = false;
+    const float* db_partial = nullptr;   // chunks x parts x M sums to add up into db, or NULL
+    int db_chunks = 0;
+    void* db[2] = {nullptr, nullptr};
+
     int num_sms = 1;
     int* status = nullptr;
     unsigned long long wait_limit_ns = 2000000000ull;

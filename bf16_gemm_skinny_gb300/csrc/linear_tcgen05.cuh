@@ -15,8 +15,11 @@
 // product of the same width; the epilogue reads both and stores act(g) * u.
 // Neither g nor u goes through memory unless they are kept for a backward pass.
 //
-// Two k sources (dx = dg Wg + du Wu): one k loop over both, one accumulator, so
-// that dx is rounded once.
+// Gradients: dx (rows are tokens, k are features) and dW (rows are features, k are
+// tokens) are tiles of one launch, the longer k loops first, so that neither waits for the other's
+// last wave.  Both read the same boxes of dz, along k or along rows.  dx of a gated
+// layer (dg Wg + du Wu) is one k loop over both sources and rounded once.  The
+// epilogue warps, idle until the first accumulator, add up the bias gradients' partial sums.
 //
 // Roles (320 threads): warp 0 loads by TMA into a ring of k slices, warp 1 issues
 // the MMAs, warps 2..9 are the epilogue, overlapped with the next tile's loop by a
@@ -25,12 +28,12 @@
 // on into whatever follows in shared memory, and those rows are not stored.
 //
 // Split k (one-CTA tiles, few tiles): the CTAs of a cluster share a tile's k
-// loop, leave FP32 partials in their own shared memory and each finish a part of
-// the columns from all of them, summed in rank order (the result does not depend
-// on timing).
+// loop; each stores its FP32 sums into the shared memory of the CTAs that finish the
+// columns, which add them up in rank order (the result does not depend on timing).
 #pragma once
 
 #include <cstdio>
+#include <type_traits>
 
 #include "bsk_internal.h"
 #include "linear_math.cuh"
@@ -42,19 +45,18 @@ namespace {
 constexpr int kLinEpiWarps = 8;                  // two per quarter of the TMEM lanes: every other kCh columns
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
 constexpr int kLinBK = 64;                       // k values per stage: one 128-byte swizzle row
-constexpr int kLinBarBytes = 512;
-constexpr int kLinSmemBytes = 232448;            // all of it: one CTA per SM, so that 512 TMEM columns are free
-constexpr int kLinRingBytes = kLinSmemBytes - 1024 - kLinBarBytes;
+constexpr int kLinBarBytes = 512 + 32 * kLinEpiWarps * 4;   // barriers, and the bias gradients' sums
+constexpr int kLinSmemBytes = 232448;            // at most
+constexpr int kFewRows = 64;                     // rows up to which the weights' stream is the bound
 constexpr int kLinMaxStages = 24;
-constexpr int kLinAccCols = 256;                 // TMEM columns of one accumulator (two of them)
 constexpr int kCh = 16;                          // columns per epilogue step: 32 bytes of 16-bit values
 constexpr int kStagePitch = 9;                   // words per row of a warp's staging buffer (odd: no bank conflicts)
 constexpr int kStageBytes = kLinEpiWarps * 32 * kStagePitch * 4;
 // FP32 weight gradients: k-blocks summed in an accumulator before they are added to
 // FP32 registers.  A tensor-core accumulation cuts each of its sums (toward zero), so
-// an error grows with their number: dW over 8192 tokens came out 2e-5 off, in segments of 256
-// tokens 1e-6, as much as FP32 arithmetic gives.
-constexpr int kSegmentKb = 16;
+// an error grows with their number: dW over 8192 tokens came out 2e-5 off, in segments of 768
+// tokens 7e-7, as much as FP32 arithmetic gives.
+constexpr int kSegmentKb = 12;
 
 enum LinearWaitSite {
     kSiteLinEmpty = 0x30,
@@ -64,32 +66,93 @@ enum LinearWaitSite {
     kSiteLinDrain = 0x34,
 };
 
-struct LinearParams {
+// A product of a launch: `tiles` tiles of one result.
+struct LinearJob {
     int rows, cols;           // of the result (weight gradient: of each source's)
-    int kbs, k_sources;       // k-blocks per source
+    int kbs, k_sources;       // k-blocks per source, sources one after the other along k
     int num_m, num_m1;        // tile rows in all, of the first source (weight gradient)
-    int num_n, num_tiles, group_m;
+    int num_n, num_tiles;
+    int a_mn;                 // A read along its rows (weight gradient)
+    int seg_kb;               // k-blocks per segment
+    uint32_t idesc;
+    void* out[2];
+    long long ldo;
+    int out_f32, accumulate, vec_out;
+};
+
+struct LinearParams {
+    LinearJob job[2];         // [1]: gradients only, may have no tiles
+    int extra;                // gradients: see tile_of()
+    int group_m;
     int a_rows;               // rows of A staged per CTA (128, or the few there are)
     int bn;                   // accumulator columns per tile
     int wcols;                // result columns per tile: bn, gated bn / 2
     int stages, a_bytes, b_bytes;
-    int seg_kb;               // weight gradient: k-blocks per segment
-    int stage_out;            // rows that no 16-byte accesses reach go through the staging buffers
+    int ring_bytes;           // the stages (and staging buffers), before the barriers
+    int stage_at;             // rows that no 16-byte accesses reach go through staging buffers here; -1: none
+    int acc_cols, tmem_cols;  // TMEM columns of an accumulator, in all
     int split;                // CTAs that share a tile's k loop (a cluster); 1: none
-    uint32_t idesc;
-    void* out[2];
-    long long ldo;
+    int prefetch_kb;          // k-blocks of the first tile's weights brought into L2 ahead
+    const uint8_t* w_rows[2];
+    long long w_ld_bytes;
     const uint16_t* bias[2];
     const uint16_t* residual;
     long long ldr;
     uint16_t* keep[2];
     long long ldk;
     int act;
-    int out_f32, accumulate;
-    int vec_out, vec_res, vec_keep, vec_bias;   // 16-byte accesses allowed
+    int vec_res, vec_keep, vec_bias;   // 16-byte accesses allowed
+    const float* db_partial;
+    int db_chunks, db_parts, db_M, db_f32, db_accumulate;
+    void* db[2];
     int* status;
     unsigned long long wait_limit_ns;
 };
+
+// Tensor maps.  Forward: x, W (Wg), Wu.  Gradients: dz_0, dz_1, W_0, W_1, x.
+struct LinearMaps {
+    CUtensorMap m[5];
+};
+
+// The i-th tile of this CTA (or pair) in `pass`; false when there is none.
+// Without split k there is one pass: tiles go to the `units` CTAs (pairs) in turn, job
+// 0 first.  With it, pass 0 is job 0, a tile per cluster (unit / split), and pass 1 job 1, a tile per
+// CTA.  Units that got one tile of job 0 fewer than the others take p.extra tiles of job 1
+// before all units go on with the rest.
+template <bool SPLIT>
+__device__ __forceinline__ bool tile_of(const LinearParams& p, int pass, int unit, int units, int i, int* job, int* tile)
+{
+    const int t0 = p.job[0].num_tiles;
+    int h;   // units up to here have one tile of job 0 more than the others (0: all the same)
+    if constexpr (SPLIT) {
+        if (pass == 0) {
+            *job = 0;
+            *tile = unit / p.split;
+            return i == 0 && *tile < t0;
+        }
+        h = t0 * p.split;
+    } else {
+        const int rounds = t0 / units;
+        h = t0 - rounds * units;
+        const int mine = rounds + (unit < h ? 1 : 0);
+        if (i < mine) {
+            *job = 0;
+            *tile = unit + i * units;
+            return true;
+        }
+        i -= mine;
+    }
+    const int late = units - h;
+    const int extra = h != 0 ? p.extra : 0;
+    *job = 1;
+    if (unit >= h && i < extra) {
+        *tile = i * late + (unit - h);
+    } else {
+        if (unit >= h) i -= extra;
+        *tile = extra * late + i * units + unit;
+    }
+    return *tile < p.job[1].num_tiles;
+}
 
 __device__ __forceinline__ bool lin_elect()
 {
@@ -113,10 +176,26 @@ __device__ __forceinline__ void lin_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
-// Whole warp: the wait's answer, the same for all lanes.
+// Whole warp: the wait's answer, the same for all lanes.  Looks at the clock and the
+// abort flag only after many tries (each suspends the warp for a while by itself).
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, int site)
 {
+    for (int i = 0; i < 256; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, site));
+}
+__device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtl& w, int site)
+{
+    for (int i = 0; i < 256; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, w, site));
+}
+
+// 16-byte store to the shared memory of a CTA of the cluster (address from mapa_shared).
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, float a, float b, float c, float d)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -276,8 +355,8 @@ __device__ __forceinline__ void act_switch(float (&v)[CH], int act)
 // a (and b, gated: u) hold the sums of `row`, columns c0 .. c0 + n - 1 of source `src`.
 // With `stage`, all lanes of a converged warp hold consecutive rows.
 template <int TYPE, int MODE, int CH>
-__device__ __forceinline__ void finish_rows(const LinearParams& p, float (&a)[CH], float (&b)[CH], int src, long long row,
-                                            int c0, int n, bool valid, uint32_t* stage)
+__device__ __forceinline__ void finish_rows(const LinearParams& p, const LinearJob& job, float (&a)[CH], float (&b)[CH],
+                                            int src, long long row, int c0, int n, bool valid, uint32_t* stage)
 {
     if constexpr (MODE == kModeLinear || MODE == kModeGated) {
         if (p.bias[0] != nullptr) {
@@ -307,33 +386,97 @@ __device__ __forceinline__ void finish_rows(const LinearParams& p, float (&a)[CH
 #pragma unroll
             for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
-        store_rows16<TYPE, CH>(static_cast<uint16_t*>(p.out[0]) + c0, p.ldo, row, a, n, p.vec_out, valid, stage);
-    } else if constexpr (MODE == kModeGradInput) {
-        store_rows16<TYPE, CH>(static_cast<uint16_t*>(p.out[0]) + c0, p.ldo, row, a, n, p.vec_out, valid, stage);
-    } else if (p.out_f32) {
-        store_rows32<CH>(static_cast<float*>(p.out[src]) + c0, p.ldo, row, a, n, p.vec_out, p.accumulate != 0, valid, stage);
+        store_rows16<TYPE, CH>(static_cast<uint16_t*>(job.out[0]) + c0, job.ldo, row, a, n, job.vec_out, valid, stage);
+    } else if (job.out_f32) {
+        store_rows32<CH>(static_cast<float*>(job.out[src]) + c0, job.ldo, row, a, n, job.vec_out, job.accumulate != 0, valid,
+                         stage);
     } else {
-        uint16_t* o = static_cast<uint16_t*>(p.out[src]) + c0;
-        if (p.accumulate) {
+        uint16_t* o = static_cast<uint16_t*>(job.out[src]) + c0;
+        if (job.accumulate) {
             float t[CH] = {};
-            load_rows<TYPE, CH>(t, o, p.ldo, row, n, p.vec_out, valid, stage);
+            load_rows<TYPE, CH>(t, o, job.ldo, row, n, job.vec_out, valid, stage);
 #pragma unroll
             for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
-        store_rows16<TYPE, CH>(o, p.ldo, row, a, n, p.vec_out, valid, stage);
+        store_rows16<TYPE, CH>(o, job.ldo, row, a, n, job.vec_out, valid, stage);
     }
 }
 
-template <int TYPE, int MODE, bool PAIR>
-__global__ void __launch_bounds__(kLinThreads, 1)
-    linear_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
-                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
-                  const __grid_constant__ LinearParams p)
+// The bias gradients: their partial sums added up, by the epilogue warps of all CTAs:
+// 32 columns a CTA and turn, every eighth chunk a warp, the warps' sums in order.
+template <int TYPE>
+__device__ __forceinline__ void sum_bias_grads(const LinearParams& p, float* sums)
+{
+    const int w = static_cast<int>(threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+    const long long total = static_cast<long long>(p.db_parts) * p.db_M;
+    for (long long e0 = static_cast<long long>(blockIdx.x) * 32; e0 < total; e0 += static_cast<long long>(gridDim.x) * 32) {
+        const long long e = e0 + lane;
+        float v = 0.f;
+        if (e < total) {
+#pragma unroll 8
+            for (int i = w; i < p.db_chunks; i += kLinEpiWarps) v += p.db_partial[i * total + e];
+        }
+        sums[w * 32 + lane] = v;
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kLinEpiWarps) : "memory");
+        if (w == 0 && e < total) {
+            v = 0.f;
+#pragma unroll
+            for (int i = 0; i < kLinEpiWarps; ++i) v += sums[i * 32 + lane];
+            const int q = e >= p.db_M ? 1 : 0;
+            const long long c = e - static_cast<long long>(q) * p.db_M;
+            if (p.db[q] != nullptr) {
+                if (p.db_f32) {
+                    float* o = static_cast<float*>(p.db[q]) + c;
+                    *o = p.db_accumulate ? *o + v : v;
+                } else {
+                    uint16_t* o = static_cast<uint16_t*>(p.db[q]) + c;
+                    *o = to_16<TYPE>(p.db_accumulate ? to_f32<TYPE>(*o) + v : v);
+                }
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kLinEpiWarps) : "memory");
+    }
+}
+
+// A tile of split k: its place, and the layout of its partial sums in the shared memory of
+// the CTA that finishes `slice` of its columns: [CTA][row][part][slice], pitch floats a row
+// (16-byte aligned and an odd number of 16 bytes: no bank conflicts).
+struct SplitTile {
+    int job, src, row0, col0;
+    int rows, width, slice, pitch;
+};
+__host__ __device__ __forceinline__ int split_slice(int width, int split)
+{
+    return ((width + split - 1) / split + 7) / 8 * 8;   // 16-byte accesses of results stay aligned
+}
+template <bool GRAD>
+__device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, int tile)
+{
+    const LinearJob& job = p.job[GRAD ? j : 0];
+    SplitTile t;
+    int pm, pn;
+    tile_coord(tile, job.num_m, job.num_n, p.group_m, &pm, &pn);
+    t.job = j;
+    t.src = GRAD && pm >= job.num_m1 ? 1 : 0;
+    t.row0 = (pm - t.src * job.num_m1) * 128;
+    t.col0 = pn * p.wcols;
+    t.rows = job.rows - t.row0 < 128 ? job.rows - t.row0 : 128;
+    t.width = job.cols - t.col0 < p.wcols ? job.cols - t.col0 : p.wcols;
+    t.slice = split_slice(t.width, p.split);
+    t.pitch = p.bn / p.wcols * t.slice + 4;
+    return t;
+}
+
+// Two CTAs of a forward kernel fit on an SM by registers: with few rows, whose
+// rings are small, the next launch's CTAs set up while this one's finish.
+template <int TYPE, int MODE, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2)
+    linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p)
 {
     constexpr bool kGated = MODE == kModeGated;
-    constexpr bool kAMn = MODE == kModeGradWeight;                              // A read along its rows
-    constexpr bool kBMn = MODE == kModeGradWeight || MODE == kModeGradInput;   // B read along its columns
+    constexpr bool kGrad = MODE == kModeGrad;
     constexpr int kTileRows = PAIR ? 256 : 128;
+    static_assert(!(PAIR && SPLIT), "pairs do not split k");
     const int S = p.stages;
 
     extern __shared__ uint8_t smem_raw[];
@@ -341,7 +484,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t sA = smem_u32(smem);
     const uint32_t sB = sA + static_cast<uint32_t>(S * p.a_bytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kLinRingBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring_bytes);
     const uint32_t full0 = smem_u32(bars);                 // kLinMaxStages each: stage loaded, consumed
     const uint32_t empty0 = full0 + 8 * kLinMaxStages;
     const uint32_t tfull0 = empty0 + 8 * kLinMaxStages;    // 2 each: accumulator ready, drained
@@ -349,12 +492,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t drain_bar = tempty0 + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kLinMaxStages + 5);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    static_assert((2 * kLinMaxStages + 5) * 8 + 8 <= kLinBarBytes, "barrier area too small");
+    static_assert((2 * kLinMaxStages + 5) * 8 + 8 <= 512, "barrier area too small");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int rank = PAIR || p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int rank = PAIR || SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     const bool leader = !PAIR || rank == 0;   // issues the MMAs
+    const int unit = static_cast<int>(blockIdx.x) / (PAIR ? 2 : 1);
+    const int units = static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -368,16 +513,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         mbar_init(drain_bar, 1);
         *abort_flag = 0u;
         fence_mbar_init();
-        prefetch_tmap(&tmA0);
-        prefetch_tmap(&tmB0);
+        prefetch_tmap(&maps.m[0]);
+        prefetch_tmap(&maps.m[1]);
+        if (kGated || kGrad) prefetch_tmap(&maps.m[2]);
     }
     __syncwarp();
     if (warp == 1) {
         if constexpr (PAIR) {
-            tmem_alloc_pair(smem_u32(tmem_slot), 2 * kLinAccCols);
+            tmem_alloc_pair(smem_u32(tmem_slot), static_cast<uint32_t>(p.tmem_cols));
             tmem_relinquish_alloc_permit_pair();
         } else {
-            tmem_alloc(smem_u32(tmem_slot), 2 * kLinAccCols);
+            tmem_alloc(smem_u32(tmem_slot), static_cast<uint32_t>(p.tmem_cols));
             tmem_relinquish_alloc_permit();
         }
     }
@@ -386,367 +532,425 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    if constexpr (!kGrad && !PAIR) {
+        // The epilogue warps bring the first weights into L2 while the kernel before
+        // this one may still run (a prefetch is coherent and delivers nothing).
+        if (warp >= 2 && p.prefetch_kb > 0) {
+            int job, tile, pm, pn;
+            if (tile_of<SPLIT>(p, 0, unit, units, 0, &job, &tile)) {
+                tile_coord(tile, p.job[0].num_m, p.job[0].num_n, p.group_m, &pm, &pn);
+                const int kb_all = p.job[0].kbs;
+                const int kb0 = static_cast<int>(static_cast<long long>(rank) * kb_all / p.split);
+                int lines = static_cast<int>(static_cast<long long>(rank + 1) * kb_all / p.split) - kb0;
+                if (lines > p.prefetch_kb) lines = p.prefetch_kb;
+                for (int r = static_cast<int>(threadIdx.x) - 64; r < p.bn; r += 32 * kLinEpiWarps) {
+                    const int half = kGated && r >= p.wcols ? 1 : 0;
+                    const int col = pn * p.wcols + r - half * p.wcols;
+                    if (col >= p.job[0].cols) continue;
+                    const uint8_t* w = p.w_rows[half] + col * p.w_ld_bytes + static_cast<long long>(kb0) * 128;
+                    for (int i = 0; i < lines; ++i) prefetch_l2(w + i * 128);
+                }
+            }
+        }
+    }
     // global memory is read and written only once the kernel before this one in the stream has completed
-    griddep_wait();
+    // (all CTAs of this launch have their TMEM by the time the next launch's may start)
     griddep_launch_dependents();
+    griddep_wait();
     const WaitCtl wc{abort_flag, p.status, p.wait_limit_ns};
     uint32_t never = 0u;
     const WaitCtl wc_drain{&never, p.status, p.wait_limit_ns};
-
-    // This CTA's (or pair's) tiles: unit, unit + units, ...; k-blocks [kb_begin, kb_end) of each.
-    const int share = PAIR ? 2 : p.split;
-    const int unit = static_cast<int>(blockIdx.x) / share;
-    const int units = static_cast<int>(gridDim.x) / share;
-    const int kb_all = p.kbs * p.k_sources;
-    const int kb_begin = PAIR ? 0 : static_cast<int>(static_cast<long long>(rank) * kb_all / p.split);
-    const int kb_end = PAIR ? kb_all : static_cast<int>(static_cast<long long>(rank + 1) * kb_all / p.split);
-
-    if (warp == 0) {
-        // ------------------------------------------------------------------
-        // loads: this CTA's rows of A and of B
-        // ------------------------------------------------------------------
-        const uint32_t lead_full0 = PAIR ? mapa_shared(full0, 0) : full0;
-        auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-            if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, x, y);
-            else tma_load_2d(dst, map, bar, x, y);
-        };
-        const int b_rows = PAIR ? p.bn / 2 : p.bn;   // rows of B (columns of the tile) staged by this CTA
-        const uint32_t tx = static_cast<uint32_t>(p.a_bytes + p.b_bytes) * (PAIR ? 2u : 1u);
-        int stage = 0;
-        uint32_t phase = 0;
-        long long issued = 0;
-        bool ok = true;
-        for (int tile = unit; ok && tile < p.num_tiles; tile += units) {
-            int pm, pn;
-            tile_coord(tile, p.num_m, p.num_n, p.group_m, &pm, &pn);
-            const int row_src = MODE == kModeGradWeight && pm >= p.num_m1 ? 1 : 0;
-            const int m0 = (pm - row_src * p.num_m1) * kTileRows + (PAIR ? rank * 128 : 0);
-            const int n0 = pn * p.wcols;
-            for (int kb = kb_begin; kb < kb_end; ++kb) {
-                ok = lin_wait(empty0 + 8 * stage, phase ^ 1u, wc, kSiteLinEmpty);
-                if (!ok) break;
-                if (lin_elect()) {
-                    if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
-                    const uint32_t bar = lead_full0 + 8 * stage;
-                    const uint32_t a_dst = sA + static_cast<uint32_t>(stage * p.a_bytes);
-                    const uint32_t b_dst = sB + static_cast<uint32_t>(stage * p.b_bytes);
-                    const int k_src = MODE == kModeGradInput && kb >= p.kbs ? 1 : 0;
-                    const int k0 = (kb - k_src * p.kbs) * kLinBK;
-                    const CUtensorMap* ma = (MODE == kModeGradWeight ? row_src : k_src) != 0 ? &tmA1 : &tmA0;
-                    if constexpr (kAMn) {
-                        load(a_dst, ma, bar, m0, k0);
-                        load(a_dst + 8192, ma, bar, m0 + 64, k0);
-                    } else {
-                        load(a_dst, ma, bar, k0, m0);
-                    }
-                    if constexpr (kGated) {
-                        if constexpr (PAIR) {
-                            load(b_dst, rank != 0 ? &tmB1 : &tmB0, bar, k0, n0);
-                        } else {
-                            load(b_dst, &tmB0, bar, k0, n0);
-                            load(b_dst + static_cast<uint32_t>(p.b_bytes / 2), &tmB1, bar, k0, n0);
-                        }
-                    } else {
-                        const int nb = n0 + (PAIR ? rank * b_rows : 0);
-                        if constexpr (kBMn) {
-                            const CUtensorMap* mb = k_src != 0 ? &tmB1 : &tmB0;
-                            for (int i = 0; i < b_rows / 64; ++i)
-                                load(b_dst + static_cast<uint32_t>(i) * 8192u, mb, bar, nb + 64 * i, k0);
-                        } else {
-                            load(b_dst, &tmB0, bar, k0, nb);
-                        }
-                    }
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (!ok && leader) {
-            // abort: the loads already issued land (waits with a limit) before the CTA can exit
-            const int pending = static_cast<int>(issued < S ? issued : S);
-            for (int j = 1; j <= pending; ++j) {
-                const int s = (stage - j + S) % S;
-                mbar_wait(full0 + 8 * s, stage - j < 0 ? phase ^ 1u : phase, wc_drain, kSiteLinDrain);
-            }
-        }
+    // Each warp's place in the rings of stages and accumulators, over all tiles and passes.
+    int stage = 0, it = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    if constexpr (kGrad) {
+        if (warp >= 2 && p.db_partial != nullptr) sum_bias_grads<TYPE>(p, reinterpret_cast<float*>(smem + p.ring_bytes + 512));
         __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------
-        // MMAs
-        // ------------------------------------------------------------------
-        if (leader) {
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            bool issued_any = false;
-            int it = 0;
-            const int seg_kb = MODE == kModeGradWeight ? p.seg_kb : kb_end - kb_begin;
-            for (int tile = unit; ok && tile < p.num_tiles; tile += units) {
-                for (int seg = kb_begin; ok && seg < kb_end; seg += seg_kb, ++it) {
-                    const int acc = it & 1;
-                    const uint32_t aph = static_cast<uint32_t>(it >> 1) & 1u;
-                    ok = PAIR ? mbar_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty)
-                              : mbar_wait(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kLinAccCols);
-                    const int seg_end = kb_end - seg < seg_kb ? kb_end : seg + seg_kb;
-                    for (int kb = seg; kb < seg_end; ++kb) {
-                        ok = lin_wait(full0 + 8 * stage, phase, wc, kSiteLinFull);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        const uint32_t a = sA + static_cast<uint32_t>(stage * p.a_bytes);
-                        const uint32_t b = sB + static_cast<uint32_t>(stage * p.b_bytes);
-                        if (lin_elect()) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                // read along k: 32 bytes of every 128-byte row; read along rows
-                                // (columns): 16 k rows of 128 bytes, 64-element blocks 8 KB apart
-                                const uint64_t ad = kAMn ? smem_desc_sw128(a + kk * 2048, 8192, 1024)
-                                                         : smem_desc_sw128(a + kk * 32, 16, 1024);
-                                const uint64_t bd = kBMn ? smem_desc_sw128(b + kk * 2048, 8192, 1024)
-                                                         : smem_desc_sw128(b + kk * 32, 16, 1024);
-                                const uint32_t more = kb != seg || kk != 0 ? 1u : 0u;
-                                if constexpr (PAIR) mma_f16_pair(d, ad, bd, p.idesc, more);
-                                else mma_f16(d, ad, bd, p.idesc, more);
-                            }
-                            if constexpr (PAIR) mma_commit_pair_multicast(empty0 + 8 * stage, 0x3);
-                            else mma_commit(empty0 + 8 * stage);
-                        }
-                        __syncwarp();
-                        issued_any = true;
-                        if (++stage == S) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                    }
+    }
+    // One pass over this CTA's tiles.  PARTIAL (pass 0 of split k): its share of a tile's k-blocks,
+    // the sums left in shared memory.
+    auto run = [&](auto partial_tag, const int pass) {
+        constexpr bool PARTIAL = decltype(partial_tag)::value;
+        // k-blocks [begin, end) of a tile of `job`
+        auto k_range = [&](const LinearJob& job, int* begin, int* end) {
+            const int all = job.kbs * job.k_sources;
+            *begin = PARTIAL ? static_cast<int>(static_cast<long long>(rank) * all / p.split) : 0;
+            *end = PARTIAL ? static_cast<int>(static_cast<long long>(rank + 1) * all / p.split) : all;
+        };
+        if (warp == 0) {
+            // ------------------------------------------------------------------
+            // loads: this CTA's rows of A and of B
+            // ------------------------------------------------------------------
+            const uint32_t lead_full0 = PAIR ? mapa_shared(full0, 0) : full0;
+            auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+                if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, x, y);
+                else tma_load_2d(dst, map, bar, x, y);
+            };
+            const int b_rows = PAIR ? p.bn / 2 : p.bn;   // rows of B (columns of the tile) staged by this CTA
+            const uint32_t tx = static_cast<uint32_t>(p.a_bytes + p.b_bytes) * (PAIR ? 2u : 1u);
+            int j, tile;
+            for (int i = 0; ok && tile_of<SPLIT>(p, pass, unit, units, i, &j, &tile); ++i) {
+                const LinearJob& job = p.job[kGrad ? j : 0];
+                int pm, pn, kb_begin, kb_end;
+                tile_coord(tile, job.num_m, job.num_n, p.group_m, &pm, &pn);
+                k_range(job, &kb_begin, &kb_end);
+                const int row_src = kGrad && pm >= job.num_m1 ? 1 : 0;
+                const int m0 = (pm - row_src * job.num_m1) * kTileRows + (PAIR ? rank * 128 : 0);
+                const int n0 = pn * p.wcols;
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
+                    ok = lin_wait(empty0 + 8 * stage, phase ^ 1u, wc, kSiteLinEmpty);
                     if (!ok) break;
                     if (lin_elect()) {
-                        if constexpr (PAIR) mma_commit_pair_multicast(tfull0 + 8 * acc, 0x3);
-                        else mma_commit(tfull0 + 8 * acc);
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
+                        const uint32_t bar = lead_full0 + 8 * stage;
+                        const uint32_t a_dst = sA + static_cast<uint32_t>(stage * p.a_bytes);
+                        const uint32_t b_dst = sB + static_cast<uint32_t>(stage * p.b_bytes);
+                        if constexpr (kGrad) {
+                            // boxes of 64 x 64: dz along k (two of 64 rows) or along rows (two of 64
+                            // rows by 64 tokens), W and x along columns
+                            const int k_src = kb >= job.kbs ? 1 : 0;
+                            const int k0 = (kb - k_src * job.kbs) * kLinBK;
+                            const CUtensorMap* ma = &maps.m[job.a_mn ? row_src : k_src];
+                            const CUtensorMap* mb = &maps.m[job.a_mn ? 4 : 2 + k_src];
+                            if (job.a_mn) {
+                                load(a_dst, ma, bar, m0, k0);
+                                load(a_dst + 8192, ma, bar, m0 + 64, k0);
+                            } else {
+                                load(a_dst, ma, bar, k0, m0);
+                                load(a_dst + 8192, ma, bar, k0, m0 + 64);
+                            }
+                            const int nb = n0 + (PAIR ? rank * b_rows : 0);
+                            for (int b = 0; b < b_rows / 64; ++b)
+                                load(b_dst + static_cast<uint32_t>(b) * 8192u, mb, bar, nb + 64 * b, k0);
+                        } else {
+                            const int k0 = kb * kLinBK;
+                            load(a_dst, &maps.m[0], bar, k0, m0);
+                            if constexpr (kGated) {
+                                if constexpr (PAIR) {
+                                    load(b_dst, &maps.m[1 + rank], bar, k0, n0);
+                                } else {
+                                    load(b_dst, &maps.m[1], bar, k0, n0);
+                                    load(b_dst + static_cast<uint32_t>(p.b_bytes / 2), &maps.m[2], bar, k0, n0);
+                                }
+                            } else {
+                                load(b_dst, &maps.m[1], bar, k0, n0 + (PAIR ? rank * b_rows : 0));
+                            }
+                        }
                     }
                     __syncwarp();
+                    ++issued;
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
-            if (!ok && issued_any) {
-                // abort: every MMA issued so far finishes before TMEM is freed
-                if (lin_elect()) {
-                    if constexpr (PAIR) mma_commit_pair_multicast(drain_bar, 0x1);
-                    else mma_commit(drain_bar);
-                }
-                __syncwarp();
-                mbar_wait(drain_bar, 0u, wc_drain, kSiteLinDrain);
-            }
-        }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------------------
-        // epilogue: 32 rows a warp (the TMEM lanes it may read), every other kCh columns
-        // ------------------------------------------------------------------
-        const int quarter = warp & 3;
-        const int half = (warp - 2) >> 2;
-        const uint32_t lead_tempty0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
-        uint32_t* stage = p.stage_out
-                              ? reinterpret_cast<uint32_t*>(smem + kLinRingBytes - kStageBytes) + (warp - 2) * 32 * kStagePitch
-                              : nullptr;
-        auto hand_back = [&](int acc) {   // this warp has read its part of the accumulator
-            tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_remote(lead_tempty0 + 8 * acc);
-                else mbar_arrive(tempty0 + 8 * acc);
+            if constexpr (PARTIAL) cluster_sync();   // (the epilogue warps' one)
+        } else if (warp == 1) {
+            // ------------------------------------------------------------------
+            // MMAs
+            // ------------------------------------------------------------------
+            if (leader) {
+                int j, tile;
+                for (int i = 0; ok && tile_of<SPLIT>(p, pass, unit, units, i, &j, &tile); ++i) {
+                    const LinearJob& job = p.job[kGrad ? j : 0];
+                    int kb_begin, kb_end;
+                    k_range(job, &kb_begin, &kb_end);
+                    const bool a_mn = kGrad && job.a_mn != 0;
+                    const uint32_t idesc = job.idesc;
+                    for (int seg = kb_begin; ok && seg < kb_end; seg += job.seg_kb, ++it) {
+                        const int acc = it & 1;
+                        const uint32_t aph = static_cast<uint32_t>(it >> 1) & 1u;
+                        ok = PAIR ? lin_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty)
+                                  : lin_wait(tempty0 + 8 * acc, aph ^ 1u, wc, kSiteLinTmemEmpty);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * p.acc_cols);
+                        const int seg_end = kb_end - seg < job.seg_kb ? kb_end : seg + job.seg_kb;
+                        for (int kb = seg; kb < seg_end; ++kb) {
+                            ok = lin_wait(full0 + 8 * stage, phase, wc, kSiteLinFull);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            const uint32_t a = sA + static_cast<uint32_t>(stage * p.a_bytes);
+                            const uint32_t b = sB + static_cast<uint32_t>(stage * p.b_bytes);
+                            if (lin_elect()) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    // read along k: 32 bytes of every 128-byte row; read along rows
+                                    // (columns): 16 k rows of 128 bytes, 64-element blocks 8 KB apart
+                                    const uint64_t ad = a_mn ? smem_desc_sw128(a + kk * 2048, 8192, 1024)
+                                                             : smem_desc_sw128(a + kk * 32, 16, 1024);
+                                    const uint64_t bd = kGrad ? smem_desc_sw128(b + kk * 2048, 8192, 1024)
+                                                              : smem_desc_sw128(b + kk * 32, 16, 1024);
+                                    const uint32_t more = kb != seg || kk != 0 ? 1u : 0u;
+                                    if constexpr (PAIR) mma_f16_pair(d, ad, bd, idesc, more);
+                                    else mma_f16(d, ad, bd, idesc, more);
+                                }
+                                if constexpr (PAIR) mma_commit_pair_multicast(empty0 + 8 * stage, 0x3);
+                                else mma_commit(empty0 + 8 * stage);
+                            }
+                            __syncwarp();
+                            ++issued;
+                            if (++stage == S) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                        if (!ok) break;
+                        if (lin_elect()) {
+                            if constexpr (PAIR) mma_commit_pair_multicast(tfull0 + 8 * acc, 0x3);
+                            else mma_commit(tfull0 + 8 * acc);
+                        }
+                        __syncwarp();
+                    }
+                }
             }
-        };
-        bool ok = true;
-        int it = 0;
-        for (int tile = unit; ok && tile < p.num_tiles; tile += units) {
-            int pm, pn;
-            tile_coord(tile, p.num_m, p.num_n, p.group_m, &pm, &pn);
-            const int src = MODE == kModeGradWeight && pm >= p.num_m1 ? 1 : 0;
-            const int m0 = (pm - src * p.num_m1) * kTileRows + (PAIR ? rank * 128 : 0) + quarter * 32;
-            const int n0 = pn * p.wcols;
-            const int row = m0 + lane;
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-            const bool any = m0 < p.rows;   // rows of this warp's to store
-            const bool valid = row < p.rows;
-            const int left = p.cols - n0;
-            const int width = left < p.wcols ? left : p.wcols;
-            // split k: partials stay in this CTA's shared memory, over the ring (whose stages the
-            // MMAs have finished reading), bn + 4 floats a row
-            float* part = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * (p.bn + 4);
-            if constexpr (MODE == kModeGradWeight) {
-                float sum[8][kCh];
+            __syncwarp();
+            if constexpr (PARTIAL) cluster_sync();
+        } else {
+            // ------------------------------------------------------------------
+            // epilogue: 32 rows a warp (the TMEM lanes it may read), every other kCh columns
+            // ------------------------------------------------------------------
+            const int quarter = warp & 3;
+            const int half = (warp - 2) >> 2;
+            const uint32_t lead_tempty0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
+            uint32_t* staging = p.stage_at >= 0 ? reinterpret_cast<uint32_t*>(smem + p.stage_at) + (warp - 2) * 32 * kStagePitch : nullptr;
+            auto hand_back = [&](int acc) {   // this warp has read its part of the accumulator
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_remote(lead_tempty0 + 8 * acc);
+                    else mbar_arrive(tempty0 + 8 * acc);
+                }
+            };
+            // Sums of the accumulator's columns c, c + 16 ... (every other 16) of a tile's segments
+            auto add_segments = [&](float (&sum)[8][kCh], const LinearJob& job, int kb_begin, int kb_end, bool any) {
+                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int c = 0; c < 8; ++c)
 #pragma unroll
-                    for (int i = 0; i < kCh; ++i) sum[j][i] = 0.f;
-                for (int seg = kb_begin; seg < kb_end; seg += p.seg_kb, ++it) {
+                    for (int e = 0; e < kCh; ++e) sum[c][e] = 0.f;
+                for (int seg = kb_begin; seg < kb_end; seg += job.seg_kb, ++it) {
                     const int acc = it & 1;
                     ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
                     if (!ok) break;
                     tc_fence_after_sync();
                     if (any) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int c = (2 * j + half) * kCh;
+                        for (int q = 0; q < 8; ++q) {
+                            const int c = (2 * q + half) * kCh;
                             if (c < p.bn) {
                                 uint32_t r[kCh];
-                                lin_tmem_ld16(t_row + acc * kLinAccCols + c, r);
+                                lin_tmem_ld16(t_row + acc * p.acc_cols + c, r);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < kCh; ++i) sum[j][i] += __uint_as_float(r[i]);
+                                for (int e = 0; e < kCh; ++e) sum[q][e] += __uint_as_float(r[e]);
                             }
                         }
                     }
                     hand_back(acc);
                 }
-                if (!ok) break;
-                if (any) {
-                    if (p.split > 1) fence_proxy_async_smem();
+            };
+            int j = 0, tile = 0;
+            if constexpr (PARTIAL) {
+                // The CTA's only tile: its sums go to the CTAs of the cluster that finish their columns,
+                // over those CTAs' rings, once all have read their stages.
+                const bool have = tile_of<SPLIT>(p, 0, unit, units, 0, &j, &tile);
+                const SplitTile t = split_tile<kGrad>(p, have ? j : 0, have ? tile : 0);
+                const LinearJob& job = p.job[kGrad ? t.job : 0];
+                const bool any = have && quarter * 32 < t.rows;
+                const int lrow = quarter * 32 + lane;
+                // 8 columns c .. of this lane's row, part 0 or (gated) 1
+                auto push = [&](const float* v, int part, int c) {
+                    const int owner = c / t.slice;
+                    const uint32_t to = mapa_shared(sA, static_cast<uint32_t>(owner)) +
+                                        static_cast<uint32_t>(((rank * t.rows + lrow) * t.pitch + part * t.slice + c - owner * t.slice) * 4);
+                    st_shared_cluster_v4(to, v[0], v[1], v[2], v[3]);
+                    st_shared_cluster_v4(to + 16u, v[4], v[5], v[6], v[7]);
+                };
+                if constexpr (kGrad) {
+                    int kb_begin, kb_end;
+                    k_range(job, &kb_begin, &kb_end);
+                    float sum[8][kCh];
+                    add_segments(sum, job, kb_begin, have ? kb_end : kb_begin, any);
+                    fence_proxy_async_smem();
+                    cluster_sync();
+                    if (ok && any && lrow < t.rows) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = (2 * j + half) * kCh;
-                        if (p.split > 1) {
-                            if (c < p.bn && valid) {
+                        for (int q = 0; q < 8; ++q) {
+                            const int c = (2 * q + half) * kCh;
+                            if (c < t.width) push(sum[q], 0, c);
+                            if (c + 8 < t.width) push(sum[q] + 8, 0, c + 8);
+                        }
+                    }
+                } else {
+                    if (have) ok = lin_wait(tfull0, 0u, wc, kSiteLinTmemFull);
+                    tc_fence_after_sync();
+                    fence_proxy_async_smem();
+                    cluster_sync();
+                    if (ok && any) {
+                        const uint32_t t_acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+                        for (int c = half * kCh; c < t.width; c += 2 * kCh) {
 #pragma unroll
-                                for (int i = 0; i < kCh; i += 4)
-                                    *reinterpret_cast<float4*>(part + c + i) =
-                                        make_float4(sum[j][i], sum[j][i + 1], sum[j][i + 2], sum[j][i + 3]);
+                            for (int part = 0; part < (kGated ? 2 : 1); ++part) {
+                                uint32_t r[kCh];
+                                lin_tmem_ld16(t_acc + part * p.wcols + c, r);
+                                tmem_ld_wait();
+                                float v[kCh];
+#pragma unroll
+                                for (int e = 0; e < kCh; ++e) v[e] = __uint_as_float(r[e]);
+                                if (lrow < t.rows) {
+                                    push(v, part, c);
+                                    if (c + 8 < t.width) push(v + 8, part, c + 8);
+                                }
                             }
-                        } else if (c < width) {
-                            finish_rows<TYPE, MODE, kCh>(p, sum[j], sum[j], src, row, n0 + c,
-                                                         width - c < kCh ? width - c : kCh, valid, stage);
                         }
                     }
                 }
             } else {
-                const int acc = it & 1;
-                ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
-                if (!ok) break;
-                ++it;
-                tc_fence_after_sync();
-                const uint32_t t_acc = t_row + static_cast<uint32_t>(acc * kLinAccCols);
-                if (any && p.split == 1) {
-#pragma unroll 1
-                    for (int c = half * kCh; c < width; c += 2 * kCh) {
-                        uint32_t ra[kCh], rb[kCh];
-                        lin_tmem_ld16(t_acc + c, ra);
-                        if constexpr (kGated) lin_tmem_ld16(t_acc + p.wcols + c, rb);
-                        tmem_ld_wait();
-                        float a[kCh], b[kCh];
+                for (int i = 0; ok && tile_of<SPLIT>(p, pass, unit, units, i, &j, &tile); ++i) {
+                    const LinearJob& job = p.job[kGrad ? j : 0];
+                    int pm, pn;
+                    tile_coord(tile, job.num_m, job.num_n, p.group_m, &pm, &pn);
+                    const int src = kGrad && pm >= job.num_m1 ? 1 : 0;
+                    const int m0 = (pm - src * job.num_m1) * kTileRows + (PAIR ? rank * 128 : 0) + quarter * 32;
+                    const int n0 = pn * p.wcols;
+                    const int row = m0 + lane;
+                    const bool any = m0 < job.rows;   // rows of this warp's to store
+                    const bool valid = row < job.rows;
+                    const int left = job.cols - n0;
+                    const int width = left < p.wcols ? left : p.wcols;
+                    if constexpr (kGrad) {
+                        int kb_begin, kb_end;
+                        k_range(job, &kb_begin, &kb_end);
+                        float sum[8][kCh];
+                        add_segments(sum, job, kb_begin, kb_end, any);
+                        if (!ok) break;
+                        if (any) {
 #pragma unroll
-                        for (int i = 0; i < kCh; ++i) {
-                            a[i] = __uint_as_float(ra[i]);
-                            b[i] = kGated ? __uint_as_float(rb[i]) : 0.f;
+                            for (int q = 0; q < 8; ++q) {
+                                const int c = (2 * q + half) * kCh;
+                                if (c < width)
+                                    finish_rows<TYPE, MODE, kCh>(p, job, sum[q], sum[q], src, row, n0 + c,
+                                                                 width - c < kCh ? width - c : kCh, valid, staging);
+                            }
                         }
-                        finish_rows<TYPE, MODE, kCh>(p, a, b, src, row, n0 + c, width - c < kCh ? width - c : kCh, valid,
-                                                     stage);
-                    }
-                } else if (any) {
-                    fence_proxy_async_smem();
+                    } else {
+                        const int acc = it & 1;
+                        ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
+                        if (!ok) break;
+                        ++it;
+                        tc_fence_after_sync();
+                        const uint32_t t_acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                               static_cast<uint32_t>(acc * p.acc_cols);
+                        if (any) {
 #pragma unroll 1
-                    for (int c = half * kCh; c < p.bn; c += 2 * kCh) {
-                        uint32_t r[kCh];
-                        lin_tmem_ld16(t_acc + c, r);
-                        tmem_ld_wait();
-                        if (valid) {
+                            for (int c = half * kCh; c < width; c += 2 * kCh) {
+                                uint32_t ra[kCh], rb[kCh];
+                                lin_tmem_ld16(t_acc + c, ra);
+                                if constexpr (kGated) lin_tmem_ld16(t_acc + p.wcols + c, rb);
+                                tmem_ld_wait();
+                                float a[kCh], b[kCh];
 #pragma unroll
-                            for (int i = 0; i < kCh; i += 4)
-                                *reinterpret_cast<uint4*>(part + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                                for (int e = 0; e < kCh; ++e) {
+                                    a[e] = __uint_as_float(ra[e]);
+                                    b[e] = kGated ? __uint_as_float(rb[e]) : 0.f;
+                                }
+                                finish_rows<TYPE, MODE, kCh>(p, job, a, b, 0, row, n0 + c, width - c < kCh ? width - c : kCh,
+                                                             valid, staging);
+                            }
+                        }
+                        hand_back(acc);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    };
+    if constexpr (!SPLIT) {
+        run(std::false_type{}, 0);
+    } else {
+        run(std::true_type{}, 0);
+        // all partial sums of this CTA's columns are in its shared memory
+        cluster_sync();
+        int j, tile;
+        if (warp >= 2 && tile_of<SPLIT>(p, 0, unit, units, 0, &j, &tile)) {
+            // 8 columns of a row per thread and turn, neighbouring threads on neighbouring
+            // rows; summed in rank order
+            constexpr int kW = 8;
+            const SplitTile t = split_tile<kGrad>(p, j, tile);
+            const int c_begin = rank * t.slice;
+            const int c_end = c_begin + t.slice < t.width ? c_begin + t.slice : t.width;
+            const int items = c_begin < c_end ? (c_end - c_begin + kW - 1) / kW * t.rows : 0;
+            for (int e = static_cast<int>(threadIdx.x) - 64; e < items; e += 32 * kLinEpiWarps) {
+                const int lrow = e % t.rows;
+                const int cl = e / t.rows * kW;
+                const float* from = reinterpret_cast<const float*>(smem) + lrow * t.pitch + cl;
+                float a[kW] = {}, b[kW] = {};
+                for (int q = 0; q < p.split; ++q, from += t.rows * t.pitch) {
+#pragma unroll
+                    for (int h = 0; h < kW; h += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(from + h);
+                        a[h] += v.x;
+                        a[h + 1] += v.y;
+                        a[h + 2] += v.z;
+                        a[h + 3] += v.w;
+                        if constexpr (kGated) {
+                            const float4 w = *reinterpret_cast<const float4*>(from + t.slice + h);
+                            b[h] += w.x;
+                            b[h + 1] += w.y;
+                            b[h + 2] += w.z;
+                            b[h + 3] += w.w;
                         }
                     }
                 }
-                hand_back(acc);
+                const int c = c_begin + cl;
+                finish_rows<TYPE, MODE, kW>(p, p.job[kGrad ? t.job : 0], a, b, t.src, t.row0 + lrow, t.col0 + c,
+                                            c_end - c < kW ? c_end - c : kW, true, nullptr);
             }
+        }
+        if constexpr (kGrad) {
+            // the ring's stages are loaded again over the partials once all have read them
+            fence_proxy_async_smem();
+            __syncthreads();
+            run(std::false_type{}, 1);
+        }
+    }
+    if (!ok && leader && warp == 0) {
+        // abort: the loads already issued land (waits with a limit) before the CTA can exit
+        const int pending = static_cast<int>(issued < S ? issued : S);
+        for (int b = 1; b <= pending; ++b) {
+            const int s = (stage - b + S) % S;
+            mbar_wait(full0 + 8 * s, stage - b < 0 ? phase ^ 1u : phase, wc_drain, kSiteLinDrain);
+        }
+    }
+    if (!ok && leader && warp == 1 && issued > 0) {
+        // abort: every MMA issued so far finishes before TMEM is freed
+        if (lin_elect()) {
+            if constexpr (PAIR) mma_commit_pair_multicast(drain_bar, 0x1);
+            else mma_commit(drain_bar);
         }
         __syncwarp();
+        mbar_wait(drain_bar, 0u, wc_drain, kSiteLinDrain);
     }
-
-    if constexpr (!PAIR) {
-        if (p.split > 1) {
-            // One tile per cluster.  Barrier 1: every CTA's partial is in its shared memory.
-            cluster_sync();
-            if (warp >= 2) {
-                // This CTA's columns of the tile (a multiple of 8, so that 16-byte accesses stay
-                // aligned), 8 columns of a row per thread and turn, neighbouring threads on
-                // neighbouring rows.
-                constexpr int kW = 8;
-                int pm, pn;
-                tile_coord(unit, p.num_m, p.num_n, p.group_m, &pm, &pn);
-                const int src = MODE == kModeGradWeight && pm >= p.num_m1 ? 1 : 0;
-                const int r0 = (pm - src * p.num_m1) * 128;
-                const int n0 = pn * p.wcols;
-                const int left = p.cols - n0;
-                const int width = left < p.wcols ? left : p.wcols;
-                const int rows = p.rows - r0 < 128 ? p.rows - r0 : 128;
-                const int slice = ((width + p.split - 1) / p.split + kW - 1) / kW * kW;
-                const int c_begin = rank * slice;
-                const int c_end = c_begin + slice < width ? c_begin + slice : width;
-                const int items = c_begin < c_end ? (c_end - c_begin + kW - 1) / kW * rows : 0;
-                for (int e = static_cast<int>(threadIdx.x) - 64; e < items; e += 32 * kLinEpiWarps) {
-                    const int lrow = e % rows;
-                    const int c = c_begin + e / rows * kW;
-                    const uint32_t base = sA + static_cast<uint32_t>((lrow * (p.bn + 4) + c) * 4);
-                    float a[kW] = {}, b[kW] = {};
-                    // four partials' loads in flight; summed in rank order
-                    for (int q0 = 0; q0 < p.split; q0 += 4) {
-                        float4 v[4][2], w[4][2];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q0 + q < p.split) {
-                                const uint32_t peer = mapa_shared(base, static_cast<uint32_t>(q0 + q));
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    v[q][i] = ld_shared_cluster_v4(peer + 16u * i);
-                                    if constexpr (kGated) w[q][i] = ld_shared_cluster_v4(peer + static_cast<uint32_t>(p.wcols) * 4u + 16u * i);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (q0 + q < p.split) {
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    a[4 * i] += v[q][i].x;
-                                    a[4 * i + 1] += v[q][i].y;
-                                    a[4 * i + 2] += v[q][i].z;
-                                    a[4 * i + 3] += v[q][i].w;
-                                    if constexpr (kGated) {
-                                        b[4 * i] += w[q][i].x;
-                                        b[4 * i + 1] += w[q][i].y;
-                                        b[4 * i + 2] += w[q][i].z;
-                                        b[4 * i + 3] += w[q][i].w;
-                                    }
-                                }
-                            }
-                        }
-                    }
-                    finish_rows<TYPE, MODE, kW>(p, a, b, src, r0 + lrow, n0 + c, c_end - c < kW ? c_end - c : kW, true,
-                                                nullptr);
-                }
-            }
-            // Barrier 2: no CTA leaves while a peer may still read its shared memory.
-            cluster_sync();
-        }
-    }
+    __syncwarp();
     tc_fence_before_sync();
     if constexpr (PAIR) cluster_sync();
     else __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
-        if constexpr (PAIR) tmem_dealloc_pair(tmem_base, 2 * kLinAccCols);
-        else tmem_dealloc(tmem_base, 2 * kLinAccCols);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem_base, static_cast<uint32_t>(p.tmem_cols));
+        else tmem_dealloc(tmem_base, static_cast<uint32_t>(p.tmem_cols));
     }
 }
 
-// 2-D tensor map, 128-byte swizzle: `inner` contiguous elements in `outer` lines.
+// 2-D tensor map, 128-byte swizzle: `inner` contiguous elements in `outer` lines, boxes of 64 x box_outer.
 inline bool lin_map(CUtensorMap* map, int type, const void* base, long long inner, long long outer, long long ld,
-                    int box_inner, int box_outer, char* msg, size_t msg_len)
+                    int box_outer, char* msg, size_t msg_len)
 {
     TmapEncodeFn enc = tmap_encoder();
     if (enc == nullptr) {
@@ -755,15 +959,15 @@ inline bool lin_map(CUtensorMap* map, int type, const void* base, long long inne
     }
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2u};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kLinBK), static_cast<cuuint32_t>(box_outer)};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(map, type == kTypeBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                            2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
-        snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for %lld x %lld, stride %lld, box %d x %d",
-                 static_cast<int>(r), inner, outer, ld, box_inner, box_outer);
+        snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for %lld x %lld, stride %lld, box 64 x %d",
+                 static_cast<int>(r), inner, outer, ld, box_outer);
         return false;
     }
     return true;
@@ -774,91 +978,209 @@ inline bool lin_aligned16(const void* p, long long ld_bytes)
     return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes)) & 15u) == 0;
 }
 
+// A job's tiles, of tile_rows x wcols.
+inline LinearJob lin_job(int rows, int cols, int k, int k_sources, int row_sources, int tile_rows, int wcols)
+{
+    LinearJob j = {};
+    j.rows = rows;
+    j.cols = cols;
+    j.kbs = (k + kLinBK - 1) / kLinBK;
+    j.k_sources = k_sources;
+    j.num_m1 = (rows + tile_rows - 1) / tile_rows;
+    j.num_m = j.num_m1 * row_sources;
+    j.num_n = (cols + wcols - 1) / wcols;
+    j.num_tiles = j.num_m * j.num_n;
+    j.seg_kb = j.kbs * k_sources;
+    return j;
+}
+
 template <int TYPE, int MODE, bool PAIR>
 int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len)
 {
     constexpr bool kGated = MODE == kModeGated;
-    constexpr bool kAMn = MODE == kModeGradWeight;
-    constexpr bool kBMn = MODE == kModeGradWeight || MODE == kModeGradInput;
+    constexpr bool kGrad = MODE == kModeGrad;
     constexpr int kTileRows = PAIR ? 256 : 128;
-    const int unit_cols = kGated ? 32 : kBMn ? 64 : 16;
-    const int bn_unit = PAIR && kBMn ? 128 : PAIR ? 32 : unit_cols;
+    const int bn_unit = PAIR ? (kGrad ? 128 : 32) : (kGrad ? 64 : kGated ? 32 : 16);
     if (g.bn < bn_unit || g.bn > 256 || g.bn % bn_unit != 0) {
         snprintf(msg, msg_len, "linear product: bad tile width %d", g.bn);
         return 1;
     }
     LinearParams p = {};
-    p.rows = g.rows;
-    p.cols = g.cols;
-    p.kbs = (g.k + kLinBK - 1) / kLinBK;
-    p.k_sources = MODE == kModeGradInput ? g.sources : 1;
-    p.num_m1 = (g.rows + kTileRows - 1) / kTileRows;
-    p.num_m = p.num_m1 * (MODE == kModeGradWeight ? g.sources : 1);
     p.bn = g.bn;
     p.wcols = kGated ? g.bn / 2 : g.bn;
-    p.num_n = (g.cols + p.wcols - 1) / p.wcols;
-    p.num_tiles = p.num_m * p.num_n;
     p.group_m = g.group_m;
-    p.a_rows = PAIR || kAMn || g.rows >= 128 ? 128 : (g.rows + 7) / 8 * 8;
-    p.a_bytes = p.a_rows * 128;
-    const int b_rows = PAIR ? g.bn / 2 : g.bn;
-    p.b_bytes = b_rows * 128;
-    const int ob = g.out_f32 ? 4 : 2;
-    p.vec_out = lin_aligned16(g.out[0], g.ldo * ob) && lin_aligned16(g.out[1], 0);
+    if constexpr (kGrad) {
+        int jobs = 0;
+        if (g.dx != nullptr) {
+            LinearJob& j = p.job[jobs++];
+            j = lin_job(g.n, g.K, g.M, g.parts, 1, kTileRows, p.wcols);
+            j.idesc = idesc_f16(TYPE == kTypeBF16, false, true, kTileRows, g.bn);
+            j.out[0] = g.dx;
+            j.ldo = g.ld_dx;
+            j.vec_out = lin_aligned16(g.dx, g.ld_dx * 2);
+        }
+        if (g.dW[0] != nullptr) {
+            LinearJob& j = p.job[jobs++];
+            j = lin_job(g.M, g.K, g.n, 1, g.parts, kTileRows, p.wcols);
+            j.a_mn = 1;
+            j.idesc = idesc_f16(TYPE == kTypeBF16, true, true, kTileRows, g.bn);
+            j.out[0] = g.dW[0];
+            j.out[1] = g.dW[1];
+            j.ldo = g.ld_dw;
+            j.out_f32 = g.grad_f32;
+            j.accumulate = g.accumulate;
+            if (g.grad_f32) j.seg_kb = kSegmentKb;
+            j.vec_out = lin_aligned16(g.dW[0], g.ld_dw * (g.grad_f32 ? 4 : 2)) && lin_aligned16(g.dW[1], 0);
+        }
+        if (jobs == 2 && p.job[1].kbs * p.job[1].k_sources > p.job[0].kbs * p.job[0].k_sources) {
+            const LinearJob t = p.job[0];   // longer k loops first
+            p.job[0] = p.job[1];
+            p.job[1] = t;
+        }
+        if (jobs == 1) {
+            p.job[1] = p.job[0];
+            p.job[1].num_tiles = 0;
+        }
+    } else {
+        LinearJob& j = p.job[0];
+        j = lin_job(g.n, g.M, g.K, 1, 1, kTileRows, p.wcols);
+        j.idesc = idesc_f16(TYPE == kTypeBF16, false, false, kTileRows, g.bn);
+        j.out[0] = g.out;
+        j.ldo = g.ldo;
+        j.vec_out = lin_aligned16(g.out, g.ldo * 2);
+    }
+    const long long tiles = static_cast<long long>(p.job[0].num_tiles) + p.job[1].num_tiles;
+    p.split = PAIR || g.split < 2 ? 1 : g.split;
+    const int kb0 = p.job[0].kbs * p.job[0].k_sources;
+    const int kb1 = p.job[1].num_tiles > 0 ? p.job[1].kbs * p.job[1].k_sources : kb0;
+    while (p.split > kb0) p.split /= 2;   // every CTA of a cluster has a k-block
+    p.bias[0] = static_cast<const uint16_t*>(g.bias[0]);
+    p.bias[1] = static_cast<const uint16_t*>(g.bias[1]);
+    p.keep[0] = static_cast<uint16_t*>(g.keep[0]);
+    p.keep[1] = static_cast<uint16_t*>(g.keep[1]);
+    p.ldk = g.ldk;
+    p.residual = static_cast<const uint16_t*>(g.residual);
+    p.ldr = g.ldr;
+    p.act = g.act;
     p.vec_res = lin_aligned16(g.residual, g.ldr * 2);
     p.vec_keep = lin_aligned16(g.keep[0], g.ldk * 2) && lin_aligned16(g.keep[1], 0);
     p.vec_bias = lin_aligned16(g.bias[0], 0) && lin_aligned16(g.bias[1], 0);
-    p.stage_out = !(p.vec_out && (p.vec_res || g.residual == nullptr) && (p.vec_keep || g.keep[0] == nullptr));
-    // (with few rows the MMA reads up to 16 KB from the start of the last stage's A, into B's stages)
-    p.stages = (kLinRingBytes - (p.stage_out ? kStageBytes : 0)) / (p.a_bytes + p.b_bytes);
-    if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
-    p.split = PAIR || g.split < 2 ? 1 : g.split;
-    while (p.split > p.kbs * p.k_sources) p.split /= 2;   // every CTA of a cluster has a k-block
-    p.seg_kb = g.out_f32 ? kSegmentKb : p.kbs * p.k_sources;
-    p.idesc = idesc_f16(TYPE == kTypeBF16, kAMn, kBMn, kTileRows, g.bn);
-    for (int i = 0; i < 2; ++i) {
-        p.out[i] = g.out[i];
-        p.bias[i] = static_cast<const uint16_t*>(g.bias[i]);
-        p.keep[i] = static_cast<uint16_t*>(g.keep[i]);
-    }
-    p.ldo = g.ldo;
-    p.residual = static_cast<const uint16_t*>(g.residual);
-    p.ldr = g.ldr;
-    p.ldk = g.ldk;
-    p.act = g.act;
-    p.out_f32 = g.out_f32;
-    p.accumulate = g.accumulate;
+    p.db_partial = g.db_partial;
+    p.db_chunks = g.db_chunks;
+    p.db_parts = g.parts;
+    p.db_M = g.M;
+    p.db_f32 = g.grad_f32;
+    p.db_accumulate = g.accumulate;
+    p.db[0] = g.db[0];
+    p.db[1] = g.db[1];
     p.status = g.status;
     p.wait_limit_ns = g.wait_limit_ns;
 
-    CUtensorMap tmA[2], tmB[2];
-    const int b_box = kBMn ? 64 : kGated ? g.bn / 2 : b_rows;
-    const int srcs = MODE == kModeGradInput || MODE == kModeGradWeight ? g.sources : 1;
-    for (int s = 0; s < 2; ++s) {
-        const void* a = s < srcs ? g.A[s] : g.A[0];
-        const bool ok_a = kAMn ? lin_map(&tmA[s], g.type, a, g.rows, g.k, g.lda, 64, kLinBK, msg, msg_len)
-                               : lin_map(&tmA[s], g.type, a, g.k, g.rows, g.lda, kLinBK, p.a_rows, msg, msg_len);
-        const void* b = s == 0 || g.B[1] == nullptr ? g.B[0] : g.B[1];
-        const bool ok_b = ok_a && (kBMn ? lin_map(&tmB[s], g.type, b, g.cols, g.k, g.ldb, 64, kLinBK, msg, msg_len)
-                                        : lin_map(&tmB[s], g.type, b, g.k, g.cols, g.ldb, kLinBK, b_box, msg, msg_len));
-        if (!ok_b) return 1;
+    // Few rows: the weights' stream is the bound, and two CTAs fit on an SM, each with half of the
+    // shared memory and of TMEM; the next launch's CTAs can be there when this one's finish.
+    p.acc_cols = 32;
+    while (p.acc_cols < g.bn) p.acc_cols *= 2;
+    const long long sms = g.num_sms > 0 ? g.num_sms : 1;
+    const bool few = !PAIR && !kGrad && g.n <= kFewRows &&
+                     (p.acc_cols <= 128 || tiles * p.split <= 2 * sms || p.split > 1);
+    // Units: each gets the same number of tiles (the last wave is not left partial).
+    const int share = PAIR ? 2 : p.split;
+    long long units = static_cast<long long>(p.job[0].num_tiles) * p.split;
+    long long per_unit = 1;
+    if (p.split > 1) {
+        if (p.job[1].num_tiles > 0) {
+            // clusters that fit on the device at once; job 0 has no more tiles than that
+            long long clusters = split_k_capacity(p.split);
+            if (clusters > sms / p.split) clusters = sms / p.split;
+            if (clusters < p.job[0].num_tiles) clusters = p.job[0].num_tiles;
+            units = clusters * p.split;
+            per_unit = 2;
+        }
+    } else {
+        units = tiles;
+        const long long most = PAIR ? sms / 2 : few ? 2 * sms : sms;
+        const long long cap = most > 0 ? most : 1;
+        per_unit = (units + cap - 1) / cap;
+        units = kGrad && p.job[1].num_tiles > 0 ? (units < cap ? units : cap) : (units + per_unit - 1) / per_unit;
+    }
+    // TMEM: two accumulators unless every unit has one tile of one segment.
+    const bool one = per_unit == 1 && (!kGrad || p.job[1].num_tiles == 0) && p.job[0].seg_kb >= kb0;
+    p.extra = kGrad ? kb0 / p.split / kb1 : 0;
+    p.tmem_cols = one ? p.acc_cols : 2 * p.acc_cols;
+
+    // Shared memory: the ring, the staging buffers behind it, the barriers.
+    p.a_rows = PAIR || kGrad || g.n >= 128 ? 128 : (g.n + 7) / 8 * 8;
+    p.a_bytes = p.a_rows * 128;
+    const int b_rows = PAIR ? g.bn / 2 : g.bn;
+    p.b_bytes = b_rows * 128;
+    const bool staged = !(p.job[0].vec_out && (p.job[1].num_tiles == 0 || p.job[1].vec_out) &&
+                          (p.vec_res || g.residual == nullptr) && (p.vec_keep || g.keep[0] == nullptr));
+    const int stage_bytes = p.a_bytes + p.b_bytes;
+    const int room = (few ? kLinSmemBytes / 2 - 1024 : kLinSmemBytes) - 1024 - kLinBarBytes - (staged ? kStageBytes : 0);
+    p.stages = room / stage_bytes;
+    if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
+    if (p.stages < 2) p.stages = 2;
+    // (with few rows the MMA reads up to 16 KB from the start of the last stage's A: inside this)
+    int ring = p.stages * stage_bytes;
+    const int reach = (p.stages - 1) * p.a_bytes + 16384;
+    if (ring < reach) ring = reach;
+    const int rows = g.n < 128 && !kGrad ? g.n : 128;
+    const int partial = p.split > 1 ? p.split * rows * (g.bn / p.wcols * split_slice(p.wcols, p.split) + 4) * 4 : 0;
+    if (ring < partial) ring = partial;
+    ring = (ring + 1023) / 1024 * 1024;
+    p.stage_at = staged ? ring : -1;
+    p.ring_bytes = ring + (staged ? kStageBytes : 0);
+    // Split k: at most two CTAs per SM (of 256 TMEM columns at most), so that no CTA of a cluster can
+    // wait for columns that a CTA of a cluster waiting for it holds.
+    int smem_bytes = 1024 + p.ring_bytes + kLinBarBytes;
+    if (p.split > 1 && smem_bytes < 80 * 1024) smem_bytes = 80 * 1024;
+    if (smem_bytes > kLinSmemBytes) {
+        snprintf(msg, msg_len, "linear product: %d bytes of shared memory needed", smem_bytes);
+        return 1;
     }
 
-    auto kern = linear_kernel<TYPE, MODE, PAIR>;
-    static SmemOptIn smem_opt;
-    cudaError_t e = smem_opt.ensure(reinterpret_cast<const void*>(kern), kLinSmemBytes);
+    if constexpr (!kGrad) {
+        // as much as the launch before leaves HBM idle for; beyond the ring's own loads it is worth nothing
+        p.prefetch_kb = few ? 8 : 0;
+        p.w_rows[0] = static_cast<const uint8_t*>(g.W[0]);
+        p.w_rows[1] = static_cast<const uint8_t*>(g.W[1]);
+        p.w_ld_bytes = g.ldw * 2;
+    }
+
+    LinearMaps maps;
+    bool ok = true;
+    if constexpr (kGrad) {
+        for (int s = 0; s < 2 && ok; ++s) {
+            const int q = s < g.parts ? s : 0;
+            ok = lin_map(&maps.m[s], g.type, g.dz[q], g.M, g.n, g.ldz, kLinBK, msg, msg_len);
+            if (g.dx != nullptr)
+                ok = ok && lin_map(&maps.m[2 + s], g.type, g.W[q], g.K, g.M, g.ldw, kLinBK, msg, msg_len);
+            else
+                maps.m[2 + s] = maps.m[0];
+        }
+        if (g.dW[0] != nullptr)
+            ok = ok && lin_map(&maps.m[4], g.type, g.x, g.K, g.n, g.ldx, kLinBK, msg, msg_len);
+        else
+            maps.m[4] = maps.m[0];
+    } else {
+        const int box = kGated ? g.bn / 2 : b_rows;
+        ok = lin_map(&maps.m[0], g.type, g.x, g.K, g.n, g.ldx, p.a_rows, msg, msg_len) &&
+             lin_map(&maps.m[1], g.type, g.W[0], g.K, g.M, g.ldw, box, msg, msg_len);
+        if (kGated && ok) ok = lin_map(&maps.m[2], g.type, g.W[1], g.K, g.M, g.ldw, box, msg, msg_len);
+        else maps.m[2] = maps.m[1];
+        maps.m[3] = maps.m[4] = maps.m[1];
+    }
+    if (!ok) return 1;
+
+    auto kern = linear_kernel<TYPE, MODE, PAIR, false>;
+    if constexpr (!PAIR) {
+        if (p.split > 1) kern = linear_kernel<TYPE, MODE, false, true>;
+    }
+    static SmemOptIn smem_opt[2];
+    cudaError_t e = smem_opt[p.split > 1 ? 1 : 0].ensure(reinterpret_cast<const void*>(kern), kLinSmemBytes);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         return 1;
-    }
-    const int share = PAIR ? 2 : p.split;
-    long long units = p.num_tiles;
-    if (p.split == 1) {
-        // every unit gets the same number of tiles (the last wave is not left partial)
-        const long long most = PAIR ? g.num_sms / 2 : g.num_sms;
-        const long long cap = most > 0 ? most : 1;
-        const long long per = (units + cap - 1) / cap;
-        units = (units + per - 1) / per;
     }
     cudaLaunchAttribute attr[2];
     int attrs = 0;
@@ -875,13 +1197,13 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
         ++attrs;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * share), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(units * (PAIR ? 2 : 1)), 1, 1);
     cfg.blockDim = dim3(kLinThreads, 1, 1);
-    cfg.dynamicSmemBytes = kLinSmemBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(attrs);
-    e = cudaLaunchKernelEx(&cfg, kern, tmA[0], tmA[1], tmB[0], tmB[1], p);
+    e = cudaLaunchKernelEx(&cfg, kern, maps, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "linear product launch failed: %s", cudaGetErrorString(e));
@@ -900,12 +1222,9 @@ int launch_linear_type(const LinearLaunch& g, cudaStream_t stream, char* msg, si
     case kModeGated:
         return g.pair ? launch_linear_instance<TYPE, kModeGated, true>(g, stream, msg, msg_len)
                       : launch_linear_instance<TYPE, kModeGated, false>(g, stream, msg, msg_len);
-    case kModeGradInput:
-        return g.pair ? launch_linear_instance<TYPE, kModeGradInput, true>(g, stream, msg, msg_len)
-                      : launch_linear_instance<TYPE, kModeGradInput, false>(g, stream, msg, msg_len);
-    case kModeGradWeight:
-        return g.pair ? launch_linear_instance<TYPE, kModeGradWeight, true>(g, stream, msg, msg_len)
-                      : launch_linear_instance<TYPE, kModeGradWeight, false>(g, stream, msg, msg_len);
+    case kModeGrad:
+        return g.pair ? launch_linear_instance<TYPE, kModeGrad, true>(g, stream, msg, msg_len)
+                      : launch_linear_instance<TYPE, kModeGrad, false>(g, stream, msg, msg_len);
     default:
         snprintf(msg, msg_len, "unknown linear mode %d", g.mode);
         return 1;
