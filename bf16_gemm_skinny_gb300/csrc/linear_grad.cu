@@ -122,11 +122,12 @@ __global__ void __launch_bounds__(kGradThreads) act_backward_kernel(const ActBac
                 grad_unpack<TYPE>(dy, vy[a]);
                 if (kNeedZ) grad_unpack<TYPE>(z, vz[a]);
                 if (GATED) grad_unpack<TYPE>(u, vu[a]);
+                float slope[kGradCols];
+                if (kNeedZ) act_values<ACT, true, kGradCols>(z, slope);   // z becomes act(z)
 #pragma unroll
                 for (int i = 0; i < kGradCols; ++i) {
-                    const float2 f = kNeedZ ? act_value_slope<ACT>(z[i]) : make_float2(0.f, 1.f);
-                    d0[i] = GATED ? dy[i] * u[i] * f.y : dy[i] * f.y;
-                    d1[i] = GATED ? dy[i] * f.x : 0.f;
+                    d0[i] = !kNeedZ ? dy[i] : GATED ? dy[i] * u[i] * slope[i] : dy[i] * slope[i];
+                    d1[i] = GATED ? dy[i] * z[i] : 0.f;
                     sum[0][i] += d0[i];
                     if (GATED) sum[kParts - 1][i] += d1[i];
                 }

@@ -52,46 +52,119 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     }
 }
 
-__device__ __forceinline__ float sigmoid_f(float v)
+// 2^x, and 1/x, by the hardware's approximations (2 units in the last place and 1).
+__device__ __forceinline__ float exp2_f(float x)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-v)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_f(float x)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
+// d[i] = 1 / d[i] of N values >= 1.  The special-function units give 16 results a clock
+// and SM, and e^v and 1/x of every value keep them busy longer than HBM takes for the values (6992 x 8512
+// outputs: 27 us): for four values one reciprocal of their product and nine multiplications.
+// Products past FP32, infinities and NaN: all one by one (one branch for the N, so that the
+// groups' latencies overlap; with a branch for each group silu cost 34 us there).
+template <int N>
+__device__ __forceinline__ void rcp_all(float (&d)[N])
+{
+    float r[N];
+    bool fine = true;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float ab = d[i] * d[i + 1], cd = d[i + 2] * d[i + 3], all = ab * cd;
+        fine = fine && all < 1e37f;
+        const float x = rcp_f(all);
+        const float rab = x * cd, rcd = x * ab;
+        r[i] = rab * d[i + 1];
+        r[i + 1] = rab * d[i];
+        r[i + 2] = rcd * d[i + 3];
+        r[i + 3] = rcd * d[i + 2];
+    }
+    if (!fine) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = rcp_f(d[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = r[i];
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC2 = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z)
+// The lower tail of the normal distribution, Phi(-|z|) = t Q(t) e^(-z^2 / 2) with t =
+// 1 / (1 + 0.4 |z| / sqrt 2): Q is a polynomial fitted here to erfc(x) e^(x^2) / (2t), x = |z| / sqrt 2, for all t in
+// (0, 1], largest relative error 1.3e-7 (the form of Press et al., Numerical Recipes, section 6.2:
+// a tail keeps its relative accuracy, where 1 + erf would cancel).
+__device__ __forceinline__ float normal_tail(float t, float e)
 {
-    if constexpr (ACT == kActRelu) return z <= 0.f ? 0.f : z;   // a NaN stays
-    else if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
-    else if constexpr (ACT == kActGelu) return z * normcdff(z);
-    else if constexpr (ACT == kActGeluTanh) return z * sigmoid_f(kGeluC2 * (z + kGeluA * z * z * z));
-    else return z;
+    float q = 0.025129861f;
+    q = fmaf(q, t, -0.091446319f);
+    q = fmaf(q, t, 0.084536198f);
+    q = fmaf(q, t, -0.0027988206f);
+    q = fmaf(q, t, 0.070713668f);
+    q = fmaf(q, t, 0.084271442f);
+    q = fmaf(q, t, 0.1039213f);
+    q = fmaf(q, t, 0.11283480f);
+    q = fmaf(q, t, 0.11283793f);
+    return q * t * e;
 }
 
-// act(z) and act'(z).
-template <int ACT>
-__device__ __forceinline__ float2 act_value_slope(float z)
+// act(z) of N values (a multiple of 4), in place; SLOPE: act'(z) beside it.
+template <int ACT, bool SLOPE, int N>
+__device__ __forceinline__ void act_values(float (&z)[N], float (&slope)[N])
 {
-    if constexpr (ACT == kActRelu) {
-        return make_float2(z <= 0.f ? 0.f : z, z <= 0.f ? 0.f : (z == z ? 1.f : z));
-    } else if constexpr (ACT == kActSilu) {
-        const float s = sigmoid_f(z);
-        return make_float2(z * s, s * (1.f + z * (1.f - s)));
-    } else if constexpr (ACT == kActGelu) {
-        const float p = normcdff(z);
-        return make_float2(z * p, p + z * kInvSqrt2Pi * __expf(-0.5f * z * z));
-    } else if constexpr (ACT == kActGeluTanh) {
-        const float s = sigmoid_f(kGeluC2 * (z + kGeluA * z * z * z));
-        // beyond 16 s is 0 or 1 and the second term 0; the clamp keeps 0 * infinity out of it
-        const float c = fminf(fmaxf(z, -16.f), 16.f);
-        return make_float2(z * s, s + c * s * (1.f - s) * (kGeluC2 * (1.f + 3.f * kGeluA * c * c)));
+    static_assert(N % 4 == 0, "reciprocals go by four");
+    if constexpr (ACT == kActNone) {
+        if constexpr (SLOPE) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) slope[i] = 1.f;
+        }
+    } else if constexpr (ACT == kActRelu) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (SLOPE) slope[i] = z[i] <= 0.f ? 0.f : (z[i] == z[i] ? 1.f : z[i]);
+            z[i] = z[i] <= 0.f ? 0.f : z[i];   // a NaN stays
+        }
     } else {
-        return make_float2(z, 1.f);
+        float r[N], e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (ACT == kActGelu) {
+                e[i] = exp2_f(z[i] * z[i] * (-0.5f * kLog2e));
+                r[i] = fmaf(fabsf(z[i]), 0.28284271247461901f, 1.f);
+            } else {
+                const float v = ACT == kActSilu ? z[i] : z[i] * fmaf(kGeluC2 * kGeluA * z[i], z[i], kGeluC2);
+                r[i] = 1.f + exp2_f(v * -kLog2e);
+            }
+        }
+        rcp_all<N>(r);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (ACT == kActGelu) {
+                const float tail = normal_tail(r[i], e[i]);
+                const float phi = z[i] <= 0.f ? tail : 1.f - tail;
+                if constexpr (SLOPE) slope[i] = fmaf(z[i] * kInvSqrt2Pi, e[i], phi);
+                z[i] *= phi;
+            } else {
+                const float s = r[i];
+                if constexpr (SLOPE && ACT == kActSilu) slope[i] = s * fmaf(z[i], 1.f - s, 1.f);
+                if constexpr (SLOPE && ACT == kActGeluTanh) {
+                    // beyond 16 s is 0 or 1 and the second term 0; the clamp keeps 0 * infinity out of it
+                    const float c = fminf(fmaxf(z[i], -16.f), 16.f);
+                    slope[i] = fmaf(c * s * (1.f - s), fmaf(3.f * kGeluC2 * kGeluA * c, c, kGeluC2), s);
+                }
+                z[i] *= s;
+            }
+        }
     }
 }
 

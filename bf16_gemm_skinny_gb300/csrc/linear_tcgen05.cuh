@@ -50,8 +50,8 @@ constexpr int kLinSmemBytes = 232448;            // at most
 constexpr int kFewRows = 64;                     // rows up to which the weights' stream is the bound
 constexpr int kLinMaxStages = 24;
 constexpr int kCh = 16;                          // columns per epilogue step: 32 bytes of 16-bit values
-constexpr int kStagePitch = 9;                   // words per row of a warp's staging buffer (odd: no bank conflicts)
-constexpr int kStageBytes = kLinEpiWarps * 32 * kStagePitch * 4;
+constexpr int kBlockBytes = 128;                 // a row of a warp's staging buffer: one line of memory
+constexpr int kStageBytes = kLinEpiWarps * 32 * kBlockBytes;
 // FP32 weight gradients: k-blocks summed in an accumulator before they are added to
 // FP32 registers.  A tensor-core accumulation cuts each of its sums (toward zero), so
 // an error grows with their number: dW over 8192 tokens came out 2e-5 off, in segments of 768
@@ -89,7 +89,7 @@ struct LinearParams {
     int wcols;                // result columns per tile: bn, gated bn / 2
     int stages, a_bytes, b_bytes;
     int ring_bytes;           // the stages (and staging buffers), before the barriers
-    int stage_at;             // rows that no 16-byte accesses reach go through staging buffers here; -1: none
+    int stage_at;             // results go through staging buffers here; -1: row by row
     int acc_cols, tmem_cols;  // TMEM columns of an accumulator, in all
     int split;                // CTAs that share a tile's k loop (a cluster); 1: none
     int prefetch_kb;          // k-blocks of the first tile's weights brought into L2 ahead
@@ -176,6 +176,14 @@ __device__ __forceinline__ void lin_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
+template <int CH>
+__device__ __forceinline__ void lin_tmem_ld(uint32_t taddr, uint32_t (&r)[CH])
+{
+    static_assert(CH == 16 || CH == 32, "16 or 32 columns");
+    if constexpr (CH == 16) lin_tmem_ld16(taddr, r);
+    else tmem_ld_32x32b_x32(taddr, r);
+}
+
 // Whole warp: the wait's answer, the same for all lanes.  Looks at the clock and the
 // abort flag only after many tries (each suspends the warp for a while by itself).
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, int site)
@@ -191,6 +199,14 @@ __device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity, 
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, w, site));
 }
 
+// Arrive on an mbarrier of the cluster without ordering this thread's earlier writes: the
+// accumulator that it hands back has been read (tcgen05.wait::ld).  A release at cluster scope would
+// wait for the results' stores to memory, every tile (6992 x 8512 x 320 on pairs: 57 us).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 16-byte store to the shared memory of a CTA of the cluster (address from mapa_shared).
 __device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, float a, float b, float c, float d)
 {
@@ -199,11 +215,8 @@ __device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, floa
 }
 
 // ---------------------------------------------------------------------------
-// Epilogue arithmetic on CH columns of one row per lane, c0 .. c0 + n - 1 of them there.
-//
-// Where rows cannot be read or written 16 bytes at a time (odd strides), a
-// whole warp exchanges its 32 rows through its staging buffer, so that neighbouring lanes
-// touch neighbouring elements; `stage` is that buffer, or NULL (each lane by itself).
+// Epilogue, row by row: each lane reads and writes its own row's CH columns, n of them there.
+// For few rows, and for the parts of split k.
 // ---------------------------------------------------------------------------
 template <int TYPE, int CH>
 __device__ __forceinline__ void load_row(float (&v)[CH], const uint16_t* p, int n, bool vec)
@@ -226,154 +239,74 @@ __device__ __forceinline__ void load_row(float (&v)[CH], const uint16_t* p, int 
     }
 }
 
-// Rows row - lane .. of a matrix with stride ld (base at column c0), one per lane of a
-// converged warp; lanes with `valid` have a row.
 template <int TYPE, int CH>
-__device__ __forceinline__ void load_rows(float (&v)[CH], const uint16_t* base, long long ld, long long row, int n,
-                                          bool vec, bool valid, uint32_t* stage)
-{
-    if (stage == nullptr || vec) {
-        if (valid) load_row<TYPE, CH>(v, base + row * ld, n, vec);
-    } else if constexpr (CH == 16) {
-        const int lane = threadIdx.x & 31;
-        const int rows = __popc(__ballot_sync(0xffffffffu, valid));   // the first lanes'
-        const int r0 = lane >> 4, c = lane & 15;
-        const long long first = row - lane;
-        uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-#pragma unroll 4
-        for (int i = 0; i < 32; i += 2) {
-            const int r = i + r0;
-            if (r < rows && c < n) st[r * (2 * kStagePitch) + c] = base[(first + r) * ld + c];
-        }
-        __syncwarp();
-        load_row<TYPE, CH>(v, st + lane * (2 * kStagePitch), valid ? n : 0, false);
-        __syncwarp();
-    }
-}
-
-template <int TYPE, int CH>
-__device__ __forceinline__ void store_rows16(uint16_t* base, long long ld, long long row, const float (&v)[CH], int n,
-                                             bool vec, bool valid, uint32_t* stage)
+__device__ __forceinline__ void store_row16(uint16_t* p, const float (&v)[CH], int n, bool vec)
 {
     uint32_t w[CH / 2];
 #pragma unroll
     for (int i = 0; i < CH / 2; ++i) w[i] = pack2<TYPE>(v[2 * i], v[2 * i + 1]);
     if (vec && n == CH) {
-        if (valid) {
-            uint4* p = reinterpret_cast<uint4*>(base + row * ld);
 #pragma unroll
-            for (int i = 0; i < CH / 8; ++i) p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
-    } else if (CH != 16 || stage == nullptr || vec) {
-        if (valid) {
-            uint16_t* p = base + row * ld;
+        for (int i = 0; i < CH / 8; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-                if (i < n) p[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
-        }
-    } else if constexpr (CH == 16) {
-        const int lane = threadIdx.x & 31;
-        const int rows = __popc(__ballot_sync(0xffffffffu, valid));
-        const int r0 = lane >> 4, c = lane & 15;
-        const long long first = row - lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) stage[lane * kStagePitch + i] = w[i];
-        __syncwarp();
-        const uint16_t* st = reinterpret_cast<const uint16_t*>(stage);
-#pragma unroll 4
-        for (int i = 0; i < 32; i += 2) {
-            const int r = i + r0;
-            if (r < rows && c < n) base[(first + r) * ld + c] = st[r * (2 * kStagePitch) + c];
-        }
-        __syncwarp();
+        for (int i = 0; i < CH; ++i)
+            if (i < n) p[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
     }
 }
 
 template <int CH>
-__device__ __forceinline__ void store_rows32(float* base, long long ld, long long row, const float (&v)[CH], int n,
-                                             bool vec, bool accumulate, bool valid, uint32_t* stage)
+__device__ __forceinline__ void store_row32(float* p, const float (&v)[CH], int n, bool vec, bool accumulate)
 {
     if (vec && n == CH) {
-        if (valid) {
-            float* p = base + row * ld;
 #pragma unroll
-            for (int i = 0; i < CH; i += 4) {
-                float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                if (accumulate) {
-                    const float4 w = *reinterpret_cast<const float4*>(p + i);
-                    t = make_float4(t.x + w.x, t.y + w.y, t.z + w.z, t.w + w.w);
-                }
-                *reinterpret_cast<float4*>(p + i) = t;
+        for (int i = 0; i < CH; i += 4) {
+            float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            if (accumulate) {
+                const float4 w = *reinterpret_cast<const float4*>(p + i);
+                t = make_float4(t.x + w.x, t.y + w.y, t.z + w.z, t.w + w.w);
             }
-        }
-    } else if (stage == nullptr || vec) {
-        if (valid) {
-            float* p = base + row * ld;
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-                if (i < n) p[i] = accumulate ? p[i] + v[i] : v[i];
+            *reinterpret_cast<float4*>(p + i) = t;
         }
     } else {
-        const int lane = threadIdx.x & 31;
-        const int rows = __popc(__ballot_sync(0xffffffffu, valid));
-        const int r0 = lane >> 3, c = lane & 7;
-        const long long first = row - lane;
 #pragma unroll
-        for (int h = 0; h < CH; h += 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) stage[lane * kStagePitch + i] = __float_as_uint(v[h + i]);
-            __syncwarp();
-#pragma unroll 4
-            for (int i = 0; i < 32; i += 4) {
-                const int r = i + r0;
-                if (r < rows && h + c < n) {
-                    float* p = base + (first + r) * ld + h + c;
-                    const float t = __uint_as_float(stage[r * kStagePitch + c]);
-                    *p = accumulate ? *p + t : t;
-                }
-            }
-            __syncwarp();
-        }
+        for (int i = 0; i < CH; ++i)
+            if (i < n) p[i] = accumulate ? p[i] + v[i] : v[i];
     }
 }
 
-template <int ACT, int CH>
-__device__ __forceinline__ void act_all(float (&v)[CH])
-{
-#pragma unroll
-    for (int i = 0; i < CH; ++i) v[i] = act_value<ACT>(v[i]);
-}
 template <int CH>
 __device__ __forceinline__ void act_switch(float (&v)[CH], int act)
 {
-    if (act == kActSilu) act_all<kActSilu>(v);
-    else if (act == kActGeluTanh) act_all<kActGeluTanh>(v);
-    else if (act == kActGelu) act_all<kActGelu>(v);
-    else if (act == kActRelu) act_all<kActRelu>(v);
+    if (act == kActSilu) act_values<kActSilu, false, CH>(v, v);
+    else if (act == kActGeluTanh) act_values<kActGeluTanh, false, CH>(v, v);
+    else if (act == kActGelu) act_values<kActGelu, false, CH>(v, v);
+    else if (act == kActRelu) act_values<kActRelu, false, CH>(v, v);
+}
+
+// v += bias[c0 ..], if there is one.
+template <int TYPE, int CH>
+__device__ __forceinline__ void add_bias_row(float (&v)[CH], const uint16_t* bias, int c0, int n, bool vec)
+{
+    if (bias == nullptr) return;
+    float t[CH];
+    load_row<TYPE, CH>(t, bias + c0, n, vec);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] += t[i];
 }
 
 // a (and b, gated: u) hold the sums of `row`, columns c0 .. c0 + n - 1 of source `src`.
-// With `stage`, all lanes of a converged warp hold consecutive rows.
 template <int TYPE, int MODE, int CH>
-__device__ __forceinline__ void finish_rows(const LinearParams& p, const LinearJob& job, float (&a)[CH], float (&b)[CH],
-                                            int src, long long row, int c0, int n, bool valid, uint32_t* stage)
+__device__ __forceinline__ void finish_row(const LinearParams& p, const LinearJob& job, float (&a)[CH], float (&b)[CH],
+                                           int src, long long row, int c0, int n)
 {
     if constexpr (MODE == kModeLinear || MODE == kModeGated) {
-        if (p.bias[0] != nullptr) {
-            float t[CH];
-            load_row<TYPE, CH>(t, p.bias[0] + c0, n, p.vec_bias);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) a[i] += t[i];
-        }
-        if (MODE == kModeGated && p.bias[1] != nullptr) {
-            float t[CH];
-            load_row<TYPE, CH>(t, p.bias[1] + c0, n, p.vec_bias);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) b[i] += t[i];
-        }
+        add_bias_row<TYPE, CH>(a, p.bias[0], c0, n, p.vec_bias);
+        if (MODE == kModeGated) add_bias_row<TYPE, CH>(b, p.bias[1], c0, n, p.vec_bias);
         if (p.keep[0] != nullptr) {
-            store_rows16<TYPE, CH>(p.keep[0] + c0, p.ldk, row, a, n, p.vec_keep, valid, stage);
-            if (MODE == kModeGated) store_rows16<TYPE, CH>(p.keep[1] + c0, p.ldk, row, b, n, p.vec_keep, valid, stage);
+            store_row16<TYPE, CH>(p.keep[0] + row * p.ldk + c0, a, n, p.vec_keep);
+            if (MODE == kModeGated) store_row16<TYPE, CH>(p.keep[1] + row * p.ldk + c0, b, n, p.vec_keep);
         }
         act_switch<CH>(a, p.act);
         if constexpr (MODE == kModeGated) {
@@ -381,24 +314,227 @@ __device__ __forceinline__ void finish_rows(const LinearParams& p, const LinearJ
             for (int i = 0; i < CH; ++i) a[i] *= b[i];
         }
         if (MODE == kModeLinear && p.residual != nullptr) {
-            float t[CH] = {};
-            load_rows<TYPE, CH>(t, p.residual + c0, p.ldr, row, n, p.vec_res, valid, stage);
+            float t[CH];
+            load_row<TYPE, CH>(t, p.residual + row * p.ldr + c0, n, p.vec_res);
 #pragma unroll
             for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
-        store_rows16<TYPE, CH>(static_cast<uint16_t*>(job.out[0]) + c0, job.ldo, row, a, n, job.vec_out, valid, stage);
+        store_row16<TYPE, CH>(static_cast<uint16_t*>(job.out[0]) + row * job.ldo + c0, a, n, job.vec_out);
     } else if (job.out_f32) {
-        store_rows32<CH>(static_cast<float*>(job.out[src]) + c0, job.ldo, row, a, n, job.vec_out, job.accumulate != 0, valid,
-                         stage);
+        store_row32<CH>(static_cast<float*>(job.out[src]) + row * job.ldo + c0, a, n, job.vec_out, job.accumulate != 0);
     } else {
-        uint16_t* o = static_cast<uint16_t*>(job.out[src]) + c0;
+        uint16_t* o = static_cast<uint16_t*>(job.out[src]) + row * job.ldo + c0;
         if (job.accumulate) {
-            float t[CH] = {};
-            load_rows<TYPE, CH>(t, o, job.ldo, row, n, job.vec_out, valid, stage);
+            float t[CH];
+            load_row<TYPE, CH>(t, o, n, job.vec_out);
 #pragma unroll
             for (int i = 0; i < CH; ++i) a[i] += t[i];
         }
-        store_rows16<TYPE, CH>(o, job.ldo, row, a, n, job.vec_out, valid, stage);
+        store_row16<TYPE, CH>(o, a, n, job.vec_out);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue through shared memory: a warp gathers a block of 32 rows by up to 128 bytes
+// (64 columns of 16 bits, 32 of FP32) in its staging buffer and moves it in whole lines, neighbouring
+// lanes on neighbouring addresses whatever the rows' alignment.  With every lane storing its own
+// row's 32 bytes, outputs went out at 11 GB/s an SM (6992 x 8512 x 320: 69 us).
+// Piece q (16 bytes) of row r lies at r * 128 + (q ^ (r & 7)) * 16: no bank conflicts either way.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint4* block_piece(uint8_t* buf, int row, int piece)
+{
+    return reinterpret_cast<uint4*>(buf + row * kBlockBytes + ((piece ^ (row & 7)) << 4));
+}
+template <typename E>
+__device__ __forceinline__ E* block_element(uint8_t* buf, int row, int col)
+{
+    const int byte = col * static_cast<int>(sizeof(E));
+    return reinterpret_cast<E*>(buf + row * kBlockBytes + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
+}
+
+// Whole warp: rows [0, rows) x n elements between the buffer and memory (first element at `g`, rows ld
+// elements apart).
+// (FLIGHT: 16-byte accesses of a lane in flight.)
+template <typename E, bool LOAD, int FLIGHT = 8>
+__device__ __forceinline__ void block_move(uint8_t* buf, E* g, long long ld, int rows, int n, bool vec)
+{
+    constexpr int kPer = 16 / static_cast<int>(sizeof(E));
+    const int lane = threadIdx.x & 31;
+    if (vec && n == 8 * kPer) {
+        const int piece = lane & 7;
+#pragma unroll FLIGHT
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            uint4* at = reinterpret_cast<uint4*>(g + r * ld + piece * kPer);
+            if (r < rows) {
+                if constexpr (LOAD) *block_piece(buf, r, piece) = *at;
+                else *at = *block_piece(buf, r, piece);
+            }
+        }
+    } else if (vec && n % kPer == 0) {
+        const int pieces = n / kPer;
+        for (int e = lane; e < rows * pieces; e += 32) {
+            const int r = e / pieces, piece = e - r * pieces;
+            uint4* at = reinterpret_cast<uint4*>(g + r * ld + piece * kPer);
+            if constexpr (LOAD) *block_piece(buf, r, piece) = *at;
+            else *at = *block_piece(buf, r, piece);
+        }
+    } else {
+        constexpr int kRowsAtOnce = FLIGHT / 2;
+#pragma unroll kRowsAtOnce
+        for (int r = 0; r < 32; ++r) {
+#pragma unroll
+            for (int h = 0; h < 8 * kPer; h += 32) {   // (up to 64 columns of 16 bits, 32 of FP32)
+                const int c = h + lane;
+                if (r < rows && c < n) {
+                    if constexpr (LOAD) *block_element<E>(buf, r, c) = g[r * ld + c];
+                    else g[r * ld + c] = *block_element<E>(buf, r, c);
+                }
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// This lane's row, CH columns of 16 bits from piece `first`: read, or rounded and written.
+template <int TYPE, int CH>
+__device__ __forceinline__ void block_get16(float (&v)[CH], uint8_t* buf, int row, int first)
+{
+#pragma unroll
+    for (int i = 0; i < CH / 8; ++i) {
+        const uint4 w = *block_piece(buf, row, first + i);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack2<TYPE>(u[k]);
+            v[8 * i + 2 * k] = f.x;
+            v[8 * i + 2 * k + 1] = f.y;
+        }
+    }
+}
+template <int TYPE, int CH>
+__device__ __forceinline__ void block_put16(uint8_t* buf, int row, int first, const float (&v)[CH])
+{
+#pragma unroll
+    for (int i = 0; i < CH / 8; ++i)
+        *block_piece(buf, row, first + i) =
+            make_uint4(pack2<TYPE>(v[8 * i], v[8 * i + 1]), pack2<TYPE>(v[8 * i + 2], v[8 * i + 3]),
+                       pack2<TYPE>(v[8 * i + 4], v[8 * i + 5]), pack2<TYPE>(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// Forward, one block: up to 64 columns c0 .. of 32 rows from `row0` (the first `rows` of them there); the
+// accumulator's columns at `t_col` (gated: u's at t_col + u_cols).  32 columns at a time: what a
+// step waits for (TMEM, the special functions, shared memory) is then shared by 32.
+template <int TYPE, int MODE>
+__device__ __forceinline__ void finish_block(const LinearParams& p, const LinearJob& job, uint8_t* buf, uint32_t t_col,
+                                             uint32_t u_cols, long long row0, int rows, int c0, int n)
+{
+    constexpr bool kGated = MODE == kModeGated;
+    constexpr int CH = 32;
+    const int lane = threadIdx.x & 31;
+    if (p.keep[0] != nullptr) {
+        // the kept pre-activations first
+#pragma unroll 1
+        for (int o = 0; o < (kGated ? 2 : 1); ++o) {
+#pragma unroll 1
+            for (int c = 0; c < n; c += CH) {
+                const int left = n - c < CH ? n - c : CH;
+                uint32_t ra[CH];
+                lin_tmem_ld<CH>(t_col + o * u_cols + c, ra);
+                tmem_ld_wait();
+                float a[CH];
+#pragma unroll
+                for (int i = 0; i < CH; ++i) a[i] = __uint_as_float(ra[i]);
+                add_bias_row<TYPE, CH>(a, p.bias[o], c0 + c, left, p.vec_bias);
+                block_put16<TYPE, CH>(buf, lane, c / 8, a);
+            }
+            __syncwarp();
+            block_move<uint16_t, false>(buf, p.keep[o] + row0 * p.ldk + c0, p.ldk, rows, n, p.vec_keep);
+        }
+    }
+    if (MODE == kModeLinear && p.residual != nullptr)
+        block_move<uint16_t, true>(buf, const_cast<uint16_t*>(p.residual) + row0 * p.ldr + c0, p.ldr, rows, n, p.vec_res);
+#pragma unroll 1
+    for (int c = 0; c < n; c += CH) {
+        const int left = n - c < CH ? n - c : CH;
+        uint32_t ra[CH], rb[CH];
+        lin_tmem_ld<CH>(t_col + c, ra);
+        if constexpr (kGated) lin_tmem_ld<CH>(t_col + u_cols + c, rb);
+        tmem_ld_wait();
+        float a[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) a[i] = __uint_as_float(ra[i]);
+        add_bias_row<TYPE, CH>(a, p.bias[0], c0 + c, left, p.vec_bias);
+        act_switch<CH>(a, p.act);
+        if constexpr (kGated) {
+            float b[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) b[i] = __uint_as_float(rb[i]);
+            add_bias_row<TYPE, CH>(b, p.bias[1], c0 + c, left, p.vec_bias);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) a[i] *= b[i];
+        } else if (p.residual != nullptr) {
+            float t[CH];
+            block_get16<TYPE, CH>(t, buf, lane, c / 8);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) a[i] += t[i];
+        }
+        block_put16<TYPE, CH>(buf, lane, c / 8, a);
+    }
+    __syncwarp();
+    block_move<uint16_t, false>(buf, static_cast<uint16_t*>(job.out[0]) + row0 * job.ldo + c0, job.ldo, rows, n, job.vec_out);
+}
+
+// Gradients: a warp's columns of a tile, 16 * i from c0 in sum[i], n of them there.
+template <int TYPE>
+__device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, float (&sum)[8][kCh], int src, long long row0,
+                                            int rows, int c0, int n)
+{
+    const int lane = threadIdx.x & 31;
+    const bool acc = job.accumulate != 0;
+    if (job.out_f32) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {   // blocks of 32 columns
+            const int left = n - 32 * g < 32 ? n - 32 * g : 32;
+            if (left > 0) {
+                float* o = static_cast<float*>(job.out[src]) + row0 * job.ldo + c0 + 32 * g;
+                if (acc) block_move<float, true, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float4 v = make_float4(sum[2 * g + q / 4][q % 4 * 4], sum[2 * g + q / 4][q % 4 * 4 + 1],
+                                           sum[2 * g + q / 4][q % 4 * 4 + 2], sum[2 * g + q / 4][q % 4 * 4 + 3]);
+                    float4* at = reinterpret_cast<float4*>(block_piece(buf, lane, q));
+                    if (acc) {
+                        const float4 w = *at;
+                        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                    }
+                    *at = v;
+                }
+                __syncwarp();
+                block_move<float, false, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {   // blocks of 64 columns
+            const int left = n - 64 * g < 64 ? n - 64 * g : 64;
+            if (left > 0) {
+                uint16_t* o = static_cast<uint16_t*>(job.out[src]) + row0 * job.ldo + c0 + 64 * g;
+                if (acc) block_move<uint16_t, true, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (acc) {
+                        float t[kCh];
+                        block_get16<TYPE, kCh>(t, buf, lane, 2 * q);
+#pragma unroll
+                        for (int i = 0; i < kCh; ++i) sum[4 * g + q][i] += t[i];
+                    }
+                    block_put16<TYPE, kCh>(buf, lane, 2 * q, sum[4 * g + q]);
+                }
+                __syncwarp();
+                block_move<uint16_t, false, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+            }
+        }
     }
 }
 
@@ -467,16 +603,20 @@ __device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, in
     return t;
 }
 
-// Two CTAs of a forward kernel fit on an SM by registers: with few rows, whose
-// rings are small, the next launch's CTAs set up while this one's finish.
-template <int TYPE, int MODE, bool PAIR, bool SPLIT>
-__global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2)
+// Kinds of kernel: few rows (forward), one CTA per tile, split k, CTA pairs.  With few rows two
+// CTAs fit on an SM by registers and shared memory, so that the next launch's CTAs set up while this
+// one's finish; split k of a forward pass likewise.
+enum LinearKind : int { kKindFew = 0, kKindOne = 1, kKindSplit = 2, kKindPair = 3 };
+
+template <int TYPE, int MODE, int KIND>
+__global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKindSplit && MODE != kModeGrad) ? 2 : 1)
     linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p)
 {
     constexpr bool kGated = MODE == kModeGated;
     constexpr bool kGrad = MODE == kModeGrad;
+    constexpr bool PAIR = KIND == kKindPair;
+    constexpr bool SPLIT = KIND == kKindSplit;
     constexpr int kTileRows = PAIR ? 256 : 128;
-    static_assert(!(PAIR && SPLIT), "pairs do not split k");
     const int S = p.stages;
 
     extern __shared__ uint8_t smem_raw[];
@@ -532,7 +672,7 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
     else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    if constexpr (!kGrad && !PAIR) {
+    if constexpr (!kGrad && (KIND == kKindFew || SPLIT)) {
         // The epilogue warps bring the first weights into L2 while the kernel before
         // this one may still run (a prefetch is coherent and delivers nothing).
         if (warp >= 2 && p.prefetch_kb > 0) {
@@ -717,16 +857,18 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
             const int quarter = warp & 3;
             const int half = (warp - 2) >> 2;
             const uint32_t lead_tempty0 = PAIR ? mapa_shared(tempty0, 0) : tempty0;
-            uint32_t* staging = p.stage_at >= 0 ? reinterpret_cast<uint32_t*>(smem + p.stage_at) + (warp - 2) * 32 * kStagePitch : nullptr;
+            uint8_t* staging = smem + p.stage_at + (warp - 2) * 32 * kBlockBytes;   // (one tile or split k: set)
             auto hand_back = [&](int acc) {   // this warp has read its part of the accumulator
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_remote(lead_tempty0 + 8 * acc);
+                    if constexpr (PAIR) mbar_arrive_remote_relaxed(lead_tempty0 + 8 * acc);
                     else mbar_arrive(tempty0 + 8 * acc);
                 }
             };
-            // Sums of the accumulator's columns c, c + 16 ... (every other 16) of a tile's segments
+            // Gradients: this warp's half of the accumulator's columns, from `half * bn / 2`, summed
+            // over a tile's segments
+            const int c_half = half * (p.bn / 2);
             auto add_segments = [&](float (&sum)[8][kCh], const LinearJob& job, int kb_begin, int kb_end, bool any) {
                 const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
@@ -741,10 +883,9 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
                     if (any) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const int c = (2 * q + half) * kCh;
-                            if (c < p.bn) {
+                            if (q * kCh < p.bn / 2) {
                                 uint32_t r[kCh];
-                                lin_tmem_ld16(t_row + acc * p.acc_cols + c, r);
+                                lin_tmem_ld16(t_row + acc * p.acc_cols + c_half + q * kCh, r);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int e = 0; e < kCh; ++e) sum[q][e] += __uint_as_float(r[e]);
@@ -781,9 +922,9 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
                     if (ok && any && lrow < t.rows) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const int c = (2 * q + half) * kCh;
-                            if (c < t.width) push(sum[q], 0, c);
-                            if (c + 8 < t.width) push(sum[q] + 8, 0, c + 8);
+                            const int c = c_half + q * kCh;
+                            if (q * kCh < p.bn / 2 && c < t.width) push(sum[q], 0, c);
+                            if (q * kCh < p.bn / 2 && c + 8 < t.width) push(sum[q] + 8, 0, c + 8);
                         }
                     }
                 } else {
@@ -821,7 +962,6 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
                     const int n0 = pn * p.wcols;
                     const int row = m0 + lane;
                     const bool any = m0 < job.rows;   // rows of this warp's to store
-                    const bool valid = row < job.rows;
                     const int left = job.cols - n0;
                     const int width = left < p.wcols ? left : p.wcols;
                     if constexpr (kGrad) {
@@ -830,15 +970,9 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
                         float sum[8][kCh];
                         add_segments(sum, job, kb_begin, kb_end, any);
                         if (!ok) break;
-                        if (any) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const int c = (2 * q + half) * kCh;
-                                if (c < width)
-                                    finish_rows<TYPE, MODE, kCh>(p, job, sum[q], sum[q], src, row, n0 + c,
-                                                                 width - c < kCh ? width - c : kCh, valid, staging);
-                            }
-                        }
+                        if (any)
+                            finish_sums<TYPE>(job, staging, sum, src, m0, job.rows - m0 < 32 ? job.rows - m0 : 32, n0 + c_half,
+                                              width - c_half < p.bn / 2 ? width - c_half : p.bn / 2);
                     } else {
                         const int acc = it & 1;
                         ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
@@ -847,22 +981,34 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
                         tc_fence_after_sync();
                         const uint32_t t_acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                                static_cast<uint32_t>(acc * p.acc_cols);
-                        if (any) {
+                        if constexpr (KIND == kKindFew) {
+                            if (any) {
 #pragma unroll 1
-                            for (int c = half * kCh; c < width; c += 2 * kCh) {
-                                uint32_t ra[kCh], rb[kCh];
-                                lin_tmem_ld16(t_acc + c, ra);
-                                if constexpr (kGated) lin_tmem_ld16(t_acc + p.wcols + c, rb);
-                                tmem_ld_wait();
-                                float a[kCh], b[kCh];
+                                for (int c = half * kCh; c < width; c += 2 * kCh) {
+                                    uint32_t ra[kCh], rb[kCh];
+                                    lin_tmem_ld16(t_acc + c, ra);
+                                    if constexpr (kGated) lin_tmem_ld16(t_acc + p.wcols + c, rb);
+                                    tmem_ld_wait();
+                                    float a[kCh], b[kCh];
 #pragma unroll
-                                for (int e = 0; e < kCh; ++e) {
-                                    a[e] = __uint_as_float(ra[e]);
-                                    b[e] = kGated ? __uint_as_float(rb[e]) : 0.f;
+                                    for (int e = 0; e < kCh; ++e) {
+                                        a[e] = __uint_as_float(ra[e]);
+                                        b[e] = kGated ? __uint_as_float(rb[e]) : 0.f;
+                                    }
+                                    if (row < job.rows)
+                                        finish_row<TYPE, MODE, kCh>(p, job, a, b, 0, row, n0 + c,
+                                                                    width - c < kCh ? width - c : kCh);
                                 }
-                                finish_rows<TYPE, MODE, kCh>(p, job, a, b, 0, row, n0 + c, width - c < kCh ? width - c : kCh,
-                                                             valid, staging);
                             }
+                        } else if (any) {
+                            // this warp's half of the columns, a multiple of 32, in blocks of up to 64
+                            const int mid = ((width + 31) / 32 + 1) / 2 * 32;
+                            const int end = half == 0 && mid < width ? mid : width;
+#pragma unroll 1
+                            for (int c = half * mid; c < end; c += 64)
+                                finish_block<TYPE, MODE>(p, job, staging, t_acc + c, p.wcols, m0,
+                                                         job.rows - m0 < 32 ? job.rows - m0 : 32, n0 + c,
+                                                         end - c < 64 ? end - c : 64);
                         }
                         hand_back(acc);
                     }
@@ -909,8 +1055,8 @@ __global__ void __launch_bounds__(kLinThreads, PAIR || MODE == kModeGrad ? 1 : 2
                     }
                 }
                 const int c = c_begin + cl;
-                finish_rows<TYPE, MODE, kW>(p, p.job[kGrad ? t.job : 0], a, b, t.src, t.row0 + lrow, t.col0 + c,
-                                            c_end - c < kW ? c_end - c : kW, true, nullptr);
+                finish_row<TYPE, MODE, kW>(p, p.job[kGrad ? t.job : 0], a, b, t.src, t.row0 + lrow, t.col0 + c,
+                                           c_end - c < kW ? c_end - c : kW);
             }
         }
         if constexpr (kGrad) {
@@ -1078,8 +1224,8 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
 
     // Few rows: the weights' stream is the bound, and two CTAs fit on an SM, each with half of the
     // shared memory and of TMEM; the next launch's CTAs can be there when this one's finish.
-    p.acc_cols = 32;
-    while (p.acc_cols < g.bn) p.acc_cols *= 2;
+    p.acc_cols = 32;   // (the epilogue reads 32 columns at a time)
+    while (p.acc_cols < (kGated ? p.wcols + (p.wcols + 31) / 32 * 32 : g.bn)) p.acc_cols *= 2;
     const long long sms = g.num_sms > 0 ? g.num_sms : 1;
     const bool few = !PAIR && !kGrad && g.n <= kFewRows &&
                      (p.acc_cols <= 128 || tiles * p.split <= 2 * sms || p.split > 1);
@@ -1113,8 +1259,7 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     p.a_bytes = p.a_rows * 128;
     const int b_rows = PAIR ? g.bn / 2 : g.bn;
     p.b_bytes = b_rows * 128;
-    const bool staged = !(p.job[0].vec_out && (p.job[1].num_tiles == 0 || p.job[1].vec_out) &&
-                          (p.vec_res || g.residual == nullptr) && (p.vec_keep || g.keep[0] == nullptr));
+    const bool staged = kGrad || (!few && p.split == 1);
     const int stage_bytes = p.a_bytes + p.b_bytes;
     const int room = (few ? kLinSmemBytes / 2 - 1024 : kLinSmemBytes) - 1024 - kLinBarBytes - (staged ? kStageBytes : 0);
     p.stages = room / stage_bytes;
@@ -1172,12 +1317,22 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     }
     if (!ok) return 1;
 
-    auto kern = linear_kernel<TYPE, MODE, PAIR, false>;
+    auto kern = linear_kernel<TYPE, MODE, PAIR ? kKindPair : kKindOne>;
+    int kind = PAIR ? kKindPair : kKindOne;
     if constexpr (!PAIR) {
-        if (p.split > 1) kern = linear_kernel<TYPE, MODE, false, true>;
+        if (p.split > 1) {
+            kern = linear_kernel<TYPE, MODE, kKindSplit>;
+            kind = kKindSplit;
+        }
+        if constexpr (!kGrad) {
+            if (p.split == 1 && few) {
+                kern = linear_kernel<TYPE, MODE, kKindFew>;
+                kind = kKindFew;
+            }
+        }
     }
-    static SmemOptIn smem_opt[2];
-    cudaError_t e = smem_opt[p.split > 1 ? 1 : 0].ensure(reinterpret_cast<const void*>(kern), kLinSmemBytes);
+    static SmemOptIn smem_opt[4];
+    cudaError_t e = smem_opt[kind].ensure(reinterpret_cast<const void*>(kern), kLinSmemBytes);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         return 1;
