@@ -469,6 +469,9 @@ int enqueue_backward(const BackwardArgs& a, void* stream, bool* launched)
     g.ldx = ldx;
     g.ldw = ldw;
     g.ldz = ld_dz;
+    g.x_padded = x != a.x;   // copies and dz have rows of whole multiples of 64
+    g.w_padded = W[0] != a.W[0];
+    g.z_padded = dz[0] != a.dy;
     g.dx = want_dx ? a.dx : nullptr;
     g.ld_dx = a.dx_stride;
     g.ld_dw = a.dw_stride;

@@ -43,6 +43,8 @@ struct LinearLaunch {
     // gradients
     const void* dz[2] = {nullptr, nullptr};   // [n, M]
     long long ldz = 0;
+    // rows of the operand may be read up to the next multiple of 64 elements (its values are not used)
+    bool x_padded = false, w_padded = false, z_padded = false;
     void* dx = nullptr;            // [n, K], NULL: not wanted
     long long ld_dx = 0;
     void* dW[2] = {nullptr, nullptr};   // [M, K], NULL: not wanted

@@ -83,11 +83,14 @@ struct LinearJob {
 struct LinearParams {
     LinearJob job[2];         // [1]: gradients only, may have no tiles
     int extra;                // gradients: see tile_of()
+    int wide_z, wide_w, wide_x;   // operands read along rows or columns: all 64-element blocks by one load
     int group_m;
     int a_rows;               // rows of A staged per CTA (128, or the few there are)
     int bn;                   // accumulator columns per tile
     int wcols;                // result columns per tile: bn, gated bn / 2
-    int stages, a_bytes, b_bytes;
+    int stages;               // ring depth, in groups of `group` k-blocks
+    int group;                // k-blocks per wait of the MMA warp
+    int a_bytes, b_bytes;     // of a k-block
     int ring_bytes;           // the stages (and staging buffers), before the barriers
     int stage_at;             // results go through staging buffers here; -1: row by row
     int acc_cols, tmem_cols;  // TMEM columns of an accumulator, in all
@@ -109,9 +112,10 @@ struct LinearParams {
     unsigned long long wait_limit_ns;
 };
 
-// Tensor maps.  Forward: x, W (Wg), Wu.  Gradients: dz_0, dz_1, W_0, W_1, x.
+// Tensor maps.  Forward: x, W (Wg), Wu.  Gradients: dz_0, dz_1, W_0, W_1, x, read along rows or
+// columns, then dz_0, dz_1 read along k.
 struct LinearMaps {
-    CUtensorMap m[5];
+    CUtensorMap m[7];
 };
 
 // The i-th tile of this CTA (or pair) in `pass`; false when there is none.
@@ -205,6 +209,24 @@ __device__ __forceinline__ bool lin_wait_cluster(uint32_t bar, uint32_t parity, 
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// A 3-D box, {64 elements, 64 rows, blocks}, from row y of block z on.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_blocks(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z)
+            : "memory");
 }
 
 // 16-byte store to the shared memory of a CTA of the cluster (address from mapa_shared).
@@ -603,13 +625,13 @@ __device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, in
     return t;
 }
 
-// Kinds of kernel: few rows (forward), one CTA per tile, split k, CTA pairs.  With few rows two
-// CTAs fit on an SM by registers and shared memory, so that the next launch's CTAs set up while this
+// Kinds of kernel: results row by row (forward, few rows or one narrow tile per CTA), through shared
+// memory, split k, CTA pairs.  With few rows two CTAs fit on an SM by registers and shared memory, so that the next launch's CTAs set up while this
 // one's finish; split k of a forward pass likewise.
-enum LinearKind : int { kKindFew = 0, kKindOne = 1, kKindSplit = 2, kKindPair = 3 };
+enum LinearKind : int { kKindDirect = 0, kKindOne = 1, kKindSplit = 2, kKindPair = 3 };
 
 template <int TYPE, int MODE, int KIND>
-__global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKindSplit && MODE != kModeGrad) ? 2 : 1)
+__global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == kKindSplit && MODE != kModeGrad) ? 2 : 1)
     linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p)
 {
     constexpr bool kGated = MODE == kModeGated;
@@ -623,7 +645,7 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t sA = smem_u32(smem);
-    const uint32_t sB = sA + static_cast<uint32_t>(S * p.a_bytes);
+    const uint32_t sB = sA + static_cast<uint32_t>(S * p.group * p.a_bytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring_bytes);
     const uint32_t full0 = smem_u32(bars);                 // kLinMaxStages each: stage loaded, consumed
     const uint32_t empty0 = full0 + 8 * kLinMaxStages;
@@ -672,7 +694,7 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
     else __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
-    if constexpr (!kGrad && (KIND == kKindFew || SPLIT)) {
+    if constexpr (!kGrad && (KIND == kKindDirect || SPLIT)) {
         // The epilogue warps bring the first weights into L2 while the kernel before
         // this one may still run (a prefetch is coherent and delivers nothing).
         if (warp >= 2 && p.prefetch_kb > 0) {
@@ -728,6 +750,14 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
                 if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, x, y);
                 else tma_load_2d(dst, map, bar, x, y);
             };
+            // 64 k rows of `blocks` 64-element blocks from element x on
+            auto load_blocks = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int k0, int blocks, bool wide) {
+                if (wide) {
+                    tma_load_blocks<PAIR>(dst, map, bar, k0, x / 64);
+                } else {
+                    for (int b = 0; b < blocks; ++b) load(dst + static_cast<uint32_t>(b) * 8192u, map, bar, x + 64 * b, k0);
+                }
+            };
             const int b_rows = PAIR ? p.bn / 2 : p.bn;   // rows of B (columns of the tile) staged by this CTA
             const uint32_t tx = static_cast<uint32_t>(p.a_bytes + p.b_bytes) * (PAIR ? 2u : 1u);
             int j, tile;
@@ -739,44 +769,43 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
                 const int row_src = kGrad && pm >= job.num_m1 ? 1 : 0;
                 const int m0 = (pm - row_src * job.num_m1) * kTileRows + (PAIR ? rank * 128 : 0);
                 const int n0 = pn * p.wcols;
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
+                for (int kb0 = kb_begin; kb0 < kb_end; kb0 += p.group) {
+                    const int count = kb_end - kb0 < p.group ? kb_end - kb0 : p.group;
                     ok = lin_wait(empty0 + 8 * stage, phase ^ 1u, wc, kSiteLinEmpty);
                     if (!ok) break;
                     if (lin_elect()) {
-                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx);
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, tx * static_cast<uint32_t>(count));
                         const uint32_t bar = lead_full0 + 8 * stage;
-                        const uint32_t a_dst = sA + static_cast<uint32_t>(stage * p.a_bytes);
-                        const uint32_t b_dst = sB + static_cast<uint32_t>(stage * p.b_bytes);
-                        if constexpr (kGrad) {
-                            // boxes of 64 x 64: dz along k (two of 64 rows) or along rows (two of 64
-                            // rows by 64 tokens), W and x along columns
-                            const int k_src = kb >= job.kbs ? 1 : 0;
-                            const int k0 = (kb - k_src * job.kbs) * kLinBK;
-                            const CUtensorMap* ma = &maps.m[job.a_mn ? row_src : k_src];
-                            const CUtensorMap* mb = &maps.m[job.a_mn ? 4 : 2 + k_src];
-                            if (job.a_mn) {
-                                load(a_dst, ma, bar, m0, k0);
-                                load(a_dst + 8192, ma, bar, m0 + 64, k0);
-                            } else {
-                                load(a_dst, ma, bar, k0, m0);
-                                load(a_dst + 8192, ma, bar, k0, m0 + 64);
-                            }
-                            const int nb = n0 + (PAIR ? rank * b_rows : 0);
-                            for (int b = 0; b < b_rows / 64; ++b)
-                                load(b_dst + static_cast<uint32_t>(b) * 8192u, mb, bar, nb + 64 * b, k0);
-                        } else {
-                            const int k0 = kb * kLinBK;
-                            load(a_dst, &maps.m[0], bar, k0, m0);
-                            if constexpr (kGated) {
-                                if constexpr (PAIR) {
-                                    load(b_dst, &maps.m[1 + rank], bar, k0, n0);
+                        uint32_t a_dst = sA + static_cast<uint32_t>(stage * p.group * p.a_bytes);
+                        uint32_t b_dst = sB + static_cast<uint32_t>(stage * p.group * p.b_bytes);
+                        for (int kb = kb0; kb < kb0 + count; ++kb) {
+                            if constexpr (kGrad) {
+                                const int k_src = kb >= job.kbs ? 1 : 0;
+                                const int k0 = (kb - k_src * job.kbs) * kLinBK;
+                                const int nb = n0 + (PAIR ? rank * b_rows : 0);
+                                if (job.a_mn) {
+                                    load_blocks(a_dst, &maps.m[row_src], bar, m0, k0, 2, p.wide_z != 0);
+                                    load_blocks(b_dst, &maps.m[4], bar, nb, k0, b_rows / 64, p.wide_x != 0);
                                 } else {
-                                    load(b_dst, &maps.m[1], bar, k0, n0);
-                                    load(b_dst + static_cast<uint32_t>(p.b_bytes / 2), &maps.m[2], bar, k0, n0);
+                                    load(a_dst, &maps.m[5 + k_src], bar, k0, m0);
+                                    load_blocks(b_dst, &maps.m[2 + k_src], bar, nb, k0, b_rows / 64, p.wide_w != 0);
                                 }
                             } else {
-                                load(b_dst, &maps.m[1], bar, k0, n0 + (PAIR ? rank * b_rows : 0));
+                                const int k0 = kb * kLinBK;
+                                load(a_dst, &maps.m[0], bar, k0, m0);
+                                if constexpr (kGated) {
+                                    if constexpr (PAIR) {
+                                        load(b_dst, &maps.m[1 + rank], bar, k0, n0);
+                                    } else {
+                                        load(b_dst, &maps.m[1], bar, k0, n0);
+                                        load(b_dst + static_cast<uint32_t>(p.b_bytes / 2), &maps.m[2], bar, k0, n0);
+                                    }
+                                } else {
+                                    load(b_dst, &maps.m[1], bar, k0, n0 + (PAIR ? rank * b_rows : 0));
+                                }
                             }
+                            a_dst += static_cast<uint32_t>(p.a_bytes);
+                            b_dst += static_cast<uint32_t>(p.b_bytes);
                         }
                     }
                     __syncwarp();
@@ -801,6 +830,15 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
                     k_range(job, &kb_begin, &kb_end);
                     const bool a_mn = kGrad && job.a_mn != 0;
                     const uint32_t idesc = job.idesc;
+                    // Operand descriptors of the first stage; addresses count 16 bytes.  An MMA's 16 k
+                    // values are 32 bytes of every 128-byte row of an operand read along k, and 16 rows of
+                    // 128 bytes of one read along rows or columns (64-element blocks 8 KB apart).
+                    const uint64_t desc_a = a_mn ? smem_desc_sw128(sA, 8192, 1024) : smem_desc_sw128(sA, 16, 1024);
+                    const uint64_t desc_b = kGrad ? smem_desc_sw128(sB, 8192, 1024) : smem_desc_sw128(sB, 16, 1024);
+                    const uint32_t step_a = a_mn ? 128u : 2u;
+                    constexpr uint32_t kStepB = kGrad ? 128u : 2u;
+                    const uint32_t step_ga = static_cast<uint32_t>(p.a_bytes) / 16u, step_gb = static_cast<uint32_t>(p.b_bytes) / 16u;
+                    const uint32_t stage_a = step_ga * static_cast<uint32_t>(p.group), stage_b = step_gb * static_cast<uint32_t>(p.group);
                     for (int seg = kb_begin; ok && seg < kb_end; seg += job.seg_kb, ++it) {
                         const int acc = it & 1;
                         const uint32_t aph = static_cast<uint32_t>(it >> 1) & 1u;
@@ -810,25 +848,24 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
                         tc_fence_after_sync();
                         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * p.acc_cols);
                         const int seg_end = kb_end - seg < job.seg_kb ? kb_end : seg + job.seg_kb;
-                        for (int kb = seg; kb < seg_end; ++kb) {
+                        for (int kb0 = seg; kb0 < seg_end; kb0 += p.group) {
+                            const int count = seg_end - kb0 < p.group ? seg_end - kb0 : p.group;
                             ok = lin_wait(full0 + 8 * stage, phase, wc, kSiteLinFull);
                             if (!ok) break;
                             tc_fence_after_sync();
-                            const uint32_t a = sA + static_cast<uint32_t>(stage * p.a_bytes);
-                            const uint32_t b = sB + static_cast<uint32_t>(stage * p.b_bytes);
+                            const uint64_t a0 = desc_a + static_cast<uint32_t>(stage) * stage_a;
+                            const uint64_t b0 = desc_b + static_cast<uint32_t>(stage) * stage_b;
                             if (lin_elect()) {
+                                auto issue = [&](uint64_t a, uint64_t b, uint32_t more) {
 #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) {
-                                    // read along k: 32 bytes of every 128-byte row; read along rows
-                                    // (columns): 16 k rows of 128 bytes, 64-element blocks 8 KB apart
-                                    const uint64_t ad = a_mn ? smem_desc_sw128(a + kk * 2048, 8192, 1024)
-                                                             : smem_desc_sw128(a + kk * 32, 16, 1024);
-                                    const uint64_t bd = kGrad ? smem_desc_sw128(b + kk * 2048, 8192, 1024)
-                                                              : smem_desc_sw128(b + kk * 32, 16, 1024);
-                                    const uint32_t more = kb != seg || kk != 0 ? 1u : 0u;
-                                    if constexpr (PAIR) mma_f16_pair(d, ad, bd, idesc, more);
-                                    else mma_f16(d, ad, bd, idesc, more);
-                                }
+                                    for (int kk = 0; kk < 4; ++kk) {
+                                        const uint32_t add = kk != 0 ? 1u : more;
+                                        if constexpr (PAIR) mma_f16_pair(d, a + kk * step_a, b + kk * kStepB, idesc, add);
+                                        else mma_f16(d, a + kk * step_a, b + kk * kStepB, idesc, add);
+                                    }
+                                };
+                                issue(a0, b0, kb0 != seg ? 1u : 0u);
+                                for (int g = 1; g < count; ++g) issue(a0 + g * step_ga, b0 + g * step_gb, 1u);
                                 if constexpr (PAIR) mma_commit_pair_multicast(empty0 + 8 * stage, 0x3);
                                 else mma_commit(empty0 + 8 * stage);
                             }
@@ -981,7 +1018,7 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
                         tc_fence_after_sync();
                         const uint32_t t_acc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                                static_cast<uint32_t>(acc * p.acc_cols);
-                        if constexpr (KIND == kKindFew) {
+                        if constexpr (KIND == kKindDirect) {
                             if (any) {
 #pragma unroll 1
                                 for (int c = half * kCh; c < width; c += 2 * kCh) {
@@ -1094,26 +1131,30 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindFew || (KIND == kKin
     }
 }
 
-// 2-D tensor map, 128-byte swizzle: `inner` contiguous elements in `outer` lines, boxes of 64 x box_outer.
+// Tensor map, 128-byte swizzle, of `inner` contiguous elements in `outer` lines.  blocks 0: boxes of
+// 64 x box_outer.  blocks > 0: the line as 64-element blocks, boxes of {64, box_outer, blocks}.
 inline bool lin_map(CUtensorMap* map, int type, const void* base, long long inner, long long outer, long long ld,
-                    int box_outer, char* msg, size_t msg_len)
+                    int box_outer, int blocks, char* msg, size_t msg_len)
 {
     TmapEncodeFn enc = tmap_encoder();
     if (enc == nullptr) {
         snprintf(msg, msg_len, "cuTensorMapEncodeTiled is not available from the driver");
         return false;
     }
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2u};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kLinBK), static_cast<cuuint32_t>(box_outer)};
-    const cuuint32_t estr[2] = {1, 1};
+    const bool flat = blocks == 0;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(flat ? inner : 64), static_cast<cuuint64_t>(outer),
+                                static_cast<cuuint64_t>((inner + 63) / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2u, 128u};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kLinBK), static_cast<cuuint32_t>(box_outer),
+                               static_cast<cuuint32_t>(flat ? 1 : blocks)};
+    const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, type == kTypeBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                           2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           flat ? 2 : 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
-        snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for %lld x %lld, stride %lld, box 64 x %d",
-                 static_cast<int>(r), inner, outer, ld, box_outer);
+        snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed (%d) for %lld x %lld, stride %lld, box 64 x %d x %d",
+                 static_cast<int>(r), inner, outer, ld, box_outer, blocks);
         return false;
     }
     return true;
@@ -1259,15 +1300,27 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     p.a_bytes = p.a_rows * 128;
     const int b_rows = PAIR ? g.bn / 2 : g.bn;
     p.b_bytes = b_rows * 128;
-    const bool staged = kGrad || (!few && p.split == 1);
+    // One narrow tile per CTA: its rows are written as they are, which takes less time from the last
+    // MMA to the end (261 x 128 x 64: 3.9 us, through shared memory 4.8).
+    const bool direct = few || (!PAIR && !kGrad && per_unit == 1 && g.bn <= 64);
+    const bool staged = kGrad || (!direct && p.split == 1);
     const int stage_bytes = p.a_bytes + p.b_bytes;
     const int room = (few ? kLinSmemBytes / 2 - 1024 : kLinSmemBytes) - 1024 - kLinBarBytes - (staged ? kStageBytes : 0);
-    p.stages = room / stage_bytes;
+    // A wait, a commit and the issue of its MMAs cost the MMA warp some 150 ns a turn, more than a
+    // small tile's MMAs of a k-block take (250 ns a k-block for every width up to 128): two or four k-blocks
+    // a turn, as far as the ring keeps a few turns.
+    const int fit = room / stage_bytes;
+    p.group = PAIR && !kGrad && g.bn == 256 ? 1 : fit >= 16 ? 4 : fit >= 6 ? 2 : 1;
+    p.stages = fit / p.group;
+    // one tile per CTA: no more than its k loop takes, so that the next launch's CTAs find room
+    if (per_unit == 1 && !kGrad) {
+        const int turns = ((kb0 + p.split - 1) / p.split + p.group - 1) / p.group;
+        if (p.stages > turns) p.stages = turns;
+    }
     if (p.stages > kLinMaxStages) p.stages = kLinMaxStages;
-    if (p.stages < 2) p.stages = 2;
-    // (with few rows the MMA reads up to 16 KB from the start of the last stage's A: inside this)
-    int ring = p.stages * stage_bytes;
-    const int reach = (p.stages - 1) * p.a_bytes + 16384;
+    // (with few rows the MMA reads up to 16 KB from the start of the last k-block's A: inside this)
+    int ring = p.stages * p.group * stage_bytes;
+    const int reach = (p.stages * p.group - 1) * p.a_bytes + 16384;
     if (ring < reach) ring = reach;
     const int rows = g.n < 128 && !kGrad ? g.n : 128;
     const int partial = p.split > 1 ? p.split * rows * (g.bn / p.wcols * split_slice(p.wcols, p.split) + 4) * 4 : 0;
@@ -1295,25 +1348,31 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     LinearMaps maps;
     bool ok = true;
     if constexpr (kGrad) {
+        // one load for a tile's blocks where a line's last block may be read whole
+        p.wide_z = g.z_padded || g.M % 64 == 0;
+        p.wide_w = g.w_padded || g.K % 64 == 0;
+        p.wide_x = g.x_padded || g.K % 64 == 0;
+        const int blocks = b_rows / 64;
         for (int s = 0; s < 2 && ok; ++s) {
             const int q = s < g.parts ? s : 0;
-            ok = lin_map(&maps.m[s], g.type, g.dz[q], g.M, g.n, g.ldz, kLinBK, msg, msg_len);
+            ok = lin_map(&maps.m[s], g.type, g.dz[q], g.M, g.n, g.ldz, kLinBK, p.wide_z ? 2 : 0, msg, msg_len) &&
+                 lin_map(&maps.m[5 + s], g.type, g.dz[q], g.M, g.n, g.ldz, 128, 0, msg, msg_len);
             if (g.dx != nullptr)
-                ok = ok && lin_map(&maps.m[2 + s], g.type, g.W[q], g.K, g.M, g.ldw, kLinBK, msg, msg_len);
+                ok = ok && lin_map(&maps.m[2 + s], g.type, g.W[q], g.K, g.M, g.ldw, kLinBK, p.wide_w ? blocks : 0, msg, msg_len);
             else
                 maps.m[2 + s] = maps.m[0];
         }
         if (g.dW[0] != nullptr)
-            ok = ok && lin_map(&maps.m[4], g.type, g.x, g.K, g.n, g.ldx, kLinBK, msg, msg_len);
+            ok = ok && lin_map(&maps.m[4], g.type, g.x, g.K, g.n, g.ldx, kLinBK, p.wide_x ? blocks : 0, msg, msg_len);
         else
             maps.m[4] = maps.m[0];
     } else {
         const int box = kGated ? g.bn / 2 : b_rows;
-        ok = lin_map(&maps.m[0], g.type, g.x, g.K, g.n, g.ldx, p.a_rows, msg, msg_len) &&
-             lin_map(&maps.m[1], g.type, g.W[0], g.K, g.M, g.ldw, box, msg, msg_len);
-        if (kGated && ok) ok = lin_map(&maps.m[2], g.type, g.W[1], g.K, g.M, g.ldw, box, msg, msg_len);
+        ok = lin_map(&maps.m[0], g.type, g.x, g.K, g.n, g.ldx, p.a_rows, 0, msg, msg_len) &&
+             lin_map(&maps.m[1], g.type, g.W[0], g.K, g.M, g.ldw, box, 0, msg, msg_len);
+        if (kGated && ok) ok = lin_map(&maps.m[2], g.type, g.W[1], g.K, g.M, g.ldw, box, 0, msg, msg_len);
         else maps.m[2] = maps.m[1];
-        maps.m[3] = maps.m[4] = maps.m[1];
+        for (int i = 3; i < 7; ++i) maps.m[i] = maps.m[1];
     }
     if (!ok) return 1;
 
@@ -1325,9 +1384,9 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
             kind = kKindSplit;
         }
         if constexpr (!kGrad) {
-            if (p.split == 1 && few) {
-                kern = linear_kernel<TYPE, MODE, kKindFew>;
-                kind = kKindFew;
+            if (p.split == 1 && direct) {
+                kern = linear_kernel<TYPE, MODE, kKindDirect>;
+                kind = kKindDirect;
             }
         }
     }
