@@ -597,11 +597,11 @@ __device__ __forceinline__ void sum_bias_grads(const LinearParams& p, float* sum
 }
 
 // A tile of split k: its place, and the layout of its partial sums in the shared memory of
-// the CTA that finishes `slice` of its columns: [CTA][row][part][slice], pitch floats a row
-// (16-byte aligned and an odd number of 16 bytes: no bank conflicts).
+// the CTA that finishes `slice` of its columns: [CTA][part][slice / 4][row][4 columns], so that the
+// 32 rows of a warp's 16-byte stores to another SM lie side by side.
 struct SplitTile {
     int job, src, row0, col0;
-    int rows, width, slice, pitch;
+    int rows, width, slice;
 };
 __host__ __device__ __forceinline__ int split_slice(int width, int split)
 {
@@ -621,7 +621,6 @@ __device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, in
     t.rows = job.rows - t.row0 < 128 ? job.rows - t.row0 : 128;
     t.width = job.cols - t.col0 < p.wcols ? job.cols - t.col0 : p.wcols;
     t.slice = split_slice(t.width, p.split);
-    t.pitch = p.bn / p.wcols * t.slice + 4;
     return t;
 }
 
@@ -944,10 +943,10 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == k
                 // 8 columns c .. of this lane's row, part 0 or (gated) 1
                 auto push = [&](const float* v, int part, int c) {
                     const int owner = c / t.slice;
-                    const uint32_t to = mapa_shared(sA, static_cast<uint32_t>(owner)) +
-                                        static_cast<uint32_t>(((rank * t.rows + lrow) * t.pitch + part * t.slice + c - owner * t.slice) * 4);
+                    const int group = ((rank * (kGated ? 2 : 1) + part) * t.slice + c - owner * t.slice) / 4;
+                    const uint32_t to = mapa_shared(sA, static_cast<uint32_t>(owner)) + static_cast<uint32_t>((group * t.rows + lrow) * 16);
                     st_shared_cluster_v4(to, v[0], v[1], v[2], v[3]);
-                    st_shared_cluster_v4(to + 16u, v[4], v[5], v[6], v[7]);
+                    st_shared_cluster_v4(to + static_cast<uint32_t>(t.rows * 16), v[4], v[5], v[6], v[7]);
                 };
                 if constexpr (kGrad) {
                     int kb_begin, kb_end;
@@ -1072,18 +1071,19 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == k
             for (int e = static_cast<int>(threadIdx.x) - 64; e < items; e += 32 * kLinEpiWarps) {
                 const int lrow = e % t.rows;
                 const int cl = e / t.rows * kW;
-                const float* from = reinterpret_cast<const float*>(smem) + lrow * t.pitch + cl;
+                const float4* from = reinterpret_cast<const float4*>(smem) + cl / 4 * t.rows + lrow;
+                const int part = t.slice / 4 * t.rows;   // of 16 bytes
                 float a[kW] = {}, b[kW] = {};
-                for (int q = 0; q < p.split; ++q, from += t.rows * t.pitch) {
+                for (int q = 0; q < p.split; ++q, from += (kGated ? 2 : 1) * part) {
 #pragma unroll
                     for (int h = 0; h < kW; h += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(from + h);
+                        const float4 v = from[h / 4 * t.rows];
                         a[h] += v.x;
                         a[h + 1] += v.y;
                         a[h + 2] += v.z;
                         a[h + 3] += v.w;
                         if constexpr (kGated) {
-                            const float4 w = *reinterpret_cast<const float4*>(from + t.slice + h);
+                            const float4 w = from[part + h / 4 * t.rows];
                             b[h] += w.x;
                             b[h + 1] += w.y;
                             b[h + 2] += w.z;
@@ -1323,7 +1323,7 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     const int reach = (p.stages * p.group - 1) * p.a_bytes + 16384;
     if (ring < reach) ring = reach;
     const int rows = g.n < 128 && !kGrad ? g.n : 128;
-    const int partial = p.split > 1 ? p.split * rows * (g.bn / p.wcols * split_slice(p.wcols, p.split) + 4) * 4 : 0;
+    const int partial = p.split > 1 ? p.split * rows * (g.bn / p.wcols) * split_slice(p.wcols, p.split) * 4 : 0;
     if (ring < partial) ring = partial;
     ring = (ring + 1023) / 1024 * 1024;
     p.stage_at = staged ? ring : -1;
