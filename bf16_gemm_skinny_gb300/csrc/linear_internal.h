@@ -65,6 +65,31 @@ struct LinearLaunch {
     int group_m = 8;
 };
 
+constexpr int kFewRows = 64;   // tokens up to which the weights' stream is the bound of a forward pass
+
+// Shared memory of a product's kernel: in all, of the barriers and of the staging buffers; of a k-block.
+constexpr int kLinSmemBytes = 232448;
+constexpr int kLinBarBytes = 512 + 1024;   // barriers, and the bias gradients' sums
+constexpr int kLinStageBytes = 32768;
+inline int linear_block_bytes(const LinearLaunch& g, bool pair, int bn)
+{
+    const int a_rows = pair || g.mode == kModeGrad || g.n >= 128 ? 128 : (g.n + 7) / 8 * 8;
+    return (a_rows + (pair ? bn / 2 : bn)) * 128;
+}
+inline int linear_ring_room(bool few, bool staged)
+{
+    return (few ? kLinSmemBytes / 2 - 1024 : kLinSmemBytes) - 1024 - kLinBarBytes - (staged ? kLinStageBytes : 0);
+}
+// k-blocks per turn of the MMA warp.  A wait, a commit and the issue of its MMAs cost some 150 ns a
+// turn, more than a small tile's MMAs of a k-block take (250 ns a k-block for every width up to 128):
+// two or four k-blocks a turn, as far as the ring keeps a few turns.  Forward on pairs of 256 columns: one, which
+// measured the same (linear prefill 397 us, with two 400); gradients there two (396 us, with one 426).
+inline int linear_group(const LinearLaunch& g, bool pair, int bn, bool few, bool staged)
+{
+    const int fit = linear_ring_room(few, staged) / linear_block_bytes(g, pair, bn);
+    return pair && g.mode != kModeGrad && bn == 256 ? 1 : fit >= 16 ? 4 : fit >= 6 ? 2 : 1;
+}
+
 // Fills in the plan (tile width, kernel, split) from the sizes; options override it.
 void plan_linear(LinearLaunch& g);
 int launch_linear(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len);

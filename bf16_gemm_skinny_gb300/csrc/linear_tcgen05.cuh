@@ -45,13 +45,10 @@ namespace {
 constexpr int kLinEpiWarps = 8;                  // two per quarter of the TMEM lanes: every other kCh columns
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
 constexpr int kLinBK = 64;                       // k values per stage: one 128-byte swizzle row
-constexpr int kLinBarBytes = 512 + 32 * kLinEpiWarps * 4;   // barriers, and the bias gradients' sums
-constexpr int kLinSmemBytes = 232448;            // at most
-constexpr int kFewRows = 64;                     // rows up to which the weights' stream is the bound
 constexpr int kLinMaxStages = 24;
 constexpr int kCh = 16;                          // columns per epilogue step: 32 bytes of 16-bit values
 constexpr int kBlockBytes = 128;                 // a row of a warp's staging buffer: one line of memory
-constexpr int kStageBytes = kLinEpiWarps * 32 * kBlockBytes;
+static_assert(kLinStageBytes == kLinEpiWarps * 32 * kBlockBytes, "staging buffers");
 // FP32 weight gradients: k-blocks summed in an accumulator before they are added to
 // FP32 registers.  A tensor-core accumulation cuts each of its sums (toward zero), so
 // an error grows with their number: dW over 8192 tokens came out 2e-5 off, in segments of 768
@@ -1305,12 +1302,8 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     const bool direct = few || (!PAIR && !kGrad && per_unit == 1 && g.bn <= 64);
     const bool staged = kGrad || (!direct && p.split == 1);
     const int stage_bytes = p.a_bytes + p.b_bytes;
-    const int room = (few ? kLinSmemBytes / 2 - 1024 : kLinSmemBytes) - 1024 - kLinBarBytes - (staged ? kStageBytes : 0);
-    // A wait, a commit and the issue of its MMAs cost the MMA warp some 150 ns a turn, more than a
-    // small tile's MMAs of a k-block take (250 ns a k-block for every width up to 128): two or four k-blocks
-    // a turn, as far as the ring keeps a few turns.
-    const int fit = room / stage_bytes;
-    p.group = PAIR && !kGrad && g.bn == 256 ? 1 : fit >= 16 ? 4 : fit >= 6 ? 2 : 1;
+    const int fit = linear_ring_room(few, staged) / stage_bytes;
+    p.group = linear_group(g, PAIR, g.bn, few, staged);
     p.stages = fit / p.group;
     // one tile per CTA: no more than its k loop takes, so that the next launch's CTAs find room
     if (per_unit == 1 && !kGrad) {
@@ -1327,7 +1320,7 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     if (ring < partial) ring = partial;
     ring = (ring + 1023) / 1024 * 1024;
     p.stage_at = staged ? ring : -1;
-    p.ring_bytes = ring + (staged ? kStageBytes : 0);
+    p.ring_bytes = ring + (staged ? kLinStageBytes : 0);
     // Split k: at most two CTAs per SM (of 256 TMEM columns at most), so that no CTA of a cluster can
     // wait for columns that a CTA of a cluster waiting for it holds.
     int smem_bytes = 1024 + p.ring_bytes + kLinBarBytes;
