@@ -483,6 +483,10 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, const Linear
         float a[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) a[i] = __uint_as_float(ra[i]);
+        if (left < CH) {   // past the tile: what TMEM held before, which is not to choose the values' path
+#pragma unroll
+            for (int i = 0; i < CH; ++i) a[i] = i < left ? a[i] : 0.f;
+        }
         add_bias_row<TYPE, CH>(a, p.bias[0], c0 + c, left, p.vec_bias);
         act_switch<CH>(a, p.act);
         if constexpr (kGated) {
@@ -1065,6 +1069,8 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == k
             const int c_begin = rank * t.slice;
             const int c_end = c_begin + t.slice < t.width ? c_begin + t.slice : t.width;
             const int items = c_begin < c_end ? (c_end - c_begin + kW - 1) / kW * t.rows : 0;
+            const LinearJob& job = p.job[kGrad ? t.job : 0];
+            const bool whole = job.vec_out && (kGrad || ((p.vec_res || p.residual == nullptr) && (p.vec_keep || p.keep[0] == nullptr)));
             for (int e = static_cast<int>(threadIdx.x) - 64; e < items; e += 32 * kLinEpiWarps) {
                 const int lrow = e % t.rows;
                 const int cl = e / t.rows * kW;
@@ -1089,8 +1095,58 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == k
                     }
                 }
                 const int c = c_begin + cl;
-                finish_row<TYPE, MODE, kW>(p, p.job[kGrad ? t.job : 0], a, b, t.src, t.row0 + lrow, t.col0 + c,
-                                           c_end - c < kW ? c_end - c : kW);
+                if (whole) {
+                    finish_row<TYPE, MODE, kW>(p, job, a, b, t.src, t.row0 + lrow, t.col0 + c, c_end - c < kW ? c_end - c : kW);
+                    continue;
+                }
+                // rows at any alignment: the results go back to where this thread's sums of CTA 0 (kept
+                // values) and CTA 1 (outputs) were, for the warps to write row by row
+                float4* kept = reinterpret_cast<float4*>(smem) + cl / 4 * t.rows + lrow;
+                float4* done = kept + (kGated ? 2 : 1) * part;
+                if constexpr (!kGrad) {
+                    const int n = c_end - c < kW ? c_end - c : kW;
+                    add_bias_row<TYPE, kW>(a, p.bias[0], t.col0 + c, n, p.vec_bias);
+                    if constexpr (kGated) add_bias_row<TYPE, kW>(b, p.bias[1], t.col0 + c, n, p.vec_bias);
+#pragma unroll
+                    for (int h = 0; h < kW; h += 4) {
+                        kept[h / 4 * t.rows] = make_float4(a[h], a[h + 1], a[h + 2], a[h + 3]);
+                        if constexpr (kGated) kept[part + h / 4 * t.rows] = make_float4(b[h], b[h + 1], b[h + 2], b[h + 3]);
+                    }
+                    act_switch<kW>(a, p.act);
+                    if constexpr (kGated) {
+#pragma unroll
+                        for (int h = 0; h < kW; ++h) a[h] *= b[h];
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < kW; h += 4) done[h / 4 * t.rows] = make_float4(a[h], a[h + 1], a[h + 2], a[h + 3]);
+            }
+            if (!whole) {
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kLinEpiWarps) : "memory");
+                const int part = t.slice * t.rows;   // of floats
+                const float* vals = reinterpret_cast<const float*>(smem);
+                for (int r = warp - 2; r < t.rows; r += kLinEpiWarps) {
+                    const long long row = t.row0 + r;
+                    for (int c = c_begin + lane; c < c_end; c += 32) {
+                        const int at = ((c - c_begin) / 4 * t.rows + r) * 4 + (c - c_begin) % 4;
+                        const int col = t.col0 + c;
+                        float v = vals[(kGated ? 2 : 1) * part + at];
+                        if constexpr (kGrad) {
+                            if (job.out_f32) {
+                                float* o = static_cast<float*>(job.out[t.src]) + row * job.ldo + col;
+                                *o = job.accumulate ? *o + v : v;
+                            } else {
+                                uint16_t* o = static_cast<uint16_t*>(job.out[t.src]) + row * job.ldo + col;
+                                *o = to_16<TYPE>(job.accumulate ? to_f32<TYPE>(*o) + v : v);
+                            }
+                        } else {
+                            if (p.keep[0] != nullptr) p.keep[0][row * p.ldk + col] = to_16<TYPE>(vals[at]);
+                            if (kGated && p.keep[1] != nullptr) p.keep[1][row * p.ldk + col] = to_16<TYPE>(vals[part + at]);
+                            if (MODE == kModeLinear && p.residual != nullptr) v += to_f32<TYPE>(p.residual[row * p.ldr + col]);
+                            static_cast<uint16_t*>(job.out[0])[row * job.ldo + col] = to_16<TYPE>(v);
+                        }
+                    }
+                }
             }
         }
         if constexpr (kGrad) {
@@ -1299,7 +1355,8 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     p.b_bytes = b_rows * 128;
     // One narrow tile per CTA: its rows are written as they are, which takes less time from the last
     // MMA to the end (261 x 128 x 64: 3.9 us, through shared memory 4.8).
-    const bool direct = few || (!PAIR && !kGrad && per_unit == 1 && g.bn <= 64);
+    const bool direct = few || (!PAIR && !kGrad && per_unit == 1 && g.bn <= 64 && p.job[0].vec_out &&
+                                (p.vec_res || g.residual == nullptr) && (p.vec_keep || g.keep[0] == nullptr));
     const bool staged = kGrad || (!direct && p.split == 1);
     const int stage_bytes = p.a_bytes + p.b_bytes;
     const int fit = linear_ring_room(few, staged) / stage_bytes;
