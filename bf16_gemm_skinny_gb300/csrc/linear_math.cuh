@@ -66,33 +66,24 @@ __device__ __forceinline__ float rcp_f(float x)
     return r;
 }
 
-// d[i] = 1 / d[i] of N values >= 1.  The special-function units give 16 results a clock
-// and SM, and e^v and 1/x of every value keep them busy longer than HBM takes for the values (6992 x 8512
-// outputs: 27 us): for four values one reciprocal of their product and nine multiplications.
-// Products past FP32, infinities and NaN: all one by one (one branch for the N, so that the
-// groups' latencies overlap; with a branch for each group silu cost 34 us there).
+// d[i] = 1 / d[i] of N values from 1 to 2^30.  The special-function units give 16 results a
+// clock and SM, and e^v and 1/x of every value keep them busy longer than HBM takes for the values
+// (6992 x 8512 outputs: 27 us): for four values one reciprocal of their product and nine multiplications.
+// A value's last bits so depend on the three beside it, and on nothing else.
 template <int N>
 __device__ __forceinline__ void rcp_all(float (&d)[N])
 {
-    float r[N];
-    bool fine = true;
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-        const float ab = d[i] * d[i + 1], cd = d[i + 2] * d[i + 3], all = ab * cd;
-        fine = fine && all < 1e37f;
-        const float x = rcp_f(all);
+        const float ab = d[i] * d[i + 1], cd = d[i + 2] * d[i + 3];
+        const float x = rcp_f(ab * cd);
         const float rab = x * cd, rcd = x * ab;
-        r[i] = rab * d[i + 1];
-        r[i + 1] = rab * d[i];
-        r[i + 2] = rcd * d[i + 3];
-        r[i + 3] = rcd * d[i + 2];
+        const float a = rab * d[i + 1], c = rcd * d[i + 3];
+        d[i + 1] = rab * d[i];
+        d[i] = a;
+        d[i + 3] = rcd * d[i + 2];
+        d[i + 2] = c;
     }
-    if (!fine) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = rcp_f(d[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = r[i];
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -135,18 +126,33 @@ __device__ __forceinline__ void act_values(float (&z)[N], float (&slope)[N])
             z[i] = z[i] <= 0.f ? 0.f : z[i];   // a NaN stays
         }
     } else {
+        // s(v) = 1 / (1 + 2^a), a = -v log2(e); above kFar the 1 counts for nothing, and s is 2^-a =
+        // 1 / (1 + 2^kFar) 2^(kFar - a): no factor of a product passes 2^30
+        constexpr float kFar = 30.f;
         float r[N], e[N];
+        bool far = false;
+        auto minus_v = [](float x) {
+            return ACT == kActSilu ? x * -kLog2e : x * fmaf(-kLog2e * kGeluC2 * kGeluA * x, x, -kLog2e * kGeluC2);
+        };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if constexpr (ACT == kActGelu) {
                 e[i] = exp2_f(z[i] * z[i] * (-0.5f * kLog2e));
-                r[i] = fmaf(fabsf(z[i]), 0.28284271247461901f, 1.f);
+                r[i] = fmaf(fminf(fabsf(z[i]), 1e6f), 0.28284271247461901f, 1.f);
             } else {
-                const float v = ACT == kActSilu ? z[i] : z[i] * fmaf(kGeluC2 * kGeluA * z[i], z[i], kGeluC2);
-                r[i] = 1.f + exp2_f(v * -kLog2e);
+                const float a = minus_v(z[i]);
+                far = far || a > kFar;
+                r[i] = 1.f + exp2_f(fminf(a, kFar));
             }
         }
         rcp_all<N>(r);
+        if (ACT != kActGelu && far) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float a = minus_v(z[i]);
+                if (a > kFar) r[i] *= exp2_f(kFar - a);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if constexpr (ACT == kActGelu) {

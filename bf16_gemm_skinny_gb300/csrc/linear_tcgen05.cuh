@@ -177,6 +177,12 @@ __device__ __forceinline__ void lin_tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "memory");
 }
 
+// A hint, as prefetch_l2().
+__device__ __forceinline__ void prefetch_l1(const void* addr)
+{
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(addr) : "memory");
+}
+
 template <int CH>
 __device__ __forceinline__ void lin_tmem_ld(uint32_t taddr, uint32_t (&r)[CH])
 {
@@ -371,10 +377,53 @@ __device__ __forceinline__ E* block_element(uint8_t* buf, int row, int col)
     return reinterpret_cast<E*>(buf + row * kBlockBytes + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
 }
 
+// Element by element, all of a turn's reads before its writes (the compiler cannot tell that
+// they do not touch).
+template <typename E, bool LOAD>
+__device__ __forceinline__ void block_move_elements(uint8_t* buf, E* g, long long ld, int rows, int n)
+{
+    constexpr int kRows = 8;
+    constexpr int kCols = kBlockBytes / static_cast<int>(sizeof(E)) / 32;   // of a lane: 2 of 16 bits, 1 of FP32
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kRows) {
+        E v[kRows][kCols];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int h = 0; h < kCols; ++h) {
+                const int c = 32 * h + lane;
+                if constexpr (LOAD) {
+                    if (r0 + i < rows && c < n) v[i][h] = g[(r0 + i) * ld + c];
+                } else {
+                    v[i][h] = *block_element<E>(buf, r0 + i, c);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int h = 0; h < kCols; ++h) {
+                const int c = 32 * h + lane;
+                if (r0 + i < rows && c < n) {
+                    if constexpr (LOAD) *block_element<E>(buf, r0 + i, c) = v[i][h];
+                    else g[(r0 + i) * ld + c] = v[i][h];
+                }
+            }
+    }
+}
+
+// The same, not inlined: in the linear kernels its registers and code would slow the common path
+// down (6992 x 8512 x 320: 45 against 36 us); in the gated ones they do not (333 x 2731 x 1024: 13.7 against 15.3).
+template <typename E, bool LOAD>
+__device__ __noinline__ void block_move_elements_call(uint8_t* buf, E* g, long long ld, int rows, int n)
+{
+    block_move_elements<E, LOAD>(buf, g, ld, rows, n);
+}
+
 // Whole warp: rows [0, rows) x n elements between the buffer and memory (first element at `g`, rows ld
 // elements apart).
-// (FLIGHT: 16-byte accesses of a lane in flight.)
-template <typename E, bool LOAD, int FLIGHT = 8>
+// (FLIGHT: 16-byte accesses of a lane in flight; 2: little of everything, beside a tile in registers.)
+template <typename E, bool LOAD, int FLIGHT, bool INLINE>
 __device__ __forceinline__ void block_move(uint8_t* buf, E* g, long long ld, int rows, int n, bool vec)
 {
     constexpr int kPer = 16 / static_cast<int>(sizeof(E));
@@ -398,14 +447,16 @@ __device__ __forceinline__ void block_move(uint8_t* buf, E* g, long long ld, int
             if constexpr (LOAD) *block_piece(buf, r, piece) = *at;
             else *at = *block_piece(buf, r, piece);
         }
+    } else if constexpr (FLIGHT == 8) {
+        if constexpr (INLINE) block_move_elements<E, LOAD>(buf, g, ld, rows, n);
+        else block_move_elements_call<E, LOAD>(buf, g, ld, rows, n);
     } else {
-        constexpr int kRowsAtOnce = FLIGHT / 2;
-#pragma unroll kRowsAtOnce
-        for (int r = 0; r < 32; ++r) {
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) {
 #pragma unroll
             for (int h = 0; h < 8 * kPer; h += 32) {   // (up to 64 columns of 16 bits, 32 of FP32)
                 const int c = h + lane;
-                if (r < rows && c < n) {
+                if (c < n) {
                     if constexpr (LOAD) *block_element<E>(buf, r, c) = g[r * ld + c];
                     else g[r * ld + c] = *block_element<E>(buf, r, c);
                 }
@@ -468,11 +519,11 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, const Linear
                 block_put16<TYPE, CH>(buf, lane, c / 8, a);
             }
             __syncwarp();
-            block_move<uint16_t, false>(buf, p.keep[o] + row0 * p.ldk + c0, p.ldk, rows, n, p.vec_keep);
+            block_move<uint16_t, false, 8, kGated>(buf, p.keep[o] + row0 * p.ldk + c0, p.ldk, rows, n, p.vec_keep);
         }
     }
     if (MODE == kModeLinear && p.residual != nullptr)
-        block_move<uint16_t, true>(buf, const_cast<uint16_t*>(p.residual) + row0 * p.ldr + c0, p.ldr, rows, n, p.vec_res);
+        block_move<uint16_t, true, 8, kGated>(buf, const_cast<uint16_t*>(p.residual) + row0 * p.ldr + c0, p.ldr, rows, n, p.vec_res);
 #pragma unroll 1
     for (int c = 0; c < n; c += CH) {
         const int left = n - c < CH ? n - c : CH;
@@ -483,10 +534,6 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, const Linear
         float a[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) a[i] = __uint_as_float(ra[i]);
-        if (left < CH) {   // past the tile: what TMEM held before, which is not to choose the values' path
-#pragma unroll
-            for (int i = 0; i < CH; ++i) a[i] = i < left ? a[i] : 0.f;
-        }
         add_bias_row<TYPE, CH>(a, p.bias[0], c0 + c, left, p.vec_bias);
         act_switch<CH>(a, p.act);
         if constexpr (kGated) {
@@ -505,7 +552,7 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, const Linear
         block_put16<TYPE, CH>(buf, lane, c / 8, a);
     }
     __syncwarp();
-    block_move<uint16_t, false>(buf, static_cast<uint16_t*>(job.out[0]) + row0 * job.ldo + c0, job.ldo, rows, n, job.vec_out);
+    block_move<uint16_t, false, 8, kGated>(buf, static_cast<uint16_t*>(job.out[0]) + row0 * job.ldo + c0, job.ldo, rows, n, job.vec_out);
 }
 
 // Gradients: a warp's columns of a tile, 16 * i from c0 in sum[i], n of them there.
@@ -521,7 +568,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
             const int left = n - 32 * g < 32 ? n - 32 * g : 32;
             if (left > 0) {
                 float* o = static_cast<float*>(job.out[src]) + row0 * job.ldo + c0 + 32 * g;
-                if (acc) block_move<float, true, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+                if (acc) block_move<float, true, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     float4 v = make_float4(sum[2 * g + q / 4][q % 4 * 4], sum[2 * g + q / 4][q % 4 * 4 + 1],
@@ -534,7 +581,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
                     *at = v;
                 }
                 __syncwarp();
-                block_move<float, false, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+                block_move<float, false, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
             }
         }
     } else {
@@ -543,7 +590,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
             const int left = n - 64 * g < 64 ? n - 64 * g : 64;
             if (left > 0) {
                 uint16_t* o = static_cast<uint16_t*>(job.out[src]) + row0 * job.ldo + c0 + 64 * g;
-                if (acc) block_move<uint16_t, true, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+                if (acc) block_move<uint16_t, true, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (acc) {
@@ -555,7 +602,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
                     block_put16<TYPE, kCh>(buf, lane, 2 * q, sum[4 * g + q]);
                 }
                 __syncwarp();
-                block_move<uint16_t, false, 2>(buf, o, job.ldo, rows, left, job.vec_out);
+                block_move<uint16_t, false, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
             }
         }
     }
@@ -1011,6 +1058,13 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == k
                             finish_sums<TYPE>(job, staging, sum, src, m0, job.rows - m0 < 32 ? job.rows - m0 : 32, n0 + c_half,
                                               width - c_half < p.bn / 2 ? width - c_half : p.bn / 2);
                     } else {
+                        // what the epilogue reads from memory, on its way while the k loop runs
+                        if (p.bias[0] != nullptr && lane * 64 < width) {
+                            prefetch_l1(p.bias[0] + n0 + lane * 64);
+                            if (kGated && p.bias[1] != nullptr) prefetch_l1(p.bias[1] + n0 + lane * 64);
+                        }
+                        if (MODE == kModeLinear && p.residual != nullptr && row < job.rows)
+                            for (int c = half * 64; c < width; c += 128) prefetch_l2(p.residual + row * p.ldr + n0 + c);
                         const int acc = it & 1;
                         ok = lin_wait(tfull0 + 8 * acc, static_cast<uint32_t>(it >> 1) & 1u, wc, kSiteLinTmemFull);
                         if (!ok) break;
