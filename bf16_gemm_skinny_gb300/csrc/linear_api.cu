@@ -615,7 +615,7 @@ void plan_linear(LinearLaunch& g)
     double best = -1.0;
     for (int pair = 0; pair < 2; ++pair) {
         if ((opt_kernel == 1 && pair) || (opt_kernel == 2 && !pair)) continue;
-        const int unit = grad ? (pair ? 128 : 64) : pair ? 64 : g.mode == kModeGated ? 32 : 16;
+        const int unit = grad ? (pair ? 128 : 64) : pair ? 32 : g.mode == kModeGated ? 32 : 16;
         for (int bn = unit; bn <= 256; bn += unit) {
             if (opt_tile > 0 ? bn != opt_tile && opt_tile % unit == 0 : bn > 48 && bn % 32 != 0) continue;
             for (int split = 1; split <= (pair ? 1 : 8); split *= 2) {

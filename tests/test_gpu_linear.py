@@ -155,7 +155,7 @@ def test_strides_and_alignment(pads, first, n, gated):
 
 
 @pytest.mark.parametrize("kernel", [1, 2])
-@pytest.mark.parametrize("tile", [16, 32, 48, 64, 96, 128, 192, 256])
+@pytest.mark.parametrize("tile", [16, 32, 48, 64, 96, 128, 160, 192, 224, 256])
 @pytest.mark.parametrize("gated", [False, True])
 def test_every_tile(kernel, tile, gated):
     bsk.set_option("linear_kernel", kernel)
