@@ -511,9 +511,9 @@ namespace bsk {
 
 // The tile, the kernel and the split of a launch: the least estimated time (us).
 //
-// The estimates are fitted to 5600 timings on GB300, back to back (forward calls of 1 to 8192 tokens, 64 to
-// 17408 features in and out, gradients from 16 tokens on; every tile, split and kernel): over those sizes
-// the plan taken is 1.5 to 2.7% slower than the best one on average (1.29 times at worst).  A k-block
+// The estimates are fitted to some 9000 timings on GB300, back to back (forward calls of 1 to 8192 tokens, 64 to
+// 17408 features in and out, gradients from 16 tokens on; every tile, split and kernel): over such sizes
+// the plan taken is 2 to 4% slower than the best one on average (1.3 times at worst).  A k-block
 // costs the MMA warp's turn (shared by the k-blocks of a turn) and its MMAs, or the time its operands take
 // on the way from L2, the more the more SMs ask for theirs; a tile's epilogue overlaps the next one's loop.
 namespace {
@@ -588,20 +588,21 @@ double grad_time(const LinearLaunch& g, const LinearChoice& c)
     const double t0 = static_cast<double>(tiles[first]), t1 = static_cast<double>(tiles[1 - first]);
     const double slots = static_cast<double>(c.pair ? (g.num_sms > 1 ? g.num_sms / 2 : 1) : split_slots(g.num_sms, c.split));
     const int group = linear_group(g, c.pair, c.bn, false, true);
-    const double turn = c.pair ? 0.211 + 0.00038 * c.bn : (group >= 2 ? 0.246 : 0.321) + 0.00028 * c.bn;
+    const double turn = c.pair ? 0.192 + 0.00062 * c.bn : (group >= 2 ? 0.237 : 0.292) + 0.00053 * c.bn;
     const double mma = turn > 0.00105 * c.bn ? turn : 0.00105 * c.bn;
     const double bytes = c.pair ? (128 + c.bn / 2) * 128.0 : (128 + c.bn) * 128.0;
     const double filled = (t0 * c.split + t1) / slots;
-    const double block = either(mma, bytes * 5.9e-6 * (0.4 + 0.6 * (filled < 1.0 ? filled : 1.0)));
+    const double block = either(mma, bytes * 6.1e-6 * (0.4 + 0.6 * (filled < 1.0 ? filled : 1.0)));
     // a tile takes its k loop or, overlapped, the epilogue of another
+    const double epilogue = 1.57 + 0.0068 * c.bn;
     const double longest = static_cast<double>(div_up(kb[first], c.split)) * block, other = static_cast<double>(kb[1 - first]) * block;
-    const double c0 = longest > 1.84 ? longest : 1.84, c1 = t1 > 0.0 ? (other > 1.84 ? other : 1.84) : 0.0;
-    const double mean = (t0 * c.split * c0 + t1 * c1) / slots + c1;
+    const double c0 = longest > epilogue ? longest : epilogue, c1 = t1 > 0.0 ? (other > epilogue ? other : epilogue) : 0.0;
+    const double mean = (t0 * c.split * c0 + t1 * c1) / slots + 0.77 * c1;
     const double rounds = static_cast<double>(div_up(tiles[first] * c.split, static_cast<long long>(slots))) * c0;
-    const double t = 3.3 + (c.split > 1 ? 2.2 : 0.0) + (mean > rounds ? mean : rounds) + 0.012 * c.bn;
+    const double t = 4.25 + (c.split > 1 ? 1.2 + 0.003 * c.bn : 0.0) + (mean > rounds ? mean : rounds) + 0.0064 * c.bn;
     const double parts = g.parts;
-    const double memory = 2.0 * (2.0 * parts * g.M * g.K + static_cast<double>(g.n) * (2.0 * g.K + parts * g.M)) / 2.4e6;
-    return either(t, memory + 2.0);
+    const double memory = 2.0 * (2.0 * parts * g.M * g.K + static_cast<double>(g.n) * (2.0 * g.K + parts * g.M)) / 3.7e6;
+    return either(t, memory + 2.5);
 }
 
 }  // namespace

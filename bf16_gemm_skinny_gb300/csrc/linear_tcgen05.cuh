@@ -1288,6 +1288,34 @@ inline LinearJob lin_job(int rows, int cols, int k, int k_sources, int row_sourc
     return j;
 }
 
+// LinearParams::extra: the number of tiles of job 1 that the units with fewer tiles of job 0 take
+// first, so that the last of all is done earliest.  Times in microseconds: a k-block's operands at 95
+// GB/s an SM, or 0.3; with split k 2.5 for the sums; a tile's results 0.0165 a column of 16 bits.
+inline int lin_extra(const LinearParams& p, int bn, long long units)
+{
+    const long long t0 = p.job[0].num_tiles * static_cast<long long>(p.split), t1 = p.job[1].num_tiles;
+    const long long late = units - (p.split > 1 ? t0 : t0 % units);
+    if (t1 == 0 || late <= 0 || late == units) return 0;
+    const double block = (128 + bn) * 0.00135 > 0.3 ? (128 + bn) * 0.00135 : 0.3;
+    const double store = (p.job[1].out_f32 ? 0.033 : 0.0165) * bn, loop = p.job[1].kbs * p.job[1].k_sources * block;
+    const double c0 = p.job[0].kbs * p.job[0].k_sources / p.split * block + (p.split > 1 ? 2.5 : 0.0);
+    const double c1 = loop > store ? loop : store;
+    double best = -1.0;
+    int extra = 0;
+    for (int e = 0; e <= 4096; ++e) {
+        const long long rest = t1 > e * late ? (t1 - e * late + units - 1) / units : 0;   // rounds of all units
+        const long long most = (t1 + late - 1) / late;
+        const double end0 = c0 + c1 * static_cast<double>(rest), end1 = c1 * static_cast<double>((e < most ? e : most) + rest);
+        const double end = end0 > end1 ? end0 : end1;
+        if (best < 0.0 || end < best) {
+            best = end;
+            extra = e;
+        }
+        if (e * late >= t1 || end1 > end0) break;
+    }
+    return extra;
+}
+
 template <int TYPE, int MODE, bool PAIR>
 int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg, size_t msg_len)
 {
@@ -1399,7 +1427,7 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     }
     // TMEM: two accumulators unless every unit has one tile of one segment.
     const bool one = per_unit == 1 && (!kGrad || p.job[1].num_tiles == 0) && p.job[0].seg_kb >= kb0;
-    p.extra = kGrad ? kb0 / p.split / kb1 : 0;
+    if constexpr (kGrad) p.extra = lin_extra(p, g.bn, units);
     p.tmem_cols = one ? p.acc_cols : 2 * p.acc_cols;
 
     // Shared memory: the ring, the staging buffers behind it, the barriers.
