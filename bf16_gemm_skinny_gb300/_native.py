@@ -71,7 +71,7 @@ EXPORTS = (
 # Tuning options and test hooks (csrc/bsk_tuning.h): exported for the tests and
 # the benchmark, not part of the C ABI.
 TUNING_EXPORTS = ("bsk_tile_coord", "bsk_set_option", "bsk_get_option", "bsk_test_wait_timeout", "bsk_plan_gemm",
-                  "bsk_plan_kv_attention")
+                  "bsk_plan_kv_attention", "bsk_plan_linear")
 
 COL_MAJOR, ROW_MAJOR = 0, 1
 BIAS_NONE, BIAS_ROW, BIAS_COLUMN = 0, 1, 2
@@ -145,6 +145,8 @@ def load():
         lib.bsk_plan_gemm.restype = i
         lib.bsk_plan_kv_attention.argtypes = [i] * 13 + [ctypes.POINTER(i)]
         lib.bsk_plan_kv_attention.restype = i
+        lib.bsk_plan_linear.argtypes = [i] * 6 + [ctypes.POINTER(i)]
+        lib.bsk_plan_linear.restype = i
         _lib = lib
         return lib
 
@@ -508,6 +510,13 @@ def plan_kv_attention(cache_type: int, num_seqs: int, num_tokens: int, max_chunk
     _check(load().bsk_plan_kv_attention(cache_type, int(one_token_each), num_seqs, num_tokens, max_chunk, num_q_heads,
                                         num_kv_heads, head_dim, max_seq_len, window, sinks, num_segments, sms, out))
     return dict(zip(("cta_rows", "tiles", "segments", "flat_rows"), list(out)))
+
+
+def plan_linear(M: int, K: int, n: int, gated: bool = False, dx: bool = False, dW: bool = False, sms: int = 152) -> dict:
+    """What a feed-forward product of these sizes would launch (test hook; launches nothing)."""
+    out = (ctypes.c_int * 3)()
+    _check(load().bsk_plan_linear(int(dx) + 2 * int(dW), int(gated), M, K, n, sms, out))
+    return dict(zip(("pair", "tile", "split"), list(out)))
 
 
 def set_option(name: str, value: int) -> None:

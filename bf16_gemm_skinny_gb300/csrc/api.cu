@@ -1120,17 +1120,29 @@ void record_error(const char* msg)
     snprintf(t_err, sizeof(t_err), "%s", msg);
 }
 
+namespace {
+
+void* driver_entry(const char* name, int version)
+{
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion(name, &p, static_cast<unsigned>(version), cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? p : nullptr;
+}
+
+}  // namespace
+
+// The encoder wants a current context, which a host thread has only from its first runtime call
+// that makes one on; a call that needs no workspace or copy gets here before any such.
 TmapEncodeFn tmap_encoder()
 {
-    static TmapEncodeFn fn = []() -> TmapEncodeFn {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<TmapEncodeFn>(p);
-    }();
+    static const TmapEncodeFn fn = reinterpret_cast<TmapEncodeFn>(driver_entry("cuTensorMapEncodeTiled", 12000));
+    static const auto current = reinterpret_cast<CUresult (*)(CUcontext*)>(driver_entry("cuCtxGetCurrent", 4000));
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (current != nullptr && current(&ctx) == CUDA_SUCCESS && ctx == nullptr && cudaGetDevice(&dev) == cudaSuccess)
+        cudaSetDevice(dev);
     return fn;
 }
 
@@ -1306,7 +1318,7 @@ int bsk_set_option(int key, long long value)
     case BSK_OPT_PAIR_M: ok = value >= 0 && value <= 2; break;
     case BSK_OPT_KV_KERNEL: ok = value >= 0 && value <= 2; break;
     case BSK_OPT_KV_WORKSPACE_KB: ok = value >= 0 && value <= 1LL << 40; break;
-    case BSK_OPT_LINEAR_KERNEL: ok = value >= 0 && value <= 3; break;
+    case BSK_OPT_LINEAR_KERNEL: ok = value >= 0 && value <= 2; break;
     case BSK_OPT_LINEAR_TILE: ok = value >= 0 && value <= 256 && value % 16 == 0; break;
     case BSK_OPT_WAIT_LIMIT_US: ok = value >= 0 && value <= 60000000; break;
     case BSK_OPT_NUM_SMS: ok = value >= 0 && value <= 100000; break;

@@ -90,7 +90,7 @@ void bsk_tile_coord(int t, int num_m, int num_n, int group_m, int* pid_m, int* p
  *   BSK_OPT_KV_WORKSPACE_KB  test hook: workspaces of chunk_attention and decode_attention larger
  *                            than this many KiB count as failed allocations (0: none do)
  *   BSK_OPT_LINEAR_KERNEL    kernel of the feed-forward layers' products: 0 automatic, 1 one CTA
- *                            per tile, 2 CTA pairs, 3 the CUDA-core kernel (forward, few tokens)
+ *                            per tile, 2 CTA pairs
  *   BSK_OPT_LINEAR_TILE      their accumulator columns per tile: 0 automatic, else a multiple of
  *                            16 up to 256 (taken where the kernel allows it); BSK_OPT_SPLIT_K
  *                            sets the CTAs that share a tile's k loop
@@ -144,6 +144,13 @@ int bsk_plan_gemm(int M, int N, int K, int a_mn_major, int b_mn_major, int fp8, 
 int bsk_plan_kv_attention(int cache_type, int one_token_each, int num_seqs, int num_tokens, int max_chunk,
                           int num_q_heads, int num_kv_heads, int head_dim, int max_seq_len, int window, int sinks,
                           int num_segments, int sms, int* plan);
+
+/*
+ * Test hook: the plan of a feed-forward product (mode 0: forward; 1: dx, 2: dW, 3: both) of n
+ * tokens, M output and K input features on `sms` SMs under the current options, written to
+ * plan[0..2]: CTA pairs (0/1), accumulator columns per tile, CTAs that share a tile's k loop.
+ */
+int bsk_plan_linear(int mode, int gated, int M, int K, int n, int sms, int* plan);
 
 /*
  * Test hook for the watchdog: launches one CTA that waits on a barrier that

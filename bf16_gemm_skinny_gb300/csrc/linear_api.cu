@@ -557,19 +557,20 @@ double forward_time(const LinearLaunch& g, const LinearChoice& c)
     const double filled = static_cast<double>(tiles * c.split) / static_cast<double>(slots);
     const double load = filled < 1.0 ? filled : 1.0;
     const int group = linear_group(g, c.pair, c.bn, few, !few);
-    const double turn = c.pair ? 0.128 + 0.00058 * c.bn : (group == 4 ? 0.086 : group == 2 ? 0.098 : 0.131) + 0.0011 * c.bn;
+    const double turn = c.pair ? (group == 1 ? 0.099 : 0.141) + 0.00056 * c.bn
+                               : (group == 4 ? 0.092 : group == 2 ? 0.11 : 0.135) + 0.00108 * c.bn;
     const double mma = turn > 0.00105 * c.bn ? turn : 0.00105 * c.bn;
     double bytes = c.pair ? (128 + c.bn / 2) * 128.0 : (a_rows + c.bn) * 128.0;
     const double per_sm = static_cast<double>(tiles * c.split) / g.num_sms;
     if (few && per_sm > 1.0) bytes *= c.split == 1 || per_sm > 2.0 ? 2.0 : per_sm;
-    const double block = either(mma, bytes * 7.3e-6 * (0.4 + 0.6 * load));
+    const double block = either(mma, bytes * 7.0e-6 * (0.4 + 0.6 * load));
     const double part = a_rows / 128.0;
-    double t = 4.2 + waves * static_cast<double>(div_up(kb, c.split)) * block + 0.0074 * c.bn * part;
-    if (c.split > 1) t += 1.3 + 0.0052 * c.bn * part + (waves - 1.0) * (4.5 + 0.0074 * c.bn);
-    else t += (waves - 1.0) * 0.0132 * c.bn;
+    double t = 4.04 + waves * static_cast<double>(div_up(kb, c.split)) * block + 0.0093 * c.bn * part;
+    if (c.split > 1) t += 1.36 + 0.0055 * c.bn * part + (waves - 1.0) * (4.1 + 0.0093 * c.bn);
+    else t += (waves - 1.0) * 0.0113 * c.bn;
     const double parts = g.parts;
-    const double memory = 2.0 * (parts * g.M * g.K + static_cast<double>(g.n) * (g.K + static_cast<double>(g.M))) / 5.1e6;
-    return either(t, memory + 2.5);
+    const double memory = 2.0 * (parts * g.M * g.K + static_cast<double>(g.n) * (g.K + static_cast<double>(g.M))) / 4.87e6;
+    return either(t, memory + 2.4);
 }
 
 double grad_time(const LinearLaunch& g, const LinearChoice& c)
@@ -737,6 +738,27 @@ int gated_linear_backward(
                          {type, true, {Wg, Wu}, w_stride, x, x_stride, {g, u}, gu_stride, dh, dh_stride, dx, dx_stride,
                           {dWg, dWu}, dw_stride, {dbias_g, dbias_u}, grad_type, accumulate, M, K, n, activation},
                          stream);
+}
+
+int bsk_plan_linear(int mode, int gated, int M, int K, int n, int sms, int* plan)
+{
+    if (plan == nullptr || M < 1 || K < 1 || n < 1 || sms < 2 || mode < 0 || mode > 3)
+        return fail(BSK_ERR_INVALID_ARG, "plan query: sizes and SM count must be positive (sms >= 2), plan non-NULL");
+    static uint16_t some;   // stands for a result; not written
+    bsk::LinearLaunch g;
+    g.mode = mode == 0 ? (gated ? bsk::kModeGated : bsk::kModeLinear) : bsk::kModeGrad;
+    g.parts = gated ? 2 : 1;
+    g.n = n;
+    g.M = M;
+    g.K = K;
+    g.num_sms = sms;
+    if (mode & 1) g.dx = &some;
+    if (mode & 2) g.dW[0] = g.dW[1] = &some;
+    bsk::plan_linear(g);
+    plan[0] = g.pair ? 1 : 0;
+    plan[1] = g.bn;
+    plan[2] = g.split;
+    return BSK_OK;
 }
 
 }  // extern "C"

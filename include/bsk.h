@@ -379,8 +379,8 @@ typedef enum bsk_grad_type {
  *
  * A stride or an address that is not a multiple of 16 bytes costs a copy of the
  * operand into a workspace (x, W..., dy without an activation).  The backward calls
- * take a workspace of 2 n M bytes for each dz and 4 M bytes for each bias and about
- * 4 chunks of tokens per SM.  Workspaces are allocated in stream order, from a pool of
+ * take a workspace of 2 n M bytes for each dz and 4 M bytes for each bias and chunk of
+ * tokens (of 16 tokens or more, 512 chunks at most).  Workspaces are allocated in stream order, from a pool of
  * the library's own that keeps up to 2 GiB mapped for later calls (in a stream that is
  * being captured, from the default pool).  Outputs overlap neither inputs (but for the
  * residual above) nor each other (BSK_ERR_INVALID_ARG).  Sizes are at most 2^31 - 1024.

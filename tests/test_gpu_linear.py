@@ -40,7 +40,7 @@ def defaults():
 class Rows:
     """A matrix in wider rows, `first` elements into its buffer, with a pattern around it that must stay."""
 
-    FILL = 0x5A5A
+    FILL = 0x7FFF   # a NaN in both 16-bit types
 
     def __init__(self, n, width, pad, first, dtype, values=None):
         self.n, self.width, self.stride = n, width, width + pad

@@ -1,0 +1,299 @@
+"""The feed-forward calls as a program uses them: a block's forward and backward pass together, in CUDA graphs,
+on other streams and host threads, chained without synchronisation."""
+import threading
+
+import pytest
+import torch
+
+import linear_reference as ref
+from bf16_gemm_skinny_gb300 import _native as bsk
+from bf16_gemm_skinny_gb300 import build as bsk_build
+from test_gpu_linear import accumulate, check, draw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    bsk_build.build()
+    torch.cuda.init()
+    yield bsk.load()
+    for k in bsk.OPTIONS:
+        bsk.set_option(k, 0)
+
+
+class Block:
+    """y = r + Wd (silu(x Wg^T) * (x Wu^T)) + bd: a gated feed-forward block on a residual stream, with its buffers."""
+
+    def __init__(self, n, hidden, width, t=torch.bfloat16, seed=0):
+        self.n, self.hidden, self.width, self.t = n, hidden, width, t
+        self.kind = bsk.TYPE_BF16 if t == torch.bfloat16 else bsk.TYPE_F16
+        self.x, self.r = draw(seed, n, width, t=t), draw(seed + 1, n, width, t=t)
+        self.wg, self.wu = (draw(seed + 2 + i, hidden, width, size=width ** -0.5, t=t) for i in range(2))
+        self.wd, self.bd = draw(seed + 4, width, hidden, size=hidden ** -0.5, t=t), draw(seed + 5, width, size=0.1, t=t)
+        self.dy = draw(seed + 6, n, width, size=0.1, t=t)
+        e = lambda *s, d=t: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+        self.h, self.g, self.u, self.y = e(n, hidden), e(n, hidden), e(n, hidden), e(n, width)
+        self.dh, self.dx = e(n, hidden), e(n, width)
+        self.dwd, self.dbd = e(width, hidden, d=torch.float32), e(width, d=torch.float32)
+        self.dwg, self.dwu = e(hidden, width, d=torch.float32), e(hidden, width, d=torch.float32)
+
+    def forward(self, stream=None):
+        n, m, k = self.n, self.hidden, self.width
+        bsk.gated_linear_enqueue(self.kind, self.wg, self.wu, k, self.x, k, None, None, self.h, m, self.g, self.u, m, m, k, n,
+                                 bsk.ACT_SILU, stream)
+        bsk.linear_act_enqueue(self.kind, self.wd, m, self.h, m, self.bd, self.r, k, self.y, k, None, k, k, m, n, bsk.ACT_NONE, stream)
+
+    def backward(self, accumulate=0, stream=None):
+        n, m, k = self.n, self.hidden, self.width
+        bsk.linear_act_backward_enqueue(self.kind, self.wd, m, self.h, m, None, k, self.dy, k, self.dh, m, self.dwd, m, self.dbd,
+                                        bsk.GRAD_F32, accumulate, k, m, n, bsk.ACT_NONE, stream)
+        bsk.gated_linear_backward_enqueue(self.kind, self.wg, self.wu, k, self.x, k, self.g, self.u, m, self.dh, m, self.dx, k,
+                                          self.dwg, self.dwu, k, None, None, bsk.GRAD_F32, accumulate, m, k, n, bsk.ACT_SILU, stream)
+
+    def outputs(self):
+        return [self.h, self.g, self.u, self.y, self.dh, self.dx, self.dwd, self.dbd, self.dwg, self.dwu]
+
+    def clone(self):
+        return [o.clone() for o in self.outputs()]
+
+    def clear(self):
+        for o in self.outputs():
+            o.fill_(float("nan"))
+
+
+@pytest.mark.parametrize("n,hidden,width", [(1, 256, 128), (5, 1000, 264), (150, 704, 520), (700, 1024, 512)])
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+def test_block(n, hidden, width, t):
+    """Each call's outputs against the formula in 64 bits on what the call before it left."""
+    b = Block(n, hidden, width, t)
+    b.forward()
+    b.backward()
+    bsk.stream_check()
+    d = lambda v: v.double()  # noqa: E731
+    h, g, u = ref.gated("silu", d(b.x), d(b.wg), d(b.wu))
+    eg = accumulate(width) * (d(b.x).abs() @ d(b.wg).abs().T)
+    eu = accumulate(width) * (d(b.x).abs() @ d(b.wu).abs().T)
+    a = ref.act("silu", g)[0]
+    ea = ref.SLOPE * eg + 2.0 ** -15 * a.abs()
+    check(b.h, h, a.abs() * eu + u.abs() * ea + ea * eu, t, "h")
+    y, _ = ref.linear("none", d(b.h), d(b.wd), d(b.bd), d(b.r))
+    ey = accumulate(hidden) * (d(b.h).abs() @ d(b.wd).abs().T + d(b.bd).abs() + d(b.r).abs())
+    check(b.y, y, ey, t, "y")
+    dh, dwd, dbd, _ = ref.linear_backward("none", d(b.h), d(b.wd), None, d(b.dy))
+    check(b.dh, dh, accumulate(width) * (d(b.dy).abs() @ d(b.wd).abs()), t, "dh")
+    check(b.dwd, dwd, accumulate(n) * (d(b.dy).abs().T @ d(b.h).abs()), torch.float32, "dWd")
+    check(b.dbd, dbd, accumulate(8 * n) * d(b.dy).abs().sum(0), torch.float32, "dbd")
+    dx, dwg, dwu, _, _, dg, du = ref.gated_backward("silu", d(b.x), d(b.wg), d(b.wu), d(b.g), d(b.u), d(b.dh))
+    eg = 2.0 ** -14 * (d(b.dh) * d(b.u)).abs()
+    eg = eg + ref.half_step(t) * (dg.abs() + eg) + ref.tiny(t)
+    eu = 2.0 ** -14 * du.abs()
+    eu = eu + ref.half_step(t) * (du.abs() + eu) + ref.tiny(t)
+    ex = eg @ d(b.wg).abs() + eu @ d(b.wu).abs()
+    check(b.dx, dx, ex + accumulate(2 * hidden) * ((dg.abs() + eg) @ d(b.wg).abs() + (du.abs() + eu) @ d(b.wu).abs()), t, "dx")
+    for got, want, e, z in ((b.dwg, dwg, eg, dg), (b.dwu, dwu, eu, du)):
+        check(got, want, e.T @ d(b.x).abs() + accumulate(n) * ((z.abs() + e).T @ d(b.x).abs()), torch.float32, "dW")
+
+
+def test_block_accumulates():
+    """Two backward passes with accumulate: twice the gradients (FP32 sums of equal values are exact)."""
+    b = Block(300, 512, 256)
+    b.forward()
+    b.backward()
+    once = [v.clone() for v in (b.dwd, b.dbd, b.dwg, b.dwu)]
+    b.backward(accumulate=1)
+    bsk.stream_check()
+    for v, o in zip((b.dwd, b.dbd, b.dwg, b.dwu), once):
+        assert torch.equal(v, 2 * o)
+
+
+def test_graphs():
+    """Two graphs of two blocks, with workspaces of their own (dz, sums, packed operands), replayed in turn
+    and after each other on new inputs: the bits of the eager calls."""
+    blocks = [Block(200, 520, 264), Block(90, 1003, 131, torch.float16, seed=50)]   # the second: unaligned rows
+    graphs = []
+    for b in blocks:
+        b.forward()
+        b.backward()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        side = torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=side):
+            b.forward(side)
+            b.backward(stream=side)
+        graphs.append(g)
+    for seed in (100, 200):
+        want = []
+        for b in blocks:
+            for v, s in ((b.x, 1.0), (b.r, 1.0), (b.dy, 0.1)):
+                v.copy_(draw(seed, *v.shape, size=s, t=v.dtype))
+                seed += 1
+            b.forward()
+            b.backward()
+            bsk.stream_check()
+            want.append(b.clone())
+            b.clear()
+        for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+            for i in order:
+                graphs[i].replay()
+            torch.cuda.synchronize()
+            for b, w in zip(blocks, want):
+                assert all(torch.equal(o, v) for o, v in zip(b.outputs(), w))
+                b.clear()
+
+
+def test_streams_side_by_side():
+    """Blocks on two streams at once, another being the current one: the bits of one after the other."""
+    blocks = [Block(120, 800, 256, seed=10), Block(60, 900, 320, seed=30)]
+    want = []
+    for b in blocks:
+        b.forward()
+        b.backward()
+        bsk.stream_check()
+        want.append(b.clone())
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for _ in range(20):
+        for b in blocks:
+            b.clear()
+        torch.cuda.synchronize()
+        for b, s in zip(blocks, streams):
+            b.forward(s)
+            b.backward(stream=s)
+        for s in streams:
+            bsk.stream_check(s)
+        for b, w in zip(blocks, want):
+            assert all(torch.equal(o, v) for o, v in zip(b.outputs(), w))
+
+
+def test_host_threads():
+    blocks = [Block(40 + 30 * i, 300 + 64 * i, 128 + 8 * i, seed=7 * i) for i in range(4)]
+    want = []
+    for b in blocks:
+        b.forward()
+        b.backward()
+        bsk.stream_check()
+        want.append(b.clone())
+        b.clear()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(b, w):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(30):
+                b.forward(s)
+                b.backward(stream=s)
+            bsk.stream_check(s)
+            assert all(torch.equal(o, v) for o, v in zip(b.outputs(), w))
+        except Exception as e:   # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(blocks, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
+@pytest.mark.parametrize("n", [1, 7, 130])
+def test_chain_on_one_residual_stream(n):
+    """Layer after layer without a synchronisation, each adding to the same residual stream in place: with and
+    without programmatic launches the same bits, and those of calls that wait for each other."""
+    t, hidden, width, layers = torch.bfloat16, 768, 256, 6
+    ws = [[draw(100 + 10 * i + k, *((hidden, width) if k < 2 else (width, hidden)), size=(width if k < 2 else hidden) ** -0.5)
+           for k in range(3)] for i in range(layers)]
+    x = draw(1, n, width)
+
+    def run(blocking):
+        y, h = x.clone(), torch.empty(n, hidden, dtype=t, device="cuda")
+        suffix = "" if blocking else "_enqueue"
+        for wg, wu, wd in ws:
+            getattr(bsk, "gated_linear" + suffix)(0, wg, wu, width, y, width, None, None, h, hidden, None, None, hidden, hidden, width,
+                                                  n, bsk.ACT_SILU)
+            getattr(bsk, "linear_act" + suffix)(0, wd, hidden, h, hidden, None, y, width, y, width, None, width, width, hidden, n,
+                                                bsk.ACT_NONE)
+        bsk.stream_check()
+        return y
+
+    want = run(True)
+    for _ in range(10):
+        assert torch.equal(run(False), want)
+    bsk.set_option("pdl", 1)
+    try:
+        assert torch.equal(run(False), want)
+    finally:
+        bsk.set_option("pdl", 0)
+
+
+def test_beside_the_other_calls():
+    """Between a GEMV, a GEMM and a packed GEMM in one stream (kernels with other needs of shared memory and TMEM)."""
+    b = Block(33, 640, 384)
+    w, x = draw(71, 1000, 384), draw(72, 9, 384)
+    y = torch.empty(9, 1000, dtype=torch.bfloat16, device="cuda")
+    a16 = torch.randn(300, 200, device="cuda").half()
+    c16 = torch.empty(300, 300, dtype=torch.half, device="cuda")
+
+    def run(wait):
+        for _ in range(3):
+            bsk.gemv_bf16_enqueue(w, x, y, 1000, 384, 9)
+            if wait:
+                torch.cuda.synchronize()
+            b.forward()
+            if wait:
+                torch.cuda.synchronize()
+            bsk.gemm_f16_enqueue(bsk.ROW_MAJOR, 0, 1, a16, 200, a16, 200, c16, 300, 300, 300, 200)
+            if wait:
+                torch.cuda.synchronize()
+            b.backward()
+            if wait:
+                torch.cuda.synchronize()
+        bsk.stream_check()
+        return b.clone() + [y.clone(), c16.clone()]
+
+    want = run(True)
+    for _ in range(5):
+        b.clear()
+        assert all(torch.equal(p, q) for p, q in zip(run(False), want))
+
+
+@pytest.mark.parametrize("call", ["linear_act", "gated_linear", "linear_act_backward", "gemm_f16"])
+def test_first_call_of_a_host_thread(call):
+    """A host thread whose first CUDA call is one that needs no workspace."""
+    n, m, k = 128, 256, 128
+    w, x, dy = draw(1, m, k), draw(2, n, k), draw(3, n, m)
+    y, dx = torch.empty(n, m, dtype=torch.bfloat16, device="cuda"), torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+    h16, b16 = w.half(), x.half()
+    c16 = torch.empty(n, m, dtype=torch.half, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    out = {"linear_act": y, "gated_linear": y, "linear_act_backward": dx, "gemm_f16": c16}[call]
+
+    def run():
+        if call == "linear_act":
+            bsk.linear_act_enqueue(0, w, k, x, k, None, None, m, y, m, None, m, m, k, n, bsk.ACT_RELU, stream)
+        elif call == "gated_linear":
+            bsk.gated_linear_enqueue(0, w, w, k, x, k, None, None, y, m, None, None, m, m, k, n, bsk.ACT_RELU, stream)
+        elif call == "linear_act_backward":
+            bsk.linear_act_backward_enqueue(0, w, k, x, k, None, m, dy, m, dx, k, None, k, None, 0, 0, m, k, n, bsk.ACT_NONE, stream)
+        else:
+            bsk.gemm_f16_enqueue(bsk.ROW_MAJOR, 0, 1, b16, k, h16, k, c16, m, n, m, k, stream=stream)
+
+    run()
+    bsk.stream_check()
+    want = out.clone()
+    out.zero_()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        try:
+            run()
+        except Exception as e:   # noqa: BLE001
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert not failed, failed
+    bsk.stream_check()
+    assert torch.equal(out, want)
