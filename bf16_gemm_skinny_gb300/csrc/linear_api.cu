@@ -565,12 +565,17 @@ double forward_time(const LinearLaunch& g, const LinearChoice& c)
     if (few && per_sm > 1.0) bytes *= c.split == 1 || per_sm > 2.0 ? 2.0 : per_sm;
     const double block = either(mma, bytes * 7.0e-6 * (0.4 + 0.6 * load));
     const double part = a_rows / 128.0;
-    double t = 4.04 + waves * static_cast<double>(div_up(kb, c.split)) * block + 0.0093 * c.bn * part;
-    if (c.split > 1) t += 1.36 + 0.0055 * c.bn * part + (waves - 1.0) * (4.1 + 0.0093 * c.bn);
-    else t += (waves - 1.0) * 0.0113 * c.bn;
+    // a column's share of the epilogue; kept values and rows that are not 16-byte aligned cost more
+    // (gated 333 x 2731 x 1024 with both: 13.1 us by tiles of 128, 15.1 by wider ones of CTA pairs)
+    const bool keep = g.keep[0] != nullptr;
+    const double more = (keep ? 0.011 : 0.0) + (g.ldo % 8 != 0 || (keep && g.ldk % 8 != 0) ? 0.005 : 0.0);
+    double t = 4.04 + waves * static_cast<double>(div_up(kb, c.split)) * block + (0.0093 + more) * c.bn * part;
+    const double join = c.split > 1 ? 1.36 + 0.0055 * c.bn * part : 0.0;   // (a part of it after the last operands from memory)
+    if (c.split > 1) t += 0.7 * join + (waves - 1.0) * (4.1 + 0.0093 * c.bn);
+    else t += (waves - 1.0) * (0.0113 + more) * c.bn;
     const double parts = g.parts;
     const double memory = 2.0 * (parts * g.M * g.K + static_cast<double>(g.n) * (g.K + static_cast<double>(g.M))) / 4.87e6;
-    return either(t, memory + 2.4);
+    return either(t, memory + 2.4) + 0.3 * join;
 }
 
 double grad_time(const LinearLaunch& g, const LinearChoice& c)

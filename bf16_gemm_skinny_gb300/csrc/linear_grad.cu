@@ -5,11 +5,12 @@
 //
 // One pass over the tokens: every value is read once, FP32 inside, dz rounded
 // once to the type, because it is an operand of the tensor cores' products next
-// (2^-9 of each term in BF16, 2^-12 in FP16, at random: the gradients' sums see
-// about as much as from their own rounding).  A bias gradient is the column sum
+// (2^-8 of each term at most in BF16, 2^-11 in FP16, either way: the gradients' sums
+// see about as much as from their own rounding).  A bias gradient is the column sum
 // of the unrounded dz: each thread keeps its columns' sums over its tokens, a
-// block adds its threads' in a fixed order and leaves one FP32 row, a second
-// kernel adds those rows in order.  No atomics: the same call gives the same bits.
+// block adds its threads' in a fixed order and leaves one FP32 row; the products'
+// kernel, or one of its own without products, adds those rows in order.  No
+// atomics: the same call gives the same bits.
 // Bound: HBM (6 bytes read and 4 written per value of a gated layer).
 #include <cstdio>
 

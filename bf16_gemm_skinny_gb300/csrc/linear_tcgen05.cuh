@@ -16,10 +16,11 @@
 // Neither g nor u goes through memory unless they are kept for a backward pass.
 //
 // Gradients: dx (rows are tokens, k are features) and dW (rows are features, k are
-// tokens) are tiles of one launch, the longer k loops first, so that neither waits for the other's
-// last wave.  Both read the same boxes of dz, along k or along rows.  dx of a gated
-// layer (dg Wg + du Wu) is one k loop over both sources and rounded once.  The
-// epilogue warps, idle until the first accumulator, add up the bias gradients' partial sums.
+// tokens) are tiles of one launch, the longer k loops first, so that neither waits
+// for the other's last wave.  Both read dz where it is, along k or along rows.  dx
+// of a gated layer (dg Wg + du Wu) is one k loop over both sources and rounded once.
+// The epilogue warps, idle until the first accumulator, add up the bias gradients'
+// partial sums.
 //
 // Roles (320 threads): warp 0 loads by TMA into a ring of k slices, warp 1 issues
 // the MMAs, warps 2..9 are the epilogue, overlapped with the next tile's loop by a
@@ -30,6 +31,11 @@
 // Split k (one-CTA tiles, few tiles): the CTAs of a cluster share a tile's k
 // loop; each stores its FP32 sums into the shared memory of the CTAs that finish the
 // columns, which add them up in rank order (the result does not depend on timing).
+//
+// Bound and figures (GB300, back to back): few rows, the weights from HBM (gated
+// 17408 x 5120, 1 token: 54.9 us, 6.5 TB/s); many, the MMAs and at the last the power
+// (gated 4096 x 17408 x 5120: 711 us, 2050 TFLOP/s, for seconds 830 us); between, the latency
+// of a k loop's operands from L2 (95 GB/s an SM) and of the launch (4 us).
 #pragma once
 
 #include <cstdio>
@@ -673,8 +679,8 @@ __device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, in
 }
 
 // Kinds of kernel: results row by row (forward, few rows or one narrow tile per CTA), through shared
-// memory, split k, CTA pairs.  With few rows two CTAs fit on an SM by registers and shared memory, so that the next launch's CTAs set up while this
-// one's finish; split k of a forward pass likewise.
+// memory, split k, CTA pairs.  With few rows two CTAs fit on an SM by registers and shared memory, so
+// that the next launch's CTAs set up while this one's finish; split k of a forward pass likewise.
 enum LinearKind : int { kKindDirect = 0, kKindOne = 1, kKindSplit = 2, kKindPair = 3 };
 
 template <int TYPE, int MODE, int KIND>
@@ -1460,10 +1466,11 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     ring = (ring + 1023) / 1024 * 1024;
     p.stage_at = staged ? ring : -1;
     p.ring_bytes = ring + (staged ? kLinStageBytes : 0);
-    // Split k: at most two CTAs per SM (of 256 TMEM columns at most), so that no CTA of a cluster can
-    // wait for columns that a CTA of a cluster waiting for it holds.
+    // Clusters: no CTA of one can wait for TMEM columns that a CTA of a cluster waiting for it holds.  Split k
+    // of a forward pass: at most two CTAs per SM, of 256 columns at most; the others one, by their
+    // registers; and none beside a cluster's CTA of the GEMMs (190 KB and more).
     int smem_bytes = 1024 + p.ring_bytes + kLinBarBytes;
-    if (p.split > 1 && smem_bytes < 80 * 1024) smem_bytes = 80 * 1024;
+    if (share > 1 && smem_bytes < 80 * 1024) smem_bytes = 80 * 1024;
     if (smem_bytes > kLinSmemBytes) {
         snprintf(msg, msg_len, "linear product: %d bytes of shared memory needed", smem_bytes);
         return 1;
