@@ -86,12 +86,19 @@ struct Matrix {
     long long bytes() const { return p != nullptr && rows > 0 && width > 0 ? ((rows - 1) * ld + width) * size : 0; }
 };
 
+// Whether two matrices share a byte.  Parts of the same wider rows (one distance between rows, each
+// within its own columns) share none; otherwise what lies between the first and the last row's end counts.
 bool overlap(const Matrix& a, const Matrix& b)
 {
     const long long ab = a.bytes(), bb = b.bytes();
     if (ab <= 0 || bb <= 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + static_cast<uintptr_t>(bb) && b0 < a0 + static_cast<uintptr_t>(ab);
+    if (!(a0 < b0 + static_cast<uintptr_t>(bb) && b0 < a0 + static_cast<uintptr_t>(ab))) return false;
+    const long long pitch = a.ld * a.size;
+    if (pitch != b.ld * b.size) return true;
+    const bool b_first = b0 < a0;
+    const long long apart = static_cast<long long>(b_first ? a0 - b0 : b0 - a0) % pitch;
+    return !((b_first ? b : a).width * (b_first ? b : a).size <= apart && apart + (b_first ? a : b).width * (b_first ? a : b).size <= pitch);
 }
 
 // Outputs overlap neither an input nor each other.  `same`: an input that may be

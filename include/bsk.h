@@ -380,10 +380,12 @@ typedef enum bsk_grad_type {
  * A stride or an address that is not a multiple of 16 bytes costs a copy of the
  * operand into a workspace (x, W..., dy without an activation).  The backward calls
  * take a workspace of 2 n M bytes for each dz and 4 M bytes for each bias and chunk of
- * tokens (of 16 tokens or more, 512 chunks at most).  Workspaces are allocated in stream order, from a pool of
- * the library's own that keeps up to 2 GiB mapped for later calls (in a stream that is
- * being captured, from the default pool).  Outputs overlap neither inputs (but for the
- * residual above) nor each other (BSK_ERR_INVALID_ARG).  Sizes are at most 2^31 - 1024.
+ * tokens (of 16 tokens or more, 512 chunks at most).  Workspaces are allocated in
+ * stream order, from a pool of the library's own that keeps up to 2 GiB mapped for
+ * later calls (in a stream that is being captured, from the default pool).
+ * Outputs overlap neither inputs (but for the residual above) nor each other
+ * (BSK_ERR_INVALID_ARG); different columns of the same wider rows do not overlap where
+ * their strides are the same number of bytes.  Sizes are at most 2^31 - 1024.
  * K = 0 is an empty sum, n = 0 gives zero gradients of weights and biases (or adds
  * nothing), M = 0 a dx of zeros.  Blocking; the _enqueue forms only launch.
  */

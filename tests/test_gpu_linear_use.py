@@ -297,3 +297,25 @@ def test_first_call_of_a_host_thread(call):
     assert not failed, failed
     bsk.stream_check()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n,m,k", [(3, 40, 64), (200, 264, 128), (130, 133, 100)])
+def test_results_side_by_side_in_the_same_rows(n, m, k):
+    """h, g and u as columns of one buffer, then dx beside x: the bits of separate buffers, and nothing else written."""
+    t = torch.bfloat16
+    x, wg, wu, dh = draw(1, n, k), draw(2, m, k, size=k ** -0.5), draw(3, m, k, size=k ** -0.5), draw(4, n, m)
+    sep = [torch.empty(n, m, dtype=t, device="cuda") for _ in range(3)]
+    dx = torch.empty(n, k, dtype=t, device="cuda")
+    bsk.gated_linear(0, wg, wu, k, x, k, None, None, sep[0], m, sep[1], sep[2], m, m, k, n, bsk.ACT_SILU)
+    bsk.gated_linear_backward(0, wg, wu, k, x, k, sep[1], sep[2], m, dh, m, dx, k, None, None, k, None, None, 0, 0, m, k, n, bsk.ACT_SILU)
+    row = 3 * m + 5
+    wide = torch.full((n, row), 7.0, dtype=t, device="cuda")
+    both = torch.full((n, 2 * k), 7.0, dtype=t, device="cuda")
+    both[:, :k] = x
+    bsk.gated_linear(0, wg, wu, k, both, 2 * k, None, None, wide, row, wide[:, m:], wide[:, 2 * m:], row, m, k, n, bsk.ACT_SILU)
+    bsk.gated_linear_backward(0, wg, wu, k, both, 2 * k, wide[:, m:], wide[:, 2 * m:], row, dh, m, both[:, k:], 2 * k, None, None, k,
+                              None, None, 0, 0, m, k, n, bsk.ACT_SILU)
+    for i in range(3):
+        assert torch.equal(wide[:, i * m:(i + 1) * m], sep[i])
+    assert bool((wide[:, 3 * m:] == 7.0).all())
+    assert torch.equal(both[:, :k], x) and torch.equal(both[:, k:], dx)

@@ -76,3 +76,42 @@ def test_bad_queries():
     for bad in (dict(M=0, K=1, n=1), dict(M=1, K=0, n=1), dict(M=1, K=1, n=0), dict(M=1, K=1, n=1, sms=1)):
         with pytest.raises(bsk.BskError):
             bsk.plan_linear(**bad)
+
+
+A = 1 << 24   # stands for a device address; nothing is read from it
+
+
+def gated(g, u, gu_stride, h=6 * A, h_stride=100):
+    bsk.gated_linear_enqueue(0, A, 2 * A, 64, 3 * A, 64, None, None, h, h_stride, g, u, gu_stride, 100, 64, 7, bsk.ACT_SILU, 0)
+
+
+@pytest.mark.parametrize("args,fits", [
+    (dict(g=7 * A, u=7 * A + 200, gu_stride=200), True),        # two halves of the same rows
+    (dict(g=7 * A + 200, u=7 * A, gu_stride=200), True),
+    (dict(g=7 * A, u=7 * A + 200, gu_stride=199), False),       # u's last column is g's first of the next row
+    (dict(g=7 * A, u=7 * A + 198, gu_stride=200), False),       # one column shared
+    (dict(g=7 * A, u=7 * A + 600 + 200, gu_stride=300), True),  # other rows of the same buffer
+    (dict(g=7 * A, u=7 * A + 600 + 402, gu_stride=300), False),
+    (dict(g=7 * A, u=7 * A + 200, gu_stride=300, h=7 * A + 400, h_stride=300), True),
+    (dict(g=7 * A, u=7 * A + 200, gu_stride=300, h=7 * A + 400, h_stride=301), False),   # not the same rows
+])
+def test_parts_of_the_same_rows(args, fits):
+    import torch
+
+    if fits and torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    with pytest.raises(bsk.BskError) as exc:
+        gated(**args)
+    assert (exc.value.status != 1) == fits, str(exc.value)   # what fits ends at the missing device
+
+
+def test_gradients_of_another_size_beside_each_other():
+    """FP32 weight gradients within rows that hold 16-bit values too: the same number of bytes apart."""
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    for dx, fits in ((8 * A + 256, True), (8 * A + 254, False)):   # dW: rows of 64 FP32 values, 512 bytes apart
+        with pytest.raises(bsk.BskError) as exc:
+            bsk.linear_act_backward_enqueue(0, A, 64, 2 * A, 64, None, 100, 4 * A, 100, dx, 256, 8 * A, 128, None, 0, 0, 100, 64, 7, 0, 0)
+        assert (exc.value.status != 1) == fits, str(exc.value)
