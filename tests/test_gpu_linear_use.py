@@ -319,3 +319,43 @@ def test_results_side_by_side_in_the_same_rows(n, m, k):
         assert torch.equal(wide[:, i * m:(i + 1) * m], sep[i])
     assert bool((wide[:, 3 * m:] == 7.0).all())
     assert torch.equal(both[:, :k], x) and torch.equal(both[:, k:], dx)
+
+
+def test_rows_far_apart():
+    """Rows 3 GB apart (offsets past 31 bits of elements and 32 of bytes): the bits of packed ones."""
+    n, m, k, far, t = 3, 72, 64, 1_500_000_008, torch.bfloat16
+    if torch.cuda.mem_get_info()[0] < 120e9:
+        pytest.skip("needs 120 GB")
+
+    def apart(rows, width, dtype=t, stride=far):
+        buf = torch.empty((rows - 1) * stride + width, dtype=dtype, device="cuda")
+        return buf.as_strided((rows, width), (stride, 1))
+
+    x, dh, wg, wu = draw(1, n, k), draw(2, n, m), draw(3, m, k, size=k ** -0.5), draw(4, m, k, size=k ** -0.5)
+    h, g, u = (torch.empty(n, m, dtype=t, device="cuda") for _ in range(3))
+    dx = torch.empty(n, k, dtype=t, device="cuda")
+    bsk.gated_linear(0, wg, wu, k, x, k, None, None, h, m, g, u, m, m, k, n, bsk.ACT_SILU)
+    bsk.gated_linear_backward(0, wg, wu, k, x, k, g, u, m, dh, m, dx, k, None, None, k, None, None, 0, 0, m, k, n, bsk.ACT_SILU)
+    xf, hf, gf, uf, dhf, dxf = apart(n, k), apart(n, m), apart(n, m), apart(n, m), apart(n, m), apart(n, k)
+    xf.copy_(x)
+    dhf.copy_(dh)
+    bsk.gated_linear(0, wg, wu, k, xf, far, None, None, hf, far, gf, uf, far, m, k, n, bsk.ACT_SILU)
+    bsk.gated_linear_backward(0, wg, wu, k, xf, far, gf, uf, far, dhf, far, dxf, far, None, None, k, None, None, 0, 0, m, k, n,
+                              bsk.ACT_SILU)
+    for a, b in ((hf, h), (gf, g), (uf, u), (dxf, dx)):
+        assert torch.equal(a, b)
+    # weights and their FP32 gradients: three output features
+    m = 3
+    dwg, dwu = (torch.zeros(m, k, device="cuda") for _ in range(2))
+    g3, u3, dh3, h3 = (v[:, :m].contiguous() for v in (g, u, dh, h))
+    bsk.gated_linear(0, wg, wu, k, x, k, None, None, h3, m, g3, u3, m, m, k, n, bsk.ACT_SILU)
+    bsk.gated_linear_backward(0, wg, wu, k, x, k, g3, u3, m, dh3, m, dx, k, dwg, dwu, k, None, None, 0, 0, m, k, n, bsk.ACT_SILU)
+    del hf, gf, uf, dxf, xf, dhf
+    wgf, wuf, dwgf, dwuf = apart(m, k), apart(m, k), apart(m, k, torch.float32), apart(m, k, torch.float32)
+    wgf.copy_(wg[:m])
+    wuf.copy_(wu[:m])
+    dx2, h2 = torch.empty_like(dx), torch.empty_like(h3)
+    bsk.gated_linear(0, wgf, wuf, far, x, k, None, None, h2, m, None, None, m, m, k, n, bsk.ACT_SILU)
+    bsk.gated_linear_backward(0, wgf, wuf, far, x, k, g3, u3, m, dh3, m, dx2, k, dwgf, dwuf, far, None, None, 0, 0, m, k, n, bsk.ACT_SILU)
+    for a, b in ((h2, h3), (dx2, dx), (dwgf, dwg), (dwuf, dwu)):
+        assert torch.equal(a, b)
