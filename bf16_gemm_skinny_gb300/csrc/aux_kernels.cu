@@ -39,6 +39,10 @@ struct PackJob {
     unsigned blocks;           // CTAs working on this job
 };
 
+struct PackJobs {
+    PackJob j[kPackJobs];
+};
+
 constexpr int kPackThreads = 256;                // warp 0: producer (one lane); warps 1..7: consumers
 constexpr int kPackConsumers = kPackThreads - 32;
 constexpr int kPackBufs = 6;                     // pieces in flight per CTA
@@ -48,8 +52,8 @@ constexpr int kPackSmem = kPackBufs * kPackBufBytes + 2 * kPackBufs * 8 + 16;
 constexpr int kPackCtasPerSm = 4;
 constexpr int kSitePack = 0x20;                  // wait site reported on a timeout
 
-// dst line l = src line l, byte for byte, for up to two operands in one launch
-// (the first j0.blocks CTAs take job 0, the rest job 1).  The TMA needs
+// dst line l = src line l, byte for byte, for up to three operands in one launch
+// (the first jobs' CTAs in turn).  The TMA needs
 // 16-byte aligned bases and leading dimensions; the pack gives unaligned
 // operands that shape in a workspace without touching the caller's buffers
 // ("MTT S4000 GEMM 优化中的分块、尾处理与并发实战复盘", section 1: inputs may not be modified).
@@ -73,7 +77,7 @@ constexpr int kSitePack = 0x20;                  // wait site reported on a time
 // bounded; on a timeout the producer waits for its copies in flight before the
 // CTA exits.
 __global__ void __launch_bounds__(kPackThreads, kPackCtasPerSm)
-    pack_kernel(PackJob j0, PackJob j1, int* status, unsigned long long limit_ns)
+    pack_kernel(const __grid_constant__ PackJobs jobs, int* status, unsigned long long limit_ns)
 {
     extern __shared__ __align__(128) uint8_t pack_smem[];
     uint8_t* const bufs = pack_smem;
@@ -92,9 +96,10 @@ __global__ void __launch_bounds__(kPackThreads, kPackCtasPerSm)
     __syncthreads();
     griddep_wait();               // the source may be the previous kernel's output
     griddep_launch_dependents();  // the GEMM's prologue may start; it waits for this grid's completion
-    const bool second = blockIdx.x >= j0.blocks;
-    const PackJob& j = second ? j1 : j0;
-    const long long b = second ? blockIdx.x - j0.blocks : blockIdx.x;
+    int which = 0;
+    long long b = blockIdx.x;
+    while (which < kPackJobs - 1 && b >= jobs.j[which].blocks) b -= jobs.j[which++].blocks;
+    const PackJob j = jobs.j[which];
     const long long u0 = j.units * b / j.blocks;
     const long long n = j.units * (b + 1) / j.blocks - u0;
 
@@ -246,13 +251,14 @@ int preload_aux_kernels(char* msg, size_t msg_len)
 int launch_pack(const PackCopy* copies, int n, int sms, bool pdl, int* status, unsigned long long limit_ns,
                 cudaStream_t stream, char* msg, size_t msg_len)
 {
-    PackJob jobs[2] = {};
+    PackJobs all = {};
+    PackJob* const jobs = all.j;
     int nj = 0;
     for (int i = 0; i < n; ++i) {
         const PackCopy& c = copies[i];
         if (c.line_bytes <= 0 || c.lines <= 0) continue;
-        if (nj == 2) {
-            snprintf(msg, msg_len, "pack: at most two copies per launch");
+        if (nj == kPackJobs) {
+            snprintf(msg, msg_len, "pack: at most %d copies per launch", kPackJobs);
             return 1;
         }
         if ((reinterpret_cast<uintptr_t>(c.dst) & 15u) != 0 || (c.ld_dst & 15) != 0 ||
@@ -275,22 +281,24 @@ int launch_pack(const PackCopy* copies, int n, int sms, bool pdl, int* status, u
     // persistent grid, split between the jobs by their bytes (at least one CTA
     // each, no more CTAs than units)
     const unsigned long long total = static_cast<unsigned long long>(sms > 0 ? sms : 1) * kPackCtasPerSm;
-    const double w0 = static_cast<double>(jobs[0].line_bytes) * static_cast<double>(jobs[0].units / jobs[0].pieces);
-    const double w1 = nj > 1 ? static_cast<double>(jobs[1].line_bytes) * static_cast<double>(jobs[1].units / jobs[1].pieces)
-                             : 0.0;
-    unsigned long long b0 = nj > 1 ? static_cast<unsigned long long>(static_cast<double>(total) * w0 / (w0 + w1) + 0.5)
-                                   : total;
-    if (b0 < 1) b0 = 1;
-    unsigned long long b1 = nj > 1 ? (total > b0 ? total - b0 : 1ull) : 0ull;
-    b0 = std::min<unsigned long long>(b0, static_cast<unsigned long long>(jobs[0].units));
-    b1 = std::min<unsigned long long>(b1, nj > 1 ? static_cast<unsigned long long>(jobs[1].units) : 0ull);
-    jobs[0].blocks = static_cast<unsigned>(b0);
-    jobs[1].blocks = static_cast<unsigned>(b1);
+    double left = 0.0;   // bytes of the jobs not yet given their CTAs
+    auto bytes = [](const PackJob& j) { return static_cast<double>(j.line_bytes) * static_cast<double>(j.units / j.pieces); };
+    for (int i = 0; i < nj; ++i) left += bytes(jobs[i]);
+    unsigned long long ctas = total, grid = 0;
+    for (int i = 0; i < nj; ++i) {
+        unsigned long long n_ctas = i + 1 < nj ? static_cast<unsigned long long>(static_cast<double>(ctas) * bytes(jobs[i]) / left + 0.5) : ctas;
+        if (n_ctas < 1) n_ctas = 1;
+        left -= bytes(jobs[i]);
+        ctas = ctas > n_ctas ? ctas - n_ctas : 1ull;
+        n_ctas = std::min<unsigned long long>(n_ctas, static_cast<unsigned long long>(jobs[i].units));
+        jobs[i].blocks = static_cast<unsigned>(n_ctas);
+        grid += n_ctas;
+    }
     static SmemOptIn smem_opt;
     cudaError_t e = smem_opt.ensure(reinterpret_cast<const void*>(pack_kernel), kPackSmem);
     if (e == cudaSuccess)
-        e = launch_kernel(pack_kernel, dim3(static_cast<unsigned>(b0 + b1)), dim3(kPackThreads),
-                          static_cast<size_t>(kPackSmem), stream, pdl, jobs[0], jobs[1], status, limit_ns);
+        e = launch_kernel(pack_kernel, dim3(static_cast<unsigned>(grid)), dim3(kPackThreads),
+                          static_cast<size_t>(kPackSmem), stream, pdl, all, status, limit_ns);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "pack launch failed: %s", cudaGetErrorString(e));
         return 1;

@@ -205,7 +205,9 @@ struct PackCopy {
     long long lines;
 };
 
-// Enqueues the n (at most two) copies in one launch on `stream`, as a
+constexpr int kPackJobs = 3;
+
+// Enqueues the n (at most kPackJobs) copies in one launch on `stream`, as a
 // programmatic dependent of the kernel before it when pdl is set.  A wait that
 // gives up after limit_ns records a timeout in `status`.  The destination's
 // leading dimension must be a multiple of 16 bytes and at least line_bytes

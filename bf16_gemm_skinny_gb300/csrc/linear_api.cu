@@ -167,21 +167,17 @@ class Packer {
     int run(int sms, bool pdl, int* status, unsigned long long limit_ns, cudaStream_t s)
     {
         char msg[256] = "";
-        for (int i = 0; i < n_; i += 2) {
-            bsk::PackCopy c[2];
-            const int n = n_ - i < 2 ? 1 : 2;
-            for (int j = 0; j < n; ++j) {
-                const Item& t = items_[i + j];
-                c[j] = {*t.p, *t.ld * 2, ws_.at(t.offset), t.padded * 2, t.width * 2, t.rows};
-            }
-            if (bsk::launch_pack(c, n, sms, pdl, status, limit_ns, s, msg, sizeof(msg)))
-                return fail(BSK_ERR_CUDA, "%s", msg);
-            for (int j = 0; j < n; ++j) {
-                const Item& t = items_[i + j];
-                *t.p = ws_.at(t.offset);
-            }
+        bsk::PackCopy c[kMost];
+        for (int i = 0; i < n_; ++i) {
+            const Item& t = items_[i];
+            c[i] = {*t.p, *t.ld * 2, ws_.at(t.offset), t.padded * 2, t.width * 2, t.rows};
         }
-        for (int i = 0; i < n_; ++i) *items_[i].ld = items_[i].padded;   // (weights share one stride: set last)
+        if (n_ > 0 && bsk::launch_pack(c, n_, sms, pdl, status, limit_ns, s, msg, sizeof(msg)))
+            return fail(BSK_ERR_CUDA, "%s", msg);
+        for (int i = 0; i < n_; ++i) {   // (weights share one stride: set after all were read)
+            *items_[i].p = ws_.at(items_[i].offset);
+            *items_[i].ld = items_[i].padded;
+        }
         return BSK_OK;
     }
 
@@ -193,7 +189,8 @@ class Packer {
         size_t offset;
     };
     Workspace& ws_;
-    Item items_[4];
+    static constexpr int kMost = bsk::kPackJobs;   // x and both weights, or x, W and dy
+    Item items_[kMost];
     int n_ = 0;
 };
 
