@@ -428,10 +428,10 @@ __device__ __noinline__ void block_move_elements_call(uint8_t* buf, E* g, long l
 
 // Whole warp: rows [0, rows) x n elements between the buffer and memory (first element at `g`, rows ld
 // elements apart).
-// (FLIGHT: 16-byte accesses of a lane in flight; 2: few, beside a tile in registers.  There the stores of
-// unaligned rows go by eight rows all the same, dW of 187 x 7695 x 2339 86 -> 64 us, at 0.5% on aligned
-// ones; the loads, when all of the tile is still in registers, by one.)
-template <typename E, bool LOAD, int FLIGHT, bool INLINE>
+// (FLIGHT: 16-byte accesses of a lane in flight; 2: few, beside a tile in registers.  There unaligned
+// rows are stored by eight all the same, and loaded, when all of the tile is still in registers, one by
+// one.  ANY: not all is whole aligned 16-byte units.)
+template <typename E, bool LOAD, int FLIGHT, bool INLINE, bool ANY = true>
 __device__ __forceinline__ void block_move(uint8_t* buf, E* g, long long ld, int rows, int n, bool vec)
 {
     constexpr int kPer = 16 / static_cast<int>(sizeof(E));
@@ -458,7 +458,7 @@ __device__ __forceinline__ void block_move(uint8_t* buf, E* g, long long ld, int
     } else if constexpr (FLIGHT == 8) {
         if constexpr (INLINE) block_move_elements<E, LOAD, 8>(buf, g, ld, rows, n);
         else block_move_elements_call<E, LOAD>(buf, g, ld, rows, n);
-    } else {
+    } else if constexpr (ANY) {
         block_move_elements<E, LOAD, LOAD ? 1 : 8>(buf, g, ld, rows, n);
     }
     __syncwarp();
@@ -554,7 +554,7 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, const Linear
 }
 
 // Gradients: a warp's columns of a tile, 16 * i from c0 in sum[i], n of them there.
-template <int TYPE>
+template <int TYPE, bool ANY>
 __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, float (&sum)[8][kCh], int src, long long row0,
                                             int rows, int c0, int n)
 {
@@ -566,7 +566,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
             const int left = n - 32 * g < 32 ? n - 32 * g : 32;
             if (left > 0) {
                 float* o = static_cast<float*>(job.out[src]) + row0 * job.ldo + c0 + 32 * g;
-                if (acc) block_move<float, true, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
+                if (acc) block_move<float, true, 2, true, ANY>(buf, o, job.ldo, rows, left, job.vec_out);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     float4 v = make_float4(sum[2 * g + q / 4][q % 4 * 4], sum[2 * g + q / 4][q % 4 * 4 + 1],
@@ -579,7 +579,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
                     *at = v;
                 }
                 __syncwarp();
-                block_move<float, false, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
+                block_move<float, false, 2, true, ANY>(buf, o, job.ldo, rows, left, job.vec_out);
             }
         }
     } else {
@@ -588,7 +588,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
             const int left = n - 64 * g < 64 ? n - 64 * g : 64;
             if (left > 0) {
                 uint16_t* o = static_cast<uint16_t*>(job.out[src]) + row0 * job.ldo + c0 + 64 * g;
-                if (acc) block_move<uint16_t, true, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
+                if (acc) block_move<uint16_t, true, 2, true, ANY>(buf, o, job.ldo, rows, left, job.vec_out);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (acc) {
@@ -600,7 +600,7 @@ __device__ __forceinline__ void finish_sums(const LinearJob& job, uint8_t* buf, 
                     block_put16<TYPE, kCh>(buf, lane, 2 * q, sum[4 * g + q]);
                 }
                 __syncwarp();
-                block_move<uint16_t, false, 2, true>(buf, o, job.ldo, rows, left, job.vec_out);
+                block_move<uint16_t, false, 2, true, ANY>(buf, o, job.ldo, rows, left, job.vec_out);
             }
         }
     }
@@ -673,9 +673,12 @@ __device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, in
 // Kinds of kernel: results row by row (forward, few rows or one narrow tile per CTA), through shared
 // memory, split k, CTA pairs.  With few rows two CTAs fit on an SM by registers and shared memory, so
 // that the next launch's CTAs set up while this one's finish; split k of a forward pass likewise.
+// ANY, gradients: results of any alignment and width.  Without them the code for unaligned rows costs no
+// registers (spills of 40 instead of 220 bytes; gated backward 4096 x 17408 x 5120 1% faster), with
+// it they are stored by eight rows (linear backward 187 x 7695 x 2339 64 us, row by row 86).
 enum LinearKind : int { kKindDirect = 0, kKindOne = 1, kKindSplit = 2, kKindPair = 3 };
 
-template <int TYPE, int MODE, int KIND>
+template <int TYPE, int MODE, int KIND, bool ANY>
 __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == kKindSplit && MODE != kModeGrad) ? 2 : 1)
     linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearParams p)
 {
@@ -1053,7 +1056,7 @@ __global__ void __launch_bounds__(kLinThreads, KIND == kKindDirect || (KIND == k
                         add_segments(sum, job, kb_begin, kb_end, any);
                         if (!ok) break;
                         if (any)
-                            finish_sums<TYPE>(job, staging, sum, src, m0, job.rows - m0 < 32 ? job.rows - m0 : 32, n0 + c_half,
+                            finish_sums<TYPE, ANY>(job, staging, sum, src, m0, job.rows - m0 < 32 ? job.rows - m0 : 32, n0 + c_half,
                                               width - c_half < p.bn / 2 ? width - c_half : p.bn / 2);
                     } else {
                         // what the epilogue reads from memory, on its way while the k loop runs
@@ -1507,22 +1510,31 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     }
     if (!ok) return 1;
 
-    auto kern = linear_kernel<TYPE, MODE, PAIR ? kKindPair : kKindOne>;
-    int kind = PAIR ? kKindPair : kKindOne;
+    constexpr int kWhole = PAIR ? kKindPair : kKindOne;
+    bool any = true;
+    if constexpr (kGrad) any = g.K % 8 != 0 || (p.job[0].num_tiles > 0 && !p.job[0].vec_out) || (p.job[1].num_tiles > 0 && !p.job[1].vec_out);
+    auto kern = linear_kernel<TYPE, MODE, kWhole, true>;
+    int kind = kWhole;
+    if constexpr (kGrad) {
+        if (!any) kern = linear_kernel<TYPE, MODE, kWhole, false>;
+    }
     if constexpr (!PAIR) {
         if (p.split > 1) {
-            kern = linear_kernel<TYPE, MODE, kKindSplit>;
+            kern = linear_kernel<TYPE, MODE, kKindSplit, true>;
             kind = kKindSplit;
+            if constexpr (kGrad) {
+                if (!any) kern = linear_kernel<TYPE, MODE, kKindSplit, false>;
+            }
         }
         if constexpr (!kGrad) {
             if (p.split == 1 && direct) {
-                kern = linear_kernel<TYPE, MODE, kKindDirect>;
+                kern = linear_kernel<TYPE, MODE, kKindDirect, true>;
                 kind = kKindDirect;
             }
         }
     }
-    static SmemOptIn smem_opt[4];
-    cudaError_t e = smem_opt[kind].ensure(reinterpret_cast<const void*>(kern), kLinSmemBytes);
+    static SmemOptIn smem_opt[8];
+    cudaError_t e = smem_opt[kind + (any ? 4 : 0)].ensure(reinterpret_cast<const void*>(kern), kLinSmemBytes);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         return 1;
