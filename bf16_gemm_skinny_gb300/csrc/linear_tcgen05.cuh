@@ -33,8 +33,8 @@
 // columns, which add them up in rank order (the result does not depend on timing).
 //
 // Bound and figures (GB300, back to back): few rows, the weights from HBM (gated
-// 17408 x 5120, 1 token: 54.9 us, 6.5 TB/s); many, the MMAs and at the last the power
-// (gated 4096 x 17408 x 5120: 711 us, 2050 TFLOP/s, for seconds 830 us); between, the latency
+// 17408 x 5120, 1 token: 53.8 us, 6.6 TB/s); many, the MMAs and at the last the power
+// (gated 4096 x 17408 x 5120: 704 us, 2070 TFLOP/s, for seconds 826 us); between, the latency
 // of a k loop's operands from L2 (95 GB/s an SM) and of the launch (4 us).
 #pragma once
 

@@ -9,6 +9,7 @@ import linear_reference as ref
 from bf16_gemm_skinny_gb300 import _native as bsk
 from bf16_gemm_skinny_gb300 import build as bsk_build
 from test_gpu_linear import accumulate, check, draw
+from test_gpu_linear_grad import backward
 
 pytestmark = pytest.mark.gpu
 
@@ -359,3 +360,19 @@ def test_rows_far_apart():
     bsk.gated_linear_backward(0, wgf, wuf, far, x, k, g3, u3, m, dh3, m, dx2, k, dwgf, dwuf, far, None, None, 0, 0, m, k, n, bsk.ACT_SILU)
     for a, b in ((h2, h3), (dx2, dx), (dwgf, dwg), (dwuf, dwu)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,m,k", [(90, 136, 259), (200, 300, 260), (40, 1000, 67), (1000, 72, 515)])
+@pytest.mark.parametrize("accumulate_into", [False, True])
+def test_gradients_of_odd_width_in_aligned_rows(n, m, k, accumulate_into):
+    """Rows 16-byte aligned, their length not whole 16-byte units: what lies between them stays (checked in backward)."""
+    to8 = lambda v: -v % 8  # noqa: E731
+    pads = (to8(k), to8(k), to8(m), to8(m), to8(k), to8(k))
+    for gated in (False, True):
+        for kernel in (0, 1, 2):
+            bsk.set_option("linear_kernel", kernel)
+            try:
+                backward(gated, n, m, k, pads=pads, accumulate_into=accumulate_into)
+                backward(gated, n, m, k, "f16", "gelu", f32=False, pads=pads, accumulate_into=accumulate_into)
+            finally:
+                bsk.set_option("linear_kernel", 0)
