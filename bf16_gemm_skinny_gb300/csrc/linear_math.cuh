@@ -164,8 +164,9 @@ __device__ __forceinline__ void act_values(float (&z)[N], float (&slope)[N])
                 const float s = r[i];
                 if constexpr (SLOPE && ACT == kActSilu) slope[i] = s * fmaf(z[i], 1.f - s, 1.f);
                 if constexpr (SLOPE && ACT == kActGeluTanh) {
-                    // beyond 16 s is 0 or 1 and the second term 0; the clamp keeps 0 * infinity out of it
-                    const float c = fminf(fmaxf(z[i], -16.f), 16.f);
+                    // beyond 16 s is 0 or 1 and the second term 0; the clamp keeps 0 * infinity out of it (and a
+                    // NaN in, which fminf would take away)
+                    const float c = z[i] > 16.f ? 16.f : z[i] < -16.f ? -16.f : z[i];
                     slope[i] = fmaf(c * s * (1.f - s), fmaf(3.f * kGeluC2 * kGeluA * c, c, kGeluC2), s);
                 }
                 z[i] *= s;

@@ -376,3 +376,50 @@ def test_gradients_of_odd_width_in_aligned_rows(n, m, k, accumulate_into):
                 backward(gated, n, m, k, "f16", "gelu", f32=False, pads=pads, accumulate_into=accumulate_into)
             finally:
                 bsk.set_option("linear_kernel", 0)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("n", [2, 70, 300])
+def test_one_bad_value_reaches_only_what_it_enters(n, act, bad):
+    m, k, j, r, c = 136, 72, 37, 1, 50
+    kind = dict(none=0, relu=1, gelu=2, gelu_tanh=3, silu=4)[act]
+    t = torch.bfloat16
+    x, w, w2, dy = draw(1, n, k), draw(2, m, k, size=k ** -0.5), draw(3, m, k, size=k ** -0.5), draw(4, n, m)
+    x[:, c] = x[:, c].abs() + 0.5
+    z, u = draw(5, n, m), draw(6, n, m)
+
+    def forward(wx):
+        y, h = (torch.empty(n, m, dtype=t, device="cuda") for _ in range(2))
+        bsk.linear_act(0, wx, k, x, k, None, None, m, y, m, None, m, m, k, n, kind)
+        bsk.gated_linear(0, wx, w2, k, x, k, None, None, h, m, None, None, m, m, k, n, kind)
+        return y, h
+
+    def backward_of(zx):
+        dx, dgx = (torch.empty(n, k, dtype=t, device="cuda") for _ in range(2))
+        dw, dg, du = (torch.empty(m, k, device="cuda") for _ in range(3))
+        db, dbg, dbu = (torch.empty(m, device="cuda") for _ in range(3))
+        bsk.linear_act_backward(0, w, k, x, k, zx, m, dy, m, dx, k, dw, k, db, 0, 0, m, k, n, kind)
+        bsk.gated_linear_backward(0, w, w2, k, x, k, zx, u, m, dy, m, dgx, k, dg, du, k, dbg, dbu, 0, 0, m, k, n, kind)
+        return (dx, dgx), (dw, db, dg, dbg, du, dbu)
+
+    wx, zx = w.clone(), z.clone()
+    wx[j, c] = bad
+    zx[r, j] = bad
+    # The activations take one reciprocal for the product of four values (of columns 4 i to 4 i + 3), each a
+    # number from 1 to 2^30 whatever its z: the three beside another z may so have other last bits (five
+    # roundings), but stay finite.  All other columns keep their bits.
+    others = [i for i in range(m) if i // 4 != j // 4]
+    beside = [i for i in range(m) if i // 4 == j // 4 and i != j]
+    for got, want in zip(forward(wx), forward(w)):
+        assert torch.equal(got[:, others], want[:, others]) and torch.isfinite(got[:, beside]).all()
+        if bad != bad:
+            assert torch.isnan(got[:, j]).all()
+    rows = [i for i in range(n) if i != r]
+    for got, want in zip(backward_of(zx), backward_of(z)):
+        for a, b in zip(got, want):
+            keep = rows if a.shape[0] == n and a.dtype == t else others
+            assert torch.equal(a[keep], b[keep])
+            assert keep is rows or torch.isfinite(a[beside]).all()
+            if bad != bad and act != "none":
+                assert torch.isnan(a[r] if keep is rows else a[j]).any()
