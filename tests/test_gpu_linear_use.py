@@ -1,5 +1,7 @@
 """The feed-forward calls as a program uses them: a block's forward and backward pass together, in CUDA graphs,
 on other streams and host threads, chained without synchronisation."""
+import math
+import random
 import threading
 
 import pytest
@@ -8,7 +10,7 @@ import torch
 import linear_reference as ref
 from bf16_gemm_skinny_gb300 import _native as bsk
 from bf16_gemm_skinny_gb300 import build as bsk_build
-from test_gpu_linear import accumulate, check, draw
+from test_gpu_linear import accumulate, check, draw, forward
 from test_gpu_linear_grad import backward
 
 pytestmark = pytest.mark.gpu
@@ -423,3 +425,41 @@ def test_one_bad_value_reaches_only_what_it_enters(n, act, bad):
             assert keep is rows or torch.isfinite(a[beside]).all()
             if bad != bad and act != "none":
                 assert torch.isnan(a[r] if keep is rows else a[j]).any()
+
+
+@pytest.mark.parametrize("kernel,split", [(0, 0), (1, 1), (1, 4), (2, 0)])
+@pytest.mark.parametrize("n,m,k", [(6, 131, 1032), (70, 520, 520), (300, 133, 1100)])
+def test_residual_in_place_in_every_kernel(kernel, split, n, m, k):
+    bsk.set_option("linear_kernel", kernel)
+    bsk.set_option("split_k", split)
+    try:
+        for keep in (False, True):
+            a = forward(False, n, m, k, residual=True, inplace=True, keep=keep)
+            assert torch.equal(a, forward(False, n, m, k, residual=True, keep=keep))
+    finally:
+        bsk.set_option("linear_kernel", 0)
+        bsk.set_option("split_k", 0)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_calls(seed):
+    rng = random.Random(seed)
+    log = lambda lo, hi: int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))  # noqa: E731
+    options = ("linear_kernel", "linear_tile", "split_k", "pdl", "group_m")
+    try:
+        for _ in range(12):
+            for name, values in zip(options, ((0, 0, 1, 2), (0, 0, 32, 64, 96, 128, 192, 256), (0, 0, 1, 2, 4, 8), (0, 0, 1), (0, 1, 3))):
+                bsk.set_option(name, rng.choice(values))
+            n, m, k = log(1, 900), log(1, 1200), log(1, 1500)
+            pads = tuple(rng.choice((0, 0, 1, 3, 8, 64)) for _ in range(6))
+            first = rng.choice((0, 0, 8, 1))
+            kind, act, gated = rng.choice(("bf16", "f16")), rng.choice(ref.ACTS), rng.random() < 0.5
+            if rng.random() < 0.5:
+                forward(gated, n, m, k, kind, act, bias=rng.random() < 0.5, residual=not gated and rng.random() < 0.5,
+                        keep=rng.random() < 0.5, pads=pads[:4], first=first, seed=seed)
+            else:
+                backward(gated, n, m, k, kind, act, f32=rng.random() < 0.5, accumulate_into=rng.random() < 0.5, pads=pads, first=first,
+                         seed=seed)
+    finally:
+        for name in options:
+            bsk.set_option(name, 0)
