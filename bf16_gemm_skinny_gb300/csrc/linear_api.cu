@@ -101,13 +101,14 @@ bool overlap(const Matrix& a, const Matrix& b)
     return !((b_first ? b : a).width * (b_first ? b : a).size <= apart && apart + (b_first ? a : b).width * (b_first ? a : b).size <= pitch);
 }
 
-// Outputs overlap neither an input nor each other.  `same`: an input that may be
-// the first output itself (same address and stride), or nullptr.
-int check_overlaps(const Matrix* out, int outs, const Matrix* in, int ins, const void* same = nullptr)
+// Outputs overlap neither an input nor each other.  `same`: index of the one input that may be
+// the first output itself (same address and stride), or -1.  An index and not an address: another operand
+// may lie where that input does, and is read while the output is written.
+int check_overlaps(const Matrix* out, int outs, const Matrix* in, int ins, int same = -1)
 {
     for (int i = 0; i < outs; ++i) {
         for (int j = 0; j < ins; ++j) {
-            if (i == 0 && same != nullptr && in[j].p == same && out[0].p == same && in[j].ld == out[0].ld) continue;
+            if (i == 0 && j == same && in[j].p == out[0].p && in[j].ld == out[0].ld) continue;
             if (overlap(out[i], in[j])) return fail(BSK_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, in[j].name);
         }
         for (int j = 0; j < i; ++j)
@@ -269,7 +270,7 @@ int enqueue_forward(const ForwardArgs& a, void* stream, bool* launched)
             if (in[i].p == nullptr) return fail(BSK_ERR_INVALID_ARG, "%s is NULL", in[i].name);
     if (a.gated && (a.keep[0] == nullptr) != (a.keep[1] == nullptr))
         return fail(BSK_ERR_INVALID_ARG, "g and u are kept together: pass both or neither");
-    if ((st = check_overlaps(out, 3, in, 6, a.residual)) != BSK_OK) return st;
+    if ((st = check_overlaps(out, 3, in, 6, 5)) != BSK_OK) return st;   // (the residual)
     if (((a.M + 15LL) / 16) * ((a.n + 127LL) / 128) > INT_MAX) return fail(BSK_ERR_INVALID_ARG, "problem too large");
 
     Context ctx;

@@ -77,6 +77,19 @@ def test_the_residual_may_be_the_output():
     assert exc.value.status != 1, str(exc.value)
 
 
+@pytest.mark.parametrize("change", [
+    dict(x=5 * A, x_stride=100),                                  # y += act(y W^T): tiles would store over rows still read
+    dict(x=5 * A, x_stride=100, K=100, w_stride=100),             # the same of a square layer
+    dict(W=5 * A, w_stride=100), dict(W=5 * A, w_stride=100, n=100),
+    dict(bias=5 * A), dict(bias=5 * A, M=99, residual_stride=100),   # a vector of M, its "stride" M + 1 that of y's rows
+    dict(x=5 * A, x_stride=100, n=1), dict(z=5 * A), dict(x=5 * A, x_stride=100, residual_stride=101)], ids=str)
+@pytest.mark.parametrize("form", ["", "_enqueue"])
+def test_no_other_operand_may_be_the_output_beside_the_residual(change, form):
+    with pytest.raises(bsk.BskError) as exc:
+        getattr(bsk, "linear_act" + form)(**{**LINEAR, "residual": 5 * A, **change}, stream=0)
+    assert exc.value.status == 1 and "overlaps" in str(exc.value), str(exc.value)
+
+
 def test_nothing_to_do_is_no_error():
     for change in (dict(M=0), dict(n=0)):
         bsk.linear_act(**{**LINEAR, "W": None, "x": None, "y": None, **change}, stream=0)
