@@ -55,11 +55,15 @@ constexpr int kLinMaxStages = 24;
 constexpr int kCh = 16;                          // columns per epilogue step: 32 bytes of 16-bit values
 constexpr int kBlockBytes = 128;                 // a row of a warp's staging buffer: one line of memory
 static_assert(kLinStageBytes == kLinEpiWarps * 32 * kBlockBytes, "staging buffers");
-// FP32 weight gradients: k-blocks summed in an accumulator before they are added to
-// FP32 registers.  A tensor-core accumulation cuts each of its sums (toward zero), so
-// an error grows with their number: dW over 8192 tokens came out 2e-5 off, in segments of 768
-// tokens 7e-7, as much as FP32 arithmetic gives.
-constexpr int kSegmentKb = 12;
+// Gradients: k-blocks summed in an accumulator before they are added to FP32 registers.  A
+// tensor-core accumulation cuts each of its sums (toward zero), so an error grows with their number: FP32 dW
+// over 8192 tokens came out 2e-5 off, in segments of 768 tokens 7e-7, as much as FP32 arithmetic gives.  Results
+// of 16 bits take longer segments: with operands of one sign the error is 2.5e-5 of the sum for 4096 terms, a
+// twentieth of FP16's half step, and in one accumulation passed it (400,003 tokens: 2.5e-3).  That costs
+// nothing: segments of 64, 128, 256 k-blocks and none took 290 us each for the gradients of 32768 x 2048 x 2048,
+// 432, 434, 440 and 436 for the gated ones of 16384 x 4096 x 1024.
+constexpr int kSegmentKb32 = 12;
+constexpr int kSegmentKb16 = 64;
 
 enum LinearWaitSite {
     kSiteLinEmpty = 0x30,
@@ -76,7 +80,7 @@ struct LinearJob {
     int num_m, num_m1;        // tile rows in all, of the first source (weight gradient)
     int num_n, num_tiles;
     int a_mn;                 // A read along its rows (weight gradient)
-    int seg_kb;               // k-blocks per segment
+    int seg_kb;               // k-blocks per segment (a multiple of a turn's, or all)
     uint32_t idesc;
     void* out[2];
     long long ldo;
@@ -1340,6 +1344,7 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
             j.idesc = idesc_f16(TYPE == kTypeBF16, false, true, kTileRows, g.bn);
             j.out[0] = g.dx;
             j.ldo = g.ld_dx;
+            if (j.seg_kb > kSegmentKb16) j.seg_kb = kSegmentKb16;
             j.vec_out = lin_aligned16(g.dx, g.ld_dx * 2);
         }
         if (g.dW[0] != nullptr) {
@@ -1352,7 +1357,7 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
             j.ldo = g.ld_dw;
             j.out_f32 = g.grad_f32;
             j.accumulate = g.accumulate;
-            if (g.grad_f32) j.seg_kb = kSegmentKb;
+            if (g.grad_f32 || j.seg_kb > kSegmentKb16) j.seg_kb = g.grad_f32 ? kSegmentKb32 : kSegmentKb16;
             j.vec_out = lin_aligned16(g.dW[0], g.ld_dw * (g.grad_f32 ? 4 : 2)) && lin_aligned16(g.dW[1], 0);
         }
         if (jobs == 2 && p.job[1].kbs * p.job[1].k_sources > p.job[0].kbs * p.job[0].k_sources) {
