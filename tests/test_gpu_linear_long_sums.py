@@ -14,7 +14,7 @@ from test_gpu_linear import KIND, check
 
 pytestmark = pytest.mark.gpu
 
-SEGMENT_16 = 64 * 64   # terms in a segment
+SEGMENT_32, SEGMENT_16 = 12 * 64, 64 * 64   # terms in a segment: FP32 weight gradients, 16-bit results
 KERNELS = [(0, 0), (1, 1), (1, 4), (2, 0)]   # the plan's choice, one CTA per tile, split over four, CTA pairs
 
 
@@ -42,6 +42,16 @@ def positive(seed, *shape, t):
 
 def error(terms, segment):
     return (segment / 8 + terms / segment + 32) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("kernel", KERNELS, ids=str)
+def test_weight_gradients_in_fp32(kernel):
+    n, m, k, t = 33_000, 200, 136, torch.float16
+    x, dy, w = positive(1, n, k, t=t), positive(2, n, m, t=t), positive(3, m, k, t=t)
+    dw = torch.full((m, k), float("nan"), device="cuda")
+    bsk.linear_act_backward(KIND["f16"], w, k, x, k, None, m, dy, m, None, k, dw, k, None, bsk.GRAD_F32, 0, m, k, n, bsk.ACT_NONE)
+    want = dy.double().T @ x.double()
+    check(dw, want, error(n, SEGMENT_32) * want, torch.float32, "dW")
 
 
 @pytest.mark.parametrize("type_", ["bf16", "f16"])
