@@ -1380,7 +1380,6 @@ int launch_linear_instance(const LinearLaunch& g, cudaStream_t stream, char* msg
     const long long tiles = static_cast<long long>(p.job[0].num_tiles) + p.job[1].num_tiles;
     p.split = PAIR || g.split < 2 ? 1 : g.split;
     const int kb0 = p.job[0].kbs * p.job[0].k_sources;
-    const int kb1 = p.job[1].num_tiles > 0 ? p.job[1].kbs * p.job[1].k_sources : kb0;
     while (p.split > kb0) p.split /= 2;   // every CTA of a cluster has a k-block
     p.bias[0] = static_cast<const uint16_t*>(g.bias[0]);
     p.bias[1] = static_cast<const uint16_t*>(g.bias[1]);
