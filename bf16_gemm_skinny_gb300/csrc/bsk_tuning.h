@@ -147,8 +147,8 @@ int bsk_plan_kv_attention(int cache_type, int one_token_each, int num_seqs, int 
 
 /*
  * Test hook: the plan of a feed-forward product (mode 0: forward; 1: dx, 2: dW, 3: both) of n
- * tokens, M output and K input features on `sms` SMs under the current options, written to
- * plan[0..2]: CTA pairs (0/1), accumulator columns per tile, CTAs that share a tile's k loop.
+ * tokens, M output and K input features, in aligned rows and without kept values (either makes wide
+ * tiles dearer in a forward plan), on `sms` SMs under the current options, written to plan[0..2]: CTA pairs (0/1), accumulator columns per tile, CTAs that share a tile's k loop.
  */
 int bsk_plan_linear(int mode, int gated, int M, int K, int n, int sms, int* plan);
 

@@ -39,7 +39,8 @@ struct ActBackwardParams {
 };
 
 // 8 values of 16 bits from p on, n of them there.  Without ALIGNED a row may start at any
-// element: the values lie in two 16-byte units, and only units that hold one of them are read.
+// element: the values lie in two 16-byte units, and only units that hold one of them are read.  Either
+// way what else such a unit holds (the next columns of wider rows, say) is read and not used.
 template <bool ALIGNED>
 struct GradValues {
     uint4 lo, hi;

@@ -62,7 +62,7 @@ struct LinearLaunch {
     bool pair = false;             // 256-row tiles on CTA pairs, else 128-row tiles
     int bn = 128;                  // accumulator columns per tile (gated: both halves)
     int split = 1;                 // one-CTA tiles: CTAs of a cluster that share a tile's k loop
-    int group_m = 8;
+    int group_m = 16;              // tile rows that neighbouring CTAs go through column by column
 };
 
 constexpr int kFewRows = 64;   // tokens up to which the weights' stream is the bound of a forward pass
@@ -82,8 +82,9 @@ inline int linear_ring_room(bool few, bool staged)
 }
 // k-blocks per turn of the MMA warp.  A wait, a commit and the issue of its MMAs cost some 150 ns a
 // turn, more than a small tile's MMAs of a k-block take (250 ns a k-block for every width up to 128):
-// two or four k-blocks a turn, as far as the ring keeps a few turns.  Forward on pairs of 256 columns: one, which
-// measured the same (linear prefill 397 us, with two 400); gradients there two (396 us, with one 426).
+// two or four k-blocks a turn, as far as the ring keeps a few turns.  Forward on pairs of 256 columns one: with
+// two, 8192 x 8192 x 1024 took 82.9 us instead of 80.8, and longer k loops the same (4096 x 5120 x 17408 393 us,
+// gated 4096 x 17408 x 5120 708).  Gradients there two (8192 x 5120 x 4096 396 us, with one 426).
 inline int linear_group(const LinearLaunch& g, bool pair, int bn, bool few, bool staged)
 {
     const int fit = linear_ring_room(few, staged) / linear_block_bytes(g, pair, bn);

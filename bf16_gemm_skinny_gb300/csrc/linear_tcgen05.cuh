@@ -33,8 +33,8 @@
 // columns, which add them up in rank order (the result does not depend on timing).
 //
 // Bound and figures (GB300, back to back): few rows, the weights from HBM (gated
-// 17408 x 5120, 1 token: 53.8 us, 6.6 TB/s); many, the MMAs and at the last the power
-// (gated 4096 x 17408 x 5120: 704 us, 2070 TFLOP/s, for seconds 826 us); between, the latency
+// 17408 x 5120, 1 token: 55.4 us, 6.4 TB/s); many, the power limit (gated 4096 x 17408 x 5120:
+// 838 us, 1740 TFLOP/s) and in short bursts the MMAs (709 us, 2060 TFLOP/s); between, the latency
 // of a k loop's operands from L2 (95 GB/s an SM) and of the launch (4 us).
 #pragma once
 
@@ -422,8 +422,10 @@ __device__ __forceinline__ void block_move_elements(uint8_t* buf, E* g, long lon
     }
 }
 
-// The same, not inlined: in the linear kernels its registers and code would slow the common path
-// down (6992 x 8512 x 320: 45 against 36 us); in the gated ones they do not (333 x 2731 x 1024: 13.7 against 15.3).
+// The same, not inlined: in the linear kernels its registers and code slow the common path down, by
+// more than unaligned rows gain (inlined / called, us: 6992 x 8512 x 320 with SiLU 78 / 72, 777 x 1031 x 4099 with
+// kept z 21.8 / 22.2, 333 x 2731 x 1024 13.1 / 13.6); in the gated ones they do not (6992 x 4256 x 320 63.5 / 64.3,
+// 333 x 2731 x 1024 with kept g and u 12.5 / 14.6, 2000 x 2731 x 1024 23.0 / 25.0).
 template <typename E, bool LOAD>
 __device__ __noinline__ void block_move_elements_call(uint8_t* buf, E* g, long long ld, int rows, int n)
 {
@@ -678,8 +680,9 @@ __device__ __forceinline__ SplitTile split_tile(const LinearParams& p, int j, in
 // memory, split k, CTA pairs.  With few rows two CTAs fit on an SM by registers and shared memory, so
 // that the next launch's CTAs set up while this one's finish; split k of a forward pass likewise.
 // ANY, gradients: results of any alignment and width.  Without them the code for unaligned rows costs no
-// registers (spills of 40 instead of 220 bytes; gated backward 4096 x 17408 x 5120 1% faster), with
-// it they are stored by eight rows (linear backward 187 x 7695 x 2339 64 us, row by row 86).
+// registers (spill stores of 36 to 48 bytes on one CTA and pairs, with it 204 to 268; split k 220 and 356; gated
+// backward 4096 x 17408 x 5120 1% faster), with it they are stored by eight rows (linear backward
+// 187 x 7695 x 2339 64 us, row by row 86).  Forward kernels spill nothing.
 enum LinearKind : int { kKindDirect = 0, kKindOne = 1, kKindSplit = 2, kKindPair = 3 };
 
 template <int TYPE, int MODE, int KIND, bool ANY>

@@ -359,7 +359,9 @@ typedef enum bsk_grad_type {
  *   W, Wg, Wu        [M, K], w_stride elements between rows
  *   x, dx            [n, K];  residual, y, z, h, g, u, dy, dh  [n, M];  their own strides.
  *                    Strides are at least the row's length; only rows' elements are
- *                    read and written, so that a matrix may be a part of wider rows
+ *                    written and only their values used, so that a matrix may be a part
+ *                    of wider rows.  Inputs are read in aligned 16-byte units: the rest of
+ *                    a unit that holds an element of a row may be read with it
  *   bias...          [M], NULL: none
  *   residual         NULL: none.  It may be y itself (same address and stride)
  *   z; g, u          forward: where to keep them for a backward pass (rounded), NULL:
@@ -370,12 +372,17 @@ typedef enum bsk_grad_type {
  *   dW..., dbias...  [M, K] with dw_stride, and [M], of grad_type; with accumulate 1
  *                    they are added to what is there
  *
- * Sums are FP32.  The activation works on the unrounded FP32 z (g, u), and every
- * output is rounded once, to nearest even.  dz (dg, du) is rounded to `type` before
- * its products with W and x (without an activation dz is dy and nothing is
- * rounded); the sums for dbias take it unrounded.  An addition to 16-bit gradients is
- * made in FP32 and rounded.  The same call gives the same bits, but another number of
- * tokens may sum in another order.
+ * Sums are FP32.  A tensor-core accumulation cuts each of its sums toward zero, which
+ * adds up where the terms have one sign: gradients are therefore summed in segments
+ * (768 terms for FP32 results: 6e-6 of the sum at most as measured, 4096 for 16-bit ones: 2.7e-5),
+ * z, g and u, over K, in one accumulation (1.1e-4 of the sum at K = 17408; FP16's half
+ * step, 4.9e-4, is reached at some 76,000).  The activation works on the unrounded FP32
+ * z (g, u), and every output is rounded once, to nearest even.  dz (dg, du) is rounded to
+ * `type` before its products with W and x (without an activation dz is dy and nothing is
+ * rounded; in FP16 values below 2^-14 lose bits there, those up to 2^-25 all, so dy wants
+ * the usual scale of the loss); the sums for dbias take it unrounded.  An addition to 16-bit
+ * gradients is made in FP32 and rounded.  The same call gives the same bits, but another
+ * number of tokens may sum in another order.
  *
  * A stride or an address that is not a multiple of 16 bytes costs a copy of the
  * operand into a workspace (x, W..., dy without an activation).  The backward calls
